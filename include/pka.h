@@ -293,6 +293,97 @@ pka_status pka_merge_states(const float* v, const float* lse, const int32_t* ind
  * the unused high bits of the last byte are 0.  out_d holds (n + 7) / 8 bytes. */
 pka_status pka_packbits(const uint8_t* bools_d, int64_t n, uint8_t* out_d, void* stream);
 
+/* Rotary positions.  The pages apply none; they stand here because an append
+ * stores keys that are already rotated.
+ *   Pair i of the first rotary_dim elements of a head, (a, b), becomes
+ *     m (a cos t - b sin t),  m (a sin t + b cos t),   t = position * f_i,
+ *   with pairs (x[i], x[i + rotary_dim/2]) or, interleaved, (x[2i], x[2i+1]);
+ *   the other elements pass unchanged.  f_i in radians a position:
+ *     PKA_ROPE_PLAIN     f_i = base^(-2i / rotary_dim)
+ *     PKA_ROPE_LINEAR    f_i / factor (positions interpolated)
+ *     PKA_ROPE_BY_PARTS  (1 - w) f_i / factor + w f_i with
+ *                        w = clamp((r_i - low_rotations) /
+ *                                  (high_rotations - low_rotations), 0, 1),
+ *                        r_i = original_len f_i / 2 pi: pairs that turn often
+ *                        over the original context keep their frequency
+ *   or the caller's own frequencies.  A base changed for longer contexts is
+ *   given as base itself.  pka_rope holds them as fractions of a turn in 64
+ *   bits; the kernels form position * f_i modulo one turn without rounding,
+ *   so every int32 position (negative ones too) has its angle to about
+ *   1e-6 radians, and those below 2^24 to 2e-7. */
+typedef enum pka_rope_scaling {
+  PKA_ROPE_PLAIN = 0,
+  PKA_ROPE_LINEAR = 1,
+  PKA_ROPE_BY_PARTS = 2
+} pka_rope_scaling;
+
+typedef struct pka_rope_params {
+  int32_t rotary_dim;        /* even, 2 .. 128                                  */
+  int32_t interleaved;       /* 0: pairs (i, i + rotary_dim/2); 1: (2i, 2i+1)   */
+  int32_t scaling;           /* pka_rope_scaling                                */
+  int32_t reserved;          /* must be zero                                    */
+  double base;               /* >= 1                                            */
+  double factor;             /* >= 1 (LINEAR, BY_PARTS)                         */
+  double original_len;       /* > 0 (BY_PARTS)                                  */
+  double low_rotations;      /* >= 0 (BY_PARTS)                                 */
+  double high_rotations;     /* > low_rotations (BY_PARTS)                      */
+  double magnitude;          /* m; <= 0: 1                                      */
+  const double* frequencies_h; /* NULL, or rotary_dim/2 frequencies of at most  */
+                             /* pi in magnitude, in place of base and scaling   */
+} pka_rope_params;
+
+/* Plain data, filled once by pka_rope_init and passed to any number of calls. */
+typedef struct pka_rope {
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float magnitude;
+  int32_t reserved;          /* must be zero                                    */
+  uint64_t turns[64];        /* f_i / 2 pi of a turn, times 2^64                */
+} pka_rope;
+
+/* Fill *rope.  Host only; no CUDA call.  PKA_ERR_INVALID_ARG for values
+ * outside the ranges above, PKA_ERR_UNSUPPORTED for rotary_dim above 128. */
+pka_status pka_rope_init(const pka_rope_params* params, pka_rope* rope);
+
+/* Rotate q [rows, q_heads, head_dim] and k [rows, k_heads, head_dim] (bf16) to
+ * the positions positions_d [rows] (int32): arithmetic in float32, one
+ * rounding to bf16.  transpose = 1 applies the transposed map (turns by -t):
+ * the gradient of transpose = 0 and, with magnitude 1, its inverse.
+ *   Row strides are in elements, so the slices of a fused projection's output
+ *   are taken as they are; heads of a row are contiguous.  q_heads or k_heads
+ *   may be 0 (its pointers are then ignored).  q_out may be q (with the same
+ *   stride), and k_out k; otherwise outputs must not overlap inputs.
+ *   PKA_ERR_INVALID_ARG: buffers not 16-byte aligned, a row stride below
+ *   heads * head_dim (rows > 1) or not a multiple of 8, rotary_dim above
+ *   head_dim; PKA_ERR_UNSUPPORTED: head_dim not in {64, 128}, over 4096 heads. */
+pka_status pka_apply_rope(const pka_rope* rope, int32_t transpose, int32_t head_dim, int64_t rows,
+                          const int32_t* positions_d, const void* q, int32_t q_heads,
+                          int64_t q_row_stride, void* q_out, int64_t q_out_row_stride,
+                          const void* k, int32_t k_heads, int64_t k_row_stride, void* k_out,
+                          int64_t k_out_row_stride, void* stream);
+
+/* pka_append_paged_kv_cache of rotated rows, in one pass: row t of request r
+ * is rotated to its logical position kv_len - n_append + t (or to
+ * positions_d[row] when that is given; its slot stays the logical one), K and
+ * V go to their page slots, and the rotated q to q_out [nnz_new, Hq, D].
+ *   q [nnz_new, Hq, D], k_new and v_new [nnz_new, Hk, D] with row strides in
+ *   elements; q and q_out may both be NULL; q_out may be q when q is
+ *   contiguous.  e4m3 pools store the rotated float32 value divided by
+ *   k_scale, rounded once, magnitudes above 448 clamped to 448.
+ *   nnz_new is the rows of the buffers: rows from append_indptr_d[batch] on
+ *   belong to no request (a padded batch) and are neither read nor written.
+ *   A row whose position lies outside its request's pages, or whose page id
+ *   lies outside [0, num_pool_pages), is not appended and PKA_ERR_METADATA is
+ *   noted in the device error word (pka_get_device_error); the indptr arrays
+ *   themselves are trusted.  Alignment and page_stride as in
+ *   pka_append_paged_kv_cache; row strides as in pka_apply_rope. */
+pka_status pka_rope_append_paged_kv_cache(
+    const pka_params* params, const pka_rope* rope, int32_t batch, int64_t nnz_new, const void* q,
+    int64_t q_row_stride, void* q_out, const void* k_new, int64_t k_row_stride, const void* v_new,
+    int64_t v_row_stride, const int32_t* positions_d, const int32_t* append_indptr_d,
+    const int32_t* kv_indptr_d, const int32_t* kv_indices_d, const int32_t* last_page_len_d,
+    void* k, void* v, int64_t page_stride, int64_t num_pool_pages, void* stream);
+
 /* pka_run for callers that cannot allocate device memory when they run
  * (no cudaMalloc while a stream is captured into a CUDA graph, engines that
  * give a kernel library no allocator and own every byte of device memory, or

@@ -20,6 +20,7 @@ PKA_NHD, PKA_HND = 0, 1
 PKA_MASK_NONE, PKA_MASK_CAUSAL, PKA_MASK_CUSTOM = 0, 1, 2
 PKA_SPLIT_OFF, PKA_SPLIT_AUTO, PKA_SPLIT_FIXED = 0, 1, 2
 PKA_KV_BF16, PKA_KV_FP8_E4M3 = 0, 1
+PKA_ROPE_PLAIN, PKA_ROPE_LINEAR, PKA_ROPE_BY_PARTS = 0, 1, 2
 
 STATUS = {0: "PKA_OK", 1: "PKA_ERR_INVALID_ARG", 2: "PKA_ERR_METADATA", 3: "PKA_ERR_UNSUPPORTED",
           4: "PKA_ERR_WORKSPACE", 5: "PKA_ERR_STALE_PLAN", 6: "PKA_ERR_CUDA",
@@ -29,7 +30,8 @@ EXPORTED = ["pka_status_str", "pka_version", "pka_validate", "pka_plan_create",
             "pka_plan_destroy", "pka_plan", "pka_plan_get_info", "pka_plan_wait", "pka_run",
             "pka_append_paged_kv_cache", "pka_merge_states", "pka_packbits",
             "pka_get_device_error", "pka_last_error", "pka_run_static_scratch",
-            "pka_plan_cascade", "pka_selftest_bounded_wait", "pka_check_indices"]
+            "pka_plan_cascade", "pka_selftest_bounded_wait", "pka_check_indices",
+            "pka_rope_init", "pka_apply_rope", "pka_rope_append_paged_kv_cache"]
 
 
 class pka_params(ctypes.Structure):
@@ -43,6 +45,21 @@ class pka_params(ctypes.Structure):
                 ("kv_dtype", ctypes.c_int32), ("k_scale", ctypes.c_float),
                 ("v_scale", ctypes.c_float), ("decode_on_tensor_cores", ctypes.c_int32),
                 ("reserved", ctypes.c_int32 * 1)]
+
+
+class pka_rope_params(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("low_rotations", ctypes.c_double),
+                ("high_rotations", ctypes.c_double), ("magnitude", ctypes.c_double),
+                ("frequencies_h", ctypes.c_void_p)]
+
+
+class pka_rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("turns", ctypes.c_uint64 * 64)]
 
 
 class pka_plan_info(ctypes.Structure):
@@ -106,6 +123,12 @@ def lib():
         L.pka_get_device_error.argtypes = [P(i32), vp]
         L.pka_selftest_bounded_wait.argtypes = [i32, i32, vp]
         L.pka_check_indices.argtypes = [P(pka_params), i32, vp, vp, vp, i64, vp, i64, P(i64)]
+        L.pka_rope_init.argtypes = [P(pka_rope_params), P(pka_rope)]
+        L.pka_apply_rope.argtypes = [P(pka_rope), i32, i32, i64, vp, vp, i32, i64, vp, i64, vp,
+                                     i32, i64, vp, i64, vp]
+        L.pka_rope_append_paged_kv_cache.argtypes = [P(pka_params), P(pka_rope), i32, i64, vp,
+                                                     i64, vp, vp, i64, vp, i64, vp, vp, vp, vp,
+                                                     vp, vp, vp, i64, i64, vp]
         L.pka_last_error.argtypes = []
         L.pka_last_error.restype = ctypes.c_char_p
         for name in EXPORTED:
@@ -180,6 +203,54 @@ def _dev_pool(t, name, params=None):
     return t.data_ptr()
 
 
+def _here(t, name, dtype, dev):
+    """Pointer of a contiguous tensor of `dtype` on CUDA device `dev` (the
+    current one, where the call launches)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _here_rows(t, name, dev, heads=None, dim=None, rows=None):
+    """(pointer, row stride) of bf16 rows [rows, heads, dim]: the heads of a
+    row contiguous, the rows at any stride (slices of a fused projection)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, heads, head_dim]")
+    n, h, d = t.shape
+    if (rows is not None and n != rows) or (heads is not None and h != heads) or \
+            (dim is not None and d != dim):
+        raise ValueError(f"{name} must be [{rows}, {heads}, {dim}], got {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (h > 1 and s1 != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), s0 if n > 1 else h * d
+
+
+def _here_pool(t, name, params, dev):
+    """Pointer of a K/V pool [pages, P, Hk, D] or [pages, Hk, P, D] of the
+    params' layout (any page stride)."""
+    page = ((params.page_size, params.num_kv_heads) if params.layout == PKA_NHD
+            else (params.num_kv_heads, params.page_size)) + (params.head_dim,)
+    p = _dev_pool(t, name, params)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    if tuple(t.shape[-3:]) != page:
+        raise ValueError(f"{name}: pages of {tuple(t.shape[-3:])}, the params say {page}")
+    return p
+
+
 def _stream(stream) -> int | None:
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
@@ -211,6 +282,29 @@ def make_params(num_qo_heads, num_kv_heads, head_dim, page_size=1, layout="NHD",
     p.k_scale, p.v_scale = k_scale, v_scale
     p.decode_on_tensor_cores = int(bool(decode_on_tensor_cores))
     return p
+
+
+_ROPE_SCALING = {"none": PKA_ROPE_PLAIN, "linear": PKA_ROPE_LINEAR, "parts": PKA_ROPE_BY_PARTS}
+
+
+def make_rope(rotary_dim, base=10000.0, interleaved=False, scaling="none", factor=1.0,
+              original_len=0.0, low_rotations=1.0, high_rotations=32.0, magnitude=1.0,
+              frequencies=None) -> pka_rope:
+    """The rotation that pka_apply_rope and pka_rope_append_paged_kv_cache take
+    (see pka_rope_init in include/pka.h).  ``frequencies``: rotary_dim / 2
+    radians a position, in place of base and scaling."""
+    p = pka_rope_params()
+    p.rotary_dim, p.interleaved = rotary_dim, int(bool(interleaved))
+    p.scaling = _ROPE_SCALING[scaling] if isinstance(scaling, str) else scaling
+    p.base, p.factor, p.original_len = base, factor, original_len
+    p.low_rotations, p.high_rotations = low_rotations, high_rotations
+    p.magnitude = magnitude
+    if frequencies is not None:
+        f = np.ascontiguousarray(frequencies, dtype=np.float64)
+        if f.shape != (rotary_dim // 2,):
+            raise ValueError(f"frequencies: {rotary_dim // 2} values, got shape {f.shape}")
+        p.frequencies_h = f.ctypes.data
+    return pka_rope_init(p)
 
 
 # ---------------------------------------------------------------------------
@@ -338,6 +432,74 @@ def pka_append_paged_kv_cache(params, k_new, v_new, append_indptr, kv_indptr, kv
         _stream(stream))
     if check:
         _check(s, "pka_append_paged_kv_cache")
+    return s
+
+
+def pka_rope_init(rope_params) -> pka_rope:
+    rope = pka_rope()
+    _check(lib().pka_rope_init(ctypes.byref(rope_params), ctypes.byref(rope)), "pka_rope_init")
+    return rope
+
+
+def pka_apply_rope(rope, positions, q=None, q_out=None, k=None, k_out=None, transpose=False,
+                   stream=None, check=True) -> int:
+    """Rotate q and / or k ([rows, heads, head_dim], rows at any stride) into
+    q_out and k_out, which may be q and k themselves."""
+    if q is None and k is None:
+        raise ValueError("pka_apply_rope: q or k")
+    dev = torch.cuda.current_device()
+    rows, _, dim = (q if q is not None else k).shape
+    qa, ka = (None, 0, 0, None, 0), (None, 0, 0, None, 0)
+    if q is not None:
+        qp, qs = _here_rows(q, "q", dev, None, dim, rows)
+        op, os_ = _here_rows(q_out, "q_out", dev, q.shape[1], dim, rows)
+        qa = (qp, q.shape[1], qs, op, os_)
+    if k is not None:
+        kp, ks = _here_rows(k, "k", dev, None, dim, rows)
+        op, os_ = _here_rows(k_out, "k_out", dev, k.shape[1], dim, rows)
+        ka = (kp, k.shape[1], ks, op, os_)
+    pos = _here(positions, "positions", torch.int32, dev)
+    if positions.numel() != rows:
+        raise ValueError(f"positions: {rows} values, got {positions.numel()}")
+    s = lib().pka_apply_rope(ctypes.byref(rope), int(bool(transpose)), dim, rows, pos, *qa, *ka,
+                             _stream(stream))
+    if check:
+        _check(s, "pka_apply_rope")
+    return s
+
+
+def pka_rope_append_paged_kv_cache(params, rope, q, q_out, k_new, v_new, append_indptr, kv_indptr,
+                                   kv_indices, last_page_len, k, v, page_stride, positions=None,
+                                   stream=None, check=True) -> int:
+    """pka_append_paged_kv_cache of rotated rows; q and q_out may be None.  k
+    and v are the pools [pages, ...]; rows past append_indptr[-1] are left."""
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    hk, d, rows = params.num_kv_heads, params.head_dim, k_new.shape[0]
+    batch = append_indptr.numel() - 1
+    qp = qs = qo = None
+    if q is not None:
+        qp, qs = _here_rows(q, "q", dev, params.num_qo_heads, d, rows)
+        _here_rows(q_out, "q_out", dev, params.num_qo_heads, d, rows)
+        qo = _here(q_out, "q_out", torch.bfloat16, dev)
+    kp, ks = _here_rows(k_new, "k_new", dev, hk, d, rows)
+    vp, vs = _here_rows(v_new, "v_new", dev, hk, d, rows)
+    pos = None
+    if positions is not None:
+        pos = _here(positions, "positions", i32, dev)
+        if positions.numel() != rows:
+            raise ValueError(f"positions: {rows} values, got {positions.numel()}")
+    if kv_indptr.numel() != batch + 1 or last_page_len.numel() != batch:
+        raise ValueError("kv_indptr and last_page_len must describe append_indptr's requests")
+    if k.dim() != 4 or v.shape != k.shape:
+        raise ValueError("k and v must be pools [pages, ...] of one shape")
+    s = lib().pka_rope_append_paged_kv_cache(
+        ctypes.byref(params), ctypes.byref(rope), batch, rows, qp, qs or 0, qo, kp, ks, vp, vs,
+        pos, _here(append_indptr, "append_indptr", i32, dev),
+        _here(kv_indptr, "kv_indptr", i32, dev), _here(kv_indices, "kv_indices", i32, dev),
+        _here(last_page_len, "last_page_len", i32, dev), _here_pool(k, "k", params, dev),
+        _here_pool(v, "v", params, dev), int(page_stride), k.shape[0], _stream(stream))
+    if check:
+        _check(s, "pka_rope_append_paged_kv_cache")
     return s
 
 

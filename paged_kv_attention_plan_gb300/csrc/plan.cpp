@@ -15,6 +15,7 @@
 #include <unordered_map>
 #include <vector>
 
+#include "pka_cache.h"
 #include "pka_internal.h"
 
 using pka::AttnArgs;
@@ -636,6 +637,8 @@ size_t kv_scratch_bytes(const pka_params* p, int64_t rows) {
 void pka::set_last_error(const char* msg) {
   std::snprintf(g_last_error, sizeof(g_last_error), "%s", msg);
 }
+
+bool pka::params_valid(const pka_params* p) { return params_ok(p); }
 
 pka_status pka::cuda_failure(cudaError_t e, const char* where) { return cuda_fail(e, where); }
 

@@ -1,0 +1,509 @@
+// Rotary positions: pka_rope_init, pka_apply_rope and the append that rotates
+// (pka_rope_append_paged_kv_cache).
+//
+// Pair i of a head, (a, b), at position n is the complex number a + i b times
+// m exp(i n f_i).  The transposed map (the gradient) turns by -n f_i.
+//
+// Angles: f_i / 2 pi is held as a 64-bit fraction of a turn, F_i.  n * F_i
+// modulo 2^64 is then the angle modulo one turn with no rounding at all, for
+// every 32-bit n, from three integer instructions; its upper 32 bits, as a
+// float in [-1, 1) half turns, go to sincospif.  A float32 product n * f_i
+// would be off by up to 2^-24 n f_i radians, 0.06 at position 1,000,000.
+#include <cmath>
+
+#include "pka_cache.h"
+#include "pka_device.cuh"
+#include "pka_internal.h"
+
+namespace pka {
+namespace {
+
+// How the pairs of a head lie in it.
+enum RopeLayout {
+  kHalf = 0,       // (x[i], x[i + R/2]), R/2 a multiple of 8: whole 16-byte pieces
+  kAdjacent = 1,   // (x[2i], x[2i + 1])
+  kScattered = 2,  // (x[i], x[i + R/2]), any other R: element by element
+};
+
+constexpr int kMaxHeads = 4096;  // of a row; keeps the launch's second grid axis small
+
+struct RopeArgs {
+  const uint16_t* q;  // [rows, q_heads, D], row stride in elements
+  const uint16_t* k;
+  const uint16_t* v;  // append only
+  uint16_t* q_out;
+  uint16_t* k_out;    // apply only
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  int64_t rows;
+  const int32_t* positions;  // [rows]; append: may be null (logical positions)
+  int q_heads, k_heads;
+  int rotary_dim;
+  float magnitude;
+  float sine_sign;           // -1 for the transposed map
+  int steps_per_part;        // head steps that one warp takes of its row
+  // append: the page table and the pools
+  int32_t batch;
+  const int32_t* append_indptr;
+  const int32_t* kv_indptr;
+  const int32_t* kv_indices;
+  const int32_t* last_page_len;
+  void* k_pool;
+  void* v_pool;
+  int64_t page_stride;
+  int64_t num_pages;
+  int page_size;
+  int layout;
+  float k_scale, v_scale;    // e4m3 pools
+  float k_inv, v_inv;        // exact reciprocal of a power-of-two scale, else 0
+  int32_t* err;
+  uint64_t turns[64];        // F_i
+};
+
+// 8 values divided by a pool's scale (correctly rounded) and rounded to
+// nearest even e4m3, magnitudes above 448 clamped; 8 codes, little-endian.
+__device__ __forceinline__ uint2 to_e4m3x8(const float (&x)[8], float scale, float inv) {
+  uint32_t pk[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float lo = inv > 0.f ? x[2 * i] * inv : __fdiv_rn(x[2 * i], scale);
+    const float hi = inv > 0.f ? x[2 * i + 1] * inv : __fdiv_rn(x[2 * i + 1], scale);
+    asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n cvt.u32.u16 %0, t;\n}"
+        : "=r"(pk[i])
+        : "f"(hi), "f"(lo));
+  }
+  return make_uint2(pk[0] | (pk[1] << 16), pk[2] | (pk[3] << 16));
+}
+
+__device__ __forceinline__ void unpack8(const uint32_t (&w)[4], float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = bf16x2_to_float2(w[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+// A lane's piece of a head: 16 bytes at element `off`, or (kScattered) the
+// eight elements elem(0) .. elem(7).
+template <int L, class F>
+__device__ __forceinline__ void load_piece(const uint16_t* p, int off, F elem, uint32_t (&w)[4]) {
+  if constexpr (L == kScattered) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = p[elem(2 * i)] | (uint32_t)p[elem(2 * i + 1)] << 16;
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4*>(p + off);
+    w[0] = x.x;
+    w[1] = x.y;
+    w[2] = x.z;
+    w[3] = x.w;
+  }
+}
+
+template <int L, class F>
+__device__ __forceinline__ void store_piece(uint16_t* p, int off, F elem, const uint32_t (&w)[4]) {
+  if constexpr (L == kScattered) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[elem(2 * i)] = (uint16_t)w[i];
+      p[elem(2 * i + 1)] = (uint16_t)(w[i] >> 16);
+    }
+  } else {
+    *reinterpret_cast<uint4*>(p + off) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <int L, class F>
+__device__ __forceinline__ void store_codes(uint8_t* p, int off, F elem, uint2 w) {
+  if constexpr (L == kScattered) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[elem(j)] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+  } else {
+    *reinterpret_cast<uint2*>(p + off) = w;
+  }
+}
+
+// Element of head h of a slot of a page.
+template <int D>
+__device__ __forceinline__ int64_t pool_offset(const RopeArgs& a, int page, int slot, int h) {
+  return (int64_t)page * a.page_stride +
+         (a.layout == PKA_NHD ? ((int64_t)slot * a.k_heads + h) * D
+                              : ((int64_t)h * a.page_size + slot) * D);
+}
+
+// A warp takes a row and walks its heads (q, then k, then v as one list).  A
+// head is D/16 units of 8 pairs; a lane keeps one unit (u) and takes it from
+// each of the 32 / (D/16) heads of a step, so its 8 sines and cosines serve
+// the whole row.  A unit is two 16-byte pieces A and B of the head: pair j is
+// (A[j], B[j]), or, for adjacent pairs, the pairs inside A and inside B.
+// Units past rotary_dim are copied bit by bit.
+template <int D, int L, bool APPEND, bool F8>
+__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int UNITS = D / 16;      // lanes of a head
+  constexpr int HPS = 32 / UNITS;    // heads of a step
+  constexpr int K = 8 / HPS;         // pairs whose sine and cosine a lane computes
+  const int lane = threadIdx.x & 31;
+  const int u = lane % UNITS, sub = lane / UNITS;
+  const int rd = a.rotary_dim;
+  const int heads = a.q_heads + (APPEND ? 2 : 1) * a.k_heads;
+
+  // where the lane's pieces lie in a head, and which of its pairs rotate
+  int off_a, off_b;
+  uint32_t turning = 0;
+  auto pair_of = [&](int j) { return L != kAdjacent ? 8 * u + j
+                                     : j < 4 ? 4 * u + j : D / 4 + 4 * u + j - 4; };
+#pragma unroll
+  for (int j = 0; j < 8; ++j) turning |= (pair_of(j) < rd / 2 ? 1u : 0u) << j;
+  if (L == kHalf) {
+    const int t = u - rd / 16;
+    off_a = t < 0 ? 8 * u : rd + 16 * t;
+    off_b = t < 0 ? 8 * u + rd / 2 : off_a + 8;
+  } else {
+    off_a = 8 * u;
+    off_b = 8 * u + D / 2;
+  }
+  // kScattered: elements of pair j
+  auto first_of = [&](int j) { const int p = 8 * u + j; return p < rd / 2 ? p : 2 * p; };
+  auto second_of = [&](int j) { const int p = 8 * u + j;
+                                return p < rd / 2 ? p + rd / 2 : 2 * p + 1; };
+
+  uint64_t turn[K];
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int p = pair_of(sub * K + i);
+    turn[i] = p < rd / 2 ? a.turns[p] : 0;
+  }
+
+  const int h0 = blockIdx.y * a.steps_per_part * HPS;
+  const int h1 = min(heads, h0 + a.steps_per_part * HPS);
+  const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  for (int64_t row = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5); row < a.rows;
+       row += nwarps) {
+    int64_t pos = 0;
+    int32_t page = -1;
+    int slot = 0;
+    if constexpr (APPEND) {
+      if (row >= a.append_indptr[a.batch]) continue;  // a row of no request
+      const int r = warp_find(a.append_indptr, a.batch, row, lane);
+      const int first = a.append_indptr[r], n_app = a.append_indptr[r + 1] - first;
+      const int kv0 = a.kv_indptr[r], pages = a.kv_indptr[r + 1] - kv0;
+      const int64_t kv_len = (int64_t)(pages - 1) * a.page_size + a.last_page_len[r];
+      pos = kv_len - n_app + (row - first);
+      const int64_t nth = pos >= 0 ? pos / a.page_size : -1;
+      if (nth >= 0 && nth < pages) {
+        page = a.kv_indices[kv0 + nth];
+        slot = (int)(pos - nth * a.page_size);
+      }
+      if (page < 0 || page >= a.num_pages) {
+        if (lane == 0) note_error(a.err, PKA_ERR_METADATA);
+        page = -1;
+      }
+    }
+    if (!APPEND || a.positions) pos = a.positions[row];
+
+
+    // sines and cosines: K pairs a lane, exchanged among the lanes of a unit
+    float c[8], s[8];
+    {
+      float ck[K], sk[K];
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        const uint64_t phase = (uint64_t)pos * turn[i] + (1ull << 31);
+        sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &sk[i], &ck[i]);
+        ck[i] *= a.magnitude;
+        sk[i] *= a.magnitude * a.sine_sign;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        c[j] = __shfl_sync(0xffffffffu, ck[j % K], (j / K) * UNITS + u);
+        s[j] = __shfl_sync(0xffffffffu, sk[j % K], (j / K) * UNITS + u);
+      }
+    }
+
+    for (int h = h0 + sub; h < h1; h += HPS) {
+      const bool is_q = h < a.q_heads;
+      const bool is_v = APPEND && h >= a.q_heads + a.k_heads;
+      const int hh = is_q ? h : is_v ? h - a.q_heads - a.k_heads : h - a.q_heads;
+      const uint16_t* src = (is_q ? a.q + row * a.q_stride
+                             : is_v ? a.v + row * a.v_stride : a.k + row * a.k_stride) +
+                            (int64_t)hh * D;
+      uint32_t wa[4], wb[4];
+      load_piece<L>(src, off_a, first_of, wa);
+      load_piece<L>(src, off_b, second_of, wb);
+      float xa[8], xb[8];
+      unpack8(wa, xa);
+      unpack8(wb, xb);
+      if (!is_v) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          // pair j: (A[j], B[j]), or adjacent elements of A (j < 4) or of B
+          float& x = L != kAdjacent ? xa[j] : j < 4 ? xa[2 * j] : xb[2 * (j - 4)];
+          float& y = L != kAdjacent ? xb[j] : j < 4 ? xa[2 * j + 1] : xb[2 * (j - 4) + 1];
+          if (turning >> j & 1) {
+            const float t = x * c[j] - y * s[j];
+            y = x * s[j] + y * c[j];
+            x = t;
+          }
+        }
+      }
+      const bool to_pool = APPEND && !is_q;
+      if (to_pool && page < 0) continue;
+      if (F8 && to_pool) {
+        const float scale = is_v ? a.v_scale : a.k_scale, inv = is_v ? a.v_inv : a.k_inv;
+        uint8_t* p = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) +
+                     pool_offset<D>(a, page, slot, hh);
+        store_codes<L>(p, off_a, first_of, to_e4m3x8(xa, scale, inv));
+        store_codes<L>(p, off_b, second_of, to_e4m3x8(xb, scale, inv));
+        continue;
+      }
+      // rotated elements rounded once to bf16; the others keep their bits
+      if (!is_v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t ya = float2_to_bf16x2(xa[2 * i], xa[2 * i + 1]);
+          const uint32_t yb = float2_to_bf16x2(xb[2 * i], xb[2 * i + 1]);
+          uint32_t ma, mb;  // the rotated halves of word i of A and of B
+          if constexpr (L == kAdjacent) {
+            ma = turning >> i & 1 ? ~0u : 0u;
+            mb = turning >> (i + 4) & 1 ? ~0u : 0u;
+          } else {
+            ma = mb = (turning >> (2 * i) & 1 ? 0xffffu : 0u) |
+                      (turning >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
+          }
+          wa[i] = (ya & ma) | (wa[i] & ~ma);
+          wb[i] = (yb & mb) | (wb[i] & ~mb);
+        }
+      }
+      uint16_t* p;
+      if (to_pool)
+        p = static_cast<uint16_t*>(is_v ? a.v_pool : a.k_pool) + pool_offset<D>(a, page, slot, hh);
+      else
+        p = (is_q ? a.q_out + row * a.q_out_stride : a.k_out + row * a.k_out_stride) +
+            (int64_t)hh * D;
+      store_piece<L>(p, off_a, first_of, wa);
+      store_piece<L>(p, off_b, second_of, wb);
+    }
+  }
+}
+
+template <int D, int L, bool APPEND, bool F8>
+cudaError_t launch(const RopeArgs& args, cudaStream_t stream) {
+  constexpr int HPS = 512 / D;  // heads of a step
+  RopeArgs a = args;
+  const int heads = a.q_heads + (APPEND ? 2 : 1) * a.k_heads;
+  const int steps = (heads + HPS - 1) / HPS;
+  const int sms = current_device_sms();
+  const int64_t warps = 32 * (int64_t)(sms > 0 ? sms : 1);
+  int64_t per = (a.rows * steps + warps - 1) / warps;
+  per = per < 1 ? 1 : per > steps ? steps : per;
+  const int parts = (int)((steps + per - 1) / per);
+  a.steps_per_part = (int)per;
+  int64_t blocks = (a.rows + 7) / 8;
+  const int64_t cap = 8 * (int64_t)(sms > 0 ? sms : 1);
+  if (blocks > cap) blocks = cap;
+  rope_kernel<D, L, APPEND, F8><<<dim3((unsigned)blocks, (unsigned)parts), 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <bool APPEND, bool F8>
+cudaError_t launch_any(const RopeArgs& a, int head_dim, bool adjacent, cudaStream_t stream) {
+  const int l = adjacent ? kAdjacent : a.rotary_dim % 16 == 0 ? kHalf : kScattered;
+  if (head_dim == 128)
+    return l == kAdjacent ? launch<128, kAdjacent, APPEND, F8>(a, stream)
+           : l == kHalf   ? launch<128, kHalf, APPEND, F8>(a, stream)
+                          : launch<128, kScattered, APPEND, F8>(a, stream);
+  return l == kAdjacent ? launch<64, kAdjacent, APPEND, F8>(a, stream)
+         : l == kHalf   ? launch<64, kHalf, APPEND, F8>(a, stream)
+                        : launch<64, kScattered, APPEND, F8>(a, stream);
+}
+
+bool rope_valid(const pka_rope* r, int head_dim) {
+  return r && r->rotary_dim >= 2 && r->rotary_dim % 2 == 0 && r->rotary_dim <= head_dim &&
+         (r->interleaved == 0 || r->interleaved == 1) && r->reserved == 0 &&
+         std::isfinite(r->magnitude);
+}
+
+void take_rope(RopeArgs* a, const pka_rope* r) {
+  a->rotary_dim = r->rotary_dim;
+  a->magnitude = r->magnitude;
+  a->sine_sign = 1.f;
+  for (int i = 0; i < r->rotary_dim / 2; ++i) a->turns[i] = r->turns[i];
+}
+
+// Rows of `heads` heads: 16-byte pieces at a row stride of whole pieces, rows apart.
+bool rows_ok(const void* p, int64_t stride, int64_t rows, int heads, int head_dim) {
+  if (!p || (reinterpret_cast<uintptr_t>(p) & 15) || (stride & 7)) return false;
+  return rows <= 1 ? stride >= 0 : stride >= (int64_t)heads * head_dim;
+}
+
+// In place or apart: the same rows, or (as far as the first bytes tell) others.
+bool out_ok(const void* in, int64_t in_stride, const void* out, int64_t out_stride) {
+  return in != out || in_stride == out_stride;
+}
+
+// Reciprocal of a power-of-two scale (exact), else 0: divide.
+float pow2_inv(float s) {
+  int e = 0;
+  return std::frexp(s, &e) == 0.5f ? std::ldexp(1.0f, 1 - e) : 0.f;
+}
+
+}  // namespace
+}  // namespace pka
+
+extern "C" {
+
+pka_status pka_rope_init(const pka_rope_params* p, pka_rope* rope) {
+  if (!p || !rope) return PKA_ERR_INVALID_ARG;
+  if (p->reserved != 0 || (p->interleaved != 0 && p->interleaved != 1)) return PKA_ERR_INVALID_ARG;
+  if (p->rotary_dim < 2 || p->rotary_dim % 2) return PKA_ERR_INVALID_ARG;
+  if (p->rotary_dim > 128) return PKA_ERR_UNSUPPORTED;
+  if (!std::isfinite(static_cast<float>(p->magnitude))) return PKA_ERR_INVALID_ARG;
+  if (!p->frequencies_h) {
+    if (!(p->base >= 1.0) || !std::isfinite(p->base)) return PKA_ERR_INVALID_ARG;
+    if (p->scaling < PKA_ROPE_PLAIN || p->scaling > PKA_ROPE_BY_PARTS) return PKA_ERR_INVALID_ARG;
+    if (p->scaling != PKA_ROPE_PLAIN && (!(p->factor >= 1.0) || !std::isfinite(p->factor)))
+      return PKA_ERR_INVALID_ARG;
+    if (p->scaling == PKA_ROPE_BY_PARTS &&
+        (!(p->original_len > 0.0) || !std::isfinite(p->original_len) ||
+         !(p->low_rotations >= 0.0) || !(p->high_rotations > p->low_rotations) ||
+         !std::isfinite(p->high_rotations)))
+      return PKA_ERR_INVALID_ARG;
+  }
+  const double pi = 3.14159265358979323846;
+  const int half = p->rotary_dim / 2;
+  pka_rope out{};
+  out.rotary_dim = p->rotary_dim;
+  out.interleaved = p->interleaved;
+  out.magnitude = p->magnitude > 0.0 ? static_cast<float>(p->magnitude) : 1.f;
+  for (int i = 0; i < half; ++i) {
+    double f;
+    if (p->frequencies_h) {
+      f = p->frequencies_h[i];
+      if (!(std::fabs(f) <= pi)) return PKA_ERR_INVALID_ARG;
+    } else {
+      f = std::pow(p->base, -2.0 * i / p->rotary_dim);
+      if (p->scaling == PKA_ROPE_LINEAR) f /= p->factor;
+      if (p->scaling == PKA_ROPE_BY_PARTS) {
+        const double turns = p->original_len * f / (2.0 * pi);
+        double keep = (turns - p->low_rotations) / (p->high_rotations - p->low_rotations);
+        keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+        f = (1.0 - keep) * (f / p->factor) + keep * f;
+      }
+    }
+    // |f| / 2 pi <= 1/2, so the fraction fits; a negative frequency is the
+    // fraction's two's complement
+    const uint64_t t = static_cast<uint64_t>(std::ldexp(std::fabs(f) / (2.0 * pi), 64));
+    out.turns[i] = f < 0.0 ? 0 - t : t;
+  }
+  *rope = out;
+  return PKA_OK;
+}
+
+pka_status pka_apply_rope(const pka_rope* rope, int32_t transpose, int32_t head_dim, int64_t rows,
+                          const int32_t* positions_d, const void* q, int32_t q_heads,
+                          int64_t q_row_stride, void* q_out, int64_t q_out_row_stride,
+                          const void* k, int32_t k_heads, int64_t k_row_stride, void* k_out,
+                          int64_t k_out_row_stride, void* stream) {
+  if (!rope || (transpose != 0 && transpose != 1) || rows < 0 || q_heads < 0 || k_heads < 0)
+    return PKA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PKA_ERR_UNSUPPORTED;
+  if (q_heads > pka::kMaxHeads || k_heads > pka::kMaxHeads) return PKA_ERR_UNSUPPORTED;
+  if (!pka::rope_valid(rope, head_dim)) return PKA_ERR_INVALID_ARG;
+  if (rows == 0 || (q_heads == 0 && k_heads == 0)) return PKA_OK;
+  if (!positions_d) return PKA_ERR_INVALID_ARG;
+  if (q_heads > 0 && (!pka::rows_ok(q, q_row_stride, rows, q_heads, head_dim) ||
+                      !pka::rows_ok(q_out, q_out_row_stride, rows, q_heads, head_dim) ||
+                      !pka::out_ok(q, q_row_stride, q_out, q_out_row_stride)))
+    return PKA_ERR_INVALID_ARG;
+  if (k_heads > 0 && (!pka::rows_ok(k, k_row_stride, rows, k_heads, head_dim) ||
+                      !pka::rows_ok(k_out, k_out_row_stride, rows, k_heads, head_dim) ||
+                      !pka::out_ok(k, k_row_stride, k_out, k_out_row_stride)))
+    return PKA_ERR_INVALID_ARG;
+  pka::RopeArgs a{};
+  pka::take_rope(&a, rope);
+  if (transpose) a.sine_sign = -1.f;
+  a.rows = rows;
+  a.positions = positions_d;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.q_stride = q_row_stride;
+  a.k_stride = k_row_stride;
+  a.q_out_stride = q_out_row_stride;
+  a.k_out_stride = k_out_row_stride;
+  a.q_heads = q_heads;
+  a.k_heads = k_heads;
+  const cudaError_t e = pka::launch_any<false, false>(a, head_dim, rope->interleaved != 0,
+                                                      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKA_OK : pka::cuda_failure(e, "rope launch");
+}
+
+pka_status pka_rope_append_paged_kv_cache(
+    const pka_params* p, const pka_rope* rope, int32_t batch, int64_t nnz_new, const void* q,
+    int64_t q_row_stride, void* q_out, const void* k_new, int64_t k_row_stride, const void* v_new,
+    int64_t v_row_stride, const int32_t* positions_d, const int32_t* append_indptr_d,
+    const int32_t* kv_indptr_d, const int32_t* kv_indices_d, const int32_t* last_page_len_d,
+    void* k, void* v, int64_t page_stride, int64_t num_pool_pages, void* stream) {
+  if (!pka::params_valid(p) || batch < 0 || nnz_new < 0 || num_pool_pages < 0)
+    return PKA_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128) return PKA_ERR_UNSUPPORTED;
+  if (p->kv_ragged) return PKA_ERR_UNSUPPORTED;
+  if (p->num_qo_heads > pka::kMaxHeads || p->num_kv_heads > pka::kMaxHeads)
+    return PKA_ERR_UNSUPPORTED;
+  if (!pka::rope_valid(rope, p->head_dim)) return PKA_ERR_INVALID_ARG;
+  if (nnz_new == 0 || batch == 0) return PKA_OK;
+  if (!append_indptr_d || !kv_indptr_d || !kv_indices_d || !last_page_len_d || !k || !v ||
+      page_stride <= 0)
+    return PKA_ERR_INVALID_ARG;
+  const bool f8 = p->kv_dtype == PKA_KV_FP8_E4M3;
+  const uintptr_t mis = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
+  if ((mis & 15) || (page_stride & (f8 ? 15 : 7))) return PKA_ERR_INVALID_ARG;
+  const int d = p->head_dim, hk = p->num_kv_heads;
+  const int64_t q_out_stride = (int64_t)p->num_qo_heads * d;
+  if (!pka::rows_ok(k_new, k_row_stride, nnz_new, hk, d) ||
+      !pka::rows_ok(v_new, v_row_stride, nnz_new, hk, d))
+    return PKA_ERR_INVALID_ARG;
+  if (!q != !q_out) return PKA_ERR_INVALID_ARG;
+  if (q && (!pka::rows_ok(q, q_row_stride, nnz_new, p->num_qo_heads, d) ||
+            !pka::rows_ok(q_out, q_out_stride, nnz_new, p->num_qo_heads, d) ||
+            !pka::out_ok(q, q_row_stride, q_out, q_out_stride)))
+    return PKA_ERR_INVALID_ARG;
+  pka::RopeArgs a{};
+  pka::take_rope(&a, rope);
+  a.rows = nnz_new;
+  a.positions = positions_d;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k_new);
+  a.v = static_cast<const uint16_t*>(v_new);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_stride = q_row_stride;
+  a.k_stride = k_row_stride;
+  a.v_stride = v_row_stride;
+  a.q_out_stride = q_out_stride;
+  a.q_heads = q ? p->num_qo_heads : 0;
+  a.k_heads = hk;
+  a.batch = batch;
+  a.append_indptr = append_indptr_d;
+  a.kv_indptr = kv_indptr_d;
+  a.kv_indices = kv_indices_d;
+  a.last_page_len = last_page_len_d;
+  a.k_pool = k;
+  a.v_pool = v;
+  a.page_stride = page_stride;
+  a.num_pages = num_pool_pages;
+  a.page_size = p->page_size;
+  a.layout = p->layout;
+  a.k_scale = p->k_scale > 0.f ? p->k_scale : 1.f;
+  a.v_scale = p->v_scale > 0.f ? p->v_scale : 1.f;
+  a.k_inv = pka::pow2_inv(a.k_scale);
+  a.v_inv = pka::pow2_inv(a.v_scale);
+  a.err = pka::device_error_word();
+  const bool adjacent = rope->interleaved != 0;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = f8 ? pka::launch_any<true, true>(a, d, adjacent, st)
+                           : pka::launch_any<true, false>(a, d, adjacent, st);
+  return e == cudaSuccess ? PKA_OK : pka::cuda_failure(e, "rope append launch");
+}
+
+}  // extern "C"
