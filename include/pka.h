@@ -384,6 +384,93 @@ pka_status pka_rope_append_paged_kv_cache(
     const int32_t* kv_indptr_d, const int32_t* kv_indices_d, const int32_t* last_page_len_d,
     void* k, void* v, int64_t page_stride, int64_t num_pool_pages, void* stream);
 
+/* The pages of the cache.  The caller owns the page table ("KV-Cache layouts",
+ * "Page table layout"); these calls keep it on the device.  Their one state is
+ * page_refs_d [num_pages] int32: the references that hold each page (table
+ * entries, and whatever else the caller counts), 0 for a free page.  Page ids
+ * chosen are always the lowest free ones, so results do not depend on timing.
+ * Violations that only the device can see are stepped around and noted in the
+ * device error word (pka_get_device_error; of several the largest code stays).
+ * Two calls on one page_refs_d must be ordered (one stream, or events). */
+
+/* Copy pages inside the pools, for every layer at once: for i < the count,
+ * slots 0 .. slots_d[i] - 1 (all when slots_d is NULL) of page src_d[i] over
+ * those of page dst_d[i], K and V.
+ *   k and v point at page 0 of the first layer's pools; page p starts
+ *   page_stride elements after page p-1, layer l layer_stride elements after
+ *   layer l-1 (ignored for one layer).  Uses params->num_kv_heads, head_dim,
+ *   page_size, layout and kv_dtype.  The count is *num_copies_d (clamped to
+ *   0 .. max_copies), or max_copies when num_copies_d is NULL: a list made on
+ *   the device needs no read-back.
+ *   The copies run at once, so no page may be written twice or both read and
+ *   written (src_d[i] == dst_d[i] is skipped).  Entries with a page id outside
+ *   [0, num_pool_pages) or slots outside 0..page_size are skipped and
+ *   PKA_ERR_METADATA is noted.  Alignment as in pka_append_paged_kv_cache
+ *   (layer_stride like page_stride); PKA_ERR_UNSUPPORTED: over 32767 layers,
+ *   pages of 2 GB, ragged K/V. */
+pka_status pka_copy_pages(const pka_params* params, int32_t num_layers, void* k, void* v,
+                          int64_t page_stride, int64_t layer_stride, int64_t num_pool_pages,
+                          const int32_t* src_d, const int32_t* dst_d, const int32_t* slots_d,
+                          int64_t max_copies, const int32_t* num_copies_d, void* stream);
+
+/* Take the n lowest free pages: their ids, ascending, to pages_d [n], one
+ * reference each.  With fewer free pages nothing is taken, pages_d is filled
+ * with -1 and PKA_ERR_WORKSPACE is noted (returned at once for n > num_pages). */
+pka_status pka_alloc_pages(int32_t* page_refs_d, int32_t num_pages, int32_t n, int32_t* pages_d,
+                           void* stream);
+
+/* Drop one reference for each entry of pages_d [n]; a page may appear several
+ * times.  An id outside [0, num_pages) and a reference that is not there are
+ * skipped and PKA_ERR_METADATA is noted. */
+pka_status pka_free_pages(int32_t* page_refs_d, int32_t num_pages, const int32_t* pages_d,
+                          int64_t n, void* stream);
+
+/* Page tables of requests that continue others (samples of one prompt, beams,
+ * a request that grows): child c continues request parent_d[c] of the given
+ * tables, or nothing (-1), and has child_indptr_d[c+1] - child_indptr_d[c] >=
+ * its parent's pages (child_indptr_d[0] == 0).
+ *   Its table gets its parent's full pages (shared: one reference more), then
+ *   fresh pages, the lowest free ids in table order over all children.  Where
+ *   the parent's last page is partly filled (last_page_len < page_size), the
+ *   child's first fresh page stands in for it and the copy is listed:
+ *   copy_src_d, copy_dst_d, copy_slots_d [num_children], in child order, for
+ *   pka_copy_pages with num_copies_d = counts_d.  counts_d [2] = copies listed,
+ *   fresh pages taken.  The parents keep their tables and references: a
+ *   request that is replaced by its children is returned with pka_free_pages.
+ *   kv_indices_d holds num_indices entries, child_indices_d num_child_indices
+ *   (child_indptr_d[num_children] of them are written).  Malformed arrays
+ *   (decreasing or past those sizes, a parent out of range, a child shorter
+ *   than its parent, last_page_len outside 1..page_size) and a lack of free
+ *   pages refuse the whole call on the device: nothing but counts_d = {-1, -1}
+ *   is written and PKA_ERR_METADATA or PKA_ERR_WORKSPACE is noted.  Page ids
+ *   outside [0, num_pages) in a parent's table are carried over and noted.
+ *   The parents' pages must be held (a reference at least).
+ *   PKA_ERR_UNSUPPORTED: more than PKA_MAX_FORK_CHILDREN children. */
+#define PKA_MAX_FORK_CHILDREN 8192
+pka_status pka_fork_pages(int32_t page_size, int32_t* page_refs_d, int32_t num_pages,
+                          int32_t num_parents, const int32_t* kv_indptr_d,
+                          const int32_t* kv_indices_d, int32_t num_indices,
+                          const int32_t* last_page_len_d, int32_t num_children,
+                          const int32_t* parent_d, const int32_t* child_indptr_d,
+                          int32_t* child_indices_d, int32_t num_child_indices,
+                          int32_t* copy_src_d, int32_t* copy_dst_d, int32_t* copy_slots_d,
+                          int32_t* counts_d, void* stream);
+
+/* Move the L live pages (those with references) into pages 0 .. L-1, with the
+ * fewest moves: the i-th free page below L, ascending, takes the i-th live
+ * page at L or above, descending.
+ *   copy_src_d, copy_dst_d [num_pages / 2]: the moves, for pka_copy_pages with
+ *   num_copies_d = counts_d.  counts_d [2] = moves, L.  page_map_d [num_pages]:
+ *   the new id of every live page, -1 for free ones.  page_refs_out_d
+ *   [num_pages] and kv_indices_out_d [num_indices]: references and table
+ *   entries under the new ids; each may be its input array.  A table entry
+ *   that names no live page stays as it is and PKA_ERR_METADATA is noted. */
+pka_status pka_compact_pages(const int32_t* page_refs_d, int32_t num_pages,
+                             const int32_t* kv_indices_d, int64_t num_indices,
+                             int32_t* page_refs_out_d, int32_t* kv_indices_out_d,
+                             int32_t* page_map_d, int32_t* copy_src_d, int32_t* copy_dst_d,
+                             int32_t* counts_d, void* stream);
+
 /* pka_run for callers that cannot allocate device memory when they run
  * (no cudaMalloc while a stream is captured into a CUDA graph, engines that
  * give a kernel library no allocator and own every byte of device memory, or

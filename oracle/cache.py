@@ -60,3 +60,79 @@ def append_slots(append_indptr, kv_indptr, kv_indices, last_page_len, page_size)
             pos = n - (a1 - a0) + t
             out.append((a0 + t, pos) + tuple(ref.token_address(pages, pos, page_size)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# The pages of the cache
+# ---------------------------------------------------------------------------
+
+def copy_pages(pool, src, dst, slots=None, *, layout="NHD"):
+    """A copy of pool [..., pages, page, heads, dim] (HND: heads, page) with the
+    first slots[i] slots of page src[i] written over those of page dst[i]."""
+    out = np.array(pool, copy=True)
+    axis = 0 if layout == "NHD" else 1
+    for i in range(len(src)):
+        n = None if slots is None else int(slots[i])
+        part = (Ellipsis, int(src[i])), (Ellipsis, int(dst[i]))
+        keep = (slice(None),) * axis + (slice(0, n),) + (slice(None),) * (2 - axis)
+        out[part[1] + keep] = pool[part[0] + keep]
+    return out
+
+
+def alloc_pages(refs, n):
+    """(page ids, new references): the n lowest pages without a reference."""
+    refs, pages = list(refs), []
+    for p, r in enumerate(refs):
+        if r <= 0 and len(pages) < n:
+            pages.append(p)
+            refs[p] = 1
+    if len(pages) < n:
+        raise MemoryError("not enough free pages")
+    return pages, refs
+
+
+def free_pages(refs, pages):
+    """References after one is dropped for each entry."""
+    refs = list(refs)
+    for p in pages:
+        if not 0 <= p < len(refs) or refs[p] <= 0:
+            raise ValueError("a reference that is not there")
+        refs[p] -= 1
+    return refs
+
+
+def fork_pages(refs, tables, lens, page_size, parent, child_pages):
+    """Tables of children.  tables / lens: page ids and token counts of the
+    parents; parent: -1 or a parent's index; child_pages: pages of each child.
+    Returns (child tables, copies [(src, dst, slots)], references)."""
+    refs, out, copies = list(refs), [], []
+    free = [p for p, r in enumerate(refs) if r <= 0][::-1]  # sharing frees none
+    for p, n in zip(parent, child_pages):
+        old = list(tables[p]) if p >= 0 else []
+        partial = len(old) > 0 and lens[p] % page_size != 0
+        shared = old[:len(old) - 1] if partial else old
+        if n - len(shared) > len(free):
+            raise MemoryError("not enough free pages")
+        fresh = [free.pop() for _ in range(n - len(shared))]
+        if partial:
+            copies.append((old[-1], fresh[0], lens[p] % page_size))
+        out.append(shared + fresh)
+        for page in shared + fresh:
+            refs[page] += 1
+    return out, copies, refs
+
+
+def compact_pages(refs, kv_indices):
+    """(references, table entries, map, moves [(src, dst)], live pages) after
+    the live pages moved to the front with the fewest moves."""
+    live = [p for p, r in enumerate(refs) if r > 0]
+    total = len(live)
+    holes = [p for p in range(total) if refs[p] <= 0]
+    movers = [p for p in reversed(live) if p >= total]
+    moves = list(zip(movers, holes))
+    to = {p: p for p in live if p < total} | dict(moves)
+    new_refs = [0] * len(refs)
+    for p, q in to.items():
+        new_refs[q] = refs[p]
+    return (new_refs, [to[p] for p in kv_indices], [to.get(p, -1) for p in range(len(refs))],
+            moves, total)

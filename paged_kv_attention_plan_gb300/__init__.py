@@ -20,7 +20,9 @@ from ._pka import (PKA_HND, PKA_KV_BF16, PKA_KV_FP8_E4M3, PKA_MASK_CAUSAL,  # no
                    pka_plan_get_info,
                    pka_plan_wait, pka_run, pka_run_static_scratch, pka_status_str, pka_validate, pka_version,
                    pka_check_indices, pka_selftest_bounded_wait,
-                   pka_apply_rope, pka_rope_append_paged_kv_cache, pka_rope_init)
+                   pka_apply_rope, pka_rope_append_paged_kv_cache, pka_rope_init,
+                   pka_alloc_pages, pka_compact_pages, pka_copy_pages, pka_fork_pages,
+                   pka_free_pages)
 
 __all__ = ["BatchAttention", "make_params", "make_rope", "PkaError"] + [n for n in _pka.EXPORTED]
 

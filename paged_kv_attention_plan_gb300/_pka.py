@@ -31,7 +31,9 @@ EXPORTED = ["pka_status_str", "pka_version", "pka_validate", "pka_plan_create",
             "pka_append_paged_kv_cache", "pka_merge_states", "pka_packbits",
             "pka_get_device_error", "pka_last_error", "pka_run_static_scratch",
             "pka_plan_cascade", "pka_selftest_bounded_wait", "pka_check_indices",
-            "pka_rope_init", "pka_apply_rope", "pka_rope_append_paged_kv_cache"]
+            "pka_rope_init", "pka_apply_rope", "pka_rope_append_paged_kv_cache",
+            "pka_copy_pages", "pka_alloc_pages", "pka_free_pages", "pka_fork_pages",
+            "pka_compact_pages"]
 
 
 class pka_params(ctypes.Structure):
@@ -129,6 +131,13 @@ def lib():
         L.pka_rope_append_paged_kv_cache.argtypes = [P(pka_params), P(pka_rope), i32, i64, vp,
                                                      i64, vp, vp, i64, vp, i64, vp, vp, vp, vp,
                                                      vp, vp, vp, i64, i64, vp]
+        L.pka_copy_pages.argtypes = [P(pka_params), i32, vp, vp, i64, i64, i64, vp, vp, vp, i64,
+                                     vp, vp]
+        L.pka_alloc_pages.argtypes = [vp, i32, i32, vp, vp]
+        L.pka_free_pages.argtypes = [vp, i32, vp, i64, vp]
+        L.pka_fork_pages.argtypes = [i32, vp, i32, i32, vp, vp, i32, vp, i32, vp, vp, vp, i32,
+                                     vp, vp, vp, vp, vp]
+        L.pka_compact_pages.argtypes = [vp, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp]
         L.pka_last_error.argtypes = []
         L.pka_last_error.restype = ctypes.c_char_p
         for name in EXPORTED:
@@ -500,6 +509,100 @@ def pka_rope_append_paged_kv_cache(params, rope, q, q_out, k_new, v_new, append_
         _here_pool(v, "v", params, dev), int(page_stride), k.shape[0], _stream(stream))
     if check:
         _check(s, "pka_rope_append_paged_kv_cache")
+    return s
+
+
+def pka_copy_pages(params, k, v, src, dst, slots=None, num_copies=None, stream=None,
+                   check=True) -> int:
+    """Copy pages src[i] over dst[i] (their first slots[i] slots) in pools
+    [pages, ...] or, for all layers at once, [layers, pages, ...] of any layer
+    and page stride.  num_copies: a device count (its first element) of the
+    entries that hold, as pka_fork_pages and pka_compact_pages write it."""
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    if k.dim() not in (4, 5) or v.shape != k.shape or v.stride() != k.stride():
+        raise ValueError("k and v must be pools [pages, ...] or [layers, pages, ...] alike")
+    layers = k.shape[0] if k.dim() == 5 else 1
+    n = src.numel()
+    if dst.numel() != n or (slots is not None and slots.numel() != n):
+        raise ValueError("src, dst and slots must have one length")
+    s = lib().pka_copy_pages(
+        ctypes.byref(params), layers, _here_pool(k, "k", params, dev),
+        _here_pool(v, "v", params, dev), k.stride(-4), k.stride(0) if layers > 1 else 0,
+        k.shape[-4], _here(src, "src", i32, dev), _here(dst, "dst", i32, dev),
+        None if slots is None else _here(slots, "slots", i32, dev), n,
+        None if num_copies is None else _here(num_copies, "num_copies", i32, dev),
+        _stream(stream))
+    if check:
+        _check(s, "pka_copy_pages")
+    return s
+
+
+def pka_alloc_pages(page_refs, pages, stream=None, check=True) -> int:
+    """Take as many pages as `pages` has room for."""
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    s = lib().pka_alloc_pages(_here(page_refs, "page_refs", i32, dev), page_refs.numel(),
+                              pages.numel(), _here(pages, "pages", i32, dev), _stream(stream))
+    if check:
+        _check(s, "pka_alloc_pages")
+    return s
+
+
+def pka_free_pages(page_refs, pages, stream=None, check=True) -> int:
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    s = lib().pka_free_pages(_here(page_refs, "page_refs", i32, dev), page_refs.numel(),
+                             _here(pages, "pages", i32, dev), pages.numel(), _stream(stream))
+    if check:
+        _check(s, "pka_free_pages")
+    return s
+
+
+def pka_fork_pages(page_size, page_refs, kv_indptr, kv_indices, last_page_len, parent,
+                   child_indptr, child_indices, copy_src, copy_dst, copy_slots, counts,
+                   stream=None, check=True) -> int:
+    """Tables of children that continue parents; the copy lists and counts go
+    to pka_copy_pages.  All arrays are device int32."""
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    parents, children = last_page_len.numel(), parent.numel()
+    if kv_indptr.numel() != parents + 1 or child_indptr.numel() != children + 1:
+        raise ValueError("an indptr has one element more than its requests")
+    if min(copy_src.numel(), copy_dst.numel(), copy_slots.numel()) < children:
+        raise ValueError("the copy lists hold one element a child")
+    if counts.numel() < 2:
+        raise ValueError("counts holds two elements")
+    s = lib().pka_fork_pages(
+        page_size, _here(page_refs, "page_refs", i32, dev), page_refs.numel(), parents,
+        _here(kv_indptr, "kv_indptr", i32, dev), _here(kv_indices, "kv_indices", i32, dev),
+        kv_indices.numel(), _here(last_page_len, "last_page_len", i32, dev), children,
+        _here(parent, "parent", i32, dev), _here(child_indptr, "child_indptr", i32, dev),
+        _here(child_indices, "child_indices", i32, dev), child_indices.numel(),
+        _here(copy_src, "copy_src", i32, dev), _here(copy_dst, "copy_dst", i32, dev),
+        _here(copy_slots, "copy_slots", i32, dev), _here(counts, "counts", i32, dev),
+        _stream(stream))
+    if check:
+        _check(s, "pka_fork_pages")
+    return s
+
+
+def pka_compact_pages(page_refs, kv_indices, page_refs_out, kv_indices_out, page_map, copy_src,
+                      copy_dst, counts, stream=None, check=True) -> int:
+    """Move the live pages to the front of the pool: the new references and
+    table entries (either may be written in place), the map and the moves."""
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    n = page_refs.numel()
+    if page_refs_out.numel() != n or page_map.numel() != n:
+        raise ValueError("page_refs_out and page_map hold one element a page")
+    if kv_indices_out.numel() != kv_indices.numel():
+        raise ValueError("kv_indices_out must have kv_indices' length")
+    if min(copy_src.numel(), copy_dst.numel()) < n // 2 or counts.numel() < 2:
+        raise ValueError("the copy lists hold one element for two pages, counts two")
+    s = lib().pka_compact_pages(
+        _here(page_refs, "page_refs", i32, dev), n, _here(kv_indices, "kv_indices", i32, dev),
+        kv_indices.numel(), _here(page_refs_out, "page_refs_out", i32, dev),
+        _here(kv_indices_out, "kv_indices_out", i32, dev), _here(page_map, "page_map", i32, dev),
+        _here(copy_src, "copy_src", i32, dev), _here(copy_dst, "copy_dst", i32, dev),
+        _here(counts, "counts", i32, dev), _stream(stream))
+    if check:
+        _check(s, "pka_compact_pages")
     return s
 
 

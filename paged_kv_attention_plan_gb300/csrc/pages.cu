@@ -1,0 +1,706 @@
+// The pages of the cache: pka_copy_pages, pka_alloc_pages, pka_free_pages,
+// pka_fork_pages and pka_compact_pages.
+//
+// The only state is page_refs, a reference count per page (0: free), so there
+// is no free list to keep in step with it: the free pages are found by
+// counting.  Every answer is the one of lowest page ids, whatever order the
+// blocks run in.  The calls that count run as one thread-block cluster: its
+// hardware barrier orders the passes over page_refs and the counts of the
+// blocks meet in distributed shared memory, with no workspace and no waiting
+// on flags.
+#include <cooperative_groups.h>
+
+#include "pka_cache.h"
+#include "pka_internal.h"
+
+namespace pka {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kClusterCtas = 8;    // blocks of a counting launch: one portable cluster
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr unsigned kAll = 0xffffffffu;
+
+// ---------------------------------------------------------------------------
+// Counting
+// ---------------------------------------------------------------------------
+
+// page_refs split among the warps of the cluster: whole 128-page strides,
+// one 16-byte load a lane.
+struct Share {
+  int64_t lo, hi;  // this warp's pages
+  int lane;
+  bool vec;        // page_refs is 16-byte aligned
+};
+
+__device__ __forceinline__ Share my_share(const int32_t* refs, int32_t num_pages) {
+  const int64_t warps = (int64_t)gridDim.x * kWarps;
+  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t per = ((num_pages + warps - 1) / warps + 127) / 128 * 128;
+  Share s;
+  s.lo = min(w * per, (int64_t)num_pages);
+  s.hi = min(s.lo + per, (int64_t)num_pages);
+  s.lane = threadIdx.x & 31;
+  s.vec = (reinterpret_cast<uintptr_t>(refs) & 15) == 0;
+  return s;
+}
+
+// References of pages p .. p+3 (those past `hi` come as `past`).
+__device__ __forceinline__ int4 refs_at(const int32_t* refs, const Share& s, int64_t p, int past) {
+  if (s.vec && p + 4 <= s.hi) return *reinterpret_cast<const int4*>(refs + p);
+  int4 r;
+  r.x = p < s.hi ? refs[p] : past;
+  r.y = p + 1 < s.hi ? refs[p + 1] : past;
+  r.z = p + 2 < s.hi ? refs[p + 2] : past;
+  r.w = p + 3 < s.hi ? refs[p + 3] : past;
+  return r;
+}
+
+// Bit k: page p + k is free (has no reference); pages past the share are not.
+__device__ __forceinline__ unsigned free_bits(const int4& r) {
+  return (r.x <= 0 ? 1u : 0u) | (r.y <= 0 ? 2u : 0u) | (r.z <= 0 ? 4u : 0u) |
+         (r.w <= 0 ? 8u : 0u);
+}
+
+__device__ __forceinline__ int count_free(const int32_t* refs, const Share& s) {
+  int n = 0;
+#pragma unroll 4
+  for (int64_t p = s.lo + 4 * s.lane; p < s.hi; p += 128)
+    n += __popc(free_bits(refs_at(refs, s, p, 1)));
+  return __reduce_add_sync(kAll, n);
+}
+
+struct Counts {
+  int warp[kWarps];
+  int block;
+};
+
+// From every warp's count: the sum over the warps before this one in the
+// cluster, and the sum over all.  Leaves the cluster barrier armed: the caller
+// ends with leave(), so that no block is gone while its counts are read.
+__device__ __forceinline__ void cluster_prefix(Counts& c, int mine, int* before, int* total) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) c.warp[warp] = mine;
+  __syncthreads();
+  if (warp == 0) {
+    const int sum = __reduce_add_sync(kAll, c.warp[lane]);
+    if (lane == 0) c.block = sum;
+  }
+  cluster.sync();
+  const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int there = lane < ctas ? cluster.map_shared_rank(&c, lane)->block : 0;
+  cluster.barrier_arrive();
+  *total = __reduce_add_sync(kAll, there);
+  *before = __reduce_add_sync(kAll, lane < rank ? there : 0) +
+            __reduce_add_sync(kAll, lane < warp ? c.warp[lane] : 0);
+}
+
+__device__ __forceinline__ void leave() { cg::this_cluster().barrier_wait(); }
+
+// Free pages of this warp's share in ascending order, the first with rank
+// `rank`, until rank `stop`: use(rank, page).
+template <class F>
+__device__ __forceinline__ void each_free(const int32_t* refs, const Share& s, int rank, int stop,
+                                          F use) {
+  const unsigned below = (1u << s.lane) - 1;
+  for (int64_t p0 = s.lo; p0 < s.hi && rank < stop; p0 += 128) {
+    const int64_t p = p0 + 4 * s.lane;
+    const unsigned bits = free_bits(refs_at(refs, s, p, 1));
+    int at = rank, all = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const unsigned b = __ballot_sync(kAll, bits >> k & 1);
+      at += __popc(b & below);
+      all += __popc(b);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (bits >> k & 1) {
+        if (at < stop) use(at, (int32_t)(p + k));
+        ++at;
+      }
+    rank += all;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Taking and returning pages
+// ---------------------------------------------------------------------------
+
+__global__ void __launch_bounds__(kThreads, 1) alloc_kernel(int32_t* refs, int32_t num_pages,
+                                                         int32_t n, int32_t* pages,
+                                                         int32_t* err) {
+  __shared__ Counts c;
+  const Share s = my_share(refs, num_pages);
+  int before, total;
+  cluster_prefix(c, count_free(refs, s), &before, &total);
+  if (total < n) {
+    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < n;
+         i += (int64_t)gridDim.x * kThreads)
+      pages[i] = -1;
+    if (blockIdx.x == 0 && threadIdx.x == 0) note_error(err, PKA_ERR_WORKSPACE);
+  } else {
+    each_free(refs, s, before, n, [&](int rank, int32_t page) {
+      pages[rank] = page;
+      refs[page] = 1;
+    });
+  }
+  leave();
+}
+
+// A page's count never stays below zero: a decrement that finds none left is
+// taken back and noted.  Exactly as many decrements succeed as there were
+// references, in whatever order they come.
+__global__ void __launch_bounds__(256) free_kernel(int32_t* refs, int32_t num_pages,
+                                                   const int32_t* pages, int64_t n, int32_t* err) {
+  bool bad = false;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int32_t p = pages[i];
+    if (p < 0 || p >= num_pages) {
+      bad = true;
+    } else if (atomicSub(refs + p, 1) <= 0) {
+      atomicAdd(refs + p, 1);
+      bad = true;
+    }
+  }
+  if (bad) note_error(err, PKA_ERR_METADATA);
+}
+
+// ---------------------------------------------------------------------------
+// Fork
+// ---------------------------------------------------------------------------
+
+struct ForkArgs {
+  int32_t* refs;
+  const int32_t* kv_indptr;
+  const int32_t* kv_indices;
+  const int32_t* last_page_len;
+  const int32_t* parent;
+  const int32_t* child_indptr;
+  int32_t* child_indices;
+  int32_t* copy_src;
+  int32_t* copy_dst;
+  int32_t* copy_slots;
+  int32_t* counts;
+  int32_t* err;
+  int32_t page_size, num_pages, num_parents, num_children;
+  int32_t num_indices, num_child_indices;
+};
+
+// What one child takes: the first `shared` entries of its parent's table,
+// then fresh pages; the first of those receives the parent's partly filled
+// last page, if it has one.
+struct Child {
+  int first;        // its first entry in child_indices
+  int shared;
+  int fresh;
+  int parent_first; // its parent's first entry in kv_indices
+  int slots;        // filled slots of the parent's partial page, or 0
+  bool ok;
+};
+
+__device__ __forceinline__ Child child_at(const ForkArgs& a, int c) {
+  Child x{};
+  const int32_t c0 = a.child_indptr[c], c1 = a.child_indptr[c + 1], p = a.parent[c];
+  x.first = c0;
+  x.ok = c0 >= 0 && c1 >= c0 && c1 <= a.num_child_indices && p >= -1 && p < a.num_parents;
+  if (!x.ok) return x;
+  int pages = 0;
+  if (p >= 0) {
+    const int32_t k0 = a.kv_indptr[p], k1 = a.kv_indptr[p + 1];
+    x.ok = k0 >= 0 && k1 >= k0 && k1 <= a.num_indices && k1 - k0 <= c1 - c0;
+    if (!x.ok) return x;
+    pages = k1 - k0;
+    x.parent_first = k0;
+    if (pages > 0) {
+      const int32_t last = a.last_page_len[p];
+      x.ok = last >= 1 && last <= a.page_size;
+      if (!x.ok) return x;
+      if (last < a.page_size) x.slots = last;
+    }
+  }
+  x.shared = pages - (x.slots > 0);
+  x.fresh = c1 - c0 - x.shared;
+  return x;
+}
+
+// Checks every child, takes the lowest free pages for all of them and writes
+// the entries that these fill, the copy list and the counts; nothing at all
+// when a child is malformed or the pages do not suffice.  Every block of the
+// cluster scans the children for itself (shared memory holds the running sum
+// of fresh pages and of copies), then writes for the free pages of its share.
+__global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a) {
+  extern __shared__ int32_t sums[];
+  int32_t* fresh_before = sums;                      // [num_children + 1]
+  int32_t* copies_before = sums + a.num_children + 1;  // [num_children]
+  __shared__ Counts c;
+  __shared__ int64_t warp_sum[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const Share s = my_share(a.refs, a.num_pages);
+  const int mine = count_free(a.refs, s);
+
+  // running sums over the children: fresh pages in the upper 32 bits, copies
+  // in the lower
+  int64_t carry = 0;
+  bool ok = true;
+  for (int c0 = 0; c0 < a.num_children; c0 += kThreads) {
+    const int i = c0 + threadIdx.x;
+    int64_t x = 0;
+    if (i < a.num_children) {
+      const Child ch = child_at(a, i);
+      ok = ok && ch.ok;
+      if (ch.ok) x = ((int64_t)ch.fresh << 32) | (ch.slots > 0 ? 1 : 0);
+    }
+    int64_t incl = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(kAll, incl, d);
+      if (lane >= d) incl += y;
+    }
+    __syncthreads();  // the previous round's warp_sum has been read
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t base = carry, all = carry;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) base += warp_sum[w];
+      all += warp_sum[w];
+    }
+    if (i < a.num_children) {
+      const int64_t excl = base + incl - x;
+      fresh_before[i] = (int32_t)(excl >> 32);
+      copies_before[i] = (int32_t)excl;
+    }
+    carry = all;
+  }
+  ok = __syncthreads_and(ok);
+  const int64_t needed = carry >> 32;
+  const int copies = (int)(uint32_t)carry;
+  if (threadIdx.x == 0) fresh_before[a.num_children] = (int32_t)needed;
+
+  int before, total;
+  cluster_prefix(c, mine, &before, &total);  // (a barrier: the sums are visible too)
+  const bool refused = !ok || total < needed;
+  if (!refused) {
+    each_free(a.refs, s, before, (int)needed, [&](int rank, int32_t page) {
+      int lo = 0, hi = a.num_children - 1;  // the last child with fresh_before <= rank
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (fresh_before[mid] <= rank) lo = mid; else hi = mid - 1;
+      }
+      const Child ch = child_at(a, lo);
+      const int nth = rank - fresh_before[lo];
+      a.child_indices[ch.first + ch.shared + nth] = page;
+      a.refs[page] = 1;
+      if (nth == 0 && ch.slots > 0) {
+        const int i = copies_before[lo];
+        a.copy_src[i] = a.kv_indices[ch.parent_first + ch.shared];
+        a.copy_dst[i] = page;
+        a.copy_slots[i] = ch.slots;
+      }
+    });
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.counts[0] = refused ? -1 : copies;
+    a.counts[1] = refused ? -1 : (int32_t)needed;
+    if (refused) note_error(a.err, ok ? PKA_ERR_WORKSPACE : PKA_ERR_METADATA);
+  }
+  leave();
+}
+
+// The shared entries of every child's table, each one reference more.  A warp
+// takes 256 entries; it looks up the children of the first and the last, and
+// where these differ each lane looks its own up between them.
+__global__ void __launch_bounds__(256) fork_share_kernel(const ForkArgs a) {
+  constexpr int CHUNK = 256;
+  if (a.counts[0] < 0) return;  // refused
+  const int lane = threadIdx.x & 31;
+  const int64_t end = a.child_indptr[a.num_children];
+  bool bad = false;
+  for (int64_t e0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * CHUNK; e0 < end;
+       e0 += (int64_t)gridDim.x * 8 * CHUNK) {
+    const int64_t e1 = min(e0 + CHUNK, end);
+    const int first = warp_find(a.child_indptr, a.num_children, e0, lane);
+    const int last = warp_find(a.child_indptr, a.num_children, e1 - 1, lane);
+    for (int64_t e = e0 + lane; e < e1; e += 32) {
+      int lo = first, hi = last;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.child_indptr[mid] <= e) lo = mid; else hi = mid - 1;
+      }
+      const Child ch = child_at(a, lo);
+      const int64_t j = e - ch.first;
+      if (j < 0 || j >= ch.shared) continue;
+      const int32_t page = a.kv_indices[ch.parent_first + j];
+      a.child_indices[e] = page;
+      if (page >= 0 && page < a.num_pages) atomicAdd(a.refs + page, 1);
+      else bad = true;
+    }
+  }
+  if (bad) note_error(a.err, PKA_ERR_METADATA);
+}
+
+// ---------------------------------------------------------------------------
+// Compact
+// ---------------------------------------------------------------------------
+
+struct CompactArgs {
+  const int32_t* refs;   // may be refs_out
+  int32_t* refs_out;
+  int32_t* map;
+  int32_t* copy_src;
+  int32_t* copy_dst;
+  int32_t* counts;
+  int32_t num_pages;
+};
+
+// With L live pages, the live pages at L and above move to the free pages
+// below L: as many of the one as of the other.  Before page p lie r(p) live
+// pages (one pass of counting), so the free page p < L is number p - r(p) of
+// its kind from below and the live page p >= L number L - 1 - r(p) of its kind
+// from above; equal numbers pair up.
+__global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs a) {
+  __shared__ Counts c;
+  const Share s = my_share(a.refs, a.num_pages);
+  const int pages = (int)(s.hi - s.lo);
+  int before, live;
+  cluster_prefix(c, pages - count_free(a.refs, s), &before, &live);
+  leave();
+
+  const unsigned below = (1u << s.lane) - 1;
+  int rank = before;  // live pages before p0
+  for (int64_t p0 = s.lo; p0 < s.hi; p0 += 128) {
+    const int64_t p = p0 + 4 * s.lane;
+    const int4 r4 = refs_at(a.refs, s, p, 0);
+    const int r[4] = {r4.x, r4.y, r4.z, r4.w};
+    int at = rank, all = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const unsigned b = __ballot_sync(kAll, r[k] > 0);
+      at += __popc(b & below);
+      all += __popc(b);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int32_t page = (int32_t)(p + k);
+      if (p + k < s.hi) {
+        if (page == live) {
+          a.counts[0] = live - at;
+          a.counts[1] = live;
+        }
+        if (page < live) {
+          if (r[k] > 0) {
+            a.map[page] = page;
+            a.refs_out[page] = r[k];
+          } else {
+            a.map[page] = -1;
+            a.copy_dst[page - at] = page;
+          }
+        } else if (r[k] > 0) {
+          a.copy_src[live - 1 - at] = page;
+        } else {
+          a.map[page] = -1;
+          a.refs_out[page] = 0;
+        }
+      }
+      at += r[k] > 0;
+    }
+    rank += all;
+  }
+  if (live == a.num_pages && blockIdx.x == 0 && threadIdx.x == 0) {
+    a.counts[0] = 0;
+    a.counts[1] = live;
+  }
+  cg::this_cluster().sync();  // both lists are whole
+  const int moves = __ldcg(a.counts);
+  for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < moves;
+       i += (int64_t)gridDim.x * kThreads) {
+    const int32_t src = __ldcg(a.copy_src + i), dst = __ldcg(a.copy_dst + i);
+    a.map[src] = dst;
+    a.refs_out[dst] = __ldcg(a.refs + src);
+    a.refs_out[src] = 0;
+  }
+}
+
+// Table entries through the map.  An entry that names no live page stays as
+// it is and is noted.
+__global__ void __launch_bounds__(256) remap_kernel(const int32_t* map, int32_t num_pages,
+                                                    const int32_t* in, int64_t n, int32_t* out,
+                                                    int32_t* err) {
+  bool bad = false;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int32_t p = in[i];
+    const int32_t to = p >= 0 && p < num_pages ? map[p] : -1;
+    bad = bad || to < 0;
+    out[i] = to < 0 ? p : to;
+  }
+  if (bad) note_error(err, PKA_ERR_METADATA);
+}
+
+// ---------------------------------------------------------------------------
+// Copy
+// ---------------------------------------------------------------------------
+
+struct CopyArgs {
+  uint8_t* k;
+  uint8_t* v;
+  int64_t page_bytes;        // between pages
+  int64_t layer_bytes;       // between layers
+  int64_t num_pages;
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* slots;      // null: whole pages
+  const int32_t* count;      // null: max_copies
+  int64_t max_copies;
+  int32_t page_size;
+  int32_t layout;
+  int32_t head_row;          // bytes of one head's row of a slot
+  int32_t slot_row;          // bytes of all heads' rows of a slot
+  int32_t* err;
+};
+
+// blockIdx.y is (layer, K or V); a warp takes 4 KB of a page, eight 16-byte
+// pieces a lane in flight.
+__global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
+  constexpr int PIECES = 8, CHUNK = PIECES * 512;
+  const int lane = threadIdx.x & 31;
+  uint8_t* pool = (blockIdx.y & 1 ? a.v : a.k) + (blockIdx.y >> 1) * a.layer_bytes;
+  const uint32_t whole = (uint32_t)a.page_size * a.slot_row;
+  const uint32_t chunks = (whole + CHUNK - 1) / CHUNK;
+  int64_t n = a.max_copies;
+  if (a.count) n = min(n, (int64_t)max(*a.count, 0));
+  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < n * chunks;
+       w += (int64_t)gridDim.x * 8) {
+    const int64_t i = w <= UINT32_MAX ? (uint32_t)w / chunks : w / chunks;
+    const uint32_t off0 = (uint32_t)(w - i * chunks) * CHUNK;
+    const int32_t src = a.src[i], dst = a.dst[i];
+    const int slots = a.slots ? a.slots[i] : a.page_size;
+    if (src < 0 || src >= a.num_pages || dst < 0 || dst >= a.num_pages || slots < 0 ||
+        slots > a.page_size) {
+      if (lane == 0) note_error(a.err, PKA_ERR_METADATA);
+      continue;
+    }
+    if (src == dst) continue;
+    const uint8_t* from = pool + src * a.page_bytes;
+    uint8_t* to = pool + dst * a.page_bytes;
+    uint4 x[PIECES];
+    bool take[PIECES];
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+      const uint32_t off = off0 + u * 512 + lane * 16;
+      take[u] = off < whole;
+      if (slots < a.page_size) {
+        // NHD: the first slots' rows lie first; HND: slot by slot in each head
+        const uint32_t slot = a.layout == PKA_NHD ? off / (uint32_t)a.slot_row
+                                                  : off / (uint32_t)a.head_row %
+                                                        (uint32_t)a.page_size;
+        take[u] = take[u] && slot < (uint32_t)slots;
+      }
+      if (take[u]) x[u] = *reinterpret_cast<const uint4*>(from + off);
+    }
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u)
+      if (take[u]) *reinterpret_cast<uint4*>(to + off0 + u * 512 + lane * 16) = x[u];
+  }
+}
+
+int blocks_for(int64_t work, int per_block, int per_sm) {
+  const int sms = current_device_sms();
+  const int64_t cap = (int64_t)per_sm * (sms > 0 ? sms : 1);
+  const int64_t b = (work + per_block - 1) / per_block;
+  return (int)(b < 1 ? 1 : b > cap ? cap : b);
+}
+
+// Launch as one cluster of kClusterCtas blocks.
+template <class... A>
+cudaError_t launch_cluster(void (*kernel)(A...), int smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kClusterCtas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = kClusterCtas;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+pka_status done(cudaError_t e, const char* where) {
+  return e == cudaSuccess ? PKA_OK : cuda_failure(e, where);
+}
+
+bool unaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; }
+
+}  // namespace
+}  // namespace pka
+
+extern "C" {
+
+pka_status pka_copy_pages(const pka_params* p, int32_t num_layers, void* k, void* v,
+                          int64_t page_stride, int64_t layer_stride, int64_t num_pool_pages,
+                          const int32_t* src_d, const int32_t* dst_d, const int32_t* slots_d,
+                          int64_t max_copies, const int32_t* num_copies_d, void* stream) {
+  if (!pka::params_valid(p) || num_layers < 0 || max_copies < 0 || num_pool_pages < 0)
+    return PKA_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128) return PKA_ERR_UNSUPPORTED;
+  if (p->kv_ragged || num_layers > 32767) return PKA_ERR_UNSUPPORTED;
+  if (num_layers == 0 || max_copies == 0) return PKA_OK;
+  if (!k || !v || !src_d || !dst_d || page_stride <= 0) return PKA_ERR_INVALID_ARG;
+  const bool f8 = p->kv_dtype == PKA_KV_FP8_E4M3;
+  const int item = f8 ? 1 : 2;
+  const uintptr_t mis = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
+  const int64_t whole16 = f8 ? 15 : 7;
+  if ((mis & 15) || (page_stride & whole16)) return PKA_ERR_INVALID_ARG;
+  if (num_layers > 1 && (layer_stride <= 0 || (layer_stride & whole16)))
+    return PKA_ERR_INVALID_ARG;
+  pka::CopyArgs a{};
+  const int64_t slot_row = (int64_t)p->num_kv_heads * p->head_dim * item;
+  if (slot_row > INT32_MAX / p->page_size) return PKA_ERR_UNSUPPORTED;  // a page of 2 GB
+  a.k = static_cast<uint8_t*>(k);
+  a.v = static_cast<uint8_t*>(v);
+  a.page_bytes = page_stride * item;
+  a.layer_bytes = num_layers > 1 ? layer_stride * item : 0;
+  a.num_pages = num_pool_pages;
+  a.src = src_d;
+  a.dst = dst_d;
+  a.slots = slots_d;
+  a.count = num_copies_d;
+  a.max_copies = max_copies;
+  a.page_size = p->page_size;
+  a.layout = p->layout;
+  a.head_row = p->head_dim * item;
+  a.slot_row = (int32_t)slot_row;
+  a.err = pka::device_error_word();
+  const int64_t chunks = (p->page_size * slot_row + 4095) / 4096;
+  const int per_sm = 16 / (2 * num_layers) > 1 ? 16 / (2 * num_layers) : 1;
+  const int x = pka::blocks_for(max_copies * chunks, 8, per_sm);
+  pka::copy_kernel<<<dim3((unsigned)x, (unsigned)(2 * num_layers)), 256, 0,
+                     static_cast<cudaStream_t>(stream)>>>(a);
+  return pka::done(cudaGetLastError(), "page copy launch");
+}
+
+pka_status pka_alloc_pages(int32_t* page_refs_d, int32_t num_pages, int32_t n, int32_t* pages_d,
+                           void* stream) {
+  if (num_pages < 0 || n < 0) return PKA_ERR_INVALID_ARG;
+  if (n == 0) return PKA_OK;
+  if (n > num_pages) return PKA_ERR_WORKSPACE;
+  if (!page_refs_d || !pages_d || pka::unaligned(page_refs_d) || pka::unaligned(pages_d))
+    return PKA_ERR_INVALID_ARG;
+  return pka::done(pka::launch_cluster(pka::alloc_kernel, 0, static_cast<cudaStream_t>(stream),
+                                       page_refs_d, num_pages, n, pages_d,
+                                       pka::device_error_word()),
+                   "page alloc launch");
+}
+
+pka_status pka_free_pages(int32_t* page_refs_d, int32_t num_pages, const int32_t* pages_d,
+                          int64_t n, void* stream) {
+  if (num_pages < 0 || n < 0) return PKA_ERR_INVALID_ARG;
+  if (n == 0) return PKA_OK;
+  if (!page_refs_d || !pages_d || pka::unaligned(page_refs_d) || pka::unaligned(pages_d))
+    return PKA_ERR_INVALID_ARG;
+  pka::free_kernel<<<pka::blocks_for(n, 256, 8), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+      page_refs_d, num_pages, pages_d, n, pka::device_error_word());
+  return pka::done(cudaGetLastError(), "page free launch");
+}
+
+pka_status pka_fork_pages(int32_t page_size, int32_t* page_refs_d, int32_t num_pages,
+                          int32_t num_parents, const int32_t* kv_indptr_d,
+                          const int32_t* kv_indices_d, int32_t num_indices,
+                          const int32_t* last_page_len_d, int32_t num_children,
+                          const int32_t* parent_d, const int32_t* child_indptr_d,
+                          int32_t* child_indices_d, int32_t num_child_indices,
+                          int32_t* copy_src_d, int32_t* copy_dst_d, int32_t* copy_slots_d,
+                          int32_t* counts_d, void* stream) {
+  if (page_size < 1 || num_pages < 0 || num_parents < 0 || num_indices < 0 || num_children < 0 ||
+      num_child_indices < 0)
+    return PKA_ERR_INVALID_ARG;
+  if (num_children > PKA_MAX_FORK_CHILDREN) return PKA_ERR_UNSUPPORTED;
+  if (!counts_d || pka::unaligned(counts_d)) return PKA_ERR_INVALID_ARG;
+  const bool parents = num_parents > 0 && (!kv_indptr_d || !last_page_len_d);
+  const bool children = num_children > 0 && (!parent_d || !child_indptr_d || !copy_src_d ||
+                                             !copy_dst_d || !copy_slots_d);
+  if (parents || children || (num_indices > 0 && !kv_indices_d) ||
+      (num_child_indices > 0 && !child_indices_d) || (num_pages > 0 && !page_refs_d))
+    return PKA_ERR_INVALID_ARG;
+  const void* arrays[] = {page_refs_d,    kv_indptr_d,     kv_indices_d, last_page_len_d,
+                          parent_d,       child_indptr_d,  child_indices_d, copy_src_d,
+                          copy_dst_d,     copy_slots_d};
+  for (const void* x : arrays)
+    if (pka::unaligned(x)) return PKA_ERR_INVALID_ARG;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (num_children == 0) return pka::done(cudaMemsetAsync(counts_d, 0, 8, st), "page fork counts");
+  pka::ForkArgs a{};
+  a.refs = page_refs_d;
+  a.kv_indptr = kv_indptr_d;
+  a.kv_indices = kv_indices_d;
+  a.last_page_len = last_page_len_d;
+  a.parent = parent_d;
+  a.child_indptr = child_indptr_d;
+  a.child_indices = child_indices_d;
+  a.copy_src = copy_src_d;
+  a.copy_dst = copy_dst_d;
+  a.copy_slots = copy_slots_d;
+  a.counts = counts_d;
+  a.err = pka::device_error_word();
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  a.num_parents = num_parents;
+  a.num_children = num_children;
+  a.num_indices = num_indices;
+  a.num_child_indices = num_child_indices;
+  const int smem = (2 * num_children + 1) * (int)sizeof(int32_t);
+  cudaError_t e = pka::ensure_dynamic_smem<pka::fork_take_kernel>(smem);
+  if (e == cudaSuccess) e = pka::launch_cluster(pka::fork_take_kernel, smem, st, a);
+  if (e != cudaSuccess) return pka::cuda_failure(e, "page fork launch");
+  if (num_child_indices == 0) return PKA_OK;
+  pka::fork_share_kernel<<<pka::blocks_for(num_child_indices, 8 * 256, 8), 256, 0, st>>>(a);
+  return pka::done(cudaGetLastError(), "page fork launch");
+}
+
+pka_status pka_compact_pages(const int32_t* page_refs_d, int32_t num_pages,
+                             const int32_t* kv_indices_d, int64_t num_indices,
+                             int32_t* page_refs_out_d, int32_t* kv_indices_out_d,
+                             int32_t* page_map_d, int32_t* copy_src_d, int32_t* copy_dst_d,
+                             int32_t* counts_d, void* stream) {
+  if (num_pages < 0 || num_indices < 0) return PKA_ERR_INVALID_ARG;
+  if (!counts_d || pka::unaligned(counts_d)) return PKA_ERR_INVALID_ARG;
+  if (num_pages > 0 && (!page_refs_d || !page_refs_out_d || !page_map_d)) return PKA_ERR_INVALID_ARG;
+  if (num_pages > 1 && (!copy_src_d || !copy_dst_d)) return PKA_ERR_INVALID_ARG;
+  if (num_indices > 0 && (!kv_indices_d || !kv_indices_out_d)) return PKA_ERR_INVALID_ARG;
+  const void* arrays[] = {page_refs_d, kv_indices_d, page_refs_out_d, kv_indices_out_d,
+                          page_map_d,  copy_src_d,   copy_dst_d};
+  for (const void* x : arrays)
+    if (pka::unaligned(x)) return PKA_ERR_INVALID_ARG;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (num_pages == 0) {
+    e = cudaMemsetAsync(counts_d, 0, 8, st);
+  } else {
+    pka::CompactArgs a{};
+    a.refs = page_refs_d;
+    a.refs_out = page_refs_out_d;
+    a.map = page_map_d;
+    a.copy_src = copy_src_d;
+    a.copy_dst = copy_dst_d;
+    a.counts = counts_d;
+    a.num_pages = num_pages;
+    e = pka::launch_cluster(pka::compact_kernel, 0, st, a);
+  }
+  if (e != cudaSuccess) return pka::cuda_failure(e, "page compact launch");
+  if (num_indices == 0) return PKA_OK;
+  pka::remap_kernel<<<pka::blocks_for(num_indices, 256, 8), 256, 0, st>>>(
+      page_map_d, num_pages, kv_indices_d, num_indices, kv_indices_out_d,
+      pka::device_error_word());
+  return pka::done(cudaGetLastError(), "page remap launch");
+}
+
+}  // extern "C"
