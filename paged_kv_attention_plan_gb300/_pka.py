@@ -212,52 +212,64 @@ def _dev_pool(t, name, params=None):
     return t.data_ptr()
 
 
-def _here(t, name, dtype, dev):
-    """Pointer of a contiguous tensor of `dtype` on CUDA device `dev` (the
-    current one, where the call launches)."""
+# The checks of the operators around the cache: their calls are a few
+# microseconds long, so each tensor is checked by one expression, and only a
+# tensor that fails it is looked at again for what to say.
+_BF16, _U8, _I32 = torch.bfloat16, torch.uint8, torch.int32
+
+
+def _refuse(t, name, dtype, dev, what):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be {what}, got {tuple(t.shape)} with strides {t.stride()}")
 
 
-def _here_rows(t, name, dev, heads=None, dim=None, rows=None):
+def _here(t, name, dtype, dev):
+    """Pointer of a contiguous tensor of `dtype` on CUDA device `dev` (the
+    current one, where the call launches)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, dev, "contiguous")
+
+
+def _here_rows(t, name, dev, rows, heads, dim):
     """(pointer, row stride) of bf16 rows [rows, heads, dim]: the heads of a
     row contiguous, the rows at any stride (slices of a fused projection)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [rows, heads, head_dim]")
-    n, h, d = t.shape
-    if (rows is not None and n != rows) or (heads is not None and h != heads) or \
-            (dim is not None and d != dim):
-        raise ValueError(f"{name} must be [{rows}, {heads}, {dim}], got {tuple(t.shape)}")
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (h > 1 and s1 != d):
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), s0 if n > 1 else h * d
+    if isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.get_device() == dev \
+            and t.shape == (rows, heads, dim):
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and (s1 == dim or heads == 1):
+            return t.data_ptr(), s0 if rows > 1 else heads * dim
+    _refuse(t, name, _BF16, dev,
+            f"{_shape(rows, heads, dim)} with the heads of a row contiguous")
+
+
+def _shape(*dims):
+    return "[" + ", ".join(map(str, dims)) + "]"
 
 
 def _here_pool(t, name, params, dev):
-    """Pointer of a K/V pool [pages, P, Hk, D] or [pages, Hk, P, D] of the
-    params' layout (any page stride)."""
-    page = ((params.page_size, params.num_kv_heads) if params.layout == PKA_NHD
-            else (params.num_kv_heads, params.page_size)) + (params.head_dim,)
-    p = _dev_pool(t, name, params)
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    if tuple(t.shape[-3:]) != page:
-        raise ValueError(f"{name}: pages of {tuple(t.shape[-3:])}, the params say {page}")
-    return p
+    """Pointer of a K/V pool [.., pages, P, Hk, D] or [.., pages, Hk, P, D] of
+    the params' layout, each page contiguous."""
+    a, b, d = params.page_size, params.num_kv_heads, params.head_dim
+    if params.layout != PKA_NHD:
+        a, b = b, a
+    dtype = _U8 if params.kv_dtype == PKA_KV_FP8_E4M3 else _BF16
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev \
+            and t.shape[-3:] == (a, b, d) and t.stride()[-3:] == (b * d, d, 1):
+        return t.data_ptr()
+    _refuse(t, name, dtype, dev, f"{_shape('..', a, b, d)} with each page contiguous")
+
+
+def _here_stream(stream, dev) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
 def _stream(stream) -> int | None:
@@ -457,22 +469,25 @@ def pka_apply_rope(rope, positions, q=None, q_out=None, k=None, k_out=None, tran
     if q is None and k is None:
         raise ValueError("pka_apply_rope: q or k")
     dev = torch.cuda.current_device()
-    rows, _, dim = (q if q is not None else k).shape
-    qa, ka = (None, 0, 0, None, 0), (None, 0, 0, None, 0)
+    rows, hq, dim = (q if q is not None else k).shape
+    hk = 0
+    qp = qo = kp = ko = None
+    qs = qos = ks = kos = 0
     if q is not None:
-        qp, qs = _here_rows(q, "q", dev, None, dim, rows)
-        op, os_ = _here_rows(q_out, "q_out", dev, q.shape[1], dim, rows)
-        qa = (qp, q.shape[1], qs, op, os_)
+        qp, qs = _here_rows(q, "q", dev, rows, hq, dim)
+        qo, qos = (qp, qs) if q_out is q else _here_rows(q_out, "q_out", dev, rows, hq, dim)
+    else:
+        hq = 0
     if k is not None:
-        kp, ks = _here_rows(k, "k", dev, None, dim, rows)
-        op, os_ = _here_rows(k_out, "k_out", dev, k.shape[1], dim, rows)
-        ka = (kp, k.shape[1], ks, op, os_)
-    pos = _here(positions, "positions", torch.int32, dev)
+        hk = k.shape[1]
+        kp, ks = _here_rows(k, "k", dev, rows, hk, dim)
+        ko, kos = (kp, ks) if k_out is k else _here_rows(k_out, "k_out", dev, rows, hk, dim)
+    pos = _here(positions, "positions", _I32, dev)
     if positions.numel() != rows:
         raise ValueError(f"positions: {rows} values, got {positions.numel()}")
-    s = lib().pka_apply_rope(ctypes.byref(rope), int(bool(transpose)), dim, rows, pos, *qa, *ka,
-                             _stream(stream))
-    if check:
+    s = lib().pka_apply_rope(ctypes.byref(rope), 1 if transpose else 0, dim, rows, pos, qp, hq, qs,
+                             qo, qos, kp, hk, ks, ko, kos, _here_stream(stream, dev))
+    if check and s:
         _check(s, "pka_apply_rope")
     return s
 
@@ -482,32 +497,37 @@ def pka_rope_append_paged_kv_cache(params, rope, q, q_out, k_new, v_new, append_
                                    stream=None, check=True) -> int:
     """pka_append_paged_kv_cache of rotated rows; q and q_out may be None.  k
     and v are the pools [pages, ...]; rows past append_indptr[-1] are left."""
-    dev, i32 = torch.cuda.current_device(), torch.int32
+    dev = torch.cuda.current_device()
     hk, d, rows = params.num_kv_heads, params.head_dim, k_new.shape[0]
     batch = append_indptr.numel() - 1
-    qp = qs = qo = None
+    qp = qo = pos = None
+    qs = 0
     if q is not None:
-        qp, qs = _here_rows(q, "q", dev, params.num_qo_heads, d, rows)
-        _here_rows(q_out, "q_out", dev, params.num_qo_heads, d, rows)
-        qo = _here(q_out, "q_out", torch.bfloat16, dev)
-    kp, ks = _here_rows(k_new, "k_new", dev, hk, d, rows)
-    vp, vs = _here_rows(v_new, "v_new", dev, hk, d, rows)
-    pos = None
+        hq = params.num_qo_heads
+        qp, qs = _here_rows(q, "q", dev, rows, hq, d)
+        qo, qos = (qp, qs) if q_out is q else _here_rows(q_out, "q_out", dev, rows, hq, d)
+        if qos != hq * d:
+            _refuse(q_out, "q_out", _BF16, dev, "contiguous")
+    kp, ks = _here_rows(k_new, "k_new", dev, rows, hk, d)
+    vp, vs = _here_rows(v_new, "v_new", dev, rows, hk, d)
     if positions is not None:
-        pos = _here(positions, "positions", i32, dev)
+        pos = _here(positions, "positions", _I32, dev)
         if positions.numel() != rows:
             raise ValueError(f"positions: {rows} values, got {positions.numel()}")
+    app = _here(append_indptr, "append_indptr", _I32, dev)
+    ptr = _here(kv_indptr, "kv_indptr", _I32, dev)
+    idx = _here(kv_indices, "kv_indices", _I32, dev)
+    last = _here(last_page_len, "last_page_len", _I32, dev)
     if kv_indptr.numel() != batch + 1 or last_page_len.numel() != batch:
         raise ValueError("kv_indptr and last_page_len must describe append_indptr's requests")
-    if k.dim() != 4 or v.shape != k.shape:
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape:
         raise ValueError("k and v must be pools [pages, ...] of one shape")
     s = lib().pka_rope_append_paged_kv_cache(
-        ctypes.byref(params), ctypes.byref(rope), batch, rows, qp, qs or 0, qo, kp, ks, vp, vs,
-        pos, _here(append_indptr, "append_indptr", i32, dev),
-        _here(kv_indptr, "kv_indptr", i32, dev), _here(kv_indices, "kv_indices", i32, dev),
-        _here(last_page_len, "last_page_len", i32, dev), _here_pool(k, "k", params, dev),
-        _here_pool(v, "v", params, dev), int(page_stride), k.shape[0], _stream(stream))
-    if check:
+        ctypes.byref(params), ctypes.byref(rope), batch, rows, qp, qs, qo, kp, ks, vp, vs, pos,
+        app, ptr, idx, last, _here_pool(k, "k", params, dev), _here_pool(v, "v", params, dev),
+        int(page_stride), shape[0], _here_stream(stream, dev))
+    if check and s:
         _check(s, "pka_rope_append_paged_kv_cache")
     return s
 
@@ -518,40 +538,41 @@ def pka_copy_pages(params, k, v, src, dst, slots=None, num_copies=None, stream=N
     [pages, ...] or, for all layers at once, [layers, pages, ...] of any layer
     and page stride.  num_copies: a device count (its first element) of the
     entries that hold, as pka_fork_pages and pka_compact_pages write it."""
-    dev, i32 = torch.cuda.current_device(), torch.int32
-    if k.dim() not in (4, 5) or v.shape != k.shape or v.stride() != k.stride():
+    dev, i32 = torch.cuda.current_device(), _I32
+    shape, strides = k.shape, k.stride()
+    if len(shape) not in (4, 5) or v.shape != shape or v.stride() != strides:
         raise ValueError("k and v must be pools [pages, ...] or [layers, pages, ...] alike")
-    layers = k.shape[0] if k.dim() == 5 else 1
+    layers = shape[0] if len(shape) == 5 else 1
     n = src.numel()
     if dst.numel() != n or (slots is not None and slots.numel() != n):
         raise ValueError("src, dst and slots must have one length")
     s = lib().pka_copy_pages(
         ctypes.byref(params), layers, _here_pool(k, "k", params, dev),
-        _here_pool(v, "v", params, dev), k.stride(-4), k.stride(0) if layers > 1 else 0,
-        k.shape[-4], _here(src, "src", i32, dev), _here(dst, "dst", i32, dev),
+        _here_pool(v, "v", params, dev), strides[-4], strides[0] if layers > 1 else 0,
+        shape[-4], _here(src, "src", i32, dev), _here(dst, "dst", i32, dev),
         None if slots is None else _here(slots, "slots", i32, dev), n,
         None if num_copies is None else _here(num_copies, "num_copies", i32, dev),
-        _stream(stream))
-    if check:
+        _here_stream(stream, dev))
+    if check and s:
         _check(s, "pka_copy_pages")
     return s
 
 
 def pka_alloc_pages(page_refs, pages, stream=None, check=True) -> int:
     """Take as many pages as `pages` has room for."""
-    dev, i32 = torch.cuda.current_device(), torch.int32
+    dev, i32 = torch.cuda.current_device(), _I32
     s = lib().pka_alloc_pages(_here(page_refs, "page_refs", i32, dev), page_refs.numel(),
-                              pages.numel(), _here(pages, "pages", i32, dev), _stream(stream))
-    if check:
+                              pages.numel(), _here(pages, "pages", i32, dev), _here_stream(stream, dev))
+    if check and s:
         _check(s, "pka_alloc_pages")
     return s
 
 
 def pka_free_pages(page_refs, pages, stream=None, check=True) -> int:
-    dev, i32 = torch.cuda.current_device(), torch.int32
+    dev, i32 = torch.cuda.current_device(), _I32
     s = lib().pka_free_pages(_here(page_refs, "page_refs", i32, dev), page_refs.numel(),
-                             _here(pages, "pages", i32, dev), pages.numel(), _stream(stream))
-    if check:
+                             _here(pages, "pages", i32, dev), pages.numel(), _here_stream(stream, dev))
+    if check and s:
         _check(s, "pka_free_pages")
     return s
 
@@ -561,7 +582,7 @@ def pka_fork_pages(page_size, page_refs, kv_indptr, kv_indices, last_page_len, p
                    stream=None, check=True) -> int:
     """Tables of children that continue parents; the copy lists and counts go
     to pka_copy_pages.  All arrays are device int32."""
-    dev, i32 = torch.cuda.current_device(), torch.int32
+    dev, i32 = torch.cuda.current_device(), _I32
     parents, children = last_page_len.numel(), parent.numel()
     if kv_indptr.numel() != parents + 1 or child_indptr.numel() != children + 1:
         raise ValueError("an indptr has one element more than its requests")
@@ -577,8 +598,8 @@ def pka_fork_pages(page_size, page_refs, kv_indptr, kv_indices, last_page_len, p
         _here(child_indices, "child_indices", i32, dev), child_indices.numel(),
         _here(copy_src, "copy_src", i32, dev), _here(copy_dst, "copy_dst", i32, dev),
         _here(copy_slots, "copy_slots", i32, dev), _here(counts, "counts", i32, dev),
-        _stream(stream))
-    if check:
+        _here_stream(stream, dev))
+    if check and s:
         _check(s, "pka_fork_pages")
     return s
 
@@ -587,7 +608,7 @@ def pka_compact_pages(page_refs, kv_indices, page_refs_out, kv_indices_out, page
                       copy_dst, counts, stream=None, check=True) -> int:
     """Move the live pages to the front of the pool: the new references and
     table entries (either may be written in place), the map and the moves."""
-    dev, i32 = torch.cuda.current_device(), torch.int32
+    dev, i32 = torch.cuda.current_device(), _I32
     n = page_refs.numel()
     if page_refs_out.numel() != n or page_map.numel() != n:
         raise ValueError("page_refs_out and page_map hold one element a page")
@@ -600,8 +621,8 @@ def pka_compact_pages(page_refs, kv_indices, page_refs_out, kv_indices_out, page
         kv_indices.numel(), _here(page_refs_out, "page_refs_out", i32, dev),
         _here(kv_indices_out, "kv_indices_out", i32, dev), _here(page_map, "page_map", i32, dev),
         _here(copy_src, "copy_src", i32, dev), _here(copy_dst, "copy_dst", i32, dev),
-        _here(counts, "counts", i32, dev), _stream(stream))
-    if check:
+        _here(counts, "counts", i32, dev), _here_stream(stream, dev))
+    if check and s:
         _check(s, "pka_compact_pages")
     return s
 

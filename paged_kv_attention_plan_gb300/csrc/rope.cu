@@ -136,9 +136,14 @@ __device__ __forceinline__ int64_t pool_offset(const RopeArgs& a, int page, int 
 // each of the 32 / (D/16) heads of a step, so its 8 sines and cosines serve
 // the whole row.  A unit is two 16-byte pieces A and B of the head: pair j is
 // (A[j], B[j]), or, for adjacent pairs, the pairs inside A and inside B.
-// Units past rotary_dim are copied bit by bit.
+// Elements past rotary_dim are copied bit by bit.  The pieces of kInFlight
+// steps are loaded before the first of them is used, the row's first ones
+// before its page and its sines are looked up.
+constexpr int kInFlight = 2;
+
 template <int D, int L, bool APPEND, bool F8>
-__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(256, F8 || L == kScattered ? 3 : 4)
+rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int UNITS = D / 16;      // lanes of a head
   constexpr int HPS = 32 / UNITS;    // heads of a step
   constexpr int K = 8 / HPS;         // pairs whose sine and cosine a lane computes
@@ -179,13 +184,41 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
   const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
   for (int64_t row = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5); row < a.rows;
        row += nwarps) {
+    uint32_t wa[kInFlight][4], wb[kInFlight][4];
+    auto load = [&](int hb) {  // the lane's pieces of heads hb + sub, + HPS, ...
+#pragma unroll
+      for (int t = 0; t < kInFlight; ++t) {
+        const int h = hb + t * HPS + sub;
+        if (h >= h1) continue;
+        const uint16_t* src;
+        if (h < a.q_heads)
+          src = a.q + row * a.q_stride + (int64_t)h * D;
+        else if (!APPEND || h < a.q_heads + a.k_heads)
+          src = a.k + row * a.k_stride + (int64_t)(h - a.q_heads) * D;
+        else
+          src = a.v + row * a.v_stride + (int64_t)(h - a.q_heads - a.k_heads) * D;
+        load_piece<L>(src, off_a, first_of, wa[t]);
+        load_piece<L>(src, off_b, second_of, wb[t]);
+      }
+    };
+    load(h0);
+
     int64_t pos = 0;
     int32_t page = -1;
     int slot = 0;
     if constexpr (APPEND) {
-      if (row >= a.append_indptr[a.batch]) continue;  // a row of no request
-      const int r = warp_find(a.append_indptr, a.batch, row, lane);
-      const int first = a.append_indptr[r], n_app = a.append_indptr[r + 1] - first;
+      // a decode step's rows are one a request: row r is tried as request r's
+      // before the search
+      const int guess = (int)min(row, (int64_t)a.batch - 1);
+      int r = guess, first = a.append_indptr[guess], last = a.append_indptr[guess + 1];
+      const int end = a.append_indptr[a.batch];
+      if (row < first || row >= last) {
+        if (row >= end) continue;  // a row of no request
+        r = warp_find(a.append_indptr, a.batch, row, lane);
+        first = a.append_indptr[r];
+        last = a.append_indptr[r + 1];
+      }
+      const int n_app = last - first;
       const int kv0 = a.kv_indptr[r], pages = a.kv_indptr[r + 1] - kv0;
       const int64_t kv_len = (int64_t)(pages - 1) * a.page_size + a.last_page_len[r];
       pos = kv_len - n_app + (row - first);
@@ -200,7 +233,6 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
       }
     }
     if (!APPEND || a.positions) pos = a.positions[row];
-
 
     // sines and cosines: K pairs a lane, exchanged among the lanes of a unit
     float c[8], s[8];
@@ -220,68 +252,76 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
       }
     }
 
-    for (int h = h0 + sub; h < h1; h += HPS) {
-      const bool is_q = h < a.q_heads;
-      const bool is_v = APPEND && h >= a.q_heads + a.k_heads;
-      const int hh = is_q ? h : is_v ? h - a.q_heads - a.k_heads : h - a.q_heads;
-      const uint16_t* src = (is_q ? a.q + row * a.q_stride
-                             : is_v ? a.v + row * a.v_stride : a.k + row * a.k_stride) +
-                            (int64_t)hh * D;
-      uint32_t wa[4], wb[4];
-      load_piece<L>(src, off_a, first_of, wa);
-      load_piece<L>(src, off_b, second_of, wb);
-      float xa[8], xb[8];
-      unpack8(wa, xa);
-      unpack8(wb, xb);
-      if (!is_v) {
+    for (int hb = h0;;) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          // pair j: (A[j], B[j]), or adjacent elements of A (j < 4) or of B
-          float& x = L != kAdjacent ? xa[j] : j < 4 ? xa[2 * j] : xb[2 * (j - 4)];
-          float& y = L != kAdjacent ? xb[j] : j < 4 ? xa[2 * j + 1] : xb[2 * (j - 4) + 1];
-          if (turning >> j & 1) {
-            const float t = x * c[j] - y * s[j];
-            y = x * s[j] + y * c[j];
-            x = t;
+      for (int t = 0; t < kInFlight; ++t) {
+        const int h = hb + t * HPS + sub;
+        if (h >= h1) continue;
+        const bool is_q = h < a.q_heads;
+        const bool is_v = APPEND && h >= a.q_heads + a.k_heads;
+        const int hh = is_q ? h : is_v ? h - a.q_heads - a.k_heads : h - a.q_heads;
+        const bool to_pool = APPEND && !is_q;
+        if (to_pool && page < 0) continue;
+        float xa[8], xb[8];
+        if (F8 || !is_v) {
+          unpack8(wa[t], xa);
+          unpack8(wb[t], xb);
+        }
+        if (!is_v) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            // pair j: (A[j], B[j]), or adjacent elements of A (j < 4) or of B
+            float& x = L != kAdjacent ? xa[j] : j < 4 ? xa[2 * j] : xb[2 * (j - 4)];
+            float& y = L != kAdjacent ? xb[j] : j < 4 ? xa[2 * j + 1] : xb[2 * (j - 4) + 1];
+            if (turning >> j & 1) {
+              const float z = x * c[j] - y * s[j];
+              y = x * s[j] + y * c[j];
+              x = z;
+            }
           }
         }
-      }
-      const bool to_pool = APPEND && !is_q;
-      if (to_pool && page < 0) continue;
-      if (F8 && to_pool) {
-        const float scale = is_v ? a.v_scale : a.k_scale, inv = is_v ? a.v_inv : a.k_inv;
-        uint8_t* p = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) +
-                     pool_offset<D>(a, page, slot, hh);
-        store_codes<L>(p, off_a, first_of, to_e4m3x8(xa, scale, inv));
-        store_codes<L>(p, off_b, second_of, to_e4m3x8(xb, scale, inv));
-        continue;
-      }
-      // rotated elements rounded once to bf16; the others keep their bits
-      if (!is_v) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t ya = float2_to_bf16x2(xa[2 * i], xa[2 * i + 1]);
-          const uint32_t yb = float2_to_bf16x2(xb[2 * i], xb[2 * i + 1]);
-          uint32_t ma, mb;  // the rotated halves of word i of A and of B
-          if constexpr (L == kAdjacent) {
-            ma = turning >> i & 1 ? ~0u : 0u;
-            mb = turning >> (i + 4) & 1 ? ~0u : 0u;
-          } else {
-            ma = mb = (turning >> (2 * i) & 1 ? 0xffffu : 0u) |
-                      (turning >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
-          }
-          wa[i] = (ya & ma) | (wa[i] & ~ma);
-          wb[i] = (yb & mb) | (wb[i] & ~mb);
+        if (F8 && to_pool) {
+          const float scale = is_v ? a.v_scale : a.k_scale, inv = is_v ? a.v_inv : a.k_inv;
+          uint8_t* p = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) +
+                       pool_offset<D>(a, page, slot, hh);
+          store_codes<L>(p, off_a, first_of, to_e4m3x8(xa, scale, inv));
+          store_codes<L>(p, off_b, second_of, to_e4m3x8(xb, scale, inv));
+          continue;
         }
+        // rotated elements rounded once to bf16; the others keep their bits
+        if (!is_v) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t ya = float2_to_bf16x2(xa[2 * i], xa[2 * i + 1]);
+            const uint32_t yb = float2_to_bf16x2(xb[2 * i], xb[2 * i + 1]);
+            uint32_t ma, mb;  // the rotated halves of word i of A and of B
+            if constexpr (L == kHalf) {
+              ma = mb = turning ? ~0u : 0u;
+            } else if constexpr (L == kAdjacent) {
+              ma = turning >> i & 1 ? ~0u : 0u;
+              mb = turning >> (i + 4) & 1 ? ~0u : 0u;
+            } else {
+              ma = mb = (turning >> (2 * i) & 1 ? 0xffffu : 0u) |
+                        (turning >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
+            }
+            wa[t][i] = (ya & ma) | (wa[t][i] & ~ma);
+            wb[t][i] = (yb & mb) | (wb[t][i] & ~mb);
+          }
+        }
+        uint16_t* p;
+        if (to_pool)
+          p = static_cast<uint16_t*>(is_v ? a.v_pool : a.k_pool) +
+              pool_offset<D>(a, page, slot, hh);
+        else if (is_q)
+          p = a.q_out + row * a.q_out_stride + (int64_t)hh * D;
+        else
+          p = a.k_out + row * a.k_out_stride + (int64_t)hh * D;
+        store_piece<L>(p, off_a, first_of, wa[t]);
+        store_piece<L>(p, off_b, second_of, wb[t]);
       }
-      uint16_t* p;
-      if (to_pool)
-        p = static_cast<uint16_t*>(is_v ? a.v_pool : a.k_pool) + pool_offset<D>(a, page, slot, hh);
-      else
-        p = (is_q ? a.q_out + row * a.q_out_stride : a.k_out + row * a.k_out_stride) +
-            (int64_t)hh * D;
-      store_piece<L>(p, off_a, first_of, wa);
-      store_piece<L>(p, off_b, second_of, wb);
+      hb += kInFlight * HPS;
+      if (hb >= h1) break;
+      load(hb);
     }
   }
 }
@@ -298,9 +338,8 @@ cudaError_t launch(const RopeArgs& args, cudaStream_t stream) {
   per = per < 1 ? 1 : per > steps ? steps : per;
   const int parts = (int)((steps + per - 1) / per);
   a.steps_per_part = (int)per;
-  int64_t blocks = (a.rows + 7) / 8;
-  const int64_t cap = 8 * (int64_t)(sms > 0 ? sms : 1);
-  if (blocks > cap) blocks = cap;
+  const int64_t blocks = (a.rows + 7) / 8;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   rope_kernel<D, L, APPEND, F8><<<dim3((unsigned)blocks, (unsigned)parts), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
