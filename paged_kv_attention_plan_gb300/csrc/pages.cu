@@ -10,6 +10,8 @@
 // on flags.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "pka_cache.h"
 #include "pka_internal.h"
 
@@ -18,7 +20,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kClusterCtas = 8;    // blocks of a counting launch: one portable cluster
+constexpr int kMaxCluster = 16;     // blocks of the largest counting launch
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr unsigned kAll = 0xffffffffu;
@@ -58,6 +60,22 @@ __device__ __forceinline__ int4 refs_at(const int32_t* refs, const Share& s, int
   return r;
 }
 
+// Walk the warp's share in order, 128 pages a step, the loads of four steps
+// in flight: use(p, r) with this lane's pages p .. p+3 and their references;
+// a false result from any lane ends the walk (after the steps loaded with it).
+template <class F>
+__device__ __forceinline__ void walk(const int32_t* refs, const Share& s, int past, F use) {
+  constexpr int U = 4;
+  for (int64_t p0 = s.lo; p0 < s.hi; p0 += 128 * U) {
+    int4 r[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) r[i] = refs_at(refs, s, p0 + 128 * i + 4 * s.lane, past);
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (p0 + 128 * i < s.hi && !use(p0 + 128 * i + 4 * s.lane, r[i])) return;
+  }
+}
+
 // Bit k: page p + k is free (has no reference); pages past the share are not.
 __device__ __forceinline__ unsigned free_bits(const int4& r) {
   return (r.x <= 0 ? 1u : 0u) | (r.y <= 0 ? 2u : 0u) | (r.z <= 0 ? 4u : 0u) |
@@ -66,10 +84,24 @@ __device__ __forceinline__ unsigned free_bits(const int4& r) {
 
 __device__ __forceinline__ int count_free(const int32_t* refs, const Share& s) {
   int n = 0;
-#pragma unroll 4
-  for (int64_t p = s.lo + 4 * s.lane; p < s.hi; p += 128)
-    n += __popc(free_bits(refs_at(refs, s, p, 1)));
+  walk(refs, s, 1, [&](int64_t, const int4& r) {
+    n += __popc(free_bits(r));
+    return true;
+  });
   return __reduce_add_sync(kAll, n);
+}
+
+// Of the set bits of a step's lanes, taken lane by lane: how many come before
+// this lane's first, and how many there are.
+__device__ __forceinline__ void rank_bits(unsigned bits, int lane, int* before, int* all) {
+  const unsigned below = (1u << lane) - 1;
+  *before = *all = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const unsigned b = __ballot_sync(kAll, bits >> k & 1);
+    *before += __popc(b & below);
+    *all += __popc(b);
+  }
 }
 
 struct Counts {
@@ -105,17 +137,12 @@ __device__ __forceinline__ void leave() { cg::this_cluster().barrier_wait(); }
 template <class F>
 __device__ __forceinline__ void each_free(const int32_t* refs, const Share& s, int rank, int stop,
                                           F use) {
-  const unsigned below = (1u << s.lane) - 1;
-  for (int64_t p0 = s.lo; p0 < s.hi && rank < stop; p0 += 128) {
-    const int64_t p = p0 + 4 * s.lane;
-    const unsigned bits = free_bits(refs_at(refs, s, p, 1));
-    int at = rank, all = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const unsigned b = __ballot_sync(kAll, bits >> k & 1);
-      at += __popc(b & below);
-      all += __popc(b);
-    }
+  if (rank >= stop) return;
+  walk(refs, s, 1, [&](int64_t p, const int4& r) {
+    const unsigned bits = free_bits(r);
+    int at, all;
+    rank_bits(bits, s.lane, &at, &all);
+    at += rank;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (bits >> k & 1) {
@@ -123,29 +150,35 @@ __device__ __forceinline__ void each_free(const int32_t* refs, const Share& s, i
         ++at;
       }
     rank += all;
-  }
+    return rank < stop;
+  });
 }
 
 // ---------------------------------------------------------------------------
 // Taking and returning pages
 // ---------------------------------------------------------------------------
 
-__global__ void __launch_bounds__(kThreads, 1) alloc_kernel(int32_t* refs, int32_t num_pages,
-                                                         int32_t n, int32_t* pages,
-                                                         int32_t* err) {
+struct AllocArgs {
+  int32_t* refs;
+  int32_t* pages;
+  int32_t* err;
+  int32_t num_pages, n;
+};
+
+__global__ void __launch_bounds__(kThreads, 1) alloc_kernel(const AllocArgs a) {
   __shared__ Counts c;
-  const Share s = my_share(refs, num_pages);
+  const Share s = my_share(a.refs, a.num_pages);
   int before, total;
-  cluster_prefix(c, count_free(refs, s), &before, &total);
-  if (total < n) {
-    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < n;
+  cluster_prefix(c, count_free(a.refs, s), &before, &total);
+  if (total < a.n) {
+    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < a.n;
          i += (int64_t)gridDim.x * kThreads)
-      pages[i] = -1;
-    if (blockIdx.x == 0 && threadIdx.x == 0) note_error(err, PKA_ERR_WORKSPACE);
+      a.pages[i] = -1;
+    if (blockIdx.x == 0 && threadIdx.x == 0) note_error(a.err, PKA_ERR_WORKSPACE);
   } else {
-    each_free(refs, s, before, n, [&](int rank, int32_t page) {
-      pages[rank] = page;
-      refs[page] = 1;
+    each_free(a.refs, s, before, a.n, [&](int rank, int32_t page) {
+      a.pages[rank] = page;
+      a.refs[page] = 1;
     });
   }
   leave();
@@ -153,18 +186,24 @@ __global__ void __launch_bounds__(kThreads, 1) alloc_kernel(int32_t* refs, int32
 
 // A page's count never stays below zero: a decrement that finds none left is
 // taken back and noted.  Exactly as many decrements succeed as there were
-// references, in whatever order they come.
+// references, in whatever order they come.  Four entries a thread, so that
+// four atomics are in flight.
 __global__ void __launch_bounds__(256) free_kernel(int32_t* refs, int32_t num_pages,
                                                    const int32_t* pages, int64_t n, int32_t* err) {
+  constexpr int U = 4;
+  const int64_t step = (int64_t)gridDim.x * blockDim.x;
   bool bad = false;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int32_t p = pages[i];
-    if (p < 0 || p >= num_pages) {
-      bad = true;
-    } else if (atomicSub(refs + p, 1) <= 0) {
-      atomicAdd(refs + p, 1);
-      bad = true;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += U * step) {
+    int32_t p[U], had[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) p[u] = i + u * step < n ? pages[i + u * step] : -1;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      had[u] = p[u] >= 0 && p[u] < num_pages ? atomicSub(refs + p[u], 1) : 1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (had[u] <= 0) atomicAdd(refs + p[u], 1);
+      bad = bad || had[u] <= 0 || (i + u * step < n && (p[u] < 0 || p[u] >= num_pages));
     }
   }
   if (bad) note_error(err, PKA_ERR_METADATA);
@@ -228,15 +267,45 @@ __device__ __forceinline__ Child child_at(const ForkArgs& a, int c) {
   return x;
 }
 
+// Shared memory of fork_take_kernel, one element a child.
+struct ChildSums {
+  int32_t* fresh_before;   // [num_children + 1] fresh pages of the children before
+  int32_t* copies_before;  // copies of the children before
+  int32_t* first;          // as in Child
+  int32_t* shared;
+  int32_t* parent_first;
+  int32_t* slots;
+};
+
+constexpr int kChildWords = 6;
+
+__device__ __forceinline__ ChildSums child_sums(int32_t* mem, int n) {
+  return {mem, mem + n + 1, mem + 2 * n + 1, mem + 3 * n + 1, mem + 4 * n + 1, mem + 5 * n + 1};
+}
+
+// The last i in [lo, hi] with ptr[i] <= x.
+__device__ __forceinline__ int find_between(const int32_t* ptr, int lo, int hi, int64_t x) {
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (ptr[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Shared entries of a table are written by the launch that takes the fresh
+// pages when there are at most this many entries (8 a thread of 8 blocks);
+// past it they go to a launch over the whole GPU.
+constexpr int kShareInTake = 65536;
+
 // Checks every child, takes the lowest free pages for all of them and writes
 // the entries that these fill, the copy list and the counts; nothing at all
 // when a child is malformed or the pages do not suffice.  Every block of the
-// cluster scans the children for itself (shared memory holds the running sum
-// of fresh pages and of copies), then writes for the free pages of its share.
+// cluster scans the children for itself into shared memory, then writes for
+// the free pages of its share.
+template <bool SHARE>
 __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a) {
-  extern __shared__ int32_t sums[];
-  int32_t* fresh_before = sums;                      // [num_children + 1]
-  int32_t* copies_before = sums + a.num_children + 1;  // [num_children]
+  extern __shared__ int32_t mem[];
+  const ChildSums sums = child_sums(mem, a.num_children);
   __shared__ Counts c;
   __shared__ int64_t warp_sum[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -255,6 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
       const Child ch = child_at(a, i);
       ok = ok && ch.ok;
       if (ch.ok) x = ((int64_t)ch.fresh << 32) | (ch.slots > 0 ? 1 : 0);
+      sums.first[i] = ch.first;
+      sums.shared[i] = ch.shared;
+      sums.parent_first[i] = ch.parent_first;
+      sums.slots[i] = ch.slots;
     }
     int64_t incl = x;
 #pragma unroll
@@ -272,51 +345,60 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
     }
     if (i < a.num_children) {
       const int64_t excl = base + incl - x;
-      fresh_before[i] = (int32_t)(excl >> 32);
-      copies_before[i] = (int32_t)excl;
+      sums.fresh_before[i] = (int32_t)(excl >> 32);
+      sums.copies_before[i] = (int32_t)excl;
     }
     carry = all;
   }
   ok = __syncthreads_and(ok);
   const int64_t needed = carry >> 32;
   const int copies = (int)(uint32_t)carry;
-  if (threadIdx.x == 0) fresh_before[a.num_children] = (int32_t)needed;
 
   int before, total;
-  cluster_prefix(c, mine, &before, &total);  // (a barrier: the sums are visible too)
+  cluster_prefix(c, mine, &before, &total);
   const bool refused = !ok || total < needed;
-  if (!refused) {
-    each_free(a.refs, s, before, (int)needed, [&](int rank, int32_t page) {
-      int lo = 0, hi = a.num_children - 1;  // the last child with fresh_before <= rank
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (fresh_before[mid] <= rank) lo = mid; else hi = mid - 1;
-      }
-      const Child ch = child_at(a, lo);
-      const int nth = rank - fresh_before[lo];
-      a.child_indices[ch.first + ch.shared + nth] = page;
-      a.refs[page] = 1;
-      if (nth == 0 && ch.slots > 0) {
-        const int i = copies_before[lo];
-        a.copy_src[i] = a.kv_indices[ch.parent_first + ch.shared];
-        a.copy_dst[i] = page;
-        a.copy_slots[i] = ch.slots;
-      }
-    });
-  }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     a.counts[0] = refused ? -1 : copies;
     a.counts[1] = refused ? -1 : (int32_t)needed;
     if (refused) note_error(a.err, ok ? PKA_ERR_WORKSPACE : PKA_ERR_METADATA);
   }
+  if (!refused) {
+    each_free(a.refs, s, before, (int)needed, [&](int rank, int32_t page) {
+      const int i = find_between(sums.fresh_before, 0, a.num_children - 1, rank);
+      const int nth = rank - sums.fresh_before[i];
+      a.child_indices[sums.first[i] + sums.shared[i] + nth] = page;
+      a.refs[page] = 1;
+      if (nth == 0 && sums.slots[i] > 0) {
+        const int to = sums.copies_before[i];
+        a.copy_src[to] = a.kv_indices[sums.parent_first[i] + sums.shared[i]];
+        a.copy_dst[to] = page;
+        a.copy_slots[to] = sums.slots[i];
+      }
+    });
+    if (SHARE) {
+      bool bad = false;
+      const int end = a.child_indptr[a.num_children];
+      for (int e = sums.first[0] + blockIdx.x * kThreads + threadIdx.x; e < end;
+           e += gridDim.x * kThreads) {
+        const int i = find_between(sums.first, 0, a.num_children - 1, e);
+        const int j = e - sums.first[i];
+        if (j >= sums.shared[i]) continue;
+        const int32_t page = a.kv_indices[sums.parent_first[i] + j];
+        a.child_indices[e] = page;
+        if (page >= 0 && page < a.num_pages) atomicAdd(a.refs + page, 1);
+        else bad = true;
+      }
+      if (bad) note_error(a.err, PKA_ERR_METADATA);
+    }
+  }
   leave();
 }
 
 // The shared entries of every child's table, each one reference more.  A warp
-// takes 256 entries; it looks up the children of the first and the last, and
-// where these differ each lane looks its own up between them.
+// takes 256 entries; where they belong to one child it is looked up once, else
+// each lane looks its own up between the children of the first and the last.
 __global__ void __launch_bounds__(256) fork_share_kernel(const ForkArgs a) {
-  constexpr int CHUNK = 256;
+  constexpr int U = 8, CHUNK = 32 * U;
   if (a.counts[0] < 0) return;  // refused
   const int lane = threadIdx.x & 31;
   const int64_t end = a.child_indptr[a.num_children];
@@ -325,21 +407,26 @@ __global__ void __launch_bounds__(256) fork_share_kernel(const ForkArgs a) {
        e0 += (int64_t)gridDim.x * 8 * CHUNK) {
     const int64_t e1 = min(e0 + CHUNK, end);
     const int first = warp_find(a.child_indptr, a.num_children, e0, lane);
-    const int last = warp_find(a.child_indptr, a.num_children, e1 - 1, lane);
-    for (int64_t e = e0 + lane; e < e1; e += 32) {
-      int lo = first, hi = last;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.child_indptr[mid] <= e) lo = mid; else hi = mid - 1;
-      }
-      const Child ch = child_at(a, lo);
+    const bool one = first + 1 >= a.num_children || a.child_indptr[first + 1] >= e1;
+    const int last = one ? first : warp_find(a.child_indptr, a.num_children, e1 - 1, lane);
+    Child ch = child_at(a, first);
+    int32_t page[U];
+    bool mine[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t e = e0 + 32 * u + lane;
+      if (!one && e < e1) ch = child_at(a, find_between(a.child_indptr, first, last, e));
       const int64_t j = e - ch.first;
-      if (j < 0 || j >= ch.shared) continue;
-      const int32_t page = a.kv_indices[ch.parent_first + j];
-      a.child_indices[e] = page;
-      if (page >= 0 && page < a.num_pages) atomicAdd(a.refs + page, 1);
-      else bad = true;
+      mine[u] = e < e1 && j >= 0 && j < ch.shared;
+      if (mine[u]) page[u] = a.kv_indices[ch.parent_first + j];
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (mine[u]) {
+        a.child_indices[e0 + 32 * u + lane] = page[u];
+        if (page[u] >= 0 && page[u] < a.num_pages) atomicAdd(a.refs + page[u], 1);
+        else bad = true;
+      }
   }
   if (bad) note_error(a.err, PKA_ERR_METADATA);
 }
@@ -355,6 +442,10 @@ struct CompactArgs {
   int32_t* copy_src;
   int32_t* copy_dst;
   int32_t* counts;
+  const int32_t* in;     // table entries; may be out
+  int32_t* out;
+  int32_t* err;
+  int64_t num_indices;
   int32_t num_pages;
 };
 
@@ -362,84 +453,92 @@ struct CompactArgs {
 // below L: as many of the one as of the other.  Before page p lie r(p) live
 // pages (one pass of counting), so the free page p < L is number p - r(p) of
 // its kind from below and the live page p >= L number L - 1 - r(p) of its kind
-// from above; equal numbers pair up.
+// from above; equal numbers pair up.  This launch writes the two lists by
+// those numbers; a moving page's entry of the map holds -2 - number until
+// move_kernel, which needs both lists whole, turns it into the new id.
 __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs a) {
   __shared__ Counts c;
   const Share s = my_share(a.refs, a.num_pages);
-  const int pages = (int)(s.hi - s.lo);
   int before, live;
-  cluster_prefix(c, pages - count_free(a.refs, s), &before, &live);
-  leave();
+  cluster_prefix(c, (int)(s.hi - s.lo) - count_free(a.refs, s), &before, &live);
 
-  const unsigned below = (1u << s.lane) - 1;
-  int rank = before;  // live pages before p0
-  for (int64_t p0 = s.lo; p0 < s.hi; p0 += 128) {
-    const int64_t p = p0 + 4 * s.lane;
-    const int4 r4 = refs_at(a.refs, s, p, 0);
+  const bool apart = a.refs != a.refs_out;
+  const bool vec_map = (reinterpret_cast<uintptr_t>(a.map) & 15) == 0;
+  const bool vec_out = (reinterpret_cast<uintptr_t>(a.refs_out) & 15) == 0;
+  int rank = before;  // live pages before the step
+  walk(a.refs, s, 0, [&](int64_t p, const int4& r4) {
     const int r[4] = {r4.x, r4.y, r4.z, r4.w};
-    int at = rank, all = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const unsigned b = __ballot_sync(kAll, r[k] > 0);
-      at += __popc(b & below);
-      all += __popc(b);
-    }
+    const unsigned bits = ~free_bits(r4) & 15u;  // live
+    int at, all;
+    rank_bits(bits, s.lane, &at, &all);
+    at += rank;
+    int m[4], o[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int32_t page = (int32_t)(p + k);
+      const bool held = bits >> k & 1;
+      m[k] = !held ? -1 : page < live ? page : -2 - (live - 1 - at);
+      o[k] = page < live ? max(r[k], 0) : 0;  // a free page below L: its mover's, later
       if (p + k < s.hi) {
         if (page == live) {
           a.counts[0] = live - at;
           a.counts[1] = live;
         }
-        if (page < live) {
-          if (r[k] > 0) {
-            a.map[page] = page;
-            a.refs_out[page] = r[k];
-          } else {
-            a.map[page] = -1;
-            a.copy_dst[page - at] = page;
-          }
-        } else if (r[k] > 0) {
-          a.copy_src[live - 1 - at] = page;
-        } else {
-          a.map[page] = -1;
-          a.refs_out[page] = 0;
-        }
+        if (!held && page < live) a.copy_dst[page - at] = page;
+        if (held && page >= live) a.copy_src[live - 1 - at] = page;
       }
-      at += r[k] > 0;
+      at += held;
     }
     rank += all;
-  }
+    if (vec_map && p + 4 <= s.hi) {
+      *reinterpret_cast<int4*>(a.map + p) = make_int4(m[0], m[1], m[2], m[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (p + k < s.hi) a.map[p + k] = m[k];
+    }
+    if (apart && vec_out && p + 4 <= s.hi) {
+      *reinterpret_cast<int4*>(a.refs_out + p) = make_int4(o[0], o[1], o[2], o[3]);
+    } else if (apart) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (p + k < s.hi) a.refs_out[p + k] = o[k];
+    }
+    return true;
+  });
   if (live == a.num_pages && blockIdx.x == 0 && threadIdx.x == 0) {
     a.counts[0] = 0;
     a.counts[1] = live;
   }
-  cg::this_cluster().sync();  // both lists are whole
-  const int moves = __ldcg(a.counts);
-  for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < moves;
-       i += (int64_t)gridDim.x * kThreads) {
-    const int32_t src = __ldcg(a.copy_src + i), dst = __ldcg(a.copy_dst + i);
-    a.map[src] = dst;
-    a.refs_out[dst] = __ldcg(a.refs + src);
-    a.refs_out[src] = 0;
-  }
+  leave();
 }
 
-// Table entries through the map.  An entry that names no live page stays as
+// The moves' references and map entries, and the table entries through the
+// map.  An entry whose page moves reads its map entry before or after it is
+// turned; either gives the new id.  An entry that names no live page stays as
 // it is and is noted.
-__global__ void __launch_bounds__(256) remap_kernel(const int32_t* map, int32_t num_pages,
-                                                    const int32_t* in, int64_t n, int32_t* out,
-                                                    int32_t* err) {
+__global__ void __launch_bounds__(256) move_kernel(const CompactArgs a) {
+  const int64_t at = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  const int64_t step = (int64_t)gridDim.x * blockDim.x;
   bool bad = false;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int32_t p = in[i];
-    const int32_t to = p >= 0 && p < num_pages ? map[p] : -1;
+  for (int64_t i = at; i < a.num_indices; i += step) {
+    const int32_t p = a.in[i];
+    int32_t to = -1;
+    if (p >= 0 && p < a.num_pages) {
+      to = *const_cast<volatile int32_t*>(a.map + p);
+      if (to < -1) to = a.copy_dst[-2 - to];
+    }
     bad = bad || to < 0;
-    out[i] = to < 0 ? p : to;
+    a.out[i] = to < 0 ? p : to;
   }
-  if (bad) note_error(err, PKA_ERR_METADATA);
+  const int moves = a.counts[0];
+  for (int64_t i = at; i < moves; i += step) {
+    const int32_t src = a.copy_src[i], dst = a.copy_dst[i];
+    a.refs_out[dst] = a.refs[src];
+    if (a.refs == a.refs_out) a.refs_out[src] = 0;
+    *const_cast<volatile int32_t*>(a.map + src) = dst;
+  }
+  if (bad) note_error(a.err, PKA_ERR_METADATA);
 }
 
 // ---------------------------------------------------------------------------
@@ -464,49 +563,85 @@ struct CopyArgs {
   int32_t* err;
 };
 
-// blockIdx.y is (layer, K or V); a warp takes 4 KB of a page, eight 16-byte
-// pieces a lane in flight.
+// Whether piece `off` (bytes into the page) lies in the first `slots` slots:
+// NHD pages hold them slot by slot, HND pages in every head.
+__device__ __forceinline__ bool in_slots(const CopyArgs& a, uint32_t off, int slots) {
+  if (slots == a.page_size) return true;
+  const uint32_t slot = a.layout == PKA_NHD
+                            ? off / (uint32_t)a.slot_row
+                            : off / (uint32_t)a.head_row % (uint32_t)a.page_size;
+  return slot < (uint32_t)slots;
+}
+
+// Entry i of the list, or false for one that is skipped.
+__device__ __forceinline__ bool copy_at(const CopyArgs& a, int64_t i, int64_t* from, int64_t* to,
+                                        int* slots, bool* bad) {
+  const int32_t src = a.src[i], dst = a.dst[i];
+  *slots = a.slots ? a.slots[i] : a.page_size;
+  if (src < 0 || src >= a.num_pages || dst < 0 || dst >= a.num_pages || *slots < 0 ||
+      *slots > a.page_size) {
+    *bad = true;
+    return false;
+  }
+  *from = src * a.page_bytes;
+  *to = dst * a.page_bytes;
+  return src != dst;
+}
+
+// blockIdx.y is (layer, K or V).  A warp moves 4 KB, eight 16-byte pieces a
+// lane in flight: a stretch of one page, or (SMALL: pages below 4 KB) pieces
+// of as many pages as that takes, each lane with its own list entries.
+template <bool SMALL>
 __global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
   constexpr int PIECES = 8, CHUNK = PIECES * 512;
   const int lane = threadIdx.x & 31;
   uint8_t* pool = (blockIdx.y & 1 ? a.v : a.k) + (blockIdx.y >> 1) * a.layer_bytes;
   const uint32_t whole = (uint32_t)a.page_size * a.slot_row;
-  const uint32_t chunks = (whole + CHUNK - 1) / CHUNK;
+  const uint32_t chunks = (whole + CHUNK - 1) / CHUNK, pieces = whole / 16;
   int64_t n = a.max_copies;
   if (a.count) n = min(n, (int64_t)max(*a.count, 0));
-  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < n * chunks;
+  const int64_t units = SMALL ? (n * pieces + 32 * PIECES - 1) / (32 * PIECES) : n * chunks;
+  bool bad = false;
+  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < units;
        w += (int64_t)gridDim.x * 8) {
-    const int64_t i = w <= UINT32_MAX ? (uint32_t)w / chunks : w / chunks;
-    const uint32_t off0 = (uint32_t)(w - i * chunks) * CHUNK;
-    const int32_t src = a.src[i], dst = a.dst[i];
-    const int slots = a.slots ? a.slots[i] : a.page_size;
-    if (src < 0 || src >= a.num_pages || dst < 0 || dst >= a.num_pages || slots < 0 ||
-        slots > a.page_size) {
-      if (lane == 0) note_error(a.err, PKA_ERR_METADATA);
-      continue;
-    }
-    if (src == dst) continue;
-    const uint8_t* from = pool + src * a.page_bytes;
-    uint8_t* to = pool + dst * a.page_bytes;
     uint4 x[PIECES];
-    bool take[PIECES];
+    if constexpr (SMALL) {
+      int64_t put[PIECES];
 #pragma unroll
-    for (int u = 0; u < PIECES; ++u) {
-      const uint32_t off = off0 + u * 512 + lane * 16;
-      take[u] = off < whole;
-      if (slots < a.page_size) {
-        // NHD: the first slots' rows lie first; HND: slot by slot in each head
-        const uint32_t slot = a.layout == PKA_NHD ? off / (uint32_t)a.slot_row
-                                                  : off / (uint32_t)a.head_row %
-                                                        (uint32_t)a.page_size;
-        take[u] = take[u] && slot < (uint32_t)slots;
+      for (int u = 0; u < PIECES; ++u) {
+        const int64_t at = w * (32 * PIECES) + u * 32 + lane;
+        put[u] = -1;
+        if (at >= n * pieces) continue;
+        const int64_t i = at <= UINT32_MAX ? (uint32_t)at / pieces : at / pieces;
+        const uint32_t off = (uint32_t)(at - i * pieces) * 16;
+        int64_t from, to;
+        int slots;
+        if (!copy_at(a, i, &from, &to, &slots, &bad) || !in_slots(a, off, slots)) continue;
+        x[u] = *reinterpret_cast<const uint4*>(pool + from + off);
+        put[u] = to + off;
       }
-      if (take[u]) x[u] = *reinterpret_cast<const uint4*>(from + off);
-    }
 #pragma unroll
-    for (int u = 0; u < PIECES; ++u)
-      if (take[u]) *reinterpret_cast<uint4*>(to + off0 + u * 512 + lane * 16) = x[u];
+      for (int u = 0; u < PIECES; ++u)
+        if (put[u] >= 0) *reinterpret_cast<uint4*>(pool + put[u]) = x[u];
+    } else {
+      const int64_t i = w <= UINT32_MAX ? (uint32_t)w / chunks : w / chunks;
+      const uint32_t off0 = (uint32_t)(w - i * chunks) * CHUNK + lane * 16;
+      int64_t from, to;
+      int slots;
+      if (!copy_at(a, i, &from, &to, &slots, &bad)) continue;
+      bool take[PIECES];
+#pragma unroll
+      for (int u = 0; u < PIECES; ++u) {
+        const uint32_t off = off0 + u * 512;
+        take[u] = off < whole && in_slots(a, off, slots);
+        if (take[u]) x[u] = *reinterpret_cast<const uint4*>(pool + from + off);
+      }
+#pragma unroll
+      for (int u = 0; u < PIECES; ++u)
+        if (take[u]) *reinterpret_cast<uint4*>(pool + to + off0 + u * 512) = x[u];
+    }
   }
+  if (bad) note_error(a.err, PKA_ERR_METADATA);
 }
 
 int blocks_for(int64_t work, int per_block, int per_sm) {
@@ -516,22 +651,39 @@ int blocks_for(int64_t work, int per_block, int per_sm) {
   return (int)(b < 1 ? 1 : b > cap ? cap : b);
 }
 
-// Launch as one cluster of kClusterCtas blocks.
-template <class... A>
-cudaError_t launch_cluster(void (*kernel)(A...), int smem, cudaStream_t stream, A... args) {
+// Blocks of a launch that counts the references of num_pages pages.
+int cluster_ctas(int32_t num_pages) {
+  return num_pages <= 16384 ? 1 : num_pages <= 131072 ? 8 : kMaxCluster;
+}
+
+// Launch as one cluster.
+template <auto Kernel, class A>
+cudaError_t launch_cluster(int ctas, int smem, cudaStream_t stream, const A& args) {
+  if (ctas > 8) {  // past the portable size: allowed once per device
+    static std::atomic<bool> set[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool tracked = dev >= 0 && dev < 64;
+    if (!tracked || !set[dev].load(std::memory_order_acquire)) {
+      e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      if (tracked) set[dev].store(true, std::memory_order_release);
+    }
+  }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kClusterCtas);
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kClusterCtas;
+  at[0].val.clusterDim.x = (unsigned)ctas;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  return cudaLaunchKernelEx(&cfg, Kernel, args);
 }
 
 pka_status done(cudaError_t e, const char* where) {
@@ -580,11 +732,17 @@ pka_status pka_copy_pages(const pka_params* p, int32_t num_layers, void* k, void
   a.head_row = p->head_dim * item;
   a.slot_row = (int32_t)slot_row;
   a.err = pka::device_error_word();
-  const int64_t chunks = (p->page_size * slot_row + 4095) / 4096;
+  const int64_t page = p->page_size * slot_row;
+  const bool small = page < 4096;
+  const int64_t units = small ? (max_copies * page + 4095) / 4096
+                              : max_copies * ((page + 4095) / 4096);
   const int per_sm = 16 / (2 * num_layers) > 1 ? 16 / (2 * num_layers) : 1;
-  const int x = pka::blocks_for(max_copies * chunks, 8, per_sm);
-  pka::copy_kernel<<<dim3((unsigned)x, (unsigned)(2 * num_layers)), 256, 0,
-                     static_cast<cudaStream_t>(stream)>>>(a);
+  const dim3 grid((unsigned)pka::blocks_for(units, 8, per_sm), (unsigned)(2 * num_layers));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (small)
+    pka::copy_kernel<true><<<grid, 256, 0, st>>>(a);
+  else
+    pka::copy_kernel<false><<<grid, 256, 0, st>>>(a);
   return pka::done(cudaGetLastError(), "page copy launch");
 }
 
@@ -595,9 +753,9 @@ pka_status pka_alloc_pages(int32_t* page_refs_d, int32_t num_pages, int32_t n, i
   if (n > num_pages) return PKA_ERR_WORKSPACE;
   if (!page_refs_d || !pages_d || pka::unaligned(page_refs_d) || pka::unaligned(pages_d))
     return PKA_ERR_INVALID_ARG;
-  return pka::done(pka::launch_cluster(pka::alloc_kernel, 0, static_cast<cudaStream_t>(stream),
-                                       page_refs_d, num_pages, n, pages_d,
-                                       pka::device_error_word()),
+  const pka::AllocArgs a{page_refs_d, pages_d, pka::device_error_word(), num_pages, n};
+  return pka::done(pka::launch_cluster<pka::alloc_kernel>(pka::cluster_ctas(num_pages), 0,
+                                                          static_cast<cudaStream_t>(stream), a),
                    "page alloc launch");
 }
 
@@ -657,11 +815,17 @@ pka_status pka_fork_pages(int32_t page_size, int32_t* page_refs_d, int32_t num_p
   a.num_children = num_children;
   a.num_indices = num_indices;
   a.num_child_indices = num_child_indices;
-  const int smem = (2 * num_children + 1) * (int)sizeof(int32_t);
-  cudaError_t e = pka::ensure_dynamic_smem<pka::fork_take_kernel>(smem);
-  if (e == cudaSuccess) e = pka::launch_cluster(pka::fork_take_kernel, smem, st, a);
+  const int smem = (pka::kChildWords * num_children + 1) * (int)sizeof(int32_t);
+  const int ctas = pka::cluster_ctas(num_pages);
+  if (num_child_indices <= pka::kShareInTake) {
+    cudaError_t e = pka::ensure_dynamic_smem<pka::fork_take_kernel<true>>(smem);
+    if (e == cudaSuccess)
+      e = pka::launch_cluster<pka::fork_take_kernel<true>>(ctas, smem, st, a);
+    return pka::done(e, "page fork launch");
+  }
+  cudaError_t e = pka::ensure_dynamic_smem<pka::fork_take_kernel<false>>(smem);
+  if (e == cudaSuccess) e = pka::launch_cluster<pka::fork_take_kernel<false>>(ctas, smem, st, a);
   if (e != cudaSuccess) return pka::cuda_failure(e, "page fork launch");
-  if (num_child_indices == 0) return PKA_OK;
   pka::fork_share_kernel<<<pka::blocks_for(num_child_indices, 8 * 256, 8), 256, 0, st>>>(a);
   return pka::done(cudaGetLastError(), "page fork launch");
 }
@@ -681,26 +845,27 @@ pka_status pka_compact_pages(const int32_t* page_refs_d, int32_t num_pages,
   for (const void* x : arrays)
     if (pka::unaligned(x)) return PKA_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (num_pages == 0) {
-    e = cudaMemsetAsync(counts_d, 0, 8, st);
-  } else {
-    pka::CompactArgs a{};
-    a.refs = page_refs_d;
-    a.refs_out = page_refs_out_d;
-    a.map = page_map_d;
-    a.copy_src = copy_src_d;
-    a.copy_dst = copy_dst_d;
-    a.counts = counts_d;
-    a.num_pages = num_pages;
-    e = pka::launch_cluster(pka::compact_kernel, 0, st, a);
-  }
+  pka::CompactArgs a{};
+  a.refs = page_refs_d;
+  a.refs_out = page_refs_out_d;
+  a.map = page_map_d;
+  a.copy_src = copy_src_d;
+  a.copy_dst = copy_dst_d;
+  a.counts = counts_d;
+  a.in = kv_indices_d;
+  a.out = kv_indices_out_d;
+  a.err = pka::device_error_word();
+  a.num_indices = num_indices;
+  a.num_pages = num_pages;
+  cudaError_t e = num_pages == 0
+                      ? cudaMemsetAsync(counts_d, 0, 8, st)
+                      : pka::launch_cluster<pka::compact_kernel>(pka::cluster_ctas(num_pages), 0,
+                                                                 st, a);
   if (e != cudaSuccess) return pka::cuda_failure(e, "page compact launch");
-  if (num_indices == 0) return PKA_OK;
-  pka::remap_kernel<<<pka::blocks_for(num_indices, 256, 8), 256, 0, st>>>(
-      page_map_d, num_pages, kv_indices_d, num_indices, kv_indices_out_d,
-      pka::device_error_word());
-  return pka::done(cudaGetLastError(), "page remap launch");
+  const int64_t work = num_indices > num_pages / 2 ? num_indices : num_pages / 2;
+  if (work == 0) return PKA_OK;
+  pka::move_kernel<<<pka::blocks_for(work, 256, 8), 256, 0, st>>>(a);
+  return pka::done(cudaGetLastError(), "page move launch");
 }
 
 }  // extern "C"
