@@ -29,28 +29,26 @@ constexpr unsigned kAll = 0xffffffffu;
 // Counting
 // ---------------------------------------------------------------------------
 
-// page_refs split among the warps of the cluster: whole 128-page strides,
-// one 16-byte load a lane.
+// page_refs split among the warps of the cluster: `per` pages each, whole
+// steps of 128 (one 16-byte load a lane).
 struct Share {
-  int64_t lo, hi;  // this warp's pages
+  uint32_t lo, hi;  // this warp's pages
   int lane;
-  bool vec;        // page_refs is 16-byte aligned
+  bool vec;         // page_refs is 16-byte aligned
 };
 
-__device__ __forceinline__ Share my_share(const int32_t* refs, int32_t num_pages) {
-  const int64_t warps = (int64_t)gridDim.x * kWarps;
-  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t per = ((num_pages + warps - 1) / warps + 127) / 128 * 128;
+__device__ __forceinline__ Share my_share(const int32_t* refs, uint32_t num_pages, uint32_t per) {
+  const uint64_t lo = (uint64_t)(blockIdx.x * kWarps + (threadIdx.x >> 5)) * per;
   Share s;
-  s.lo = min(w * per, (int64_t)num_pages);
-  s.hi = min(s.lo + per, (int64_t)num_pages);
+  s.lo = (uint32_t)min(lo, (uint64_t)num_pages);
+  s.hi = (uint32_t)min(lo + per, (uint64_t)num_pages);
   s.lane = threadIdx.x & 31;
   s.vec = (reinterpret_cast<uintptr_t>(refs) & 15) == 0;
   return s;
 }
 
 // References of pages p .. p+3 (those past `hi` come as `past`).
-__device__ __forceinline__ int4 refs_at(const int32_t* refs, const Share& s, int64_t p, int past) {
+__device__ __forceinline__ int4 refs_at(const int32_t* refs, const Share& s, uint32_t p, int past) {
   if (s.vec && p + 4 <= s.hi) return *reinterpret_cast<const int4*>(refs + p);
   int4 r;
   r.x = p < s.hi ? refs[p] : past;
@@ -62,18 +60,23 @@ __device__ __forceinline__ int4 refs_at(const int32_t* refs, const Share& s, int
 
 // Walk the warp's share in order, 128 pages a step, the loads of four steps
 // in flight: use(p, r) with this lane's pages p .. p+3 and their references;
-// a false result from any lane ends the walk (after the steps loaded with it).
+// a false result (of the whole warp) ends the walk.
 template <class F>
 __device__ __forceinline__ void walk(const int32_t* refs, const Share& s, int past, F use) {
   constexpr int U = 4;
-  for (int64_t p0 = s.lo; p0 < s.hi; p0 += 128 * U) {
-    int4 r[U];
+  uint32_t p = s.lo + 4 * s.lane;
+  uint32_t left = s.hi - s.lo;
+  if (s.vec)
+    for (; left >= 128 * U; left -= 128 * U, p += 128 * U) {
+      int4 r[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) r[i] = refs_at(refs, s, p0 + 128 * i + 4 * s.lane, past);
+      for (int i = 0; i < U; ++i) r[i] = *reinterpret_cast<const int4*>(refs + p + 128 * i);
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (p0 + 128 * i < s.hi && !use(p0 + 128 * i + 4 * s.lane, r[i])) return;
-  }
+      for (int i = 0; i < U; ++i)
+        if (!use(p + 128 * i, r[i])) return;
+    }
+  for (; left > 0; left -= min(left, 128u), p += 128)
+    if (!use(p, refs_at(refs, s, p, past))) return;
 }
 
 // Bit k: page p + k is free (has no reference); pages past the share are not.
@@ -84,8 +87,8 @@ __device__ __forceinline__ unsigned free_bits(const int4& r) {
 
 __device__ __forceinline__ int count_free(const int32_t* refs, const Share& s) {
   int n = 0;
-  walk(refs, s, 1, [&](int64_t, const int4& r) {
-    n += __popc(free_bits(r));
+  walk(refs, s, 1, [&](uint32_t, const int4& r) {
+    n += (r.x <= 0) + (r.y <= 0) + (r.z <= 0) + (r.w <= 0);
     return true;
   });
   return __reduce_add_sync(kAll, n);
@@ -117,38 +120,57 @@ __device__ __forceinline__ void cluster_prefix(Counts& c, int mine, int* before,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) c.warp[warp] = mine;
   __syncthreads();
-  if (warp == 0) {
-    const int sum = __reduce_add_sync(kAll, c.warp[lane]);
-    if (lane == 0) c.block = sum;
-  }
+  const int own = c.warp[lane];
+  const int block = __reduce_add_sync(kAll, own);
+  *before = __reduce_add_sync(kAll, lane < warp ? own : 0);
+  *total = block;
+  if (gridDim.x == 1) return;
+  if (threadIdx.x == 0) c.block = block;
   cluster.sync();
-  const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int there = lane < ctas ? cluster.map_shared_rank(&c, lane)->block : 0;
+  const int there = lane < gridDim.x ? cluster.map_shared_rank(&c, lane)->block : 0;
   cluster.barrier_arrive();
   *total = __reduce_add_sync(kAll, there);
-  *before = __reduce_add_sync(kAll, lane < rank ? there : 0) +
-            __reduce_add_sync(kAll, lane < warp ? c.warp[lane] : 0);
+  *before += __reduce_add_sync(kAll, lane < blockIdx.x ? there : 0);
 }
 
-__device__ __forceinline__ void leave() { cg::this_cluster().barrier_wait(); }
+__device__ __forceinline__ void leave() {
+  if (gridDim.x > 1) cg::this_cluster().barrier_wait();
+}
 
-// Free pages of this warp's share in ascending order, the first with rank
-// `rank`, until rank `stop`: use(rank, page).
-template <class F>
-__device__ __forceinline__ void each_free(const int32_t* refs, const Share& s, int rank, int stop,
+// Take the free pages of this warp's share in ascending order, the first with
+// rank `rank`, until rank `stop`: use(rank, page).  ALONE: nobody else changes
+// a reference meanwhile, so a lane stores its four pages at once.
+template <bool ALONE, class F>
+__device__ __forceinline__ void take_free(int32_t* refs, const Share& s, int rank, int stop,
                                           F use) {
   if (rank >= stop) return;
-  walk(refs, s, 1, [&](int64_t p, const int4& r) {
+  walk(refs, s, 1, [&](uint32_t p, const int4& r) {
     const unsigned bits = free_bits(r);
     int at, all;
     rank_bits(bits, s.lane, &at, &all);
     at += rank;
+    unsigned taken = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (bits >> k & 1) {
-        if (at < stop) use(at, (int32_t)(p + k));
+        if (at < stop) {
+          use(at, (int32_t)(p + k));
+          taken |= 1u << k;
+        }
         ++at;
       }
+    // one reference each
+    if (taken) {
+      if (ALONE && s.vec && p + 4 <= s.hi) {
+        *reinterpret_cast<int4*>(refs + p) =
+            make_int4(taken & 1 ? 1 : r.x, taken & 2 ? 1 : r.y, taken & 4 ? 1 : r.z,
+                      taken & 8 ? 1 : r.w);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (taken >> k & 1) refs[p + k] = 1;
+      }
+    }
     rank += all;
     return rank < stop;
   });
@@ -163,11 +185,12 @@ struct AllocArgs {
   int32_t* pages;
   int32_t* err;
   int32_t num_pages, n;
+  uint32_t per;          // pages a warp counts
 };
 
 __global__ void __launch_bounds__(kThreads, 1) alloc_kernel(const AllocArgs a) {
   __shared__ Counts c;
-  const Share s = my_share(a.refs, a.num_pages);
+  const Share s = my_share(a.refs, a.num_pages, a.per);
   int before, total;
   cluster_prefix(c, count_free(a.refs, s), &before, &total);
   if (total < a.n) {
@@ -176,9 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1) alloc_kernel(const AllocArgs a) {
       a.pages[i] = -1;
     if (blockIdx.x == 0 && threadIdx.x == 0) note_error(a.err, PKA_ERR_WORKSPACE);
   } else {
-    each_free(a.refs, s, before, a.n, [&](int rank, int32_t page) {
+    take_free<true>(a.refs, s, before, a.n, [&](int rank, int32_t page) {
       a.pages[rank] = page;
-      a.refs[page] = 1;
     });
   }
   leave();
@@ -228,6 +250,7 @@ struct ForkArgs {
   int32_t* err;
   int32_t page_size, num_pages, num_parents, num_children;
   int32_t num_indices, num_child_indices;
+  uint32_t per;          // pages a warp counts
 };
 
 // What one child takes: the first `shared` entries of its parent's table,
@@ -310,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
   __shared__ int64_t warp_sum[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  const Share s = my_share(a.refs, a.num_pages);
+  const Share s = my_share(a.refs, a.num_pages, a.per);
   const int mine = count_free(a.refs, s);
 
   // running sums over the children: fresh pages in the upper 32 bits, copies
@@ -338,11 +361,14 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
     __syncthreads();  // the previous round's warp_sum has been read
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int64_t base = carry, all = carry;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) base += warp_sum[w];
-      all += warp_sum[w];
+    int64_t sum = warp_sum[lane];  // and, in every warp, of the warps
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(kAll, sum, d);
+      if (lane >= d) sum += y;
     }
+    const int64_t base = carry + (warp > 0 ? __shfl_sync(kAll, sum, warp - 1) : 0);
+    const int64_t all = carry + __shfl_sync(kAll, sum, 31);
     if (i < a.num_children) {
       const int64_t excl = base + incl - x;
       sums.fresh_before[i] = (int32_t)(excl >> 32);
@@ -363,11 +389,10 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
     if (refused) note_error(a.err, ok ? PKA_ERR_WORKSPACE : PKA_ERR_METADATA);
   }
   if (!refused) {
-    each_free(a.refs, s, before, (int)needed, [&](int rank, int32_t page) {
+    take_free<!SHARE>(a.refs, s, before, (int)needed, [&](int rank, int32_t page) {
       const int i = find_between(sums.fresh_before, 0, a.num_children - 1, rank);
       const int nth = rank - sums.fresh_before[i];
       a.child_indices[sums.first[i] + sums.shared[i] + nth] = page;
-      a.refs[page] = 1;
       if (nth == 0 && sums.slots[i] > 0) {
         const int to = sums.copies_before[i];
         a.copy_src[to] = a.kv_indices[sums.parent_first[i] + sums.shared[i]];
@@ -394,11 +419,32 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
   leave();
 }
 
-// The shared entries of every child's table, each one reference more.  A warp
+// References that an entry of child c adds.  Children of one parent share the
+// same pages, so where that saves atomics (a parent of kLongTable pages or
+// more; few enough children to look through) the first of its children adds
+// for all of them and the others nothing.
+constexpr int kLongTable = 256, kFewChildren = 1024;
+
+__device__ __forceinline__ int adds_of(const ForkArgs& a, int c, const Child& ch, int lane) {
+  if (ch.shared < kLongTable || a.num_children > kFewChildren) return 1;
+  const int32_t p = a.parent[c];
+  int kids = 0, earlier = 0;
+  for (int i = lane; i < a.num_children; i += 32) {
+    const bool same = a.parent[i] == p;
+    kids += same;
+    earlier += same && i < c;
+  }
+  kids = __reduce_add_sync(kAll, kids);
+  return __reduce_add_sync(kAll, earlier) > 0 ? 0 : kids;
+}
+
+// The shared entries of every child's table and their references.  A warp
 // takes 256 entries; where they belong to one child it is looked up once, else
-// each lane looks its own up between the children of the first and the last.
+// each lane looks its own up between the children of the first and the last
+// (of which alone may be longer than the 256).
 __global__ void __launch_bounds__(256) fork_share_kernel(const ForkArgs a) {
   constexpr int U = 8, CHUNK = 32 * U;
+  static_assert(CHUNK <= kLongTable, "a long table inside a chunk would be missed");
   if (a.counts[0] < 0) return;  // refused
   const int lane = threadIdx.x & 31;
   const int64_t end = a.child_indptr[a.num_children];
@@ -410,22 +456,31 @@ __global__ void __launch_bounds__(256) fork_share_kernel(const ForkArgs a) {
     const bool one = first + 1 >= a.num_children || a.child_indptr[first + 1] >= e1;
     const int last = one ? first : warp_find(a.child_indptr, a.num_children, e1 - 1, lane);
     Child ch = child_at(a, first);
+    const int adds_first = adds_of(a, first, ch, lane);
+    const int adds_last = one ? adds_first : adds_of(a, last, child_at(a, last), lane);
     int32_t page[U];
-    bool mine[U];
+    int adds[U];  // -1: not a shared entry
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t e = e0 + 32 * u + lane;
-      if (!one && e < e1) ch = child_at(a, find_between(a.child_indptr, first, last, e));
+      int c = first;
+      if (!one && e < e1) {
+        c = find_between(a.child_indptr, first, last, e);
+        ch = child_at(a, c);
+      }
       const int64_t j = e - ch.first;
-      mine[u] = e < e1 && j >= 0 && j < ch.shared;
-      if (mine[u]) page[u] = a.kv_indices[ch.parent_first + j];
+      adds[u] = -1;
+      if (e < e1 && j >= 0 && j < ch.shared) {
+        page[u] = a.kv_indices[ch.parent_first + j];
+        adds[u] = c == first ? adds_first : c == last ? adds_last : 1;
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (mine[u]) {
+      if (adds[u] >= 0) {
         a.child_indices[e0 + 32 * u + lane] = page[u];
-        if (page[u] >= 0 && page[u] < a.num_pages) atomicAdd(a.refs + page[u], 1);
-        else bad = true;
+        if (page[u] < 0 || page[u] >= a.num_pages) bad = true;
+        else if (adds[u] > 0) atomicAdd(a.refs + page[u], adds[u]);
       }
   }
   if (bad) note_error(a.err, PKA_ERR_METADATA);
@@ -447,6 +502,7 @@ struct CompactArgs {
   int32_t* err;
   int64_t num_indices;
   int32_t num_pages;
+  uint32_t per;          // pages a warp counts
 };
 
 // With L live pages, the live pages at L and above move to the free pages
@@ -458,7 +514,7 @@ struct CompactArgs {
 // move_kernel, which needs both lists whole, turns it into the new id.
 __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs a) {
   __shared__ Counts c;
-  const Share s = my_share(a.refs, a.num_pages);
+  const Share s = my_share(a.refs, a.num_pages, a.per);
   int before, live;
   cluster_prefix(c, (int)(s.hi - s.lo) - count_free(a.refs, s), &before, &live);
 
@@ -466,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs 
   const bool vec_map = (reinterpret_cast<uintptr_t>(a.map) & 15) == 0;
   const bool vec_out = (reinterpret_cast<uintptr_t>(a.refs_out) & 15) == 0;
   int rank = before;  // live pages before the step
-  walk(a.refs, s, 0, [&](int64_t p, const int4& r4) {
+  walk(a.refs, s, 0, [&](uint32_t p, const int4& r4) {
     const int r[4] = {r4.x, r4.y, r4.z, r4.w};
     const unsigned bits = ~free_bits(r4) & 15u;  // live
     int at, all;
@@ -656,6 +712,12 @@ int cluster_ctas(int32_t num_pages) {
   return num_pages <= 16384 ? 1 : num_pages <= 131072 ? 8 : kMaxCluster;
 }
 
+// Pages that each warp of such a launch counts: whole steps of 128.
+uint32_t pages_per_warp(int32_t num_pages) {
+  const int64_t warps = (int64_t)cluster_ctas(num_pages) * kWarps;
+  return (uint32_t)((num_pages + warps * 128 - 1) / (warps * 128) * 128);
+}
+
 // Launch as one cluster.
 template <auto Kernel, class A>
 cudaError_t launch_cluster(int ctas, int smem, cudaStream_t stream, const A& args) {
@@ -753,7 +815,8 @@ pka_status pka_alloc_pages(int32_t* page_refs_d, int32_t num_pages, int32_t n, i
   if (n > num_pages) return PKA_ERR_WORKSPACE;
   if (!page_refs_d || !pages_d || pka::unaligned(page_refs_d) || pka::unaligned(pages_d))
     return PKA_ERR_INVALID_ARG;
-  const pka::AllocArgs a{page_refs_d, pages_d, pka::device_error_word(), num_pages, n};
+  const pka::AllocArgs a{page_refs_d, pages_d, pka::device_error_word(), num_pages, n,
+                         pka::pages_per_warp(num_pages)};
   return pka::done(pka::launch_cluster<pka::alloc_kernel>(pka::cluster_ctas(num_pages), 0,
                                                           static_cast<cudaStream_t>(stream), a),
                    "page alloc launch");
@@ -815,6 +878,7 @@ pka_status pka_fork_pages(int32_t page_size, int32_t* page_refs_d, int32_t num_p
   a.num_children = num_children;
   a.num_indices = num_indices;
   a.num_child_indices = num_child_indices;
+  a.per = pka::pages_per_warp(num_pages);
   const int smem = (pka::kChildWords * num_children + 1) * (int)sizeof(int32_t);
   const int ctas = pka::cluster_ctas(num_pages);
   if (num_child_indices <= pka::kShareInTake) {
@@ -857,6 +921,7 @@ pka_status pka_compact_pages(const int32_t* page_refs_d, int32_t num_pages,
   a.err = pka::device_error_word();
   a.num_indices = num_indices;
   a.num_pages = num_pages;
+  a.per = pka::pages_per_warp(num_pages);
   cudaError_t e = num_pages == 0
                       ? cudaMemsetAsync(counts_d, 0, 8, st)
                       : pka::launch_cluster<pka::compact_kernel>(pka::cluster_ctas(num_pages), 0,

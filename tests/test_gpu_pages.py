@@ -183,6 +183,22 @@ def test_fork_beams_with_long_tables():
     _check_fork(1, refs, lens, indptr, ids, last, parent, lens[parent] + 1)
 
 
+@pytest.mark.parametrize("children", [700, 1500])
+def test_fork_long_and_short_tables_together(children):
+    """Tables of one page beside tables of hundreds and tens of thousands, in
+    any order, around the lengths (255..257 shared pages) and counts where the
+    references of long tables are added together."""
+    rng = np.random.default_rng(children)
+    lens = np.array([1, 255, 256, 257, 700, 1, 3, 40000])
+    indptr, ids, last = _parents(rng, lens, 1, 400000)
+    refs = np.zeros(400000, np.int32)
+    refs[ids] = 1
+    parent = rng.choice([-1, 0, 1, 2, 3, 4, 5, 6], children).astype(np.int32)
+    parent[[3, 4, 650]] = 7
+    grown = np.where(parent >= 0, lens[np.maximum(parent, 0)], 0) + rng.integers(0, 2, children)
+    _check_fork(1, refs, lens, indptr, ids, last, parent, grown)
+
+
 def test_fork_with_every_page_taken():
     """Exactly as many free pages as needed, then one fewer."""
     rng = np.random.default_rng(6)
