@@ -253,17 +253,26 @@ def _shape(*dims):
     return "[" + ", ".join(map(str, dims)) + "]"
 
 
-def _here_pool(t, name, params, dev):
-    """Pointer of a K/V pool [.., pages, P, Hk, D] or [.., pages, Hk, P, D] of
-    the params' layout, each page contiguous."""
+def _here_pools(k, v, params, dev):
+    """(pointer of k, of v, their shape, their strides) of K/V pools alike,
+    [.., pages, P, Hk, D] or [.., pages, Hk, P, D] of the params' layout, each
+    page contiguous."""
     a, b, d = params.page_size, params.num_kv_heads, params.head_dim
     if params.layout != PKA_NHD:
         a, b = b, a
     dtype = _U8 if params.kv_dtype == PKA_KV_FP8_E4M3 else _BF16
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev \
-            and t.shape[-3:] == (a, b, d) and t.stride()[-3:] == (b * d, d, 1):
-        return t.data_ptr()
-    _refuse(t, name, dtype, dev, f"{_shape('..', a, b, d)} with each page contiguous")
+    if isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor) and k.dtype is dtype \
+            and v.dtype is dtype and k.get_device() == dev and v.get_device() == dev:
+        shape, strides = k.shape, k.stride()
+        if shape[-3:] == (a, b, d) and strides[-3:] == (b * d, d, 1) and v.shape == shape \
+                and v.stride() == strides:
+            return k.data_ptr(), v.data_ptr(), shape, strides
+    what = f"{_shape('..', a, b, d)} with each page contiguous"
+    for t, name in ((k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev \
+                or t.shape[-3:] != (a, b, d) or t.stride()[-3:] != (b * d, d, 1):
+            _refuse(t, name, dtype, dev, what)
+    raise ValueError("k and v must have one shape and the same strides")
 
 
 def _here_stream(stream, dev) -> int:
@@ -520,12 +529,12 @@ def pka_rope_append_paged_kv_cache(params, rope, q, q_out, k_new, v_new, append_
     last = _here(last_page_len, "last_page_len", _I32, dev)
     if kv_indptr.numel() != batch + 1 or last_page_len.numel() != batch:
         raise ValueError("kv_indptr and last_page_len must describe append_indptr's requests")
-    shape = k.shape
-    if len(shape) != 4 or v.shape != shape:
-        raise ValueError("k and v must be pools [pages, ...] of one shape")
+    kpool, vpool, shape, _ = _here_pools(k, v, params, dev)
+    if len(shape) != 4:
+        raise ValueError("k and v must be pools [pages, ...]")
     s = lib().pka_rope_append_paged_kv_cache(
         ctypes.byref(params), ctypes.byref(rope), batch, rows, qp, qs, qo, kp, ks, vp, vs, pos,
-        app, ptr, idx, last, _here_pool(k, "k", params, dev), _here_pool(v, "v", params, dev),
+        app, ptr, idx, last, kpool, vpool,
         int(page_stride), shape[0], _here_stream(stream, dev))
     if check and s:
         _check(s, "pka_rope_append_paged_kv_cache")
@@ -539,16 +548,15 @@ def pka_copy_pages(params, k, v, src, dst, slots=None, num_copies=None, stream=N
     and page stride.  num_copies: a device count (its first element) of the
     entries that hold, as pka_fork_pages and pka_compact_pages write it."""
     dev, i32 = torch.cuda.current_device(), _I32
-    shape, strides = k.shape, k.stride()
-    if len(shape) not in (4, 5) or v.shape != shape or v.stride() != strides:
-        raise ValueError("k and v must be pools [pages, ...] or [layers, pages, ...] alike")
+    kp, vp, shape, strides = _here_pools(k, v, params, dev)
+    if len(shape) not in (4, 5):
+        raise ValueError("k and v must be pools [pages, ...] or [layers, pages, ...]")
     layers = shape[0] if len(shape) == 5 else 1
     n = src.numel()
     if dst.numel() != n or (slots is not None and slots.numel() != n):
         raise ValueError("src, dst and slots must have one length")
     s = lib().pka_copy_pages(
-        ctypes.byref(params), layers, _here_pool(k, "k", params, dev),
-        _here_pool(v, "v", params, dev), strides[-4], strides[0] if layers > 1 else 0,
+        ctypes.byref(params), layers, kp, vp, strides[-4], strides[0] if layers > 1 else 0,
         shape[-4], _here(src, "src", i32, dev), _here(dst, "dst", i32, dev),
         None if slots is None else _here(slots, "slots", i32, dev), n,
         None if num_copies is None else _here(num_copies, "num_copies", i32, dev),

@@ -29,19 +29,32 @@ constexpr unsigned kAll = 0xffffffffu;
 // Counting
 // ---------------------------------------------------------------------------
 
-// page_refs split among the warps of the cluster: `per` pages each, whole
-// steps of 128 (one 16-byte load a lane).
+// page_refs split among the warps of the cluster, tile by tile in turn (so
+// that every block has its part of the lowest pages, which a call wants
+// first): row i of tiles is tiles i * warps .. i * warps + warps - 1, one a
+// warp, at most kRows rows.
+constexpr int kRows = 32;
+constexpr uint32_t kTile = 512;  // of one row: less, where that suffices; of more: multiples
+
 struct Share {
-  uint32_t lo, hi;  // this warp's pages
+  uint32_t lo, hi;  // the pages of this warp's tile
   int lane;
   bool vec;         // page_refs is 16-byte aligned
 };
 
-__device__ __forceinline__ Share my_share(const int32_t* refs, uint32_t num_pages, uint32_t per) {
-  const uint64_t lo = (uint64_t)(blockIdx.x * kWarps + (threadIdx.x >> 5)) * per;
+struct Tiling {
+  uint32_t tile;    // pages of a tile
+  int rows;
+};
+
+__device__ __forceinline__ Share tile_at(const int32_t* refs, uint32_t num_pages, const Tiling& t,
+                                         int row) {
+  const uint32_t warps = gridDim.x * kWarps;
+  const uint64_t lo =
+      (uint64_t)(row * warps + blockIdx.x * kWarps + (threadIdx.x >> 5)) * t.tile;
   Share s;
   s.lo = (uint32_t)min(lo, (uint64_t)num_pages);
-  s.hi = (uint32_t)min(lo + per, (uint64_t)num_pages);
+  s.hi = (uint32_t)min(lo + t.tile, (uint64_t)num_pages);
   s.lane = threadIdx.x & 31;
   s.vec = (reinterpret_cast<uintptr_t>(refs) & 15) == 0;
   return s;
@@ -58,28 +71,29 @@ __device__ __forceinline__ int4 refs_at(const int32_t* refs, const Share& s, uin
   return r;
 }
 
-// Walk the warp's share in order, 128 pages a step, the loads of four steps
-// in flight: use(p, r) with this lane's pages p .. p+3 and their references;
-// a false result (of the whole warp) ends the walk.
+// Walk a tile in order, 128 pages a step, the loads of four steps in flight:
+// use(p, r) with this lane's pages p .. p+3 and their references; a false
+// result (of the whole warp) ends the walk.
 template <class F>
 __device__ __forceinline__ void walk(const int32_t* refs, const Share& s, int past, F use) {
   constexpr int U = 4;
   uint32_t p = s.lo + 4 * s.lane;
-  uint32_t left = s.hi - s.lo;
-  if (s.vec)
-    for (; left >= 128 * U; left -= 128 * U, p += 128 * U) {
-      int4 r[U];
+  for (uint32_t left = s.hi - s.lo; left > 0; left -= min(left, 128u * U), p += 128 * U) {
+    int4 r[U];
+    if (s.vec && left >= 128 * U) {
 #pragma unroll
       for (int i = 0; i < U; ++i) r[i] = *reinterpret_cast<const int4*>(refs + p + 128 * i);
+    } else {
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (!use(p + 128 * i, r[i])) return;
+      for (int i = 0; i < U; ++i) r[i] = refs_at(refs, s, p + 128 * i, past);
     }
-  for (; left > 0; left -= min(left, 128u), p += 128)
-    if (!use(p, refs_at(refs, s, p, past))) return;
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (128u * i < left && !use(p + 128 * i, r[i])) return;
+  }
 }
 
-// Bit k: page p + k is free (has no reference); pages past the share are not.
+// Bit k: page p + k is free (has no reference); pages past the tile are not.
 __device__ __forceinline__ unsigned free_bits(const int4& r) {
   return (r.x <= 0 ? 1u : 0u) | (r.y <= 0 ? 2u : 0u) | (r.z <= 0 ? 4u : 0u) |
          (r.w <= 0 ? 8u : 0u);
@@ -95,85 +109,121 @@ __device__ __forceinline__ int count_free(const int32_t* refs, const Share& s) {
 }
 
 // Of the set bits of a step's lanes, taken lane by lane: how many come before
-// this lane's first, and how many there are.
+// this lane's first, and how many there are.  A lane has 0 to 4; three ballots
+// carry the binary digits.
 __device__ __forceinline__ void rank_bits(unsigned bits, int lane, int* before, int* all) {
   const unsigned below = (1u << lane) - 1;
-  *before = *all = 0;
+  const int n = __popc(bits);
+  const unsigned b0 = __ballot_sync(kAll, n & 1), b1 = __ballot_sync(kAll, n & 2),
+                 b2 = __ballot_sync(kAll, n & 4);
+  *before = __popc(b0 & below) + 2 * __popc(b1 & below) + 4 * __popc(b2 & below);
+  *all = __popc(b0) + 2 * __popc(b1) + 4 * __popc(b2);
+}
+
+__device__ __forceinline__ int inclusive_sum(int x, int lane) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const unsigned b = __ballot_sync(kAll, bits >> k & 1);
-    *before += __popc(b & below);
-    *all += __popc(b);
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(kAll, x, d);
+    if (lane >= d) x += y;
   }
+  return x;
 }
 
 struct Counts {
-  int warp[kWarps];
-  int block;
+  int tile[kRows][kWarps];  // pages counted in a tile; then in the block's tiles before it
+  int block[kRows];         // in the block's tiles of a row
+  int before[kRows];        // in the row's tiles of the blocks before
+  int row[kRows];           // in a row
 };
 
-// From every warp's count: the sum over the warps before this one in the
-// cluster, and the sum over all.  Leaves the cluster barrier armed: the caller
-// ends with leave(), so that no block is gone while its counts are read.
-__device__ __forceinline__ void cluster_prefix(Counts& c, int mine, int* before, int* total) {
-  cg::cluster_group cluster = cg::this_cluster();
+// Counts the free (or live) pages of every tile.  Lane i gets the number of
+// such pages before this warp's tile of row i, and every lane their total.
+// Leaves the cluster barrier armed: the caller ends with leave(), so that no
+// block is gone while its counts are read.
+__device__ __forceinline__ int count_pages(Counts& c, const int32_t* refs, uint32_t num_pages,
+                                           const Tiling& t, bool live, int* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) c.warp[warp] = mine;
+  for (int i = 0; i < t.rows; ++i) {
+    const Share s = tile_at(refs, num_pages, t, i);
+    const int n = count_free(refs, s);
+    if (lane == 0) c.tile[i][warp] = live ? (int)(s.hi - s.lo) - n : n;
+  }
   __syncthreads();
-  const int own = c.warp[lane];
-  const int block = __reduce_add_sync(kAll, own);
-  *before = __reduce_add_sync(kAll, lane < warp ? own : 0);
-  *total = block;
-  if (gridDim.x == 1) return;
-  if (threadIdx.x == 0) c.block = block;
-  cluster.sync();
-  const int there = lane < gridDim.x ? cluster.map_shared_rank(&c, lane)->block : 0;
-  cluster.barrier_arrive();
-  *total = __reduce_add_sync(kAll, there);
-  *before += __reduce_add_sync(kAll, lane < blockIdx.x ? there : 0);
+  int block = 0;
+  if (warp < t.rows) {  // a warp a row
+    const int n = c.tile[warp][lane], upto = inclusive_sum(n, lane);
+    c.tile[warp][lane] = upto - n;
+    block = __shfl_sync(kAll, upto, 31);
+    if (lane == 0) {
+      c.block[warp] = c.row[warp] = block;
+      c.before[warp] = 0;
+    }
+  }
+  if (gridDim.x > 1) {
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    if (warp < t.rows) {
+      const int there = lane < gridDim.x ? cluster.map_shared_rank(&c, lane)->block[warp] : 0;
+      const int row = __reduce_add_sync(kAll, there);
+      const int before = __reduce_add_sync(kAll, lane < blockIdx.x ? there : 0);
+      if (lane == 0) {
+        c.row[warp] = row;
+        c.before[warp] = before;
+      }
+    }
+    cluster.barrier_arrive();
+  }
+  __syncthreads();
+  const int row = lane < t.rows ? c.row[lane] : 0;
+  const int upto = inclusive_sum(row, lane);
+  *total = __shfl_sync(kAll, upto, 31);
+  return lane < t.rows ? upto - row + c.before[lane] + c.tile[lane][warp] : 0;
 }
 
 __device__ __forceinline__ void leave() {
   if (gridDim.x > 1) cg::this_cluster().barrier_wait();
 }
 
-// Take the free pages of this warp's share in ascending order, the first with
-// rank `rank`, until rank `stop`: use(rank, page).  ALONE: nobody else changes
+// Take the first `stop` free pages of all: use(rank, page) for those of this
+// warp's tiles.  `before` is count_pages' answer.  ALONE: nobody else changes
 // a reference meanwhile, so a lane stores its four pages at once.
 template <bool ALONE, class F>
-__device__ __forceinline__ void take_free(int32_t* refs, const Share& s, int rank, int stop,
-                                          F use) {
-  if (rank >= stop) return;
-  walk(refs, s, 1, [&](uint32_t p, const int4& r) {
-    const unsigned bits = free_bits(r);
-    int at, all;
-    rank_bits(bits, s.lane, &at, &all);
-    at += rank;
-    unsigned taken = 0;
+__device__ __forceinline__ void take_free(int32_t* refs, uint32_t num_pages, const Tiling& t,
+                                          int before, int stop, F use) {
+  for (int i = 0; i < t.rows; ++i) {
+    int rank = __shfl_sync(kAll, before, i);
+    if (rank >= stop) return;
+    const Share s = tile_at(refs, num_pages, t, i);
+    walk(refs, s, 1, [&](uint32_t p, const int4& r) {
+      const unsigned bits = free_bits(r);
+      int first, all;
+      rank_bits(bits, s.lane, &first, &all);
+      first += rank;
+      unsigned taken = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (bits >> k & 1) {
-        if (at < stop) {
+      for (int k = 0; k < 4; ++k) {
+        const int at = first + __popc(bits & ((1u << k) - 1));
+        if ((bits >> k & 1) && at < stop) {
           use(at, (int32_t)(p + k));
           taken |= 1u << k;
         }
-        ++at;
       }
-    // one reference each
-    if (taken) {
-      if (ALONE && s.vec && p + 4 <= s.hi) {
-        *reinterpret_cast<int4*>(refs + p) =
-            make_int4(taken & 1 ? 1 : r.x, taken & 2 ? 1 : r.y, taken & 4 ? 1 : r.z,
-                      taken & 8 ? 1 : r.w);
-      } else {
+      // one reference each
+      if (taken) {
+        if (ALONE && s.vec && p + 4 <= s.hi) {
+          *reinterpret_cast<int4*>(refs + p) =
+              make_int4(taken & 1 ? 1 : r.x, taken & 2 ? 1 : r.y, taken & 4 ? 1 : r.z,
+                        taken & 8 ? 1 : r.w);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (taken >> k & 1) refs[p + k] = 1;
+          for (int k = 0; k < 4; ++k)
+            if (taken >> k & 1) refs[p + k] = 1;
+        }
       }
-    }
-    rank += all;
-    return rank < stop;
-  });
+      rank += all;
+      return rank < stop;
+    });
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -185,21 +235,20 @@ struct AllocArgs {
   int32_t* pages;
   int32_t* err;
   int32_t num_pages, n;
-  uint32_t per;          // pages a warp counts
+  Tiling tiling;
 };
 
 __global__ void __launch_bounds__(kThreads, 1) alloc_kernel(const AllocArgs a) {
   __shared__ Counts c;
-  const Share s = my_share(a.refs, a.num_pages, a.per);
-  int before, total;
-  cluster_prefix(c, count_free(a.refs, s), &before, &total);
+  int total;
+  const int before = count_pages(c, a.refs, a.num_pages, a.tiling, false, &total);
   if (total < a.n) {
     for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < a.n;
          i += (int64_t)gridDim.x * kThreads)
       a.pages[i] = -1;
     if (blockIdx.x == 0 && threadIdx.x == 0) note_error(a.err, PKA_ERR_WORKSPACE);
   } else {
-    take_free<true>(a.refs, s, before, a.n, [&](int rank, int32_t page) {
+    take_free<true>(a.refs, a.num_pages, a.tiling, before, a.n, [&](int rank, int32_t page) {
       a.pages[rank] = page;
     });
   }
@@ -250,7 +299,7 @@ struct ForkArgs {
   int32_t* err;
   int32_t page_size, num_pages, num_parents, num_children;
   int32_t num_indices, num_child_indices;
-  uint32_t per;          // pages a warp counts
+  Tiling tiling;
 };
 
 // What one child takes: the first `shared` entries of its parent's table,
@@ -265,29 +314,29 @@ struct Child {
   bool ok;
 };
 
-__device__ __forceinline__ Child child_at(const ForkArgs& a, int c) {
+__device__ __forceinline__ Child child_at(const ForkArgs& a, int32_t c0, int32_t c1, int32_t p) {
   Child x{};
-  const int32_t c0 = a.child_indptr[c], c1 = a.child_indptr[c + 1], p = a.parent[c];
   x.first = c0;
   x.ok = c0 >= 0 && c1 >= c0 && c1 <= a.num_child_indices && p >= -1 && p < a.num_parents;
-  if (!x.ok) return x;
-  int pages = 0;
-  if (p >= 0) {
-    const int32_t k0 = a.kv_indptr[p], k1 = a.kv_indptr[p + 1];
-    x.ok = k0 >= 0 && k1 >= k0 && k1 <= a.num_indices && k1 - k0 <= c1 - c0;
-    if (!x.ok) return x;
-    pages = k1 - k0;
-    x.parent_first = k0;
-    if (pages > 0) {
-      const int32_t last = a.last_page_len[p];
-      x.ok = last >= 1 && last <= a.page_size;
-      if (!x.ok) return x;
-      if (last < a.page_size) x.slots = last;
-    }
+  int32_t k0 = 0, k1 = 0, last = 1;
+  if (x.ok && p >= 0) {
+    k0 = a.kv_indptr[p];
+    k1 = a.kv_indptr[p + 1];
+    last = a.last_page_len[p];
   }
+  const int pages = k1 - k0;
+  x.ok = x.ok && k0 >= 0 && pages >= 0 && k1 <= a.num_indices && pages <= c1 - c0 &&
+         (pages == 0 || (last >= 1 && last <= a.page_size));
+  if (!x.ok) return x;
+  x.parent_first = k0;
+  x.slots = pages > 0 && last < a.page_size ? last : 0;
   x.shared = pages - (x.slots > 0);
   x.fresh = c1 - c0 - x.shared;
   return x;
+}
+
+__device__ __forceinline__ Child child_at(const ForkArgs& a, int c) {
+  return child_at(a, a.child_indptr[c], a.child_indptr[c + 1], a.parent[c]);
 }
 
 // Shared memory of fork_take_kernel, one element a child.
@@ -333,8 +382,11 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
   __shared__ int64_t warp_sum[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  const Share s = my_share(a.refs, a.num_pages, a.per);
-  const int mine = count_free(a.refs, s);
+  // (the first round's loads go out before the counting)
+  const int i0 = min((int)threadIdx.x, a.num_children - 1);
+  const int32_t first = a.child_indptr[i0], end = a.child_indptr[i0 + 1], parent = a.parent[i0];
+  int total;
+  const int before = count_pages(c, a.refs, a.num_pages, a.tiling, false, &total);
 
   // running sums over the children: fresh pages in the upper 32 bits, copies
   // in the lower
@@ -344,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
     const int i = c0 + threadIdx.x;
     int64_t x = 0;
     if (i < a.num_children) {
-      const Child ch = child_at(a, i);
+      const Child ch = c0 == 0 ? child_at(a, first, end, parent) : child_at(a, i);
       ok = ok && ch.ok;
       if (ch.ok) x = ((int64_t)ch.fresh << 32) | (ch.slots > 0 ? 1 : 0);
       sums.first[i] = ch.first;
@@ -379,9 +431,6 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
   ok = __syncthreads_and(ok);
   const int64_t needed = carry >> 32;
   const int copies = (int)(uint32_t)carry;
-
-  int before, total;
-  cluster_prefix(c, mine, &before, &total);
   const bool refused = !ok || total < needed;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     a.counts[0] = refused ? -1 : copies;
@@ -389,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
     if (refused) note_error(a.err, ok ? PKA_ERR_WORKSPACE : PKA_ERR_METADATA);
   }
   if (!refused) {
-    take_free<!SHARE>(a.refs, s, before, (int)needed, [&](int rank, int32_t page) {
+    const auto fill = [&](int rank, int32_t page) {
       const int i = find_between(sums.fresh_before, 0, a.num_children - 1, rank);
       const int nth = rank - sums.fresh_before[i];
       a.child_indices[sums.first[i] + sums.shared[i] + nth] = page;
@@ -399,11 +448,12 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
         a.copy_dst[to] = page;
         a.copy_slots[to] = sums.slots[i];
       }
-    });
+    };
+    take_free<!SHARE>(a.refs, a.num_pages, a.tiling, before, (int)needed, fill);
     if (SHARE) {
       bool bad = false;
-      const int end = a.child_indptr[a.num_children];
-      for (int e = sums.first[0] + blockIdx.x * kThreads + threadIdx.x; e < end;
+      const int stop = a.child_indptr[a.num_children];
+      for (int e = sums.first[0] + blockIdx.x * kThreads + threadIdx.x; e < stop;
            e += gridDim.x * kThreads) {
         const int i = find_between(sums.first, 0, a.num_children - 1, e);
         const int j = e - sums.first[i];
@@ -502,7 +552,7 @@ struct CompactArgs {
   int32_t* err;
   int64_t num_indices;
   int32_t num_pages;
-  uint32_t per;          // pages a warp counts
+  Tiling tiling;
 };
 
 // With L live pages, the live pages at L and above move to the free pages
@@ -512,16 +562,11 @@ struct CompactArgs {
 // from above; equal numbers pair up.  This launch writes the two lists by
 // those numbers; a moving page's entry of the map holds -2 - number until
 // move_kernel, which needs both lists whole, turns it into the new id.
-__global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs a) {
-  __shared__ Counts c;
-  const Share s = my_share(a.refs, a.num_pages, a.per);
-  int before, live;
-  cluster_prefix(c, (int)(s.hi - s.lo) - count_free(a.refs, s), &before, &live);
-
+__device__ __forceinline__ void number_tile(const CompactArgs& a, const Share& s, int rank,
+                                            int live) {
   const bool apart = a.refs != a.refs_out;
   const bool vec_map = (reinterpret_cast<uintptr_t>(a.map) & 15) == 0;
   const bool vec_out = (reinterpret_cast<uintptr_t>(a.refs_out) & 15) == 0;
-  int rank = before;  // live pages before the step
   walk(a.refs, s, 0, [&](uint32_t p, const int4& r4) {
     const int r[4] = {r4.x, r4.y, r4.z, r4.w};
     const unsigned bits = ~free_bits(r4) & 15u;  // live
@@ -562,11 +607,42 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs 
     }
     return true;
   });
-  if (live == a.num_pages && blockIdx.x == 0 && threadIdx.x == 0) {
-    a.counts[0] = 0;
+}
+
+// One row of tiles is numbered where it was counted.  More are too much for
+// the cluster's few blocks: they go to number_kernel, each tile's count before
+// it in the map entry of its first page (which that tile alone reads and
+// overwrites) and L in counts[1].  500,009 pages: 14.4 us in one launch.
+__global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs a) {
+  __shared__ Counts c;
+  int live;
+  const int before = count_pages(c, a.refs, a.num_pages, a.tiling, true, &live);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && (a.tiling.rows > 1 || live == a.num_pages)) {
+    a.counts[0] = 0;  // unless a page has the number L
     a.counts[1] = live;
   }
+  for (int i = 0; i < a.tiling.rows; ++i) {
+    const int rank = __shfl_sync(kAll, before, i);
+    const Share s = tile_at(a.refs, a.num_pages, a.tiling, i);
+    if (a.tiling.rows == 1)
+      number_tile(a, s, rank, live);
+    else if (s.lane == 0 && s.lo < s.hi)
+      a.map[s.lo] = rank;
+  }
   leave();
+}
+
+__global__ void __launch_bounds__(256) number_kernel(const CompactArgs a) {
+  const uint64_t lo = (blockIdx.x * 8ull + (threadIdx.x >> 5)) * a.tiling.tile;
+  if (lo >= (uint64_t)a.num_pages) return;
+  Share s;
+  s.lo = (uint32_t)lo;
+  s.hi = (uint32_t)min(lo + a.tiling.tile, (uint64_t)a.num_pages);
+  s.lane = threadIdx.x & 31;
+  s.vec = (reinterpret_cast<uintptr_t>(a.refs) & 15) == 0;
+  const int live = *const_cast<volatile int32_t*>(a.counts + 1);
+  const int rank = __shfl_sync(kAll, a.map[s.lo], 0);
+  number_tile(a, s, rank, live);
 }
 
 // The moves' references and map entries, and the table entries through the
@@ -707,15 +783,23 @@ int blocks_for(int64_t work, int per_block, int per_sm) {
   return (int)(b < 1 ? 1 : b > cap ? cap : b);
 }
 
-// Blocks of a launch that counts the references of num_pages pages.
+// Blocks of a launch that counts the references of num_pages pages.  Taking
+// one page and returning it takes, in us, with 1 / 8 / 16 blocks: 4.5 / 5.5 /
+// 6.1 in a pool of 8,192 pages, 6.6 / 5.5 / 6.4 in 131,072, 14 / 6.8 / 7.1 in
+// 500,000 and 32 / 9.1 / 9.0 in 1,500,007 (two launches, both in it).
 int cluster_ctas(int32_t num_pages) {
-  return num_pages <= 16384 ? 1 : num_pages <= 131072 ? 8 : kMaxCluster;
+  return num_pages <= 16384 ? 1 : num_pages <= 262144 ? 8 : kMaxCluster;
 }
 
-// Pages that each warp of such a launch counts: whole steps of 128.
-uint32_t pages_per_warp(int32_t num_pages) {
-  const int64_t warps = (int64_t)cluster_ctas(num_pages) * kWarps;
-  return (uint32_t)((num_pages + warps * 128 - 1) / (warps * 128) * 128);
+Tiling tiling_of(int32_t num_pages) {
+  const uint64_t warps = (uint64_t)cluster_ctas(num_pages) * kWarps, n = (uint64_t)num_pages;
+  const uint64_t share = (n + warps * 128 - 1) / (warps * 128) * 128;  // of one row, in steps
+  Tiling t;
+  t.tile = share <= kTile ? (uint32_t)share
+                          : (uint32_t)((n + warps * kRows * kTile - 1) / (warps * kRows * kTile)) *
+                                kTile;
+  t.rows = n == 0 ? 0 : (int)((n + warps * t.tile - 1) / (warps * t.tile));
+  return t;
 }
 
 // Launch as one cluster.
@@ -816,7 +900,7 @@ pka_status pka_alloc_pages(int32_t* page_refs_d, int32_t num_pages, int32_t n, i
   if (!page_refs_d || !pages_d || pka::unaligned(page_refs_d) || pka::unaligned(pages_d))
     return PKA_ERR_INVALID_ARG;
   const pka::AllocArgs a{page_refs_d, pages_d, pka::device_error_word(), num_pages, n,
-                         pka::pages_per_warp(num_pages)};
+                         pka::tiling_of(num_pages)};
   return pka::done(pka::launch_cluster<pka::alloc_kernel>(pka::cluster_ctas(num_pages), 0,
                                                           static_cast<cudaStream_t>(stream), a),
                    "page alloc launch");
@@ -878,7 +962,7 @@ pka_status pka_fork_pages(int32_t page_size, int32_t* page_refs_d, int32_t num_p
   a.num_children = num_children;
   a.num_indices = num_indices;
   a.num_child_indices = num_child_indices;
-  a.per = pka::pages_per_warp(num_pages);
+  a.tiling = pka::tiling_of(num_pages);
   const int smem = (pka::kChildWords * num_children + 1) * (int)sizeof(int32_t);
   const int ctas = pka::cluster_ctas(num_pages);
   if (num_child_indices <= pka::kShareInTake) {
@@ -921,12 +1005,18 @@ pka_status pka_compact_pages(const int32_t* page_refs_d, int32_t num_pages,
   a.err = pka::device_error_word();
   a.num_indices = num_indices;
   a.num_pages = num_pages;
-  a.per = pka::pages_per_warp(num_pages);
+  a.tiling = pka::tiling_of(num_pages);
   cudaError_t e = num_pages == 0
                       ? cudaMemsetAsync(counts_d, 0, 8, st)
                       : pka::launch_cluster<pka::compact_kernel>(pka::cluster_ctas(num_pages), 0,
                                                                  st, a);
   if (e != cudaSuccess) return pka::cuda_failure(e, "page compact launch");
+  if (a.tiling.rows > 1) {
+    const int64_t tiles = (num_pages + (int64_t)a.tiling.tile - 1) / a.tiling.tile;
+    pka::number_kernel<<<(unsigned)((tiles + 7) / 8), 256, 0, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return pka::cuda_failure(e, "page numbering launch");
+  }
   const int64_t work = num_indices > num_pages / 2 ? num_indices : num_pages / 2;
   if (work == 0) return PKA_OK;
   pka::move_kernel<<<pka::blocks_for(work, 256, 8), 256, 0, st>>>(a);
