@@ -25,6 +25,12 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr unsigned kAll = 0xffffffffu;
 
+// A call's second launch starts when the blocks of its first are all running
+// (start_next) and waits (after_previous) for their end before it reads or
+// writes what they write; what it does before that overlaps with them.
+__device__ __forceinline__ void start_next() { cudaTriggerProgrammaticLaunchCompletion(); }
+__device__ __forceinline__ void after_previous() { cudaGridDependencySynchronize(); }
+
 // ---------------------------------------------------------------------------
 // Counting
 // ---------------------------------------------------------------------------
@@ -382,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
   __shared__ int64_t warp_sum[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  if (!SHARE) start_next();
   // (the first round's loads go out before the counting)
   const int i0 = min((int)threadIdx.x, a.num_children - 1);
   const int32_t first = a.child_indptr[i0], end = a.child_indptr[i0 + 1], parent = a.parent[i0];
@@ -438,8 +445,13 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
     if (refused) note_error(a.err, ok ? PKA_ERR_WORKSPACE : PKA_ERR_METADATA);
   }
   if (!refused) {
+    const float per_rank = needed > 0 ? (float)a.num_children / (float)needed : 0.f;
     const auto fill = [&](int rank, int32_t page) {
-      const int i = find_between(sums.fresh_before, 0, a.num_children - 1, rank);
+      // where every child takes equally many, this is the child of that rank
+      int i = min((int)(((float)rank + 0.5f) * per_rank), a.num_children - 1);
+      const int upto = i + 1 < a.num_children ? sums.fresh_before[i + 1] : (int)needed;
+      if (rank < sums.fresh_before[i] || rank >= upto)
+        i = find_between(sums.fresh_before, 0, a.num_children - 1, rank);
       const int nth = rank - sums.fresh_before[i];
       a.child_indices[sums.first[i] + sums.shared[i] + nth] = page;
       if (nth == 0 && sums.slots[i] > 0) {
@@ -495,8 +507,8 @@ __device__ __forceinline__ int adds_of(const ForkArgs& a, int c, const Child& ch
 __global__ void __launch_bounds__(256) fork_share_kernel(const ForkArgs a) {
   constexpr int U = 8, CHUNK = 32 * U;
   static_assert(CHUNK <= kLongTable, "a long table inside a chunk would be missed");
-  if (a.counts[0] < 0) return;  // refused
   const int lane = threadIdx.x & 31;
+  bool waited = false;
   const int64_t end = a.child_indptr[a.num_children];
   bool bad = false;
   for (int64_t e0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * CHUNK; e0 < end;
@@ -525,6 +537,11 @@ __global__ void __launch_bounds__(256) fork_share_kernel(const ForkArgs a) {
         adds[u] = c == first ? adds_first : c == last ? adds_last : 1;
       }
     }
+    if (!waited) {  // the first chunk was read while the fresh pages were taken
+      after_previous();
+      if (*const_cast<volatile int32_t*>(a.counts) < 0) return;  // refused
+      waited = true;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (adds[u] >= 0) {
@@ -533,6 +550,7 @@ __global__ void __launch_bounds__(256) fork_share_kernel(const ForkArgs a) {
         else if (adds[u] > 0) atomicAdd(a.refs + page[u], adds[u]);
       }
   }
+  if (!waited) after_previous();  // no warp ends the launch before its first ended
   if (bad) note_error(a.err, PKA_ERR_METADATA);
 }
 
@@ -615,6 +633,7 @@ __device__ __forceinline__ void number_tile(const CompactArgs& a, const Share& s
 // overwrites) and L in counts[1].  500,009 pages: 14.4 us in one launch.
 __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs a) {
   __shared__ Counts c;
+  start_next();
   int live;
   const int before = count_pages(c, a.refs, a.num_pages, a.tiling, true, &live);
   if (blockIdx.x == 0 && threadIdx.x == 0 && (a.tiling.rows > 1 || live == a.num_pages)) {
@@ -633,7 +652,9 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs 
 }
 
 __global__ void __launch_bounds__(256) number_kernel(const CompactArgs a) {
+  start_next();
   const uint64_t lo = (blockIdx.x * 8ull + (threadIdx.x >> 5)) * a.tiling.tile;
+  after_previous();
   if (lo >= (uint64_t)a.num_pages) return;
   Share s;
   s.lo = (uint32_t)lo;
@@ -641,7 +662,7 @@ __global__ void __launch_bounds__(256) number_kernel(const CompactArgs a) {
   s.lane = threadIdx.x & 31;
   s.vec = (reinterpret_cast<uintptr_t>(a.refs) & 15) == 0;
   const int live = *const_cast<volatile int32_t*>(a.counts + 1);
-  const int rank = __shfl_sync(kAll, a.map[s.lo], 0);
+  const int rank = __shfl_sync(kAll, *const_cast<volatile int32_t*>(a.map + s.lo), 0);
   number_tile(a, s, rank, live);
 }
 
@@ -650,6 +671,7 @@ __global__ void __launch_bounds__(256) number_kernel(const CompactArgs a) {
 // turned; either gives the new id.  An entry that names no live page stays as
 // it is and is noted.
 __global__ void __launch_bounds__(256) move_kernel(const CompactArgs a) {
+  after_previous();
   const int64_t at = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
   const int64_t step = (int64_t)gridDim.x * blockDim.x;
   bool bad = false;
@@ -658,14 +680,14 @@ __global__ void __launch_bounds__(256) move_kernel(const CompactArgs a) {
     int32_t to = -1;
     if (p >= 0 && p < a.num_pages) {
       to = *const_cast<volatile int32_t*>(a.map + p);
-      if (to < -1) to = a.copy_dst[-2 - to];
+      if (to < -1) to = __ldcg(a.copy_dst + (-2 - to));
     }
     bad = bad || to < 0;
     a.out[i] = to < 0 ? p : to;
   }
-  const int moves = a.counts[0];
+  const int moves = __ldcg(a.counts);
   for (int64_t i = at; i < moves; i += step) {
-    const int32_t src = a.copy_src[i], dst = a.copy_dst[i];
+    const int32_t src = __ldcg(a.copy_src + i), dst = __ldcg(a.copy_dst + i);
     a.refs_out[dst] = a.refs[src];
     if (a.refs == a.refs_out) a.refs_out[src] = 0;
     *const_cast<volatile int32_t*>(a.map + src) = dst;
@@ -832,6 +854,21 @@ cudaError_t launch_cluster(int ctas, int smem, cudaStream_t stream, const A& arg
   return cudaLaunchKernelEx(&cfg, Kernel, args);
 }
 
+// Launch behind the call's previous launch, which lets it start early.
+template <class A>
+cudaError_t launch_behind(void (*kernel)(A), int blocks, cudaStream_t stream, const A& args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
 pka_status done(cudaError_t e, const char* where) {
   return e == cudaSuccess ? PKA_OK : cuda_failure(e, where);
 }
@@ -974,8 +1011,9 @@ pka_status pka_fork_pages(int32_t page_size, int32_t* page_refs_d, int32_t num_p
   cudaError_t e = pka::ensure_dynamic_smem<pka::fork_take_kernel<false>>(smem);
   if (e == cudaSuccess) e = pka::launch_cluster<pka::fork_take_kernel<false>>(ctas, smem, st, a);
   if (e != cudaSuccess) return pka::cuda_failure(e, "page fork launch");
-  pka::fork_share_kernel<<<pka::blocks_for(num_child_indices, 8 * 256, 8), 256, 0, st>>>(a);
-  return pka::done(cudaGetLastError(), "page fork launch");
+  return pka::done(pka::launch_behind(pka::fork_share_kernel,
+                                      pka::blocks_for(num_child_indices, 8 * 256, 8), st, a),
+                   "page fork launch");
 }
 
 pka_status pka_compact_pages(const int32_t* page_refs_d, int32_t num_pages,
@@ -1013,14 +1051,13 @@ pka_status pka_compact_pages(const int32_t* page_refs_d, int32_t num_pages,
   if (e != cudaSuccess) return pka::cuda_failure(e, "page compact launch");
   if (a.tiling.rows > 1) {
     const int64_t tiles = (num_pages + (int64_t)a.tiling.tile - 1) / a.tiling.tile;
-    pka::number_kernel<<<(unsigned)((tiles + 7) / 8), 256, 0, st>>>(a);
-    e = cudaGetLastError();
+    e = pka::launch_behind(pka::number_kernel, (int)((tiles + 7) / 8), st, a);
     if (e != cudaSuccess) return pka::cuda_failure(e, "page numbering launch");
   }
   const int64_t work = num_indices > num_pages / 2 ? num_indices : num_pages / 2;
   if (work == 0) return PKA_OK;
-  pka::move_kernel<<<pka::blocks_for(work, 256, 8), 256, 0, st>>>(a);
-  return pka::done(cudaGetLastError(), "page move launch");
+  return pka::done(pka::launch_behind(pka::move_kernel, pka::blocks_for(work, 256, 8), st, a),
+                   "page move launch");
 }
 
 }  // extern "C"

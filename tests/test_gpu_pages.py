@@ -509,6 +509,57 @@ def test_fork_append_attend_return_compact_attend(layout, page, kv):
     assert pka.pka_get_device_error() == 0
 
 
+def test_captured_large_fork_and_compact_replay():
+    """The forms of several launches (tables past 65,536 entries, a pool past
+    262,144 pages), captured and replayed back to back on other inputs."""
+    rng = np.random.default_rng(12)
+    pool = 300_000
+    lens = rng.integers(2000, 4000, 20)
+    indptr, ids, last = _parents(rng, lens, 1, pool)
+    parent = rng.integers(0, 20, 50).astype(np.int32)
+    pages = lens[parent] + 1
+    child = np.concatenate([[0], np.cumsum(pages)]).astype(np.int32)
+    r, idx = i32(np.zeros(pool)), i32(ids)
+    table = torch.empty(int(child[-1]), dtype=torch.int32, device="cuda")
+    src, dst, slots = (torch.empty(50, dtype=torch.int32, device="cuda") for _ in range(3))
+    counts = torch.empty(2, dtype=torch.int32, device="cuda")
+    held, r2, page_map = torch.empty_like(r), torch.empty_like(r), torch.empty_like(r)
+    table2 = torch.empty_like(table)
+    cs, cd = (torch.empty(pool // 2, dtype=torch.int32, device="cuda") for _ in range(2))
+    ccounts = torch.empty(2, dtype=torch.int32, device="cuda")
+    fixed = [i32(a) for a in (indptr, last, parent, child)]
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        pka.pka_fork_pages(1, r, fixed[0], idx, fixed[1], fixed[2], fixed[3], table, src, dst,
+                           slots, counts, stream=stream)
+        pka.pka_compact_pages(r, table, r2, table2, page_map, cs, cd, ccounts, stream=stream)
+        held.copy_(r)
+        pka.pka_free_pages(r, table, stream=stream)
+    for seed in (1, 2, 3):
+        rng = np.random.default_rng(seed)
+        ids = rng.permutation(pool)[:len(ids)].astype(np.int32)
+        refs = np.zeros(pool, np.int32)
+        refs[ids] = 1
+        r.copy_(i32(refs))
+        idx.copy_(i32(ids))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        tables = [ids[indptr[i]:indptr[i + 1]].tolist() for i in range(20)]
+        want, copies, after = cache.fork_pages(refs, tables, lens, 1, parent, pages)
+        flat = np.concatenate(want)
+        assert np.array_equal(_host(table), flat) and not copies
+        assert np.array_equal(_host(held), after) and np.array_equal(_host(r), refs)
+        w_refs, w_table, w_map, moves, live = cache.compact_pages(after, flat)
+        assert np.array_equal(_host(r2), w_refs) and np.array_equal(_host(table2), w_table)
+        assert np.array_equal(_host(page_map), w_map)
+        assert _host(ccounts).tolist() == [len(moves), live]
+        got = np.stack(_host(cs, cd), 1)[:len(moves)]
+        assert np.array_equal(got, np.array(moves, np.int32))
+    assert pka.pka_get_device_error() == 0
+
+
 def test_captured_fork_and_return_replays():
     """Fork, copy and return captured (their first calls of this process may
     be these) and replayed with other tables and another pool content."""
