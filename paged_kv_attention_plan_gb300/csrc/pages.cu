@@ -190,9 +190,42 @@ __device__ __forceinline__ void leave() {
   if (gridDim.x > 1) cg::this_cluster().barrier_wait();
 }
 
+// Take the free ones (`bits`) of a step's pages, the first with rank *rank, as
+// long as ranks stay below `stop`: use(rank, page) and one reference each.
+// False when there is nothing left to take.  ALONE: nobody else changes a
+// reference meanwhile, so a lane stores its four pages at once.
+template <bool ALONE, class F>
+__device__ __forceinline__ bool take_step(int32_t* refs, const Share& s, uint32_t p, const int4& r,
+                                          unsigned bits, int* rank, int stop, F use) {
+  int first, all;
+  rank_bits(bits, s.lane, &first, &all);
+  first += *rank;
+  unsigned taken = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int at = first + __popc(bits & ((1u << k) - 1));
+    if ((bits >> k & 1) && at < stop) {
+      use(at, (int32_t)(p + k));
+      taken |= 1u << k;
+    }
+  }
+  if (taken) {
+    if (ALONE && s.vec && p + 4 <= s.hi) {
+      *reinterpret_cast<int4*>(refs + p) =
+          make_int4(taken & 1 ? 1 : r.x, taken & 2 ? 1 : r.y, taken & 4 ? 1 : r.z,
+                    taken & 8 ? 1 : r.w);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (taken >> k & 1) refs[p + k] = 1;
+    }
+  }
+  *rank += all;
+  return *rank < stop;
+}
+
 // Take the first `stop` free pages of all: use(rank, page) for those of this
-// warp's tiles.  `before` is count_pages' answer.  ALONE: nobody else changes
-// a reference meanwhile, so a lane stores its four pages at once.
+// warp's tiles.  `before` is count_pages' answer.
 template <bool ALONE, class F>
 __device__ __forceinline__ void take_free(int32_t* refs, uint32_t num_pages, const Tiling& t,
                                           int before, int stop, F use) {
@@ -201,33 +234,7 @@ __device__ __forceinline__ void take_free(int32_t* refs, uint32_t num_pages, con
     if (rank >= stop) return;
     const Share s = tile_at(refs, num_pages, t, i);
     walk(refs, s, 1, [&](uint32_t p, const int4& r) {
-      const unsigned bits = free_bits(r);
-      int first, all;
-      rank_bits(bits, s.lane, &first, &all);
-      first += rank;
-      unsigned taken = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int at = first + __popc(bits & ((1u << k) - 1));
-        if ((bits >> k & 1) && at < stop) {
-          use(at, (int32_t)(p + k));
-          taken |= 1u << k;
-        }
-      }
-      // one reference each
-      if (taken) {
-        if (ALONE && s.vec && p + 4 <= s.hi) {
-          *reinterpret_cast<int4*>(refs + p) =
-              make_int4(taken & 1 ? 1 : r.x, taken & 2 ? 1 : r.y, taken & 4 ? 1 : r.z,
-                        taken & 8 ? 1 : r.w);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (taken >> k & 1) refs[p + k] = 1;
-        }
-      }
-      rank += all;
-      return rank < stop;
+      return take_step<ALONE>(refs, s, p, r, free_bits(r), &rank, stop, use);
     });
   }
 }
@@ -244,8 +251,18 @@ struct AllocArgs {
   Tiling tiling;
 };
 
+// From this many pages on, and with more than a row of tiles, they are taken
+// by a launch of their own.
+constexpr int kTakeInPlace = 8192;
+
+// SPLIT: the taking is left to take_kernel, over the whole GPU.  Each tile's
+// count before it travels in the tile's first free page, whose reference count
+// holds -1 - count until that page, the first of its tile to be taken, gets
+// its reference; tiles that give nothing stay as they are.
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) alloc_kernel(const AllocArgs a) {
   __shared__ Counts c;
+  if (SPLIT) start_next();
   int total;
   const int before = count_pages(c, a.refs, a.num_pages, a.tiling, false, &total);
   if (total < a.n) {
@@ -253,12 +270,51 @@ __global__ void __launch_bounds__(kThreads, 1) alloc_kernel(const AllocArgs a) {
          i += (int64_t)gridDim.x * kThreads)
       a.pages[i] = -1;
     if (blockIdx.x == 0 && threadIdx.x == 0) note_error(a.err, PKA_ERR_WORKSPACE);
-  } else {
+  } else if (!SPLIT) {
     take_free<true>(a.refs, a.num_pages, a.tiling, before, a.n, [&](int rank, int32_t page) {
       a.pages[rank] = page;
     });
+  } else {
+    for (int i = 0; i < a.tiling.rows; ++i) {
+      const int rank = __shfl_sync(kAll, before, i);
+      if (rank >= a.n) break;
+      const Share s = tile_at(a.refs, a.num_pages, a.tiling, i);
+      walk(a.refs, s, 1, [&](uint32_t p, const int4& r) {
+        const unsigned bits = free_bits(r), lanes = __ballot_sync(kAll, bits != 0);
+        if (lanes && s.lane == __ffs(lanes) - 1) a.refs[p + __ffs(bits) - 1] = -1 - rank;
+        return lanes == 0;
+      });
+    }
   }
   leave();
+}
+
+// A warp a tile: the first free page carries the tile's first rank, or 0 in a
+// tile that gives nothing.
+__global__ void __launch_bounds__(256) take_kernel(const AllocArgs a) {
+  const uint64_t lo = (blockIdx.x * 8ull + (threadIdx.x >> 5)) * a.tiling.tile;
+  after_previous();
+  if (lo >= (uint64_t)a.num_pages) return;
+  Share s;
+  s.lo = (uint32_t)lo;
+  s.hi = (uint32_t)min(lo + a.tiling.tile, (uint64_t)a.num_pages);
+  s.lane = threadIdx.x & 31;
+  s.vec = (reinterpret_cast<uintptr_t>(a.refs) & 15) == 0;
+  int rank = -1;  // not met the first free page yet
+  walk(a.refs, s, 1, [&](uint32_t p, const int4& r) {
+    const unsigned bits = free_bits(r);
+    if (rank < 0) {
+      const unsigned lanes = __ballot_sync(kAll, bits != 0);
+      if (!lanes) return true;
+      const int k = __ffs(bits) - 1;
+      const int mark = k == 0 ? r.x : k == 1 ? r.y : k == 2 ? r.z : r.w;
+      rank = -1 - __shfl_sync(kAll, mark, __ffs(lanes) - 1);
+      if (rank < 0) return false;
+    }
+    return take_step<true>(a.refs, s, p, r, bits, &rank, a.n, [&](int at, int32_t page) {
+      a.pages[at] = page;
+    });
+  });
 }
 
 // A page's count never stays below zero: a decrement that finds none left is
@@ -627,6 +683,36 @@ __device__ __forceinline__ void number_tile(const CompactArgs& a, const Share& s
   });
 }
 
+// The moves' references and map entries, and the table entries through the
+// map.  An entry whose page moves reads its map entry before or after it is
+// turned; either gives the new id.  An entry that names no live page stays as
+// it is and is noted.  (In the first launch, for one block and a small table,
+// this took as long: 5.6 us against 3.2 + 2.7.)
+__global__ void __launch_bounds__(256) move_kernel(const CompactArgs a) {
+  after_previous();
+  const int64_t at = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  const int64_t step = (int64_t)gridDim.x * blockDim.x;
+  bool bad = false;
+  for (int64_t i = at; i < a.num_indices; i += step) {
+    const int32_t p = a.in[i];
+    int32_t to = -1;
+    if (p >= 0 && p < a.num_pages) {
+      to = *const_cast<volatile int32_t*>(a.map + p);
+      if (to < -1) to = a.copy_dst[-2 - to];
+    }
+    bad = bad || to < 0;
+    a.out[i] = to < 0 ? p : to;
+  }
+  const int moves = a.counts[0];
+  for (int64_t i = at; i < moves; i += step) {
+    const int32_t src = a.copy_src[i], dst = a.copy_dst[i];
+    a.refs_out[dst] = a.refs[src];
+    if (a.refs == a.refs_out) a.refs_out[src] = 0;
+    *const_cast<volatile int32_t*>(a.map + src) = dst;
+  }
+  if (bad) note_error(a.err, PKA_ERR_METADATA);
+}
+
 // One row of tiles is numbered where it was counted.  More are too much for
 // the cluster's few blocks: they go to number_kernel, each tile's count before
 // it in the map entry of its first page (which that tile alone reads and
@@ -664,35 +750,6 @@ __global__ void __launch_bounds__(256) number_kernel(const CompactArgs a) {
   const int live = *const_cast<volatile int32_t*>(a.counts + 1);
   const int rank = __shfl_sync(kAll, *const_cast<volatile int32_t*>(a.map + s.lo), 0);
   number_tile(a, s, rank, live);
-}
-
-// The moves' references and map entries, and the table entries through the
-// map.  An entry whose page moves reads its map entry before or after it is
-// turned; either gives the new id.  An entry that names no live page stays as
-// it is and is noted.
-__global__ void __launch_bounds__(256) move_kernel(const CompactArgs a) {
-  after_previous();
-  const int64_t at = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-  const int64_t step = (int64_t)gridDim.x * blockDim.x;
-  bool bad = false;
-  for (int64_t i = at; i < a.num_indices; i += step) {
-    const int32_t p = a.in[i];
-    int32_t to = -1;
-    if (p >= 0 && p < a.num_pages) {
-      to = *const_cast<volatile int32_t*>(a.map + p);
-      if (to < -1) to = __ldcg(a.copy_dst + (-2 - to));
-    }
-    bad = bad || to < 0;
-    a.out[i] = to < 0 ? p : to;
-  }
-  const int moves = __ldcg(a.counts);
-  for (int64_t i = at; i < moves; i += step) {
-    const int32_t src = __ldcg(a.copy_src + i), dst = __ldcg(a.copy_dst + i);
-    a.refs_out[dst] = a.refs[src];
-    if (a.refs == a.refs_out) a.refs_out[src] = 0;
-    *const_cast<volatile int32_t*>(a.map + src) = dst;
-  }
-  if (bad) note_error(a.err, PKA_ERR_METADATA);
 }
 
 // ---------------------------------------------------------------------------
@@ -938,9 +995,15 @@ pka_status pka_alloc_pages(int32_t* page_refs_d, int32_t num_pages, int32_t n, i
     return PKA_ERR_INVALID_ARG;
   const pka::AllocArgs a{page_refs_d, pages_d, pka::device_error_word(), num_pages, n,
                          pka::tiling_of(num_pages)};
-  return pka::done(pka::launch_cluster<pka::alloc_kernel>(pka::cluster_ctas(num_pages), 0,
-                                                          static_cast<cudaStream_t>(stream), a),
-                   "page alloc launch");
+  const int ctas = pka::cluster_ctas(num_pages);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a.tiling.rows == 1 || n <= pka::kTakeInPlace)
+    return pka::done(pka::launch_cluster<pka::alloc_kernel<false>>(ctas, 0, st, a),
+                     "page alloc launch");
+  cudaError_t e = pka::launch_cluster<pka::alloc_kernel<true>>(ctas, 0, st, a);
+  const int64_t tiles = (num_pages + (int64_t)a.tiling.tile - 1) / a.tiling.tile;
+  if (e == cudaSuccess) e = pka::launch_behind(pka::take_kernel, (int)((tiles + 7) / 8), st, a);
+  return pka::done(e, "page alloc launch");
 }
 
 pka_status pka_free_pages(int32_t* page_refs_d, int32_t num_pages, const int32_t* pages_d,

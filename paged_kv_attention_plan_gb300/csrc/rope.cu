@@ -333,7 +333,7 @@ cudaError_t launch(const RopeArgs& args, cudaStream_t stream) {
   const int heads = a.q_heads + (APPEND ? 2 : 1) * a.k_heads;
   const int steps = (heads + HPS - 1) / HPS;
   const int sms = current_device_sms();
-  const int64_t warps = 32 * (int64_t)(sms > 0 ? sms : 1);
+  const int64_t warps = (APPEND ? 64 : 256) * (int64_t)(sms > 0 ? sms : 1);
   int64_t per = (a.rows * steps + warps - 1) / warps;
   per = per < 1 ? 1 : per > steps ? steps : per;
   const int parts = (int)((steps + per - 1) / per);
