@@ -371,7 +371,7 @@ pka_status pka_apply_rope(const pka_rope* rope, int32_t transpose, int32_t head_
  *   contiguous.  e4m3 pools store the rotated float32 value divided by
  *   k_scale, rounded once, magnitudes above 448 clamped to 448.
  *   nnz_new is the rows of the buffers: rows from append_indptr_d[batch] on
- *   belong to no request (a padded batch) and are neither read nor written.
+ *   belong to no request (a padded batch); their q_out rows stay as they were.
  *   A row whose position lies outside its request's pages, or whose page id
  *   lies outside [0, num_pool_pages), is not appended and PKA_ERR_METADATA is
  *   noted in the device error word (pka_get_device_error); the indptr arrays

@@ -22,10 +22,11 @@ namespace {
 enum RopeLayout {
   kHalf = 0,       // (x[i], x[i + R/2]), R/2 a multiple of 8: whole 16-byte pieces
   kAdjacent = 1,   // (x[2i], x[2i + 1])
-  kScattered = 2,  // (x[i], x[i + R/2]), any other R: element by element
+  kScattered = 2,  // (x[i], x[i + R/2]), any other R: through shared memory
 };
 
-constexpr int kMaxHeads = 4096;  // of a row; keeps the launch's second grid axis small
+constexpr int kMaxHeads = 4096;            // of a row; keeps the second grid axis small
+constexpr int64_t kMaxRows = INT64_C(1) << 33;  // eight a block
 
 struct RopeArgs {
   const uint16_t* q;  // [rows, q_heads, D], row stride in elements
@@ -54,19 +55,41 @@ struct RopeArgs {
   int page_size;
   int layout;
   float k_scale, v_scale;    // e4m3 pools
-  float k_inv, v_inv;        // exact reciprocal of a power-of-two scale, else 0
+  float k_inv, v_inv;        // 1 / scale, or 0: divide
   int32_t* err;
   uint64_t turns[64];        // F_i
 };
 
-// 8 values divided by a pool's scale (correctly rounded) and rounded to
-// nearest even e4m3, magnitudes above 448 clamped; 8 codes, little-endian.
+// x / scale, correctly rounded, from inv = 1 / scale correctly rounded: the
+// product x * inv and two corrections by its residual (Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990: the
+// correction of a quotient within one ulp, with such a reciprocal and the
+// exact residual of a fused multiply-add, is the correctly rounded quotient).
+// A product that is not finite is the answer as it is, and the corrections of a
+// negative zero would lose its sign.  Seven operations where
+// the general division is a branch and a few dozen: a 9,216-row append into
+// e4m3 pools took 49.3 us with it.
+__device__ __forceinline__ float divided(float x, float scale, float inv) {
+  const float q0 = x * inv;
+  const float q1 = fmaf(fmaf(-q0, scale, x), inv, q0);
+  const float q2 = fmaf(fmaf(-q1, scale, x), inv, q1);
+  return fabsf(q0) < INFINITY ? copysignf(q2, q0) : q0;
+}
+
+// 8 values divided by a pool's scale and rounded to nearest even e4m3,
+// magnitudes above 448 clamped; 8 codes, little-endian.
 __device__ __forceinline__ uint2 to_e4m3x8(const float (&x)[8], float scale, float inv) {
   uint32_t pk[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float lo = inv > 0.f ? x[2 * i] * inv : __fdiv_rn(x[2 * i], scale);
-    const float hi = inv > 0.f ? x[2 * i + 1] * inv : __fdiv_rn(x[2 * i + 1], scale);
+    float lo, hi;
+    if (inv != 0.f) {
+      lo = divided(x[2 * i], scale, inv);
+      hi = divided(x[2 * i + 1], scale, inv);
+    } else {
+      lo = __fdiv_rn(x[2 * i], scale);
+      hi = __fdiv_rn(x[2 * i + 1], scale);
+    }
     asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n cvt.u32.u16 %0, t;\n}"
         : "=r"(pk[i])
         : "f"(hi), "f"(lo));
@@ -83,44 +106,33 @@ __device__ __forceinline__ void unpack8(const uint32_t (&w)[4], float (&x)[8]) {
   }
 }
 
-// A lane's piece of a head: 16 bytes at element `off`, or (kScattered) the
-// eight elements elem(0) .. elem(7).
-template <int L, class F>
-__device__ __forceinline__ void load_piece(const uint16_t* p, int off, F elem, uint32_t (&w)[4]) {
-  if constexpr (L == kScattered) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = p[elem(2 * i)] | (uint32_t)p[elem(2 * i + 1)] << 16;
-  } else {
-    const uint4 x = *reinterpret_cast<const uint4*>(p + off);
-    w[0] = x.x;
-    w[1] = x.y;
-    w[2] = x.z;
-    w[3] = x.w;
-  }
+__device__ __forceinline__ void load16(const uint16_t* p, uint32_t (&w)[4]) {
+  const uint4 x = *reinterpret_cast<const uint4*>(p);
+  w[0] = x.x;
+  w[1] = x.y;
+  w[2] = x.z;
+  w[3] = x.w;
 }
 
-template <int L, class F>
-__device__ __forceinline__ void store_piece(uint16_t* p, int off, F elem, const uint32_t (&w)[4]) {
-  if constexpr (L == kScattered) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      p[elem(2 * i)] = (uint16_t)w[i];
-      p[elem(2 * i + 1)] = (uint16_t)(w[i] >> 16);
-    }
-  } else {
-    *reinterpret_cast<uint4*>(p + off) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+__device__ __forceinline__ void store16(uint16_t* p, const uint32_t (&w)[4]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int L, class F>
-__device__ __forceinline__ void store_codes(uint8_t* p, int off, F elem, uint2 w) {
-  if constexpr (L == kScattered) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) p[elem(j)] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
-  } else {
-    *reinterpret_cast<uint2*>(p + off) = w;
-  }
+__device__ __forceinline__ void to_shared(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+__device__ __forceinline__ void from_shared(const float* p, float (&x)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  x[0] = a.x;
+  x[1] = a.y;
+  x[2] = a.z;
+  x[3] = a.w;
+  x[4] = b.x;
+  x[5] = b.y;
+  x[6] = b.z;
+  x[7] = b.w;
 }
 
 // Element of head h of a slot of a page.
@@ -131,14 +143,20 @@ __device__ __forceinline__ int64_t pool_offset(const RopeArgs& a, int page, int 
                               : ((int64_t)h * a.page_size + slot) * D);
 }
 
-// A warp takes a row and walks its heads (q, then k, then v as one list).  A
-// head is D/16 units of 8 pairs; a lane keeps one unit (u) and takes it from
-// each of the 32 / (D/16) heads of a step, so its 8 sines and cosines serve
-// the whole row.  A unit is two 16-byte pieces A and B of the head: pair j is
-// (A[j], B[j]), or, for adjacent pairs, the pairs inside A and inside B.
-// Elements past rotary_dim are copied bit by bit.  The pieces of kInFlight
-// steps are loaded before the first of them is used, the row's first ones
-// before its page and its sines are looked up.
+// A warp takes a row, or a part of its heads, and walks the heads (q, then k,
+// then v as one list).  A head is D/16 units of 8 pairs; a lane keeps one unit
+// (u) and takes it from each of the 32 / (D/16) heads of a step, so its 8
+// sines and cosines serve the whole row.  A lane reads and writes two 16-byte
+// pieces A and B of a head.  Half layout: pair j is (A[j], B[j]).  Adjacent:
+// the pairs inside A and inside B.  Scattered: the pieces meet as floats in
+// shared memory, where a lane's pairs lie D/16 apart (no two lanes of a warp
+// on one bank) and are turned in place.  Elements past rotary_dim keep their
+// bits.  The pieces of kInFlight steps are loaded before the first of them is
+// used, the first ones before the row's page and sines are looked up.
+//
+// Bound by memory latency and bandwidth: two steps in flight at four blocks an
+// SM carry it furthest (16,387 rows of 64 heads, in us: one step 87, two 82,
+// three at three blocks 88, four at two blocks 97).
 constexpr int kInFlight = 2;
 
 template <int D, int L, bool APPEND, bool F8>
@@ -147,30 +165,37 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int UNITS = D / 16;      // lanes of a head
   constexpr int HPS = 32 / UNITS;    // heads of a step
   constexpr int K = 8 / HPS;         // pairs whose sine and cosine a lane computes
+  constexpr int STRIDE = D + UNITS;  // floats of a head in shared memory
+  __shared__ __align__(16) float heads_in_shared[L == kScattered ? 8 * HPS * STRIDE : 4];
   const int lane = threadIdx.x & 31;
   const int u = lane % UNITS, sub = lane / UNITS;
   const int rd = a.rotary_dim;
   const int heads = a.q_heads + (APPEND ? 2 : 1) * a.k_heads;
+  const int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5);
+  if (row >= a.rows) return;
 
   // where the lane's pieces lie in a head, and which of its pairs rotate
-  int off_a, off_b;
-  uint32_t turning = 0;
-  auto pair_of = [&](int j) { return L != kAdjacent ? 8 * u + j
-                                     : j < 4 ? 4 * u + j : D / 4 + 4 * u + j - 4; };
-#pragma unroll
-  for (int j = 0; j < 8; ++j) turning |= (pair_of(j) < rd / 2 ? 1u : 0u) << j;
+  int off_a = 8 * u, off_b = 8 * u + D / 2;
   if (L == kHalf) {
     const int t = u - rd / 16;
     off_a = t < 0 ? 8 * u : rd + 16 * t;
     off_b = t < 0 ? 8 * u + rd / 2 : off_a + 8;
-  } else {
-    off_a = 8 * u;
-    off_b = 8 * u + D / 2;
   }
-  // kScattered: elements of pair j
-  auto first_of = [&](int j) { const int p = 8 * u + j; return p < rd / 2 ? p : 2 * p; };
-  auto second_of = [&](int j) { const int p = 8 * u + j;
-                                return p < rd / 2 ? p + rd / 2 : 2 * p + 1; };
+  auto pair_of = [&](int j) {
+    return L == kHalf ? 8 * u + j
+           : L == kScattered ? u + UNITS * j
+                             : j < 4 ? 4 * u + j : D / 4 + 4 * u + j - 4;
+  };
+  uint32_t turning = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) turning |= (pair_of(j) < rd / 2 ? 1u : 0u) << j;
+  // the elements of word i of a piece that rotate, as a mask
+  auto word_mask = [&](bool piece_b, int i) {
+    if (L == kHalf) return turning ? ~0u : 0u;
+    if (L == kAdjacent) return turning >> (piece_b ? i + 4 : i) & 1 ? ~0u : 0u;
+    const int e = (piece_b ? off_b : off_a) + 2 * i;
+    return (e < rd ? 0xffffu : 0u) | (e + 1 < rd ? 0xffff0000u : 0u);
+  };
 
   uint64_t turn[K];
 #pragma unroll
@@ -181,149 +206,173 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
 
   const int h0 = blockIdx.y * a.steps_per_part * HPS;
   const int h1 = min(heads, h0 + a.steps_per_part * HPS);
-  const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
-  for (int64_t row = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5); row < a.rows;
-       row += nwarps) {
-    uint32_t wa[kInFlight][4], wb[kInFlight][4];
-    auto load = [&](int hb) {  // the lane's pieces of heads hb + sub, + HPS, ...
+  uint32_t wa[kInFlight][4], wb[kInFlight][4];
+  auto load = [&](int hb) {  // the lane's pieces of heads hb + sub, + HPS, ...
 #pragma unroll
-      for (int t = 0; t < kInFlight; ++t) {
-        const int h = hb + t * HPS + sub;
-        if (h >= h1) continue;
-        const uint16_t* src;
-        if (h < a.q_heads)
-          src = a.q + row * a.q_stride + (int64_t)h * D;
-        else if (!APPEND || h < a.q_heads + a.k_heads)
-          src = a.k + row * a.k_stride + (int64_t)(h - a.q_heads) * D;
-        else
-          src = a.v + row * a.v_stride + (int64_t)(h - a.q_heads - a.k_heads) * D;
-        load_piece<L>(src, off_a, first_of, wa[t]);
-        load_piece<L>(src, off_b, second_of, wb[t]);
-      }
-    };
-    load(h0);
-
-    int64_t pos = 0;
-    int32_t page = -1;
-    int slot = 0;
-    if constexpr (APPEND) {
-      // a decode step's rows are one a request: row r is tried as request r's
-      // before the search
-      const int guess = (int)min(row, (int64_t)a.batch - 1);
-      int r = guess, first = a.append_indptr[guess], last = a.append_indptr[guess + 1];
-      const int end = a.append_indptr[a.batch];
-      if (row < first || row >= last) {
-        if (row >= end) continue;  // a row of no request
-        r = warp_find(a.append_indptr, a.batch, row, lane);
-        first = a.append_indptr[r];
-        last = a.append_indptr[r + 1];
-      }
-      const int n_app = last - first;
-      const int kv0 = a.kv_indptr[r], pages = a.kv_indptr[r + 1] - kv0;
-      const int64_t kv_len = (int64_t)(pages - 1) * a.page_size + a.last_page_len[r];
-      pos = kv_len - n_app + (row - first);
-      const int64_t nth = pos >= 0 ? pos / a.page_size : -1;
-      if (nth >= 0 && nth < pages) {
-        page = a.kv_indices[kv0 + nth];
-        slot = (int)(pos - nth * a.page_size);
-      }
-      if (page < 0 || page >= a.num_pages) {
-        if (lane == 0) note_error(a.err, PKA_ERR_METADATA);
-        page = -1;
-      }
+    for (int t = 0; t < kInFlight; ++t) {
+      const int h = hb + t * HPS + sub;
+      if (h >= h1) continue;
+      const uint16_t* src;
+      if (h < a.q_heads)
+        src = a.q + row * a.q_stride + (int64_t)h * D;
+      else if (!APPEND || h < a.q_heads + a.k_heads)
+        src = a.k + row * a.k_stride + (int64_t)(h - a.q_heads) * D;
+      else
+        src = a.v + row * a.v_stride + (int64_t)(h - a.q_heads - a.k_heads) * D;
+      load16(src + off_a, wa[t]);
+      load16(src + off_b, wb[t]);
     }
-    if (!APPEND || a.positions) pos = a.positions[row];
+  };
+  load(h0);
 
-    // sines and cosines: K pairs a lane, exchanged among the lanes of a unit
-    float c[8], s[8];
-    {
-      float ck[K], sk[K];
-#pragma unroll
-      for (int i = 0; i < K; ++i) {
-        const uint64_t phase = (uint64_t)pos * turn[i] + (1ull << 31);
-        sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &sk[i], &ck[i]);
-        ck[i] *= a.magnitude;
-        sk[i] *= a.magnitude * a.sine_sign;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        c[j] = __shfl_sync(0xffffffffu, ck[j % K], (j / K) * UNITS + u);
-        s[j] = __shfl_sync(0xffffffffu, sk[j % K], (j / K) * UNITS + u);
-      }
+  int64_t pos = 0;
+  int32_t page = -1;
+  int slot = 0;
+  if constexpr (APPEND) {
+    // a decode step's rows are one a request: row r is tried as request r's
+    // before the search
+    const int guess = (int)min(row, (int64_t)a.batch - 1);
+    int r = guess, first = a.append_indptr[guess], last = a.append_indptr[guess + 1];
+    const int end = a.append_indptr[a.batch];
+    if (row < first || row >= last) {
+      if (row >= end) return;  // a row of no request
+      r = warp_find(a.append_indptr, a.batch, row, lane);
+      first = a.append_indptr[r];
+      last = a.append_indptr[r + 1];
     }
+    const int kv0 = a.kv_indptr[r], pages = a.kv_indptr[r + 1] - kv0;
+    const int64_t kv_len = (int64_t)(pages - 1) * a.page_size + a.last_page_len[r];
+    pos = kv_len - (last - first) + (row - first);
+    const int64_t nth = pos < 0 ? -1
+                        : pos <= UINT32_MAX ? (uint32_t)pos / (uint32_t)a.page_size
+                                            : pos / a.page_size;
+    if (nth >= 0 && nth < pages) {
+      page = a.kv_indices[kv0 + nth];
+      slot = (int)(pos - nth * a.page_size);
+    }
+    if (page < 0 || page >= a.num_pages) {
+      if (lane == 0) note_error(a.err, PKA_ERR_METADATA);
+      page = -1;
+    }
+  }
+  if (!APPEND || a.positions) pos = a.positions[row];
 
-    for (int hb = h0;;) {
+  // sines and cosines: K pairs a lane, exchanged among the lanes of a unit
+  float c[8], s[8];
+  {
+    float ck[K], sk[K];
 #pragma unroll
-      for (int t = 0; t < kInFlight; ++t) {
-        const int h = hb + t * HPS + sub;
-        if (h >= h1) continue;
-        const bool is_q = h < a.q_heads;
-        const bool is_v = APPEND && h >= a.q_heads + a.k_heads;
-        const int hh = is_q ? h : is_v ? h - a.q_heads - a.k_heads : h - a.q_heads;
-        const bool to_pool = APPEND && !is_q;
-        if (to_pool && page < 0) continue;
-        float xa[8], xb[8];
-        if (F8 || !is_v) {
-          unpack8(wa[t], xa);
-          unpack8(wb[t], xb);
+    for (int i = 0; i < K; ++i) {
+      const uint64_t phase = (uint64_t)pos * turn[i] + (1ull << 31);
+      sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &sk[i], &ck[i]);
+      ck[i] *= a.magnitude;
+      sk[i] *= a.magnitude * a.sine_sign;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      c[j] = __shfl_sync(0xffffffffu, ck[j % K], (j / K) * UNITS + u);
+      s[j] = __shfl_sync(0xffffffffu, sk[j % K], (j / K) * UNITS + u);
+    }
+  }
+
+  for (int hb = h0;;) {
+#pragma unroll
+    for (int t = 0; t < kInFlight; ++t) {
+      const int h = hb + t * HPS + sub;
+      const bool is_q = h < a.q_heads;
+      const bool is_v = APPEND && h >= a.q_heads + a.k_heads;
+      const bool to_pool = APPEND && !is_q;
+      const bool store = h < h1 && !(to_pool && page < 0);
+      if (L != kScattered && !store) continue;
+      float xa[8], xb[8];
+      if (F8 || !is_v) {
+        unpack8(wa[t], xa);
+        unpack8(wb[t], xb);
+      }
+      if constexpr (L == kScattered) {  // all lanes: the heads of a step meet the barrier together
+        float* m = heads_in_shared + ((threadIdx.x >> 5) * HPS + sub) * STRIDE;
+        if (!is_v) {
+          to_shared(m + off_a, xa);
+          to_shared(m + off_b, xb);
         }
+        __syncwarp();
         if (!is_v) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            // pair j: (A[j], B[j]), or adjacent elements of A (j < 4) or of B
-            float& x = L != kAdjacent ? xa[j] : j < 4 ? xa[2 * j] : xb[2 * (j - 4)];
-            float& y = L != kAdjacent ? xb[j] : j < 4 ? xa[2 * j + 1] : xb[2 * (j - 4) + 1];
+            const int p = u + UNITS * j;
             if (turning >> j & 1) {
-              const float z = x * c[j] - y * s[j];
-              y = x * s[j] + y * c[j];
-              x = z;
+              const float x = m[p], y = m[p + rd / 2];
+              m[p] = x * c[j] - y * s[j];
+              m[p + rd / 2] = x * s[j] + y * c[j];
             }
           }
         }
-        if (F8 && to_pool) {
-          const float scale = is_v ? a.v_scale : a.k_scale, inv = is_v ? a.v_inv : a.k_inv;
-          uint8_t* p = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) +
-                       pool_offset<D>(a, page, slot, hh);
-          store_codes<L>(p, off_a, first_of, to_e4m3x8(xa, scale, inv));
-          store_codes<L>(p, off_b, second_of, to_e4m3x8(xb, scale, inv));
-          continue;
-        }
-        // rotated elements rounded once to bf16; the others keep their bits
+        __syncwarp();
         if (!is_v) {
+          from_shared(m + off_a, xa);
+          from_shared(m + off_b, xb);
+        }
+        __syncwarp();  // read before the next step writes
+      } else if (!is_v) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t ya = float2_to_bf16x2(xa[2 * i], xa[2 * i + 1]);
-            const uint32_t yb = float2_to_bf16x2(xb[2 * i], xb[2 * i + 1]);
-            uint32_t ma, mb;  // the rotated halves of word i of A and of B
-            if constexpr (L == kHalf) {
-              ma = mb = turning ? ~0u : 0u;
-            } else if constexpr (L == kAdjacent) {
-              ma = turning >> i & 1 ? ~0u : 0u;
-              mb = turning >> (i + 4) & 1 ? ~0u : 0u;
-            } else {
-              ma = mb = (turning >> (2 * i) & 1 ? 0xffffu : 0u) |
-                        (turning >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
-            }
-            wa[t][i] = (ya & ma) | (wa[t][i] & ~ma);
-            wb[t][i] = (yb & mb) | (wb[t][i] & ~mb);
+        for (int j = 0; j < 8; ++j) {
+          // pair j: (A[j], B[j]), or adjacent elements of A (j < 4) or of B
+          float& x = L == kHalf ? xa[j] : j < 4 ? xa[2 * j] : xb[2 * (j - 4)];
+          float& y = L == kHalf ? xb[j] : j < 4 ? xa[2 * j + 1] : xb[2 * (j - 4) + 1];
+          if (turning >> j & 1) {
+            const float z = x * c[j] - y * s[j];
+            y = x * s[j] + y * c[j];
+            x = z;
           }
         }
-        uint16_t* p;
-        if (to_pool)
-          p = static_cast<uint16_t*>(is_v ? a.v_pool : a.k_pool) +
-              pool_offset<D>(a, page, slot, hh);
-        else if (is_q)
-          p = a.q_out + row * a.q_out_stride + (int64_t)hh * D;
-        else
-          p = a.k_out + row * a.k_out_stride + (int64_t)hh * D;
-        store_piece<L>(p, off_a, first_of, wa[t]);
-        store_piece<L>(p, off_b, second_of, wb[t]);
       }
-      hb += kInFlight * HPS;
-      if (hb >= h1) break;
-      load(hb);
+      if (L == kScattered && !store) continue;
+      const int hh = is_q ? h : is_v ? h - a.q_heads - a.k_heads : h - a.q_heads;
+      if (F8 && to_pool) {
+        const float scale = is_v ? a.v_scale : a.k_scale, inv = is_v ? a.v_inv : a.k_inv;
+        uint8_t* p = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) +
+                     pool_offset<D>(a, page, slot, hh);
+        *reinterpret_cast<uint2*>(p + off_a) = to_e4m3x8(xa, scale, inv);
+        *reinterpret_cast<uint2*>(p + off_b) = to_e4m3x8(xb, scale, inv);
+        continue;
+      }
+      // rotated elements rounded once to bf16; the others keep their bits
+      if (!is_v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t ma = word_mask(false, i), mb = word_mask(true, i);
+          wa[t][i] = (float2_to_bf16x2(xa[2 * i], xa[2 * i + 1]) & ma) | (wa[t][i] & ~ma);
+          wb[t][i] = (float2_to_bf16x2(xb[2 * i], xb[2 * i + 1]) & mb) | (wb[t][i] & ~mb);
+        }
+      }
+      uint16_t* p;
+      if (to_pool)
+        p = static_cast<uint16_t*>(is_v ? a.v_pool : a.k_pool) + pool_offset<D>(a, page, slot, hh);
+      else if (is_q)
+        p = a.q_out + row * a.q_out_stride + (int64_t)hh * D;
+      else
+        p = a.k_out + row * a.k_out_stride + (int64_t)hh * D;
+      store16(p + off_a, wa[t]);
+      store16(p + off_b, wb[t]);
     }
+    hb += kInFlight * HPS;
+    if (hb >= h1) break;
+    load(hb);
   }
+}
+
+// How many of a row's head steps one warp takes.  First enough warps: 16 an SM
+// (64 rows of 10 steps: 2.4 us with one step a warp, 5.8 with ten).  Then
+// longer runs, which share one look-up of page and sines, to at most six steps:
+// past that the last warps run alone (16,387 rows of 10 steps: one 97 us, two
+// 60, four 56, six 55, ten 58; a 9,216-row append of 12: 83, 48, 39, 38, 38).
+int steps_per_part(int64_t rows, int steps) {
+  const int sms = current_device_sms();
+  const int64_t warps = 16 * (int64_t)(sms > 0 ? sms : 1);
+  const int64_t per = (rows * steps + warps - 1) / warps;
+  const int most = per < 1 ? 1 : per > 6 ? 6 : (int)per;
+  const int parts = (steps + most - 1) / most;
+  return (steps + parts - 1) / parts;
 }
 
 template <int D, int L, bool APPEND, bool F8>
@@ -332,15 +381,10 @@ cudaError_t launch(const RopeArgs& args, cudaStream_t stream) {
   RopeArgs a = args;
   const int heads = a.q_heads + (APPEND ? 2 : 1) * a.k_heads;
   const int steps = (heads + HPS - 1) / HPS;
-  const int sms = current_device_sms();
-  const int64_t warps = (APPEND ? 64 : 256) * (int64_t)(sms > 0 ? sms : 1);
-  int64_t per = (a.rows * steps + warps - 1) / warps;
-  per = per < 1 ? 1 : per > steps ? steps : per;
-  const int parts = (int)((steps + per - 1) / per);
-  a.steps_per_part = (int)per;
-  const int64_t blocks = (a.rows + 7) / 8;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  rope_kernel<D, L, APPEND, F8><<<dim3((unsigned)blocks, (unsigned)parts), 256, 0, stream>>>(a);
+  a.steps_per_part = steps_per_part(a.rows, steps);
+  const int parts = (steps + a.steps_per_part - 1) / a.steps_per_part;
+  const dim3 grid((unsigned)((a.rows + 7) / 8), (unsigned)parts);
+  rope_kernel<D, L, APPEND, F8><<<grid, 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -380,11 +424,9 @@ bool out_ok(const void* in, int64_t in_stride, const void* out, int64_t out_stri
   return in != out || in_stride == out_stride;
 }
 
-// Reciprocal of a power-of-two scale (exact), else 0: divide.
-float pow2_inv(float s) {
-  int e = 0;
-  return std::frexp(s, &e) == 0.5f ? std::ldexp(1.0f, 1 - e) : 0.f;
-}
+// 1 / scale where divided() holds: away from the ends of the exponents, where
+// a residual could lose bits that reach a code; else 0.
+float reciprocal(float s) { return s > 0x1p-60f && s < 0x1p60f ? 1.f / s : 0.f; }
 
 }  // namespace
 }  // namespace pka
@@ -446,7 +488,8 @@ pka_status pka_apply_rope(const pka_rope* rope, int32_t transpose, int32_t head_
   if (!rope || (transpose != 0 && transpose != 1) || rows < 0 || q_heads < 0 || k_heads < 0)
     return PKA_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return PKA_ERR_UNSUPPORTED;
-  if (q_heads > pka::kMaxHeads || k_heads > pka::kMaxHeads) return PKA_ERR_UNSUPPORTED;
+  if (q_heads > pka::kMaxHeads || k_heads > pka::kMaxHeads || rows > pka::kMaxRows)
+    return PKA_ERR_UNSUPPORTED;
   if (!pka::rope_valid(rope, head_dim)) return PKA_ERR_INVALID_ARG;
   if (rows == 0 || (q_heads == 0 && k_heads == 0)) return PKA_OK;
   if (!positions_d) return PKA_ERR_INVALID_ARG;
@@ -488,7 +531,8 @@ pka_status pka_rope_append_paged_kv_cache(
     return PKA_ERR_INVALID_ARG;
   if (p->head_dim != 64 && p->head_dim != 128) return PKA_ERR_UNSUPPORTED;
   if (p->kv_ragged) return PKA_ERR_UNSUPPORTED;
-  if (p->num_qo_heads > pka::kMaxHeads || p->num_kv_heads > pka::kMaxHeads)
+  if (p->num_qo_heads > pka::kMaxHeads || p->num_kv_heads > pka::kMaxHeads ||
+      nnz_new > pka::kMaxRows)
     return PKA_ERR_UNSUPPORTED;
   if (!pka::rope_valid(rope, p->head_dim)) return PKA_ERR_INVALID_ARG;
   if (nnz_new == 0 || batch == 0) return PKA_OK;
@@ -535,8 +579,8 @@ pka_status pka_rope_append_paged_kv_cache(
   a.layout = p->layout;
   a.k_scale = p->k_scale > 0.f ? p->k_scale : 1.f;
   a.v_scale = p->v_scale > 0.f ? p->v_scale : 1.f;
-  a.k_inv = pka::pow2_inv(a.k_scale);
-  a.v_inv = pka::pow2_inv(a.v_scale);
+  a.k_inv = pka::reciprocal(a.k_scale);
+  a.v_inv = pka::reciprocal(a.v_scale);
   a.err = pka::device_error_word();
   const bool adjacent = rope->interleaved != 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

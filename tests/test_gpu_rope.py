@@ -298,6 +298,29 @@ def test_append_rotated_e4m3(layout, page_size, d, rotary, interleaved, scales):
                   interleaved=interleaved)
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.3, 0.004, 2.5, 1.0 / 3.0, 7.0, 1e-3, 0.02, 448.0, 1e-20,
+                                   1e-17, 3e30])
+def test_append_e4m3_codes_of_every_bf16_value(scale):
+    """V of every bit pattern, divided by the scale and rounded: the codes that
+    pka_append_paged_kv_cache stores, infinities and NaN among them."""
+    v = np.arange(1 << 16, dtype=np.uint16).reshape(256, 2, 128)
+    k = np.zeros_like(v)
+    params = pka.make_params(8, 2, 128, 16, kv_dtype="e4m3", v_scale=scale)
+    pools = [torch.zeros(16, 16, 2, 128, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    table = [i32(x) for x in ([0, 256], [0, 16], np.arange(16), [16])]
+    pka.pka_rope_append_paged_kv_cache(params, _rope(128)[0], None, None, bf16(k), bf16(v), *table,
+                                       pools[0], pools[1], pools[0].stride(0))
+    pka.pka_append_paged_kv_cache(params, bf16(k), bf16(v), *table, pools[2], pools[3],
+                                  pools[2].stride(0))
+    torch.cuda.synchronize()
+    got = pools[1].cpu().numpy().reshape(v.shape)
+    assert np.array_equal(got, pools[3].cpu().numpy().reshape(v.shape))
+    with np.errstate(all="ignore"):
+        finite = np.isfinite(ref.bf16_bits_to_f64(v))
+        want = ref.quantize_kv_e4m3(v, scale)
+    assert np.array_equal(got[finite], want[finite])
+
+
 def test_append_padded_batch_and_given_positions():
     b = _batch(3, 4, "NHD", 128)
     _check_append(b, dict(scaling="parts"), 128, pad=21, magnitude=1.2)
