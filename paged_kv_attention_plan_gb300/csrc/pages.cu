@@ -818,18 +818,24 @@ __global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
     uint4 x[PIECES];
     if constexpr (SMALL) {
       int64_t put[PIECES];
+      const int64_t at = w * (32 * PIECES) + lane;
+      int64_t i = at <= UINT32_MAX ? (uint32_t)at / pieces : at / pieces;
+      uint32_t piece = (uint32_t)(at - i * pieces);
 #pragma unroll
       for (int u = 0; u < PIECES; ++u) {
-        const int64_t at = w * (32 * PIECES) + u * 32 + lane;
-        put[u] = -1;
-        if (at >= n * pieces) continue;
-        const int64_t i = at <= UINT32_MAX ? (uint32_t)at / pieces : at / pieces;
-        const uint32_t off = (uint32_t)(at - i * pieces) * 16;
         int64_t from, to;
         int slots;
-        if (!copy_at(a, i, &from, &to, &slots, &bad) || !in_slots(a, off, slots)) continue;
-        x[u] = *reinterpret_cast<const uint4*>(pool + from + off);
-        put[u] = to + off;
+        put[u] = -1;
+        if (i < n && copy_at(a, i, &from, &to, &slots, &bad) && in_slots(a, piece * 16, slots)) {
+          x[u] = *reinterpret_cast<const uint4*>(pool + from + piece * 16);
+          put[u] = to + piece * 16;
+        }
+        i += 32 / pieces;  // 32 pieces on
+        piece += 32 % pieces;
+        if (piece >= pieces) {
+          piece -= pieces;
+          ++i;
+        }
       }
 #pragma unroll
       for (int u = 0; u < PIECES; ++u)

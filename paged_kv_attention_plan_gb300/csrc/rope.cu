@@ -118,6 +118,14 @@ __device__ __forceinline__ void store16(uint16_t* p, const uint32_t (&w)[4]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Word w becomes (lo, hi) in bf16 where these are rotated: the first `turned`
+// of the two elements.
+__device__ __forceinline__ void round_turned(uint32_t& w, float lo, float hi, int turned) {
+  if (turned <= 0) return;
+  const uint32_t y = float2_to_bf16x2(lo, hi);
+  w = turned > 1 ? y : (y & 0xffffu) | (w & 0xffff0000u);
+}
+
 __device__ __forceinline__ void to_shared(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -133,14 +141,6 @@ __device__ __forceinline__ void from_shared(const float* p, float (&x)[8]) {
   x[5] = b.y;
   x[6] = b.z;
   x[7] = b.w;
-}
-
-// Element of head h of a slot of a page.
-template <int D>
-__device__ __forceinline__ int64_t pool_offset(const RopeArgs& a, int page, int slot, int h) {
-  return (int64_t)page * a.page_stride +
-         (a.layout == PKA_NHD ? ((int64_t)slot * a.k_heads + h) * D
-                              : ((int64_t)h * a.page_size + slot) * D);
 }
 
 // A warp takes a row, or a part of its heads, and walks the heads (q, then k,
@@ -174,12 +174,13 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
   const int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5);
   if (row >= a.rows) return;
 
-  // where the lane's pieces lie in a head, and which of its pairs rotate
-  int off_a = 8 * u, off_b = 8 * u + D / 2;
+  // where the lane's pieces lie in a head (B `apart` elements behind A), and
+  // which of its pairs rotate
+  int off_a = 8 * u, apart = D / 2;
   if (L == kHalf) {
     const int t = u - rd / 16;
-    off_a = t < 0 ? 8 * u : rd + 16 * t;
-    off_b = t < 0 ? 8 * u + rd / 2 : off_a + 8;
+    if (t >= 0) off_a = rd + 16 * t;
+    apart = t < 0 ? rd / 2 : 8;
   }
   auto pair_of = [&](int j) {
     return L == kHalf ? 8 * u + j
@@ -189,14 +190,6 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
   uint32_t turning = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) turning |= (pair_of(j) < rd / 2 ? 1u : 0u) << j;
-  // the elements of word i of a piece that rotate, as a mask
-  auto word_mask = [&](bool piece_b, int i) {
-    if (L == kHalf) return turning ? ~0u : 0u;
-    if (L == kAdjacent) return turning >> (piece_b ? i + 4 : i) & 1 ? ~0u : 0u;
-    const int e = (piece_b ? off_b : off_a) + 2 * i;
-    return (e < rd ? 0xffffu : 0u) | (e + 1 < rd ? 0xffff0000u : 0u);
-  };
-
   uint64_t turn[K];
 #pragma unroll
   for (int i = 0; i < K; ++i) {
@@ -204,6 +197,11 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
     turn[i] = p < rd / 2 ? a.turns[p] : 0;
   }
 
+  // head h of the row starts at D * h of one of these
+  const int64_t at_q = row * a.q_stride + off_a;
+  const int64_t at_k = row * a.k_stride - (int64_t)a.q_heads * D + off_a;
+  const int64_t at_v = APPEND ? row * a.v_stride - (int64_t)(a.q_heads + a.k_heads) * D + off_a : 0;
+  const int k_end = a.q_heads + a.k_heads;
   const int h0 = blockIdx.y * a.steps_per_part * HPS;
   const int h1 = min(heads, h0 + a.steps_per_part * HPS);
   uint32_t wa[kInFlight][4], wb[kInFlight][4];
@@ -212,15 +210,12 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
     for (int t = 0; t < kInFlight; ++t) {
       const int h = hb + t * HPS + sub;
       if (h >= h1) continue;
-      const uint16_t* src;
-      if (h < a.q_heads)
-        src = a.q + row * a.q_stride + (int64_t)h * D;
-      else if (!APPEND || h < a.q_heads + a.k_heads)
-        src = a.k + row * a.k_stride + (int64_t)(h - a.q_heads) * D;
-      else
-        src = a.v + row * a.v_stride + (int64_t)(h - a.q_heads - a.k_heads) * D;
-      load16(src + off_a, wa[t]);
-      load16(src + off_b, wb[t]);
+      const uint16_t* src = h < a.q_heads               ? a.q + at_q
+                            : !APPEND || h < k_end ? a.k + at_k
+                                                   : a.v + at_v;
+      src += h * D;
+      load16(src, wa[t]);
+      load16(src + apart, wb[t]);
     }
   };
   load(h0);
@@ -275,25 +270,29 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
     }
   }
 
+  // where head h goes: D * h behind out_q, or head_step * (its number) in the pool
+  const int64_t out_q = row * a.q_out_stride + off_a;
+  const int64_t out_k = row * a.k_out_stride - (int64_t)a.q_heads * D + off_a;
+  const int64_t head_step = a.layout == PKA_NHD ? D : (int64_t)a.page_size * D;
+  const int64_t in_pool = (int64_t)page * a.page_stride +
+                          (int64_t)slot * (a.layout == PKA_NHD ? a.k_heads * D : D) + off_a;
+
   for (int hb = h0;;) {
 #pragma unroll
     for (int t = 0; t < kInFlight; ++t) {
       const int h = hb + t * HPS + sub;
-      const bool is_q = h < a.q_heads;
-      const bool is_v = APPEND && h >= a.q_heads + a.k_heads;
-      const bool to_pool = APPEND && !is_q;
+      const bool is_v = APPEND && h >= k_end;
+      const bool to_pool = APPEND && h >= a.q_heads;
       const bool store = h < h1 && !(to_pool && page < 0);
       if (L != kScattered && !store) continue;
       float xa[8], xb[8];
-      if (F8 || !is_v) {
+      if constexpr (L == kScattered) {  // all lanes: the heads of a step meet the barriers together
+        float* m = heads_in_shared + ((threadIdx.x >> 5) * HPS + sub) * STRIDE;
         unpack8(wa[t], xa);
         unpack8(wb[t], xb);
-      }
-      if constexpr (L == kScattered) {  // all lanes: the heads of a step meet the barrier together
-        float* m = heads_in_shared + ((threadIdx.x >> 5) * HPS + sub) * STRIDE;
         if (!is_v) {
           to_shared(m + off_a, xa);
-          to_shared(m + off_b, xb);
+          to_shared(m + off_a + apart, xb);
         }
         __syncwarp();
         if (!is_v) {
@@ -310,50 +309,66 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
         __syncwarp();
         if (!is_v) {
           from_shared(m + off_a, xa);
-          from_shared(m + off_b, xb);
-        }
-        __syncwarp();  // read before the next step writes
-      } else if (!is_v) {
+          from_shared(m + off_a + apart, xb);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          // pair j: (A[j], B[j]), or adjacent elements of A (j < 4) or of B
-          float& x = L == kHalf ? xa[j] : j < 4 ? xa[2 * j] : xb[2 * (j - 4)];
-          float& y = L == kHalf ? xb[j] : j < 4 ? xa[2 * j + 1] : xb[2 * (j - 4) + 1];
-          if (turning >> j & 1) {
-            const float z = x * c[j] - y * s[j];
-            y = x * s[j] + y * c[j];
-            x = z;
+          for (int i = 0; i < 4; ++i) {
+            round_turned(wa[t][i], xa[2 * i], xa[2 * i + 1], rd - (off_a + 2 * i));
+            round_turned(wb[t][i], xb[2 * i], xb[2 * i + 1], rd - (off_a + apart + 2 * i));
           }
         }
-      }
-      if (L == kScattered && !store) continue;
-      const int hh = is_q ? h : is_v ? h - a.q_heads - a.k_heads : h - a.q_heads;
-      if (F8 && to_pool) {
-        const float scale = is_v ? a.v_scale : a.k_scale, inv = is_v ? a.v_inv : a.k_inv;
-        uint8_t* p = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) +
-                     pool_offset<D>(a, page, slot, hh);
-        *reinterpret_cast<uint2*>(p + off_a) = to_e4m3x8(xa, scale, inv);
-        *reinterpret_cast<uint2*>(p + off_b) = to_e4m3x8(xb, scale, inv);
-        continue;
-      }
-      // rotated elements rounded once to bf16; the others keep their bits
-      if (!is_v) {
+        __syncwarp();  // read before the next step writes
+        if (!store) continue;
+      } else if (F8 || (L == kHalf && turning && !is_v)) {
+        unpack8(wa[t], xa);
+        unpack8(wb[t], xb);
+        if (!is_v) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t ma = word_mask(false, i), mb = word_mask(true, i);
-          wa[t][i] = (float2_to_bf16x2(xa[2 * i], xa[2 * i + 1]) & ma) | (wa[t][i] & ~ma);
-          wb[t][i] = (float2_to_bf16x2(xb[2 * i], xb[2 * i + 1]) & mb) | (wb[t][i] & ~mb);
+          for (int j = 0; j < 8; ++j) {
+            // pair j: (A[j], B[j]), or adjacent elements of A (j < 4) or of B
+            float& x = L == kHalf ? xa[j] : j < 4 ? xa[2 * j] : xb[2 * (j - 4)];
+            float& y = L == kHalf ? xb[j] : j < 4 ? xa[2 * j + 1] : xb[2 * (j - 4) + 1];
+            if (L == kHalf ? turning != 0 : (turning >> j & 1) != 0) {
+              const float z = x * c[j] - y * s[j];
+              y = x * s[j] + y * c[j];
+              x = z;
+              if (L == kAdjacent) (j < 4 ? wa[t][j & 3] : wb[t][j & 3]) = float2_to_bf16x2(x, y);
+            }
+          }
+          if (L == kHalf && turning) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              wa[t][i] = float2_to_bf16x2(xa[2 * i], xa[2 * i + 1]);
+              wb[t][i] = float2_to_bf16x2(xb[2 * i], xb[2 * i + 1]);
+            }
+          }
+        }
+      } else if (L == kAdjacent && !is_v) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint32_t& w = j < 4 ? wa[t][j & 3] : wb[t][j & 3];
+          const float2 f = bf16x2_to_float2(w);
+          if (turning >> j & 1)
+            w = float2_to_bf16x2(f.x * c[j] - f.y * s[j], f.x * s[j] + f.y * c[j]);
         }
       }
-      uint16_t* p;
-      if (to_pool)
-        p = static_cast<uint16_t*>(is_v ? a.v_pool : a.k_pool) + pool_offset<D>(a, page, slot, hh);
-      else if (is_q)
-        p = a.q_out + row * a.q_out_stride + (int64_t)hh * D;
-      else
-        p = a.k_out + row * a.k_out_stride + (int64_t)hh * D;
-      store16(p + off_a, wa[t]);
-      store16(p + off_b, wb[t]);
+      // rotated elements are rounded once, to bf16 or to a code; the others keep their bits
+      if (!to_pool) {
+        uint16_t* p = (h < a.q_heads ? a.q_out + out_q : a.k_out + out_k) + h * D;
+        store16(p, wa[t]);
+        store16(p + apart, wb[t]);
+        continue;
+      }
+      const int64_t at = in_pool + (h - (is_v ? k_end : a.q_heads)) * head_step;
+      if constexpr (F8) {
+        const float scale = is_v ? a.v_scale : a.k_scale, inv = is_v ? a.v_inv : a.k_inv;
+        uint8_t* p = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) + at;
+        *reinterpret_cast<uint2*>(p) = to_e4m3x8(xa, scale, inv);
+        *reinterpret_cast<uint2*>(p + apart) = to_e4m3x8(xb, scale, inv);
+      } else {
+        uint16_t* p = static_cast<uint16_t*>(is_v ? a.v_pool : a.k_pool) + at;
+        store16(p, wa[t]);
+        store16(p + apart, wb[t]);
+      }
     }
     hb += kInFlight * HPS;
     if (hb >= h1) break;
