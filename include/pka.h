@@ -391,7 +391,9 @@ pka_status pka_rope_append_paged_kv_cache(
  * chosen are always the lowest free ones, so results do not depend on timing.
  * Violations that only the device can see are stepped around and noted in the
  * device error word (pka_get_device_error; of several the largest code stays).
- * Two calls on one page_refs_d must be ordered (one stream, or events). */
+ * Two calls on one page_refs_d must be ordered (one stream, or events): a call
+ * may keep its own marks in the counts of free pages until it ends.  Counts
+ * are never negative. */
 
 /* Copy pages inside the pools, for every layer at once: for i < the count,
  * slots 0 .. slots_d[i] - 1 (all when slots_d is NULL) of page src_d[i] over
@@ -444,7 +446,8 @@ pka_status pka_free_pages(int32_t* page_refs_d, int32_t num_pages, const int32_t
  *   pages refuse the whole call on the device: nothing but counts_d = {-1, -1}
  *   is written and PKA_ERR_METADATA or PKA_ERR_WORKSPACE is noted.  Page ids
  *   outside [0, num_pages) in a parent's table are carried over and noted.
- *   The parents' pages must be held (a reference at least).
+ *   The parents' pages must be held (a reference at least), and no two arrays
+ *   of the call may overlap (the children's tables are not written in place).
  *   PKA_ERR_UNSUPPORTED: more than PKA_MAX_FORK_CHILDREN children. */
 #define PKA_MAX_FORK_CHILDREN 8192
 pka_status pka_fork_pages(int32_t page_size, int32_t* page_refs_d, int32_t num_pages,
@@ -502,7 +505,8 @@ pka_status pka_run_static_scratch(pka_plan_t plan, const pka_params* params, con
 const char* pka_last_error(void);
 
 /* Read and clear the device error word written by kernels that gave up on a
- * barrier (0 = none, else a pka_status).  Synchronises `stream`. */
+ * barrier, and by the calls that note violations only the device can see
+ * (0 = none, else a pka_status).  Synchronises `stream`. */
 pka_status pka_get_device_error(int32_t* code, void* stream);
 
 /* Host check of a page table ("Deep Dive - FlashInfer", "Where FlashInfer

@@ -14,15 +14,13 @@ from ._pka import (PKA_HND, PKA_KV_BF16, PKA_KV_FP8_E4M3, PKA_MASK_CAUSAL,  # no
                    PKA_MASK_CUSTOM, PKA_MASK_NONE, PKA_NHD,
                    PKA_ROPE_BY_PARTS, PKA_ROPE_LINEAR, PKA_ROPE_PLAIN,
                    PKA_SPLIT_AUTO, PKA_SPLIT_FIXED, PKA_SPLIT_OFF, PkaError, make_params,
-                   make_rope,
-                   pka_append_paged_kv_cache, pka_get_device_error, pka_last_error, pka_merge_states,
+                   make_rope, pka_alloc_pages, pka_append_paged_kv_cache, pka_apply_rope,
+                   pka_check_indices, pka_compact_pages, pka_copy_pages, pka_fork_pages,
+                   pka_free_pages, pka_get_device_error, pka_last_error, pka_merge_states,
                    pka_packbits, pka_plan, pka_plan_cascade, pka_plan_create, pka_plan_destroy,
-                   pka_plan_get_info,
-                   pka_plan_wait, pka_run, pka_run_static_scratch, pka_status_str, pka_validate, pka_version,
-                   pka_check_indices, pka_selftest_bounded_wait,
-                   pka_apply_rope, pka_rope_append_paged_kv_cache, pka_rope_init,
-                   pka_alloc_pages, pka_compact_pages, pka_copy_pages, pka_fork_pages,
-                   pka_free_pages)
+                   pka_plan_get_info, pka_plan_wait, pka_rope_append_paged_kv_cache,
+                   pka_rope_init, pka_run, pka_run_static_scratch, pka_selftest_bounded_wait,
+                   pka_status_str, pka_validate, pka_version)
 
 __all__ = ["BatchAttention", "make_params", "make_rope", "PkaError"] + [n for n in _pka.EXPORTED]
 

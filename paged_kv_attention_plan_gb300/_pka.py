@@ -475,10 +475,11 @@ def pka_apply_rope(rope, positions, q=None, q_out=None, k=None, k_out=None, tran
                    stream=None, check=True) -> int:
     """Rotate q and / or k ([rows, heads, head_dim], rows at any stride) into
     q_out and k_out, which may be q and k themselves."""
-    if q is None and k is None:
-        raise ValueError("pka_apply_rope: q or k")
+    some = q if q is not None else k
+    if not isinstance(some, torch.Tensor) or some.dim() != 3:
+        raise ValueError("q and k must be [rows, heads, head_dim], one of them given")
     dev = torch.cuda.current_device()
-    rows, hq, dim = (q if q is not None else k).shape
+    rows, hq, dim = some.shape
     hk = 0
     qp = qo = kp = ko = None
     qs = qos = ks = kos = 0
@@ -488,7 +489,7 @@ def pka_apply_rope(rope, positions, q=None, q_out=None, k=None, k_out=None, tran
     else:
         hq = 0
     if k is not None:
-        hk = k.shape[1]
+        hk = k.shape[-2]
         kp, ks = _here_rows(k, "k", dev, rows, hk, dim)
         ko, kos = (kp, ks) if k_out is k else _here_rows(k_out, "k_out", dev, rows, hk, dim)
     pos = _here(positions, "positions", _I32, dev)
@@ -570,7 +571,8 @@ def pka_alloc_pages(page_refs, pages, stream=None, check=True) -> int:
     """Take as many pages as `pages` has room for."""
     dev, i32 = torch.cuda.current_device(), _I32
     s = lib().pka_alloc_pages(_here(page_refs, "page_refs", i32, dev), page_refs.numel(),
-                              pages.numel(), _here(pages, "pages", i32, dev), _here_stream(stream, dev))
+                              pages.numel(), _here(pages, "pages", i32, dev),
+                              _here_stream(stream, dev))
     if check and s:
         _check(s, "pka_alloc_pages")
     return s
@@ -579,7 +581,8 @@ def pka_alloc_pages(page_refs, pages, stream=None, check=True) -> int:
 def pka_free_pages(page_refs, pages, stream=None, check=True) -> int:
     dev, i32 = torch.cuda.current_device(), _I32
     s = lib().pka_free_pages(_here(page_refs, "page_refs", i32, dev), page_refs.numel(),
-                             _here(pages, "pages", i32, dev), pages.numel(), _here_stream(stream, dev))
+                             _here(pages, "pages", i32, dev), pages.numel(),
+                             _here_stream(stream, dev))
     if check and s:
         _check(s, "pka_free_pages")
     return s

@@ -20,7 +20,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kMaxCluster = 16;     // blocks of the largest counting launch
+constexpr int kMaxCluster = 16;  // blocks of the largest counting launch
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr unsigned kAll = 0xffffffffu;
@@ -40,7 +40,7 @@ __device__ __forceinline__ void after_previous() { cudaGridDependencySynchronize
 // first): row i of tiles is tiles i * warps .. i * warps + warps - 1, one a
 // warp, at most kRows rows.
 constexpr int kRows = 32;
-constexpr uint32_t kTile = 512;  // of one row: less, where that suffices; of more: multiples
+constexpr uint32_t kTile = 512;  // pages; less where one row suffices, else multiples of it
 
 struct Share {
   uint32_t lo, hi;  // the pages of this warp's tile
@@ -633,9 +633,10 @@ struct CompactArgs {
 // below L: as many of the one as of the other.  Before page p lie r(p) live
 // pages (one pass of counting), so the free page p < L is number p - r(p) of
 // its kind from below and the live page p >= L number L - 1 - r(p) of its kind
-// from above; equal numbers pair up.  This launch writes the two lists by
+// from above; equal numbers pair up.  number_tile writes the two lists by
 // those numbers; a moving page's entry of the map holds -2 - number until
-// move_kernel, which needs both lists whole, turns it into the new id.
+// move_kernel, which needs both lists whole, turns it into the new id.  `rank`
+// is r of the tile's first page, `live` is L.
 __device__ __forceinline__ void number_tile(const CompactArgs& a, const Share& s, int rank,
                                             int live) {
   const bool apart = a.refs != a.refs_out;
@@ -1042,6 +1043,7 @@ pka_status pka_fork_pages(int32_t page_size, int32_t* page_refs_d, int32_t num_p
   if (parents || children || (num_indices > 0 && !kv_indices_d) ||
       (num_child_indices > 0 && !child_indices_d) || (num_pages > 0 && !page_refs_d))
     return PKA_ERR_INVALID_ARG;
+  if (num_child_indices > 0 && child_indices_d == kv_indices_d) return PKA_ERR_INVALID_ARG;
   const void* arrays[] = {page_refs_d,    kv_indptr_d,     kv_indices_d, last_page_len_d,
                           parent_d,       child_indptr_d,  child_indices_d, copy_src_d,
                           copy_dst_d,     copy_slots_d};
@@ -1092,7 +1094,8 @@ pka_status pka_compact_pages(const int32_t* page_refs_d, int32_t num_pages,
                              int32_t* counts_d, void* stream) {
   if (num_pages < 0 || num_indices < 0) return PKA_ERR_INVALID_ARG;
   if (!counts_d || pka::unaligned(counts_d)) return PKA_ERR_INVALID_ARG;
-  if (num_pages > 0 && (!page_refs_d || !page_refs_out_d || !page_map_d)) return PKA_ERR_INVALID_ARG;
+  if (num_pages > 0 && (!page_refs_d || !page_refs_out_d || !page_map_d))
+    return PKA_ERR_INVALID_ARG;
   if (num_pages > 1 && (!copy_src_d || !copy_dst_d)) return PKA_ERR_INVALID_ARG;
   if (num_indices > 0 && (!kv_indices_d || !kv_indices_out_d)) return PKA_ERR_INVALID_ARG;
   const void* arrays[] = {page_refs_d, kv_indices_d, page_refs_out_d, kv_indices_out_d,
@@ -1113,10 +1116,16 @@ pka_status pka_compact_pages(const int32_t* page_refs_d, int32_t num_pages,
   a.num_indices = num_indices;
   a.num_pages = num_pages;
   a.tiling = pka::tiling_of(num_pages);
-  cudaError_t e = num_pages == 0
-                      ? cudaMemsetAsync(counts_d, 0, 8, st)
-                      : pka::launch_cluster<pka::compact_kernel>(pka::cluster_ctas(num_pages), 0,
-                                                                 st, a);
+  if (num_pages == 0) {  // every entry names a page that is not there
+    cudaError_t e = cudaMemsetAsync(counts_d, 0, 8, st);
+    if (e == cudaSuccess && num_indices > 0) {
+      pka::move_kernel<<<pka::blocks_for(num_indices, 256, 8), 256, 0, st>>>(a);
+      e = cudaGetLastError();
+    }
+    return pka::done(e, "page compact launch");
+  }
+  cudaError_t e =
+      pka::launch_cluster<pka::compact_kernel>(pka::cluster_ctas(num_pages), 0, st, a);
   if (e != cudaSuccess) return pka::cuda_failure(e, "page compact launch");
   if (a.tiling.rows > 1) {
     const int64_t tiles = (num_pages + (int64_t)a.tiling.tile - 1) / a.tiling.tile;
@@ -1124,7 +1133,7 @@ pka_status pka_compact_pages(const int32_t* page_refs_d, int32_t num_pages,
     if (e != cudaSuccess) return pka::cuda_failure(e, "page numbering launch");
   }
   const int64_t work = num_indices > num_pages / 2 ? num_indices : num_pages / 2;
-  if (work == 0) return PKA_OK;
+  if (work == 0) return PKA_OK;  // one page, no entry: nothing moves
   return pka::done(pka::launch_behind(pka::move_kernel, pka::blocks_for(work, 256, 8), st, a),
                    "page move launch");
 }

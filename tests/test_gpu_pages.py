@@ -310,6 +310,16 @@ def test_compact_matches_the_list_walk(n, live, in_place):
     assert pka.pka_get_device_error() == 0
 
 
+def test_compact_of_an_empty_pool():
+    empty, t = torch.empty(0, dtype=torch.int32, device="cuda"), i32([0, 4])
+    counts = i32([5, 5])
+    pka.pka_compact_pages(empty, t, empty, t, empty, empty, empty, counts)
+    assert _host(counts).tolist() == [0, 0] and _host(t).tolist() == [0, 4]
+    assert pka.pka_get_device_error() == METADATA
+    pka.pka_compact_pages(empty, empty, empty, empty, empty, empty, empty, counts)
+    assert pka.pka_get_device_error() == 0
+
+
 def test_compact_leaves_and_notes_entries_of_no_live_page():
     refs = np.array([0, 2, 0, 1, 0, 1], np.int32)
     d, t = i32(refs), i32([1, 3, 0, -4, 6, 5])
@@ -392,6 +402,49 @@ def test_copy_counts_from_the_device_and_skips():
     assert pka.pka_get_device_error() == METADATA
     assert np.array_equal(run(src, dst, slots=[4, -1, 5, 2]), want([0, 3], [8, 11], [4, 2]))
     assert pka.pka_get_device_error() == METADATA
+
+
+def test_binding_refuses_what_it_cannot_pass(monkeypatch):
+    """Shapes, types, layouts and devices that never reach the library."""
+    def t(*shape, dtype=torch.int32):
+        return torch.zeros(*shape, dtype=dtype, device="cuda")
+    bf = torch.bfloat16
+    params, rope = pka.make_params(2, 2, 64, 4), pka.make_rope(64)
+    k, ids, q = t(3, 5, 4, 2, 64, dtype=bf), t(2), t(6, 2, 64, dtype=bf)
+    calls = [
+        (ValueError, lambda: pka.pka_copy_pages(params, k, k[:, :4], ids, ids)),
+        (ValueError, lambda: pka.pka_copy_pages(params, k, k, ids, t(3))),
+        (ValueError, lambda: pka.pka_copy_pages(params, k.transpose(2, 3), k.transpose(2, 3), ids,
+                                                ids)),
+        (TypeError, lambda: pka.pka_copy_pages(params, k.float(), k.float(), ids, ids)),
+        (TypeError, lambda: pka.pka_copy_pages(params, k, k, ids.long(), ids.long())),
+        (TypeError, lambda: pka.pka_copy_pages(params, k.cpu(), k.cpu(), ids, ids)),
+        (TypeError, lambda: pka.pka_alloc_pages(t(4).cpu(), ids)),
+        (ValueError, lambda: pka.pka_alloc_pages(t(8)[::2], ids)),
+        (ValueError, lambda: pka.pka_fork_pages(4, t(9), t(2), t(3), t(2), ids, t(3), t(4), ids,
+                                                ids, ids, t(2))),
+        (ValueError, lambda: pka.pka_fork_pages(4, t(9), t(2), t(3), t(1), ids, t(3), t(4), t(1),
+                                                ids, ids, t(2))),
+        (ValueError, lambda: pka.pka_compact_pages(t(9), t(3), t(8), t(3), t(9), t(4), t(4), t(2))),
+        (ValueError, lambda: pka.pka_compact_pages(t(9), t(3), t(9), t(3), t(9), t(3), t(4), t(2))),
+        (ValueError, lambda: pka.pka_apply_rope(rope, t(6))),
+        (ValueError, lambda: pka.pka_apply_rope(rope, t(5), q, q)),
+        (ValueError, lambda: pka.pka_apply_rope(rope, t(6), q, t(6, 3, 64, dtype=bf))),
+        (ValueError, lambda: pka.pka_apply_rope(rope, t(6), q.transpose(0, 1), q)),
+        (TypeError, lambda: pka.pka_apply_rope(rope, t(6), q.half(), q)),
+        (TypeError, lambda: pka.pka_apply_rope(rope, t(6), q, None)),
+        (ValueError, lambda: pka.pka_rope_append_paged_kv_cache(
+            params, rope, None, None, q, q, t(3), t(2), t(1), t(1), k[0], k[1], k.stride(1))),
+    ]
+    for error, call in calls:
+        with pytest.raises(error):
+            call()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (lambda: pka.pka_free_pages(t(4), ids),
+                 lambda: pka.pka_apply_rope(rope, t(6), q, q),
+                 lambda: pka.pka_copy_pages(params, k, k, ids, ids)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
 
 
 def test_copy_and_append_past_32_bit_offsets():

@@ -61,7 +61,7 @@ def test_free_refusals(refs, pages, ids, n, want):
 
 
 def _fork(P=4, refs=A, pages=10, parents=2, ptr=A, idx=A, n_idx=5, last=A, children=3, parent=A,
-          child=A, table=A, n_table=9, src=A, dst=A, slots=A, counts=A):
+          child=A, table=2 * A, n_table=9, src=A, dst=A, slots=A, counts=A):
     return _pka.lib().pka_fork_pages(P, refs, pages, parents, ptr, idx, n_idx, last, children,
                                      parent, child, table, n_table, src, dst, slots, counts, None)
 
@@ -73,7 +73,8 @@ def _fork(P=4, refs=A, pages=10, parents=2, ptr=A, idx=A, n_idx=5, last=A, child
     (dict(idx=None), INVALID), (dict(last=None), INVALID), (dict(parent=None), INVALID),
     (dict(child=None), INVALID), (dict(table=None), INVALID), (dict(src=None), INVALID),
     (dict(dst=None), INVALID), (dict(slots=None), INVALID), (dict(counts=None), INVALID),
-    (dict(table=A + 2), INVALID), (dict(counts=A + 1), INVALID)])
+    (dict(table=A + 2), INVALID), (dict(counts=A + 1), INVALID),
+    (dict(idx=2 * A), INVALID)])  # tables written over the parents' own
 def test_fork_refusals(kw, want):
     assert _fork(**kw) == want
 

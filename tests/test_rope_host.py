@@ -119,7 +119,8 @@ def test_append_refuses_bad_params():
     assert _append(params=p(page_size=0)) == INVALID
     assert _append(params=p(layout=7)) == INVALID
     assert _append(params=p(kv_dtype="e4m3"), stride=4104) == INVALID
-    assert _append(rope=pka.make_rope(128), params=p(head_dim=64), qs=512, ks=128, vs=128) == INVALID
+    assert _append(rope=pka.make_rope(128), params=p(head_dim=64), qs=512, ks=128,
+                   vs=128) == INVALID
 
 
 def test_binding_refuses_host_tensors(monkeypatch):
