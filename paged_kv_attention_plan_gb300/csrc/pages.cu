@@ -251,9 +251,11 @@ struct AllocArgs {
   Tiling tiling;
 };
 
-// From this many pages on, and with more than a row of tiles, they are taken
-// by a launch of their own.
-constexpr int kTakeInPlace = 8192;
+// More pages than these, in a pool of more than a row of tiles, are taken by a
+// launch of their own.  Taken from 1,500,007 pages and returned, in us, in
+// place / in a second launch: 8,192 pages 11.4 / 11.9, 32,768 11.6 / 12.1,
+// 131,072 17.4 / 15.0.
+constexpr int kTakeInPlace = 65536;
 
 // SPLIT: the taking is left to take_kernel, over the whole GPU.  Each tile's
 // count before it travels in the tile's first free page, whose reference count
@@ -426,10 +428,11 @@ __device__ __forceinline__ int find_between(const int32_t* ptr, int lo, int hi, 
   return lo;
 }
 
-// Shared entries of a table are written by the launch that takes the fresh
-// pages when there are at most this many entries (8 a thread of 8 blocks);
-// past it they go to a launch over the whole GPU.
-constexpr int kShareInTake = 65536;
+// At most this many entries are shared by the launch that takes the fresh
+// pages; more go to a launch over the whole GPU.  Fork and return, in us, in
+// one / in two launches: 4,004 entries 8.9 / 9.1, 16,008 9.6 / 9.6, 64,016
+// 14.8 / 10.5, 917,760 67 / 23.
+constexpr int kShareInTake = 4096;
 
 // Checks every child, takes the lowest free pages for all of them and writes
 // the entries that these fill, the copy list and the counts; nothing at all
@@ -540,7 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
 // References that an entry of child c adds.  Children of one parent share the
 // same pages, so where that saves atomics (a parent of kLongTable pages or
 // more; few enough children to look through) the first of its children adds
-// for all of them and the others nothing.
+// for all of them and the others nothing (64 tables of 3,584 pages into 256 and
+// back: 23.0 us against 25.7).
 constexpr int kLongTable = 256, kFewChildren = 1024;
 
 __device__ __forceinline__ int adds_of(const ForkArgs& a, int c, const Child& ch, int lane) {
@@ -717,7 +721,8 @@ __global__ void __launch_bounds__(256) move_kernel(const CompactArgs a) {
 // One row of tiles is numbered where it was counted.  More are too much for
 // the cluster's few blocks: they go to number_kernel, each tile's count before
 // it in the map entry of its first page (which that tile alone reads and
-// overwrites) and L in counts[1].  500,009 pages: 14.4 us in one launch.
+// overwrites) and L in counts[1].  500,009 pages: 14.4 us in this launch, 9.8
+// in the two, which overlap with the next.
 __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs a) {
   __shared__ Counts c;
   start_next();
@@ -801,8 +806,11 @@ __device__ __forceinline__ bool copy_at(const CopyArgs& a, int64_t i, int64_t* f
 }
 
 // blockIdx.y is (layer, K or V).  A warp moves 4 KB, eight 16-byte pieces a
-// lane in flight: a stretch of one page, or (SMALL: pages below 4 KB) pieces
-// of as many pages as that takes, each lane with its own list entries.
+// lane in flight: a stretch of one page, or (SMALL) pieces of as many pages as
+// that takes, each lane with its own list entries.  Bound by memory bandwidth:
+// 4,001 pages of 32 KB, K and V in four layers, take 310 us, 6.77 TB/s.  In us,
+// a stretch / SMALL: 60,000 pages of 64 B 18.9 / 5.7, of 1 KB 44.9 / 39.9, of
+// 2 KB 76.4 / 76.5, 20,000 of 8 KB 100.1 / 100.0.
 template <bool SMALL>
 __global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
   constexpr int PIECES = 8, CHUNK = PIECES * 512;
@@ -870,12 +878,11 @@ int blocks_for(int64_t work, int per_block, int per_sm) {
 }
 
 // Blocks of a launch that counts the references of num_pages pages.  Taking
-// one page and returning it takes, in us, with 1 / 8 / 16 blocks: 4.5 / 5.5 /
-// 6.1 in a pool of 8,192 pages, 6.6 / 5.5 / 6.4 in 131,072, 14 / 6.8 / 7.1 in
-// 500,000 and 32 / 9.1 / 9.0 in 1,500,007 (two launches, both in it).
-int cluster_ctas(int32_t num_pages) {
-  return num_pages <= 16384 ? 1 : num_pages <= 262144 ? 8 : kMaxCluster;
-}
+// one page / an 11th of them and returning it, in us, with 1 and with 16
+// blocks: pool of 1,024 4.1 / 4.1 and 4.7 / 4.8, 8,192 4.3 / 5.4 and 5.0 / 6.3,
+// 32,768 5.3 / 7.6 and 5.6 / 6.6, 131,072 8.9 / 13.5 and 5.6 / 7.2, 1,500,007
+// 46 / 63 and 9.0 / 14.3.  Compacting 16,384: 9.4 and 7.2.
+int cluster_ctas(int32_t num_pages) { return num_pages <= 8192 ? 1 : kMaxCluster; }
 
 Tiling tiling_of(int32_t num_pages) {
   const uint64_t warps = (uint64_t)cluster_ctas(num_pages) * kWarps, n = (uint64_t)num_pages;
@@ -891,7 +898,7 @@ Tiling tiling_of(int32_t num_pages) {
 // Launch as one cluster.
 template <auto Kernel, class A>
 cudaError_t launch_cluster(int ctas, int smem, cudaStream_t stream, const A& args) {
-  if (ctas > 8) {  // past the portable size: allowed once per device
+  if (ctas > 1) {  // past the portable size of 8: allowed once per device
     static std::atomic<bool> set[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -980,7 +987,7 @@ pka_status pka_copy_pages(const pka_params* p, int32_t num_layers, void* k, void
   a.slot_row = (int32_t)slot_row;
   a.err = pka::device_error_word();
   const int64_t page = p->page_size * slot_row;
-  const bool small = page < 4096;
+  const bool small = page < 2048;
   const int64_t units = small ? (max_copies * page + 4095) / 4096
                               : max_copies * ((page + 4095) / 4096);
   const int per_sm = 16 / (2 * num_layers) > 1 ? 16 / (2 * num_layers) : 1;
