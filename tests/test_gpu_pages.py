@@ -263,6 +263,22 @@ def test_fork_carries_a_bad_page_over_and_notes_it():
     assert pka.pka_get_device_error() == METADATA
 
 
+@pytest.mark.parametrize("length,children", [(40, 6), (900, 30)])
+def test_fork_of_parents_that_share_pages(length, children):
+    """Parents with a common prefix (already forked once), one page listed twice
+    in a table: every entry of every child is one reference more."""
+    rng = np.random.default_rng(length)
+    pool = 20 * length
+    lens = np.array([length, length, length + 3])
+    indptr, ids, last = _parents(rng, lens, 1, pool)
+    ids[indptr[1]:indptr[1] + length // 2] = ids[:length // 2]
+    ids[indptr[2]:indptr[2] + length // 3] = ids[:length // 3]
+    ids[indptr[2] + length // 3] = ids[0]
+    refs = np.bincount(ids, minlength=pool).astype(np.int32)
+    parent = rng.integers(0, 3, children).astype(np.int32)
+    _check_fork(1, refs, lens, indptr, ids, last, parent, lens[parent] + 2)
+
+
 def test_fork_of_nothing():
     refs = i32([1, 0])
     empty = torch.empty(0, dtype=torch.int32, device="cuda")
@@ -307,6 +323,36 @@ def test_compact_matches_the_list_walk(n, live, in_place):
     assert np.all(got[m:] == -5)
     if not in_place:
         assert np.array_equal(_host(d), refs) and np.array_equal(_host(t), idx)
+    assert pka.pka_get_device_error() == 0
+
+
+@pytest.mark.parametrize("n", [700, 300_001])
+def test_arrays_at_any_4_byte_address(n):
+    """Arrays that start 4, 8 and 12 bytes past a 16-byte boundary."""
+    rng = np.random.default_rng(n)
+    refs = _refs(rng, n, n // 2)
+
+    def off(a, by):
+        return i32(np.concatenate([np.full(by, -77), a]))[by:]
+
+    for by in (1, 2, 3):
+        d, out, page_map = off(refs, by), off(np.zeros(n), by), off(np.zeros(n), 4 - by)
+        table = off(np.flatnonzero(refs), by)
+        src, dst = (off(np.zeros(n // 2), by) for _ in range(2))
+        counts = off(np.zeros(2), by)
+        pka.pka_compact_pages(d, table, out, table, page_map, src, dst, counts)
+        w_refs, w_to, w_map, moves, live = cache.compact_pages(refs, np.flatnonzero(refs))
+        assert np.array_equal(_host(out), w_refs) and np.array_equal(_host(table), w_to)
+        assert np.array_equal(_host(page_map), w_map)
+        assert _host(counts).tolist() == [len(moves), live]
+        assert np.array_equal(np.stack(_host(src, dst), 1)[:len(moves)],
+                              np.array(moves, np.int32).reshape(-1, 2))
+        pages = off(np.zeros(n // 3), by)
+        pka.pka_alloc_pages(d, pages)
+        want = np.flatnonzero(refs == 0)[:n // 3]
+        assert np.array_equal(_host(pages), want)
+        pka.pka_free_pages(d, pages)
+        assert np.array_equal(_host(d), refs)
     assert pka.pka_get_device_error() == 0
 
 
@@ -559,6 +605,59 @@ def test_fork_append_attend_return_compact_attend(layout, page, kv):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
     pka.pka_free_pages(r, table)
     assert not _host(r).any()
+    assert pka.pka_get_device_error() == 0
+
+
+def test_calls_at_once_on_streams_and_graphs():
+    """Takes and compactions of two pools at the same time, on two streams and
+    from two captured graphs: no call keeps anything another could meet."""
+    rng = np.random.default_rng(13)
+    pools = [_refs(rng, n, n // 2) for n in (300_000, 400_000)]
+    work = []
+    for refs in pools:
+        r = i32(refs)
+        d = dict(r=r, pages=torch.empty(100_000, dtype=torch.int32, device="cuda"),
+                 out=torch.empty_like(r), table=i32(np.flatnonzero(refs)),
+                 map=torch.empty_like(r), counts=i32([0, 0]), stream=torch.cuda.Stream())
+        d["to"] = torch.empty_like(d["table"])
+        d["src"], d["dst"] = (torch.empty(len(refs) // 2, dtype=torch.int32, device="cuda")
+                              for _ in range(2))
+        work.append(d)
+
+    def step(d):
+        pka.pka_alloc_pages(d["r"], d["pages"], stream=d["stream"])
+        pka.pka_free_pages(d["r"], d["pages"], stream=d["stream"])
+        pka.pka_compact_pages(d["r"], d["table"], d["out"], d["to"], d["map"], d["src"], d["dst"],
+                              d["counts"], stream=d["stream"])
+
+    def check():
+        torch.cuda.synchronize()
+        for refs, d in zip(pools, work):
+            assert np.array_equal(_host(d["r"]), refs)
+            assert np.array_equal(_host(d["pages"]), np.flatnonzero(refs == 0)[:100_000])
+            w_refs, w_to, w_map, moves, live = cache.compact_pages(refs, np.flatnonzero(refs))
+            assert np.array_equal(_host(d["out"]), w_refs)
+            assert np.array_equal(_host(d["to"]), w_to) and np.array_equal(_host(d["map"]), w_map)
+            assert _host(d["counts"]).tolist() == [len(moves), live]
+            for name in ("pages", "out", "to", "map"):
+                d[name].fill_(-9)
+
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for d in work:
+            step(d)
+    check()
+    graphs = [torch.cuda.CUDAGraph() for _ in work]
+    for d, g in zip(work, graphs):
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=d["stream"]):
+            step(d)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for d, g in zip(work, graphs):
+            with torch.cuda.stream(d["stream"]):
+                g.replay()
+    check()
     assert pka.pka_get_device_error() == 0
 
 

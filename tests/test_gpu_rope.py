@@ -102,6 +102,24 @@ def test_row_and_head_counts(rows, hq, hk):
             _assert_rotated(bits_of(y), x, pos, freqs, interleaved=False)
 
 
+def test_no_rows():
+    """Calls without rows, or without requests, do nothing."""
+    rope, _ = _rope(64)
+    q, pos = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda"), i32([])
+    pka.pka_apply_rope(rope, pos, q, q, q, q)
+    params = pka.make_params(4, 4, 64, 4)
+    pool = torch.zeros(3, 4, 4, 64, dtype=torch.bfloat16, device="cuda")
+    table = [i32(x) for x in ([0, 0], [0, 1], [2], [3])]
+    pka.pka_rope_append_paged_kv_cache(params, rope, q, q, q, q, *table, pool, pool, pool.stride(0))
+    one = torch.ones(1, 4, 64, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros_like(one)
+    for t in (table, [i32(x) for x in ([0], [0], [], [])]):  # a padded row of no request
+        pka.pka_rope_append_paged_kv_cache(params, rope, one, out, one, one, *t, pool, pool,
+                                           pool.stride(0))
+    torch.cuda.synchronize()
+    assert not pool.any() and not out.any() and pka.pka_get_device_error() == 0
+
+
 @pytest.mark.parametrize("scaling", ["none", "linear", "parts"])
 def test_far_positions_and_scaling(scaling):
     """Angles of positions up to the largest int32, and of negative ones."""
