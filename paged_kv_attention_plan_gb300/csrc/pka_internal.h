@@ -5,6 +5,7 @@
 
 #include <atomic>
 #include <cstring>
+#include <mutex>
 
 #include "pka.h"
 #include "pka_plan_image.h"
@@ -81,21 +82,21 @@ struct MapCache {
 
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) for `Kernel` only when
 // the current device has not yet been given at least `bytes` (a larger limit
-// set earlier covers every smaller launch).
+// set earlier covers every smaller launch).  Limits are set one at a time and
+// only ever raised, so a record never says more than the device allows.
 template <auto Kernel>
 cudaError_t ensure_dynamic_smem(int bytes) {
   static std::atomic<int> set[64];
+  static std::mutex mu;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const bool tracked = dev >= 0 && dev < 64;
   if (tracked && set[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+  std::lock_guard<std::mutex> lock(mu);
+  if (tracked && set[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && tracked) {
-    int cur = set[dev].load(std::memory_order_relaxed);
-    while (cur < bytes && !set[dev].compare_exchange_weak(cur, bytes, std::memory_order_acq_rel)) {
-    }
-  }
+  if (e == cudaSuccess && tracked) set[dev].store(bytes, std::memory_order_release);
   return e;
 }
 
