@@ -392,8 +392,10 @@ pka_status pka_rope_append_paged_kv_cache(
  * Violations that only the device can see are stepped around and noted in the
  * device error word (pka_get_device_error; of several the largest code stays).
  * Two calls on one page_refs_d must be ordered (one stream, or events): a call
- * may keep its own marks in the counts of free pages until it ends.  Counts
- * are never negative. */
+ * may keep its own marks in the counts of free pages until it ends.  Host
+ * threads may share such a stream: the launches of a call follow one another.
+ * Between calls counts are never negative.  After PKA_ERR_CUDA, which may come
+ * between two launches, the counts and outputs of the call are undefined. */
 
 /* Copy pages inside the pools, for every layer at once: for i < the count,
  * slots 0 .. slots_d[i] - 1 (all when slots_d is NULL) of page src_d[i] over

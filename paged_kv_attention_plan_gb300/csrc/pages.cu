@@ -11,6 +11,7 @@
 #include <cooperative_groups.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "pka_cache.h"
 #include "pka_internal.h"
@@ -946,6 +947,16 @@ pka_status done(cudaError_t e, const char* where) {
 
 bool unaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; }
 
+// Held by every call on an array of counts while it launches.  A large take
+// keeps marks in the counts between its two launches, and a compaction relies
+// on what it counted until its last one, so no other thread's call on the array
+// may come between them in the stream that the threads share.
+std::mutex& launches_of(const int32_t* refs) {
+  static std::mutex table[64];
+  const uint64_t a = reinterpret_cast<uintptr_t>(refs) >> 8;
+  return table[(a ^ a >> 6 ^ a >> 12 ^ a >> 18) % 64];
+}
+
 }  // namespace
 }  // namespace pka
 
@@ -1011,6 +1022,7 @@ pka_status pka_alloc_pages(int32_t* page_refs_d, int32_t num_pages, int32_t n, i
                          pka::tiling_of(num_pages)};
   const int ctas = pka::cluster_ctas(num_pages);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const std::lock_guard<std::mutex> lock(pka::launches_of(page_refs_d));
   if (a.tiling.rows == 1 || n <= pka::kTakeInPlace)
     return pka::done(pka::launch_cluster<pka::alloc_kernel<false>>(ctas, 0, st, a),
                      "page alloc launch");
@@ -1026,6 +1038,7 @@ pka_status pka_free_pages(int32_t* page_refs_d, int32_t num_pages, const int32_t
   if (n == 0) return PKA_OK;
   if (!page_refs_d || !pages_d || pka::unaligned(page_refs_d) || pka::unaligned(pages_d))
     return PKA_ERR_INVALID_ARG;
+  const std::lock_guard<std::mutex> lock(pka::launches_of(page_refs_d));
   pka::free_kernel<<<pka::blocks_for(n, 256, 8), 256, 0, static_cast<cudaStream_t>(stream)>>>(
       page_refs_d, num_pages, pages_d, n, pka::device_error_word());
   return pka::done(cudaGetLastError(), "page free launch");
@@ -1080,6 +1093,7 @@ pka_status pka_fork_pages(int32_t page_size, int32_t* page_refs_d, int32_t num_p
   a.tiling = pka::tiling_of(num_pages);
   const int smem = (pka::kChildWords * num_children + 1) * (int)sizeof(int32_t);
   const int ctas = pka::cluster_ctas(num_pages);
+  const std::lock_guard<std::mutex> lock(pka::launches_of(page_refs_d));
   if (num_child_indices <= pka::kShareInTake) {
     cudaError_t e = pka::ensure_dynamic_smem<pka::fork_take_kernel<true>>(smem);
     if (e == cudaSuccess)
@@ -1131,6 +1145,13 @@ pka_status pka_compact_pages(const int32_t* page_refs_d, int32_t num_pages,
     }
     return pka::done(e, "page compact launch");
   }
+  std::mutex& in = pka::launches_of(page_refs_d);
+  std::mutex& out = pka::launches_of(page_refs_out_d);
+  std::unique_lock<std::mutex> lock_in(in, std::defer_lock), lock_out(out, std::defer_lock);
+  if (&in == &out)
+    lock_in.lock();
+  else
+    std::lock(lock_in, lock_out);
   cudaError_t e =
       pka::launch_cluster<pka::compact_kernel>(pka::cluster_ctas(num_pages), 0, st, a);
   if (e != cudaSuccess) return pka::cuda_failure(e, "page compact launch");

@@ -1,6 +1,8 @@
 """GPU parity of the page operators (copy, take, return, fork, compact) with
 the reference that walks lists: whole numbers and moved bits, so all of it is
 exact."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -755,4 +757,48 @@ def test_captured_fork_and_return_replays():
         got = bits_of(t)
         for w in range(2):
             assert np.array_equal(got[:, :, w], cache.copy_pages(x[:, :, w], s, e, n))
+    assert pka.pka_get_device_error() == 0
+
+
+def test_large_takes_beside_small_ones_on_one_stream():
+    """Two host threads share a stream and a pool: one takes and returns by the
+    form of two launches, the other a few pages at a time.  A call's launches
+    follow one another, so every take is whole and every page comes back."""
+    rng = np.random.default_rng(17)
+    refs = _refs(rng, 400_000, 40_000)
+    r, stream, rounds = i32(refs), torch.cuda.Stream(), 400
+    large = torch.full((rounds, 70_000), -9, dtype=torch.int32, device="cuda")
+    small = torch.full((20_000, 64), -9, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    start, over, taken, errors = threading.Barrier(2), threading.Event(), [0], []
+
+    def take(rows, until):
+        try:
+            start.wait(timeout=60)
+            for pages in rows:
+                pka.pka_alloc_pages(r, pages, stream=stream)
+                pka.pka_free_pages(r, pages, stream=stream)
+                if until is None:
+                    taken[0] += 1
+                    if over.is_set():
+                        return
+        except Exception as e:  # shown by the test's own thread
+            errors.append(e)
+        finally:
+            if until is not None:
+                until.set()
+
+    threads = [threading.Thread(target=take, args=a) for a in ((list(large), over),
+                                                               (list(small), None))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    got, few = _host(large, small[:taken[0]])
+    free = refs == 0
+    for pages in (got, few):
+        assert pages.min() >= 0 and np.all(np.diff(pages, axis=1) > 0) and free[pages].all()
+    assert np.array_equal(_host(r), refs)
     assert pka.pka_get_device_error() == 0
