@@ -390,7 +390,8 @@ pka_status pka_rope_append_paged_kv_cache(
  * entries, and whatever else the caller counts), 0 for a free page.  Page ids
  * chosen are always the lowest free ones, so results do not depend on timing.
  * Violations that only the device can see are stepped around and noted in the
- * device error word (pka_get_device_error; of several the largest code stays).
+ * device error word (pka_get_device_error; of several the largest code stays),
+ * but for one that pka_fork_pages names.
  * Two calls on one page_refs_d must be ordered (one stream, or events): a call
  * may keep its own marks in the counts of free pages until it ends.  Host
  * threads may share such a stream: the launches of a call follow one another.
@@ -448,10 +449,14 @@ pka_status pka_free_pages(int32_t* page_refs_d, int32_t num_pages, const int32_t
  *   pages refuse the whole call on the device: nothing but counts_d = {-1, -1}
  *   is written and PKA_ERR_METADATA or PKA_ERR_WORKSPACE is noted.  Page ids
  *   outside [0, num_pages) in a parent's table are carried over and noted.
- *   The parents' pages must be held (a reference at least), and no two arrays
- *   of the call may overlap (the children's tables are not written in place).
+ *   The parents' pages must be held (a reference at least).  With
+ *   num_child_indices up to PKA_FORK_CHECKED_INDICES one that is not refuses
+ *   the call as a malformed array does; a larger fork does not look for it, and
+ *   may give such a page out as a fresh one too.  No two arrays of the call may
+ *   overlap (the children's tables are not written in place).
  *   PKA_ERR_UNSUPPORTED: more than PKA_MAX_FORK_CHILDREN children. */
 #define PKA_MAX_FORK_CHILDREN 8192
+#define PKA_FORK_CHECKED_INDICES 4096
 pka_status pka_fork_pages(int32_t page_size, int32_t* page_refs_d, int32_t num_pages,
                           int32_t num_parents, const int32_t* kv_indptr_d,
                           const int32_t* kv_indices_d, int32_t num_indices,

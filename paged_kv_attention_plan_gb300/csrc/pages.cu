@@ -141,20 +141,29 @@ struct Counts {
   int block[kRows];         // in the block's tiles of a row
   int before[kRows];        // in the row's tiles of the blocks before
   int row[kRows];           // in a row
+  int flag;                 // FLAG: set by the block before it counts
+  int any_flag;             // FLAG: set by any block of the cluster
 };
 
-// Counts the free (or live) pages of every tile.  Lane i gets the number of
-// such pages before this warp's tile of row i, and every lane their total.
-// Leaves the cluster barrier armed: the caller ends with leave(), so that no
-// block is gone while its counts are read.
-__device__ __forceinline__ int count_pages(Counts& c, const int32_t* refs, uint32_t num_pages,
-                                           const Tiling& t, bool live, int* total) {
+// Counts the free (or live) pages of this warp's tiles.
+__device__ __forceinline__ void count_tiles(Counts& c, const int32_t* refs, uint32_t num_pages,
+                                            const Tiling& t, bool live) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = 0; i < t.rows; ++i) {
     const Share s = tile_at(refs, num_pages, t, i);
     const int n = count_free(refs, s);
     if (lane == 0) c.tile[i][warp] = live ? (int)(s.hi - s.lo) - n : n;
   }
+}
+
+// Adds up what count_tiles counted.  Lane i gets the number of such pages
+// before this warp's tile of row i, and every lane their total.  Leaves the
+// cluster barrier armed: the caller ends with leave(), so that no block is gone
+// while its counts are read.  FLAG: c.any_flag, which the caller set to its own
+// c.flag, becomes that of any block.
+template <bool FLAG>
+__device__ __forceinline__ int add_counts(Counts& c, const Tiling& t, int* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __syncthreads();
   int block = 0;
   if (warp < t.rows) {  // a warp a row
@@ -178,6 +187,11 @@ __device__ __forceinline__ int count_pages(Counts& c, const int32_t* refs, uint3
         c.before[warp] = before;
       }
     }
+    if (FLAG && warp == 0) {
+      const int there = lane < gridDim.x ? cluster.map_shared_rank(&c, lane)->flag : 0;
+      const bool any = __any_sync(kAll, there != 0);
+      if (lane == 0) c.any_flag = any;
+    }
     cluster.barrier_arrive();
   }
   __syncthreads();
@@ -185,6 +199,12 @@ __device__ __forceinline__ int count_pages(Counts& c, const int32_t* refs, uint3
   const int upto = inclusive_sum(row, lane);
   *total = __shfl_sync(kAll, upto, 31);
   return lane < t.rows ? upto - row + c.before[lane] + c.tile[lane][warp] : 0;
+}
+
+__device__ __forceinline__ int count_pages(Counts& c, const int32_t* refs, uint32_t num_pages,
+                                           const Tiling& t, bool live, int* total) {
+  count_tiles(c, refs, num_pages, t, live);
+  return add_counts<false>(c, t, total);
 }
 
 __device__ __forceinline__ void leave() {
@@ -226,7 +246,7 @@ __device__ __forceinline__ bool take_step(int32_t* refs, const Share& s, uint32_
 }
 
 // Take the first `stop` free pages of all: use(rank, page) for those of this
-// warp's tiles.  `before` is count_pages' answer.
+// warp's tiles.  `before` is add_counts' answer.
 template <bool ALONE, class F>
 __device__ __forceinline__ void take_free(int32_t* refs, uint32_t num_pages, const Tiling& t,
                                           int before, int stop, F use) {
@@ -431,15 +451,19 @@ __device__ __forceinline__ int find_between(const int32_t* ptr, int lo, int hi, 
 
 // At most this many entries are shared by the launch that takes the fresh
 // pages; more go to a launch over the whole GPU.  Fork and return, in us, in
-// one / in two launches: 4,004 entries 8.9 / 9.1, 16,008 9.6 / 9.6, 64,016
-// 14.8 / 10.5, 917,760 67 / 23.
-constexpr int kShareInTake = 4096;
+// one / in two launches: 32 entries 7.2 / 7.6, 1,032 7.7 / 8.6, 4,004 9.9 / 9.6
+// (and a launch less for the host), 16,008 9.6 / 9.6 and 64,016 14.8 / 10.5
+// before the one looked for pages that nobody holds, which costs it 0.3 to 0.8.
+constexpr int kShareInTake = PKA_FORK_CHECKED_INDICES;
 
 // Checks every child, takes the lowest free pages for all of them and writes
 // the entries that these fill, the copy list and the counts; nothing at all
 // when a child is malformed or the pages do not suffice.  Every block of the
 // cluster scans the children for itself into shared memory, then writes for
-// the free pages of its share.
+// the free pages of its share.  SHARE: the parents' pages are looked up before
+// the counts meet, whose barrier then tells every block whether all are held;
+// so no page is free to one block and shared by another, and the references
+// that the shared entries add leave the free pages as they were counted.
 template <bool SHARE>
 __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a) {
   extern __shared__ int32_t mem[];
@@ -452,8 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
   // (the first round's loads go out before the counting)
   const int i0 = min((int)threadIdx.x, a.num_children - 1);
   const int32_t first = a.child_indptr[i0], end = a.child_indptr[i0 + 1], parent = a.parent[i0];
-  int total;
-  const int before = count_pages(c, a.refs, a.num_pages, a.tiling, false, &total);
+  int total = 0, before = 0;
+  count_tiles(c, a.refs, a.num_pages, a.tiling, false);
+  if (!SHARE) before = add_counts<false>(c, a.tiling, &total);
 
   // running sums over the children: fresh pages in the upper 32 bits, copies
   // in the lower
@@ -496,6 +521,34 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
     carry = all;
   }
   ok = __syncthreads_and(ok);
+  constexpr int U = kShareInTake / kThreads;
+  static_assert(U * kThreads == kShareInTake, "entries of the smallest launch");
+  const int e0 = sums.first[0] + blockIdx.x * kThreads + threadIdx.x;
+  int32_t page_of[U];
+  unsigned named = 0, shares = 0;  // bit u: entry e0 + u * (threads of the launch) names or shares
+  if (SHARE) {                     // page_of[u] of its parent
+    const int stop = a.child_indptr[a.num_children];  // at most kShareInTake when ok
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int e = e0 + u * gridDim.x * kThreads;
+      if (!ok || e >= stop) break;
+      const int i = find_between(sums.first, 0, a.num_children - 1, e);
+      const int j = e - sums.first[i], shared = sums.shared[i];
+      if (j >= shared + (sums.slots[i] > 0)) continue;
+      page_of[u] = a.kv_indices[sums.parent_first[i] + j];
+      named |= 1u << u;
+      if (j < shared) shares |= 1u << u;
+    }
+    bool unheld = false;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if ((named >> u & 1) && page_of[u] >= 0 && page_of[u] < a.num_pages)
+        unheld |= a.refs[page_of[u]] <= 0;
+    unheld = __syncthreads_or(unheld);
+    if (threadIdx.x == 0) c.flag = c.any_flag = unheld;
+    before = add_counts<true>(c, a.tiling, &total);
+    ok = ok && !c.any_flag;
+  }
   const int64_t needed = carry >> 32;
   const int copies = (int)(uint32_t)carry;
   const bool refused = !ok || total < needed;
@@ -524,15 +577,11 @@ __global__ void __launch_bounds__(kThreads, 1) fork_take_kernel(const ForkArgs a
     take_free<!SHARE>(a.refs, a.num_pages, a.tiling, before, (int)needed, fill);
     if (SHARE) {
       bool bad = false;
-      const int stop = a.child_indptr[a.num_children];
-      for (int e = sums.first[0] + blockIdx.x * kThreads + threadIdx.x; e < stop;
-           e += gridDim.x * kThreads) {
-        const int i = find_between(sums.first, 0, a.num_children - 1, e);
-        const int j = e - sums.first[i];
-        if (j >= sums.shared[i]) continue;
-        const int32_t page = a.kv_indices[sums.parent_first[i] + j];
-        a.child_indices[e] = page;
-        if (page >= 0 && page < a.num_pages) atomicAdd(a.refs + page, 1);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!(shares >> u & 1)) continue;
+        a.child_indices[e0 + u * gridDim.x * kThreads] = page_of[u];
+        if (page_of[u] >= 0 && page_of[u] < a.num_pages) atomicAdd(a.refs + page_of[u], 1);
         else bad = true;
       }
       if (bad) note_error(a.err, PKA_ERR_METADATA);

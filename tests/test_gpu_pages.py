@@ -802,3 +802,26 @@ def test_large_takes_beside_small_ones_on_one_stream():
         assert pages.min() >= 0 and np.all(np.diff(pages, axis=1) > 0) and free[pages].all()
     assert np.array_equal(_host(r), refs)
     assert pka.pka_get_device_error() == 0
+
+
+@pytest.mark.parametrize("pool", [200, 20_000])  # one block and a cluster
+@pytest.mark.parametrize("page,where", [(4, 0), (4, 9), (4, -1), (1, 17)])
+def test_fork_refuses_a_parent_page_that_nobody_holds(pool, page, where):
+    """A shared page, or the partly filled one that would be copied, without a
+    reference: nothing is written, whether or not the page would be taken."""
+    rng = np.random.default_rng(pool + page)
+    lens = np.array([38, 21])
+    indptr, ids, last = _parents(rng, lens, page, pool)
+    refs = np.zeros(pool, np.int32)
+    refs[ids] = 1
+    parent = np.array([1, 0, 0, -1], np.int32)
+    pages = (indptr[1:] - indptr[:-1])[parent] + np.array([1, 0, 2, 0])
+    _check_fork(page, refs, lens, indptr, ids, last, parent, pages)
+    gap = ids[indptr[1] + where] if where < 0 else ids[where]
+    refs[gap] = 0
+    _, got = _fork(page, refs, indptr, ids, last, parent, pages)
+    _refused(got, refs, METADATA)
+    # a parent that no child continues may name what it will
+    child = np.where(parent == 0, 1, parent)
+    pages = (indptr[1:] - indptr[:-1])[1] + np.array([1, 0, 2, 0])
+    _check_fork(page, refs, lens, indptr, ids, last, child, pages)
