@@ -530,9 +530,11 @@ def pka_rope_append_paged_kv_cache(params, rope, q, q_out, k_new, v_new, append_
     last = _here(last_page_len, "last_page_len", _I32, dev)
     if kv_indptr.numel() != batch + 1 or last_page_len.numel() != batch:
         raise ValueError("kv_indptr and last_page_len must describe append_indptr's requests")
-    kpool, vpool, shape, _ = _here_pools(k, v, params, dev)
+    kpool, vpool, shape, strides = _here_pools(k, v, params, dev)
     if len(shape) != 4:
         raise ValueError("k and v must be pools [pages, ...]")
+    if page_stride != strides[0] and shape[0] > 1:
+        raise ValueError(f"page_stride: the pools' is {strides[0]}, got {page_stride}")
     s = lib().pka_rope_append_paged_kv_cache(
         ctypes.byref(params), ctypes.byref(rope), batch, rows, qp, qs, qo, kp, ks, vp, vs, pos,
         app, ptr, idx, last, kpool, vpool,

@@ -167,3 +167,36 @@ def test_oracle_transpose():
     assert abs(left - right) <= 1e-10
     back = cache.rope(cache.rope(x, pos, f), pos, f, transpose=True)
     assert np.abs(back - x).max() <= 1e-12
+
+
+def test_binding_refuses_a_page_stride_that_is_not_the_pools(monkeypatch):
+    """The pools know where their pages lie; another stride would reach past
+    them.  (Checked on host tensors, with the library's entry replaced.)"""
+    calls = []
+
+    class Library:
+        @staticmethod
+        def pka_rope_append_paged_kv_cache(*args):
+            calls.append(args)
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # host tensors' device
+    monkeypatch.setattr(_pka, "lib", lambda: Library)
+    rope, params = _pka.pka_rope(), pka.make_params(2, 2, 64, 4)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)  # noqa
+    x = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    both = torch.zeros(5, 2, 4, 2, 64, dtype=torch.bfloat16)  # K and V pages in turn
+
+    def append(k, v, stride):
+        return pka.pka_rope_append_paged_kv_cache(params, rope, None, None, x, x, i32(0, 1),
+                                                  i32(0, 1), i32(0), i32(1), k, v, stride, stream=0)
+
+    k, v = both[:, 0], both[:, 1]
+    apart = k.contiguous(), v.contiguous()
+    assert append(k, v, k.stride(0)) == 0 and append(*apart, apart[0].stride(0)) == 0
+    assert append(k[:1], v[:1], 512) == 0  # one page: its stride leads nowhere
+    assert len(calls) == 3
+    for pools, stride in (((k, v), apart[0].stride(0)), (apart, k.stride(0)), ((k, v), 0)):
+        with pytest.raises(ValueError, match="page_stride"):
+            append(*pools, stride)
+    assert len(calls) == 3
