@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -128,6 +129,16 @@ pka_status cuda_failure(cudaError_t e, const char* where);
 // Multiprocessor count of the current device (cached per device; 0 if the
 // query fails).
 int current_device_sms();
+
+// Reciprocal of a power-of-two scale of e4m3 pools, with which a product is the
+// exact quotient; 0 (divide) for every other scale, and for powers of two whose
+// reciprocal is no float32.
+inline float pow2_reciprocal(float scale) {
+  int e = 0;
+  if (std::frexp(scale, &e) != 0.5f) return 0.f;
+  const float inv = std::ldexp(1.0f, 1 - e);
+  return std::isfinite(inv) ? inv : 0.f;
+}
 
 // Decode launch geometry shared by the planner and the kernel: a decode CTA
 // covers `heads_per_cta` kv heads (at most 8, one consumer warp each, so that

@@ -55,7 +55,7 @@ struct RopeArgs {
   int page_size;
   int layout;
   float k_scale, v_scale;    // e4m3 pools
-  float k_inv, v_inv;        // exact reciprocal of a power-of-two scale, else 0
+  float k_inv, v_inv;        // pow2_reciprocal of these
   int32_t* err;
   uint64_t turns[64];        // F_i
 };
@@ -421,12 +421,6 @@ bool out_ok(const void* in, int64_t in_stride, const void* out, int64_t out_stri
   return in != out || in_stride == out_stride;
 }
 
-// Reciprocal of a power-of-two scale (exact), else 0: divide.
-float pow2_inv(float s) {
-  int e = 0;
-  return std::frexp(s, &e) == 0.5f ? std::ldexp(1.0f, 1 - e) : 0.f;
-}
-
 }  // namespace
 }  // namespace pka
 
@@ -578,8 +572,8 @@ pka_status pka_rope_append_paged_kv_cache(
   a.layout = p->layout;
   a.k_scale = p->k_scale > 0.f ? p->k_scale : 1.f;
   a.v_scale = p->v_scale > 0.f ? p->v_scale : 1.f;
-  a.k_inv = pka::pow2_inv(a.k_scale);
-  a.v_inv = pka::pow2_inv(a.v_scale);
+  a.k_inv = pka::pow2_reciprocal(a.k_scale);
+  a.v_inv = pka::pow2_reciprocal(a.v_scale);
   a.err = pka::device_error_word();
   const bool adjacent = rope->interleaved != 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

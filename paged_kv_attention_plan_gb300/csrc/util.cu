@@ -470,16 +470,11 @@ cudaError_t launch_append(const pka_params& p, int32_t batch, const uint16_t* k_
                           int64_t page_stride, cudaStream_t stream) {
   const int64_t threads = nnz * 32;  // one warp per appended row
   const float ks = p.k_scale > 0.f ? p.k_scale : 1.f, vs = p.v_scale > 0.f ? p.v_scale : 1.f;
-  // reciprocal of a power-of-two scale (exact), else 0: divide
-  auto pow2_inv = [](float s) {
-    int e = 0;
-    return std::frexp(s, &e) == 0.5f ? std::ldexp(1.0f, 1 - e) : 0.f;
-  };
   if (p.kv_dtype == PKA_KV_FP8_E4M3)
     append_kernel<true><<<grid_for(threads, 256), 256, 0, stream>>>(
         k_new, v_new, append_indptr, batch, nnz, kv_indptr, kv_indices, last_page_len, k, v,
-        page_stride, p.num_kv_heads, p.head_dim, p.page_size, p.layout, ks, vs, pow2_inv(ks),
-        pow2_inv(vs));
+        page_stride, p.num_kv_heads, p.head_dim, p.page_size, p.layout, ks, vs,
+        pow2_reciprocal(ks), pow2_reciprocal(vs));
   else
     append_kernel<false><<<grid_for(threads, 256), 256, 0, stream>>>(
         k_new, v_new, append_indptr, batch, nnz, kv_indptr, kv_indices, last_page_len, k, v,

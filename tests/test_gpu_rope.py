@@ -466,3 +466,31 @@ def test_captured_on_another_stream_and_replayed():
         _assert_rotated(bits_of(k)[page, :, slot], b.k_new, pos, freqs, interleaved=True)
         assert np.array_equal(bits_of(v)[page, :, slot], b.v_new)
         _assert_rotated(bits_of(q_out), b.q, pos, freqs, interleaved=True)
+
+
+@pytest.mark.parametrize("exponent", [-149, -140, -128, -127, -126, 127])
+def test_e4m3_codes_of_scales_at_the_ends_of_the_exponents(exponent):
+    """Powers of two whose reciprocal is no float32, or barely one: zeros keep
+    their code, every other value has that of its quotient."""
+    scale = 2.0 ** exponent
+    v = np.arange(1 << 16, dtype=np.uint16).reshape(256, 2, 128)
+    params = pka.make_params(8, 2, 128, 16, kv_dtype="e4m3", k_scale=scale, v_scale=scale)
+    pools = [torch.zeros(16, 16, 2, 128, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    table = [i32(x) for x in ([0, 256], [0, 16], np.arange(16), [16])]
+    pka.pka_rope_append_paged_kv_cache(params, _rope(128)[0], None, None, bf16(v), bf16(v), *table,
+                                       pools[0], pools[1], pools[0].stride(0),
+                                       positions=i32(np.zeros(256)))
+    pka.pka_append_paged_kv_cache(params, bf16(v), bf16(v), *table, pools[2], pools[3],
+                                  pools[2].stride(0))
+    torch.cuda.synchronize()
+    got = [p.cpu().numpy().reshape(v.shape) for p in pools]
+    with np.errstate(all="ignore"):
+        x = ref.bf16_bits_to_f64(v)
+        finite, want = np.isfinite(x), ref.quantize_kv_e4m3(v, scale)
+    for codes in got[1:]:
+        assert np.array_equal(codes[finite], want[finite])
+    # K of position 0 is x c - y s with c = 1 and s = 0, where both of a pair are finite; a
+    # zero may lose its sign
+    pair = finite & np.roll(finite, 64, axis=2)
+    assert np.array_equal(got[0][pair & (x != 0)], want[pair & (x != 0)])
+    assert not np.any(got[0][pair & (x == 0)] & 0x7F)
