@@ -353,9 +353,10 @@ pka_status pka_rope_init(const pka_rope_params* params, pka_rope* rope);
  *   are taken as they are; heads of a row are contiguous.  q_heads or k_heads
  *   may be 0 (its pointers are then ignored).  q_out may be q (with the same
  *   stride), and k_out k; otherwise outputs must not overlap inputs.
- *   PKA_ERR_INVALID_ARG: buffers not 16-byte aligned, a row stride below
- *   heads * head_dim (rows > 1) or not a multiple of 8, rotary_dim above
- *   head_dim; PKA_ERR_UNSUPPORTED: head_dim not in {64, 128}, over 4096 heads. */
+ *   PKA_ERR_INVALID_ARG: rows not 16-byte aligned, positions not 4-byte
+ *   aligned, a row stride below heads * head_dim (rows > 1) or not a multiple
+ *   of 8, rotary_dim above head_dim; PKA_ERR_UNSUPPORTED: head_dim not in
+ *   {64, 128}, over 4096 heads. */
 pka_status pka_apply_rope(const pka_rope* rope, int32_t transpose, int32_t head_dim, int64_t rows,
                           const int32_t* positions_d, const void* q, int32_t q_heads,
                           int64_t q_row_stride, void* q_out, int64_t q_out_row_stride,

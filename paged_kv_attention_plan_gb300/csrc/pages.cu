@@ -994,8 +994,6 @@ pka_status done(cudaError_t e, const char* where) {
   return e == cudaSuccess ? PKA_OK : cuda_failure(e, where);
 }
 
-bool unaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; }
-
 // Held by every call on an array of counts while it launches.  A large take
 // keeps marks in the counts between its two launches, and a compaction relies
 // on what it counted until its last one, so no other thread's call on the array
@@ -1021,6 +1019,9 @@ pka_status pka_copy_pages(const pka_params* p, int32_t num_layers, void* k, void
   if (p->kv_ragged || num_layers > 32767) return PKA_ERR_UNSUPPORTED;
   if (num_layers == 0 || max_copies == 0) return PKA_OK;
   if (!k || !v || !src_d || !dst_d || page_stride <= 0) return PKA_ERR_INVALID_ARG;
+  if (pka::unaligned(src_d) || pka::unaligned(dst_d) || pka::unaligned(slots_d) ||
+      pka::unaligned(num_copies_d))
+    return PKA_ERR_INVALID_ARG;
   const bool f8 = p->kv_dtype == PKA_KV_FP8_E4M3;
   const int item = f8 ? 1 : 2;
   const uintptr_t mis = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);

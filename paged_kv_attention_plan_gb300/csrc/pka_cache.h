@@ -11,6 +11,9 @@ namespace pka {
 // Whether the enums, counts and scales of *p are in range (plan.cpp).
 bool params_valid(const pka_params* p);
 
+// Whether an int32 array starts where none can (null does not).
+inline bool unaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; }
+
 #ifdef __CUDACC__
 // Note a violation that a kernel found (and stepped around) in the device
 // error word: the largest code stays, whichever thread comes first.

@@ -485,7 +485,7 @@ pka_status pka_apply_rope(const pka_rope* rope, int32_t transpose, int32_t head_
     return PKA_ERR_UNSUPPORTED;
   if (!pka::rope_valid(rope, head_dim)) return PKA_ERR_INVALID_ARG;
   if (rows == 0 || (q_heads == 0 && k_heads == 0)) return PKA_OK;
-  if (!positions_d) return PKA_ERR_INVALID_ARG;
+  if (!positions_d || pka::unaligned(positions_d)) return PKA_ERR_INVALID_ARG;
   if (q_heads > 0 && (!pka::rows_ok(q, q_row_stride, rows, q_heads, head_dim) ||
                       !pka::rows_ok(q_out, q_out_row_stride, rows, q_heads, head_dim) ||
                       !pka::out_ok(q, q_row_stride, q_out, q_out_row_stride)))
@@ -532,6 +532,8 @@ pka_status pka_rope_append_paged_kv_cache(
   if (!append_indptr_d || !kv_indptr_d || !kv_indices_d || !last_page_len_d || !k || !v ||
       page_stride <= 0)
     return PKA_ERR_INVALID_ARG;
+  for (const int32_t* x : {positions_d, append_indptr_d, kv_indptr_d, kv_indices_d, last_page_len_d})
+    if (pka::unaligned(x)) return PKA_ERR_INVALID_ARG;
   const bool f8 = p->kv_dtype == PKA_KV_FP8_E4M3;
   const uintptr_t mis = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
   if ((mis & 15) || (page_stride & (f8 ? 15 : 7))) return PKA_ERR_INVALID_ARG;

@@ -148,3 +148,10 @@ def test_reference_copy_slots():
     assert np.array_equal(nhd[1, :2], x[0, :2]) and np.array_equal(nhd[1, 2:], x[1, 2:])
     hnd = cache.copy_pages(x, [0], [1], [1], layout="HND")
     assert np.array_equal(hnd[1, :, :1], x[0, :, :1]) and np.array_equal(hnd[1, :, 1:], x[1, :, 1:])
+
+
+@pytest.mark.parametrize("name", ["src", "dst", "slots", "count"])
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_copy_refuses_lists_off_their_alignment(name, off):
+    """int32 arrays start at multiples of 4 bytes; the kernels could not read others."""
+    assert _copy(**{name: A + off}) == INVALID

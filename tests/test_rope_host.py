@@ -200,3 +200,11 @@ def test_binding_refuses_a_page_stride_that_is_not_the_pools(monkeypatch):
         with pytest.raises(ValueError, match="page_stride"):
             append(*pools, stride)
     assert len(calls) == 3
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_arrays_off_their_alignment_are_refused(off):
+    """int32 arrays start at multiples of 4 bytes; the kernels could not read others."""
+    assert _apply(pos=A + off) == INVALID
+    for name in ("pos", "app", "ptr", "idx", "last"):
+        assert _append(**{name: A + off}) == INVALID
