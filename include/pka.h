@@ -454,7 +454,8 @@ pka_status pka_free_pages(int32_t* page_refs_d, int32_t num_pages, const int32_t
  *   num_child_indices up to PKA_FORK_CHECKED_INDICES one that is not refuses
  *   the call as a malformed array does; a larger fork does not look for it, and
  *   may give such a page out as a fresh one too.  No two arrays of the call may
- *   overlap (the children's tables are not written in place).
+ *   overlap (the children's tables are not written in place: over the parents'
+ *   they are PKA_ERR_INVALID_ARG).
  *   PKA_ERR_UNSUPPORTED: more than PKA_MAX_FORK_CHILDREN children. */
 #define PKA_MAX_FORK_CHILDREN 8192
 #define PKA_FORK_CHECKED_INDICES 4096

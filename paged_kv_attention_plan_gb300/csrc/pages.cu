@@ -1105,6 +1105,11 @@ pka_status pka_fork_pages(int32_t page_size, int32_t* page_refs_d, int32_t num_p
   if (page_size < 1 || num_pages < 0 || num_parents < 0 || num_indices < 0 || num_children < 0 ||
       num_child_indices < 0)
     return PKA_ERR_INVALID_ARG;
+  const uintptr_t table = reinterpret_cast<uintptr_t>(child_indices_d);
+  const uintptr_t parents_table = reinterpret_cast<uintptr_t>(kv_indices_d);
+  if (table < parents_table + 4 * (uintptr_t)num_indices &&
+      parents_table < table + 4 * (uintptr_t)num_child_indices)
+    return PKA_ERR_INVALID_ARG;
   if (num_children > PKA_MAX_FORK_CHILDREN) return PKA_ERR_UNSUPPORTED;
   if (!counts_d || pka::unaligned(counts_d)) return PKA_ERR_INVALID_ARG;
   const bool parents = num_parents > 0 && (!kv_indptr_d || !last_page_len_d);
@@ -1113,7 +1118,6 @@ pka_status pka_fork_pages(int32_t page_size, int32_t* page_refs_d, int32_t num_p
   if (parents || children || (num_indices > 0 && !kv_indices_d) ||
       (num_child_indices > 0 && !child_indices_d) || (num_pages > 0 && !page_refs_d))
     return PKA_ERR_INVALID_ARG;
-  if (num_child_indices > 0 && child_indices_d == kv_indices_d) return PKA_ERR_INVALID_ARG;
   const void* arrays[] = {page_refs_d,    kv_indptr_d,     kv_indices_d, last_page_len_d,
                           parent_d,       child_indptr_d,  child_indices_d, copy_src_d,
                           copy_dst_d,     copy_slots_d};

@@ -155,3 +155,13 @@ def test_reference_copy_slots():
 def test_copy_refuses_lists_off_their_alignment(name, off):
     """int32 arrays start at multiples of 4 bytes; the kernels could not read others."""
     assert _copy(**{name: A + off}) == INVALID
+
+
+@pytest.mark.parametrize("table,n_table,idx,n_idx,refused", [
+    (A, 8, A + 28, 5, True), (A + 16, 8, A, 5, True), (A + 8, 2, A, 50, True),
+    (A, 50, A + 40, 1, True), (A, 8, A + 32, 5, False), (A + 20, 8, A, 5, False)])
+def test_fork_refuses_tables_that_overlap(table, n_table, idx, n_idx, refused):
+    """Children's tables written over any part of the parents'; tables that only
+    meet go on to the next refusal, of the number of children."""
+    status = _fork(table=table, n_table=n_table, idx=idx, n_idx=n_idx, children=8193)
+    assert status == (INVALID if refused else UNSUPPORTED)
