@@ -825,3 +825,65 @@ def test_fork_refuses_a_parent_page_that_nobody_holds(pool, page, where):
     child = np.where(parent == 0, 1, parent)
     pages = (indptr[1:] - indptr[:-1])[1] + np.array([1, 0, 2, 0])
     _check_fork(page, refs, lens, indptr, ids, last, child, pages)
+
+
+@pytest.mark.parametrize("what", ["parent_high", "parent_low", "short", "decreasing", "past_end",
+                                  "last_zero", "last_high", "indptr", "indptr_past", "pages"])
+def test_large_fork_refused(what):
+    """The form of two launches: the second reads tables that the first has not
+    checked yet, and neither writes anything."""
+    rng = np.random.default_rng(19)
+    lens = np.array([9001, 5005, 12000])
+    indptr, ids, last = _parents(rng, lens, 4, 20_000)
+    refs = np.zeros(20_000, np.int32)
+    refs[ids] = 1
+    parent, pages = np.array([0, 1, 2, 0, -1], np.int32), np.array([2251, 1253, 3001, 2252, 2])
+    status = METADATA
+    if what == "parent_high":
+        parent[2] = 3
+    if what == "parent_low":
+        parent[2] = -2
+    if what == "short":
+        pages[3] = 2250
+    if what == "decreasing":
+        pages[4] = -1
+    if what == "last_zero":
+        last[1] = 0
+    if what == "last_high":
+        last[1] = 5
+    if what == "indptr":
+        indptr[1], indptr[2] = indptr[2], indptr[1]
+    if what == "indptr_past":
+        indptr[3] = 99_999
+    if what == "pages":  # one free page too few
+        refs[np.flatnonzero(refs == 0)[7:]] = 1
+        status = WORKSPACE
+    _, got = _fork(4, refs, indptr, ids, last, parent, pages, room=-1 if what == "past_end" else 9)
+    _refused(got, refs, status)
+
+
+def test_large_fork_takes_the_last_free_page():
+    rng = np.random.default_rng(20)
+    lens = np.array([9001, 5005, 12000])
+    indptr, ids, last = _parents(rng, lens, 4, 20_000)
+    refs = np.zeros(20_000, np.int32)
+    refs[ids] = 1
+    refs[np.flatnonzero(refs == 0)[8:]] = 1
+    parent, pages = np.array([0, 1, 2, 0, -1], np.int32), np.array([2251, 1253, 3001, 2252, 2])
+    _check_fork(4, refs, lens, indptr, ids, last, parent, pages)
+
+
+@pytest.mark.parametrize("free", [0, 69_999, 70_000])
+def test_large_take_with_too_few_free_takes_none(free):
+    """The form of two launches: refused one page short, whole with the last."""
+    rng = np.random.default_rng(free)
+    refs = _refs(rng, 400_000, 400_000 - free)
+    d, pages = i32(refs), torch.full((70_000,), 5, dtype=torch.int32, device="cuda")
+    pka.pka_alloc_pages(d, pages)
+    if free == 70_000:
+        assert np.array_equal(_host(pages), np.flatnonzero(refs == 0))
+        assert np.array_equal(_host(d), np.maximum(refs, 1))
+        assert pka.pka_get_device_error() == 0
+    else:
+        assert np.all(_host(pages) == -1) and np.array_equal(_host(d), refs)
+        assert pka.pka_get_device_error() == WORKSPACE

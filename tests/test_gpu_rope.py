@@ -494,3 +494,28 @@ def test_e4m3_codes_of_scales_at_the_ends_of_the_exponents(exponent):
     pair = finite & np.roll(finite, 64, axis=2)
     assert np.array_equal(got[0][pair & (x != 0)], want[pair & (x != 0)])
     assert not np.any(got[0][pair & (x == 0)] & 0x7F)
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.25, 0.3, 0.02, 7.0])
+@pytest.mark.parametrize("d,rotary,interleaved", [(128, 128, False), (128, 64, True),
+                                                  (64, 20, False)])
+def test_k_codes_of_position_0_are_the_plain_appends(d, rotary, interleaved, scale):
+    """At position 0 the rotation is the identity, so K's codes are those of
+    pka_append_paged_kv_cache, every finite bf16 value among them."""
+    x = np.arange(1 << 16, dtype=np.uint16)
+    x = x[(x & 0x7F80) != 0x7F80]
+    x = np.resize(x, (len(x) // (2 * d) + 1) * 2 * d).reshape(-1, 2, d)
+    rows = len(x)
+    params = pka.make_params(2, 2, d, 16, kv_dtype="e4m3", k_scale=scale, v_scale=scale)
+    pages = -(-rows // 16)
+    pools = [torch.zeros(pages, 16, 2, d, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    table = [i32(a) for a in ([0, rows], [0, pages], np.arange(pages), [rows - 16 * (pages - 1)])]
+    pka.pka_rope_append_paged_kv_cache(params, _rope(rotary, interleaved)[0], None, None, bf16(x),
+                                       bf16(x), *table, pools[0], pools[1], pools[0].stride(0),
+                                       positions=i32(np.zeros(rows)))
+    pka.pka_append_paged_kv_cache(params, bf16(x), bf16(x), *table, pools[2], pools[3],
+                                  pools[2].stride(0))
+    torch.cuda.synchronize()
+    got, want = (p.cpu().numpy().reshape(-1, 2, d)[:rows] for p in (pools[0], pools[2]))
+    some = (x & 0x7FFF) != 0  # x c - y s of a negative zero may be a positive one
+    assert np.array_equal(got[some], want[some]) and not np.any(got[~some] & 0x7F)
