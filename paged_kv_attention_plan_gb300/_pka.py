@@ -474,7 +474,8 @@ def pka_rope_init(rope_params) -> pka_rope:
 def pka_apply_rope(rope, positions, q=None, q_out=None, k=None, k_out=None, transpose=False,
                    stream=None, check=True) -> int:
     """Rotate q and / or k ([rows, heads, head_dim], rows at any stride) into
-    q_out and k_out, which may be q and k themselves."""
+    q_out and k_out, which may be q and k themselves.  Autograd does not see the
+    call: a backward pass calls it with transpose on the outputs' gradients."""
     some = q if q is not None else k
     if not isinstance(some, torch.Tensor) or some.dim() != 3:
         raise ValueError("q and k must be [rows, heads, head_dim], one of them given")
@@ -506,7 +507,8 @@ def pka_rope_append_paged_kv_cache(params, rope, q, q_out, k_new, v_new, append_
                                    kv_indices, last_page_len, k, v, page_stride, positions=None,
                                    stream=None, check=True) -> int:
     """pka_append_paged_kv_cache of rotated rows; q and q_out may be None.  k
-    and v are the pools [pages, ...]; rows past append_indptr[-1] are left."""
+    and v are the pools [pages, ...] and page_stride theirs; rows past
+    append_indptr[-1] are left."""
     dev = torch.cuda.current_device()
     hk, d, rows = params.num_kv_heads, params.head_dim, k_new.shape[0]
     batch = append_indptr.numel() - 1
@@ -593,8 +595,8 @@ def pka_free_pages(page_refs, pages, stream=None, check=True) -> int:
 def pka_fork_pages(page_size, page_refs, kv_indptr, kv_indices, last_page_len, parent,
                    child_indptr, child_indices, copy_src, copy_dst, copy_slots, counts,
                    stream=None, check=True) -> int:
-    """Tables of children that continue parents; the copy lists and counts go
-    to pka_copy_pages.  All arrays are device int32."""
+    """Tables of children that continue parents, whose pages are held; the copy
+    lists and counts go to pka_copy_pages.  All arrays are device int32."""
     dev, i32 = torch.cuda.current_device(), _I32
     parents, children = last_page_len.numel(), parent.numel()
     if kv_indptr.numel() != parents + 1 or child_indptr.numel() != children + 1:
