@@ -135,15 +135,16 @@ __device__ __forceinline__ void from_shared(const float* p, float (&x)[8]) {
 // kInFlight steps are loaded before the first of them is used, the first ones
 // before the row's page and sines are looked up.
 //
-// Whole pieces are bound by memory bandwidth: each element is read once and written once, and
-// 16,387 rows of 64 heads of 128 take 79.4 us, 6.76 TB/s, the rate of a plain
-// copy.  Two steps in flight at four blocks an SM are enough and leave the
-// registers for it (16,387 rows of 40 heads, in us: one step 54.9, two 51.6,
-// three at three blocks 51.8, four at two blocks 59.1).
+// Whole pieces are bound by memory bandwidth: each element is read once and
+// written once, and 16,387 rows of 64 heads of 128 take 79.4 us, 6.76 TB/s, the
+// rate of a plain copy.  Two steps in flight at four blocks an SM are enough
+// and leave the registers for it (16,387 rows of 40 heads, in us: one step
+// 54.9, two 51.6, three at three blocks 51.8, four at two blocks 59.1).
 // Scattered pairs wait for shared memory and take 1.5 to 1.9 times as long as
 // a copy; the rotation alone spills 44 to 48 bytes there at four blocks an SM,
-// 12 at three (in us, three / four blocks: 8,192 rows of 40 heads with 40 of 128 elements turned 46.6 /
-// 42.4, 16,387 with 126 88.2 / 93.4, an append of 9,216 with 40 50.6 / 46.3).
+// 12 at three (in us, three / four blocks: 8,192 rows of 40 heads with 40 of
+// 128 elements turned 46.6 / 42.4, 16,387 with 126 88.2 / 93.4, an append of
+// 9,216 with 40 50.6 / 46.3).
 // Into e4m3 pools both pieces are held as floats: three blocks, 80 registers
 // and 12 to 36 bytes spilled.
 constexpr int kInFlight = 2;
@@ -539,7 +540,8 @@ pka_status pka_rope_append_paged_kv_cache(
   if (!append_indptr_d || !kv_indptr_d || !kv_indices_d || !last_page_len_d || !k || !v ||
       page_stride <= 0)
     return PKA_ERR_INVALID_ARG;
-  for (const int32_t* x : {positions_d, append_indptr_d, kv_indptr_d, kv_indices_d, last_page_len_d})
+  for (const int32_t* x :
+       {positions_d, append_indptr_d, kv_indptr_d, kv_indices_d, last_page_len_d})
     if (pka::unaligned(x)) return PKA_ERR_INVALID_ARG;
   const bool f8 = p->kv_dtype == PKA_KV_FP8_E4M3;
   const uintptr_t mis = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
