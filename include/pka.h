@@ -87,8 +87,33 @@ typedef enum pka_mask_mode {
  * graph_max_kv_tokens rows (the keys of all rows with qo_len >= 2 of any
  * plan must fit); without that capacity graph mode refuses such rows
  * (PKA_ERR_UNSUPPORTED), and a plan whose rows outgrow it gets
- * PKA_ERR_WORKSPACE. */
-typedef enum pka_kv_dtype { PKA_KV_BF16 = 0, PKA_KV_FP8_E4M3 = 1 } pka_kv_dtype;
+ * PKA_ERR_WORKSPACE.
+ * PKA_KV_INT4_G32 / _G64 / _G128: the pools hold 4-bit codes with a step and
+ * an origin for each group of 32, 64 or 128 elements of a head (at most a
+ * head): code c stands for origin + step * c.  A page is one run of bytes:
+ *   codes [P, Hk, D/2] (HND [Hk, P, D/2]), element 2i of a head in the low half
+ *     of byte i, element 2i + 1 in the high half;
+ *   words [P, Hk, D/group] (HND [Hk, P, D/group]), 32 bits each: the step as
+ *     bf16 in the low half, the origin as bf16 in the high half;
+ * padded to a multiple of 16 bytes (pka_kv_page_bytes).  k and v point at page
+ * 0, page_stride is in bytes, a multiple of 16 and at least a page.  k_scale
+ * and v_scale are not used.  Appends store, for a group's least and greatest
+ * element lo and hi, step = bf16((hi - lo) / 15), origin = bf16(lo) and the
+ * codes round((x - origin) / step) clamped to 0 .. 15 (nearest, ties to even;
+ * differences and quotients in float32); a group whose hi - lo is not finite
+ * (NaN, infinities) is stored as NaN, and one whose step would be no normal
+ * bf16 as its origin alone.  Decode rows read the codes and words without
+ * rounding them; rows with qo_len >= 2 (and decode_on_tensor_cores) read a bf16
+ * scratch as over e4m3 pools, each value rounded once more, to bf16.  Paged
+ * K/V only (PKA_ERR_UNSUPPORTED for ragged, for a group above head_dim and for
+ * pages of 2 GB); everything else as over e4m3 pools. */
+typedef enum pka_kv_dtype {
+  PKA_KV_BF16 = 0,
+  PKA_KV_FP8_E4M3 = 1,
+  PKA_KV_INT4_G32 = 2,
+  PKA_KV_INT4_G64 = 3,
+  PKA_KV_INT4_G128 = 4
+} pka_kv_dtype;
 typedef enum pka_split_mode {
   PKA_SPLIT_OFF = 0,    /* one work item per (request, head block, q tile)   */
   PKA_SPLIT_AUTO = 1,   /* planner balances keys across CTAs, merges splits  */
@@ -115,8 +140,8 @@ typedef struct pka_params {
    * available in graph mode; prefill rows are not split. */
   int32_t graph_max_batch;     /* the most requests of any plan                */
   int32_t graph_max_qo_rows;   /* the most query rows; q and o hold this many   */
-  int32_t graph_max_kv_tokens; /* ragged K/V: the most K/V rows; e4m3 pools:    */
-                               /* the most keys of rows with qo_len >= 2       */
+  int32_t graph_max_kv_tokens; /* ragged K/V: the most K/V rows; e4m3 and 4-bit */
+                               /* pools: the most keys of rows with qo_len >= 2 */
   int32_t kv_dtype;            /* pka_kv_dtype of the K/V pools                 */
   float k_scale;               /* PKA_KV_FP8_E4M3: scale of K codes (<= 0: 1)    */
   float v_scale;               /* PKA_KV_FP8_E4M3: scale of V codes (<= 0: 1)    */
@@ -148,8 +173,8 @@ typedef struct pka_plan_info {
   int32_t num_decode_joins;  /* split (decode row, kv head) pairs that the     */
                              /* decode kernel merges itself (their g qo heads  */
                              /* are among num_merge_tasks)                     */
-  int32_t kv_scratch_rows;   /* e4m3 K/V: bf16 rows decoded for the tensor-core */
-                             /* rows in the float workspace (0 otherwise)       */
+  int32_t kv_scratch_rows;   /* e4m3 and 4-bit K/V: bf16 rows decoded for the   */
+                             /* tensor-core rows in the float workspace (else 0) */
   int32_t reserved[3];
 } pka_plan_info;
 
@@ -214,7 +239,7 @@ pka_status pka_plan(pka_plan_t plan, const pka_params* params, int32_t batch,
  *   after the sum of kv_indptr[l'][num_nodes[l']] over l' < l.  Each level's
  *   work writes fp32 partial states to the float workspace and the merge
  *   kernel combines every row's states into O and LSE in the same pka_run.
- *   Supported: paged K/V (bf16 or e4m3 pools), mask none or causal, split
+ *   Supported: paged K/V (pools of every type), mask none or causal, split
  *   off/auto/fixed, up to PKA_MAX_CASCADE_LEVELS levels; ragged K/V, custom
  *   masks and graph mode return PKA_ERR_UNSUPPORTED.  Workspace rules and errors as in pka_plan;
  *   rows split differently between levels give PKA_ERR_METADATA. */
@@ -268,7 +293,11 @@ pka_status pka_run(pka_plan_t plan, const pka_params* params, const void* q, con
  *   append_indptr_d[batch].  k_new / v_new are bf16; e4m3 pools
  *   (params->kv_dtype) store each value divided by k_scale / v_scale, rounded
  *   to the nearest e4m3 value (ties to even), magnitudes above 448 clamped to
- *   448.  Buffers 16-byte aligned, page_stride a multiple of 16 bytes;
+ *   448; 4-bit pools store codes and words as pka_kv_dtype says (there, rows
+ *   from append_indptr_d[batch] on are left out, and a row whose position lies
+ *   outside its request's pages is not appended and PKA_ERR_METADATA is noted
+ *   in the device error word; PKA_ERR_UNSUPPORTED: over 4096 kv heads, 2^33
+ *   rows).  Buffers 16-byte aligned, page_stride a multiple of 16 bytes;
  *   PKA_ERR_INVALID_ARG otherwise. */
 pka_status pka_append_paged_kv_cache(const pka_params* params, int32_t batch, const void* k_new,
                                      const void* v_new, const int32_t* append_indptr_d,
@@ -276,6 +305,33 @@ pka_status pka_append_paged_kv_cache(const pka_params* params, int32_t batch, co
                                      const int32_t* kv_indices_d,
                                      const int32_t* last_page_len_d, void* k, void* v,
                                      int64_t page_stride, void* stream);
+
+/* Bytes of one page of the K (or V) pool: P * Hk * D * 2 (bf16), P * Hk * D
+ * (e4m3), or for 4-bit pools the codes and words, padded to a multiple of 16.
+ * Host only; no CUDA call.  PKA_ERR_UNSUPPORTED for ragged K/V, head_dim not
+ * in {64, 128} and a group above head_dim. */
+pka_status pka_kv_page_bytes(const pka_params* params, int64_t* bytes);
+
+/* The counterpart of the appends: cached rows back as bf16, of pools of every
+ * type (e4m3: code times k_scale / v_scale; 4-bit: origin + step * code; both
+ * computed in float32 and rounded once to bf16).
+ *   Row t of request r, read_indptr_d[r] .. read_indptr_d[r+1], is its logical
+ *   position begin_d[r] + t (begin_d NULL: t); it goes to k_out and v_out
+ *   [nnz, Hk, D], either of which may be NULL (not read).  nnz is the rows of
+ *   the buffers: those from read_indptr_d[batch] on stay as they were.
+ *   A row whose position lies outside its request's keys, or whose page id
+ *   lies outside [0, num_pool_pages), stays as it was and PKA_ERR_METADATA is
+ *   noted in the device error word; the indptr arrays themselves are trusted.
+ *   The outputs must not overlap the pools.  Alignment and page_stride as in
+ *   pka_append_paged_kv_cache, index arrays 4-byte aligned;
+ *   PKA_ERR_UNSUPPORTED: ragged K/V, over 4096 kv heads, 2^33 rows. */
+pka_status pka_read_paged_kv_cache(const pka_params* params, int32_t batch,
+                                   const int32_t* begin_d, const int32_t* read_indptr_d,
+                                   int64_t nnz, const int32_t* kv_indptr_d,
+                                   const int32_t* kv_indices_d, const int32_t* last_page_len_d,
+                                   const void* k, const void* v, int64_t page_stride,
+                                   int64_t num_pool_pages, void* k_out, void* v_out,
+                                   void* stream);
 
 /* merge_states ("Deep Dive - FlashInfer", "A worked split-KV example"):
  *   For every row r and head h, merge the states s = indptr_d[r] ..
@@ -370,7 +426,8 @@ pka_status pka_apply_rope(const pka_rope* rope, int32_t transpose, int32_t head_
  *   q [nnz_new, Hq, D], k_new and v_new [nnz_new, Hk, D] with row strides in
  *   elements; q and q_out may both be NULL; q_out may be q when q is
  *   contiguous.  e4m3 pools store the rotated float32 value divided by
- *   k_scale, rounded once, magnitudes above 448 clamped to 448.
+ *   k_scale, rounded once, magnitudes above 448 clamped to 448; 4-bit pools
+ *   store the groups of the rotated float32 values as pka_kv_dtype says.
  *   nnz_new is the rows of the buffers: rows from append_indptr_d[batch] on
  *   belong to no request (a padded batch); their q_out rows stay as they were.
  *   A row whose position lies outside its request's pages, or whose page id
@@ -411,7 +468,8 @@ pka_status pka_rope_append_paged_kv_cache(
  *   The copies run at once, so no page may be written twice or both read and
  *   written (src_d[i] == dst_d[i] is skipped).  Entries with a page id outside
  *   [0, num_pool_pages) or slots outside 0..page_size are skipped and
- *   PKA_ERR_METADATA is noted.  Alignment as in pka_append_paged_kv_cache
+ *   PKA_ERR_METADATA is noted.  Pages of 4-bit pools are copied with their
+ *   words.  Alignment as in pka_append_paged_kv_cache
  *   (layer_stride like page_stride); PKA_ERR_UNSUPPORTED: over 32767 layers,
  *   pages of 2 GB, ragged K/V. */
 pka_status pka_copy_pages(const pka_params* params, int32_t num_layers, void* k, void* v,

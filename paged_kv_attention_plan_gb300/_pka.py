@@ -20,6 +20,7 @@ PKA_NHD, PKA_HND = 0, 1
 PKA_MASK_NONE, PKA_MASK_CAUSAL, PKA_MASK_CUSTOM = 0, 1, 2
 PKA_SPLIT_OFF, PKA_SPLIT_AUTO, PKA_SPLIT_FIXED = 0, 1, 2
 PKA_KV_BF16, PKA_KV_FP8_E4M3 = 0, 1
+PKA_KV_INT4_G32, PKA_KV_INT4_G64, PKA_KV_INT4_G128 = 2, 3, 4
 PKA_ROPE_PLAIN, PKA_ROPE_LINEAR, PKA_ROPE_BY_PARTS = 0, 1, 2
 
 STATUS = {0: "PKA_OK", 1: "PKA_ERR_INVALID_ARG", 2: "PKA_ERR_METADATA", 3: "PKA_ERR_UNSUPPORTED",
@@ -33,7 +34,7 @@ EXPORTED = ["pka_status_str", "pka_version", "pka_validate", "pka_plan_create",
             "pka_plan_cascade", "pka_selftest_bounded_wait", "pka_check_indices",
             "pka_rope_init", "pka_apply_rope", "pka_rope_append_paged_kv_cache",
             "pka_copy_pages", "pka_alloc_pages", "pka_free_pages", "pka_fork_pages",
-            "pka_compact_pages"]
+            "pka_compact_pages", "pka_kv_page_bytes", "pka_read_paged_kv_cache"]
 
 
 class pka_params(ctypes.Structure):
@@ -138,6 +139,9 @@ def lib():
         L.pka_fork_pages.argtypes = [i32, vp, i32, i32, vp, vp, i32, vp, i32, vp, vp, vp, i32,
                                      vp, vp, vp, vp, vp]
         L.pka_compact_pages.argtypes = [vp, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp]
+        L.pka_kv_page_bytes.argtypes = [P(pka_params), P(i64)]
+        L.pka_read_paged_kv_cache.argtypes = [P(pka_params), i32, vp, vp, i64, vp, vp, vp, vp, vp,
+                                              i64, i64, vp, vp, vp]
         L.pka_last_error.argtypes = []
         L.pka_last_error.restype = ctypes.c_char_p
         for name in EXPORTED:
@@ -199,17 +203,29 @@ def _dev(t, name, dtype):
 
 def _dev_pool(t, name, params=None):
     """K/V pool: the last three dims contiguous; pages may be strided (5-D view).
-    bf16, or uint8 e4m3 codes when the params say so."""
+    bf16, or uint8 e4m3 codes or 4-bit pages [pages, bytes] when the params say so."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    want = (torch.uint8 if params is not None and params.kv_dtype == PKA_KV_FP8_E4M3
+    want = (torch.uint8 if params is not None and params.kv_dtype != PKA_KV_BF16
             else torch.bfloat16)
     if t.dtype != want:
         raise TypeError(f"{name} must be {want}, got {t.dtype}")
+    if params is not None and params.kv_dtype >= PKA_KV_INT4_G32:
+        _int4_pages(t, name, params)
+        return t.data_ptr()
     if t.dim() >= 3 and (t.stride(-1) != 1 or t.stride(-2) != t.shape[-1]
                          or t.stride(-3) != t.shape[-1] * t.shape[-2]):
         raise ValueError(f"{name}: the last three dims must be contiguous")
     return t.data_ptr()
+
+
+def _int4_pages(t, name, params):
+    """4-bit pages: [.., pages, bytes], the bytes of a page (pka_kv_page_bytes) contiguous."""
+    size = _page_bytes(params)
+    if t.dim() < 2 or t.shape[-1] != size or t.stride(-1) != 1 or \
+            (t.shape[-2] > 1 and t.stride(-2) < size):
+        raise ValueError(f"{name} must be [.., pages, {size}] with each page contiguous, got "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
 
 
 # The checks of the operators around the cache: their calls are a few
@@ -256,7 +272,21 @@ def _shape(*dims):
 def _here_pools(k, v, params, dev):
     """(pointer of k, of v, their shape, their strides) of K/V pools alike,
     [.., pages, P, Hk, D] or [.., pages, Hk, P, D] of the params' layout, each
-    page contiguous."""
+    page contiguous.  4-bit pools [.., pages, bytes] come back with two further
+    axes of length 1, so that the pages' axis is the fourth from the end."""
+    if params.kv_dtype >= PKA_KV_INT4_G32:
+        size = _page_bytes(params)
+        if isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor) and k.dtype is _U8 \
+                and v.dtype is _U8 and k.get_device() == dev and v.get_device() == dev:
+            shape, strides = k.shape, k.stride()
+            if len(shape) > 1 and shape[-1] == size and strides[-1] == 1 and v.shape == shape \
+                    and v.stride() == strides:
+                return k.data_ptr(), v.data_ptr(), shape + (1, 1), strides + (1, 1)
+        for t, name in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor) or t.dtype is not _U8 or t.get_device() != dev \
+                    or t.dim() < 2 or t.shape[-1] != size or t.stride(-1) != 1:
+                _refuse(t, name, _U8, dev, f"[.., pages, {size}] with each page contiguous")
+        raise ValueError("k and v must have one shape and the same strides")
     a, b, d = params.page_size, params.num_kv_heads, params.head_dim
     if params.layout != PKA_NHD:
         a, b = b, a
@@ -287,6 +317,10 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_KV_DTYPES = {"bf16": PKA_KV_BF16, "e4m3": PKA_KV_FP8_E4M3, "int4_g32": PKA_KV_INT4_G32,
+              "int4_g64": PKA_KV_INT4_G64, "int4_g128": PKA_KV_INT4_G128}
+
+
 def make_params(num_qo_heads, num_kv_heads, head_dim, page_size=1, layout="NHD",
                 mask_mode="causal", sm_scale=0.0, kv_ragged=False, split_mode="auto",
                 fixed_split_pages=1, num_sms=0, graph_max_batch=0, graph_max_qo_rows=0,
@@ -307,8 +341,7 @@ def make_params(num_qo_heads, num_kv_heads, head_dim, page_size=1, layout="NHD",
     p.graph_max_batch = graph_max_batch
     p.graph_max_qo_rows = graph_max_qo_rows
     p.graph_max_kv_tokens = graph_max_kv_tokens
-    p.kv_dtype = ({"bf16": PKA_KV_BF16, "e4m3": PKA_KV_FP8_E4M3}[kv_dtype]
-                  if isinstance(kv_dtype, str) else kv_dtype)
+    p.kv_dtype = _KV_DTYPES[kv_dtype] if isinstance(kv_dtype, str) else kv_dtype
     p.k_scale, p.v_scale = k_scale, v_scale
     p.decode_on_tensor_cores = int(bool(decode_on_tensor_cores))
     return p
@@ -462,6 +495,63 @@ def pka_append_paged_kv_cache(params, k_new, v_new, append_indptr, kv_indptr, kv
         _stream(stream))
     if check:
         _check(s, "pka_append_paged_kv_cache")
+    return s
+
+
+def pka_kv_page_bytes(params) -> int:
+    """Bytes of one page of the K (or V) pool."""
+    n = ctypes.c_int64()
+    _check(lib().pka_kv_page_bytes(ctypes.byref(params), ctypes.byref(n)), "pka_kv_page_bytes")
+    return n.value
+
+
+def _page_bytes(params) -> int:
+    """pka_kv_page_bytes of 4-bit params, without the call: the checks of a few
+    microseconds' calls use it."""
+    group = 32 << (params.kv_dtype - PKA_KV_INT4_G32)
+    d = params.head_dim
+    return (params.page_size * params.num_kv_heads * (d // 2 + d // group * 4) + 15) & ~15
+
+
+def pka_read_paged_kv_cache(params, begin, read_indptr, kv_indptr, kv_indices, last_page_len, k, v,
+                            page_stride, k_out=None, v_out=None, stream=None, check=True) -> int:
+    """Cached rows back as bf16: row t of request r (read_indptr) is its logical
+    position begin[r] + t (begin None: t).  k and v are the pools [pages, ...] and
+    page_stride theirs; k_out and v_out [rows, num_kv_heads, head_dim], one of
+    which may be None; rows past read_indptr[-1] are left."""
+    dev = torch.cuda.current_device()
+    some = k_out if k_out is not None else v_out
+    if not isinstance(some, torch.Tensor) or some.dim() != 3:
+        raise ValueError("k_out and v_out must be [rows, num_kv_heads, head_dim], one of them "
+                         "given")
+    rows, batch = some.shape[0], read_indptr.numel() - 1
+    shape = (rows, params.num_kv_heads, params.head_dim)
+    outs = []
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None and isinstance(t, torch.Tensor) and t.shape != shape:
+            raise ValueError(f"{name} must be {_shape(*shape)}, got {tuple(t.shape)}")
+        outs.append(None if t is None else _here(t, name, _BF16, dev))
+    at = None
+    if begin is not None:
+        at = _here(begin, "begin", _I32, dev)
+        if begin.numel() != batch:
+            raise ValueError(f"begin: {batch} values, got {begin.numel()}")
+    ind = _here(read_indptr, "read_indptr", _I32, dev)
+    ptr = _here(kv_indptr, "kv_indptr", _I32, dev)
+    idx = _here(kv_indices, "kv_indices", _I32, dev)
+    last = _here(last_page_len, "last_page_len", _I32, dev)
+    if kv_indptr.numel() != batch + 1 or last_page_len.numel() != batch:
+        raise ValueError("kv_indptr and last_page_len must describe read_indptr's requests")
+    kpool, vpool, pshape, strides = _here_pools(k, v, params, dev)
+    if len(pshape) != 4:
+        raise ValueError("k and v must be pools [pages, ...]")
+    if page_stride != strides[0] and pshape[0] > 1:
+        raise ValueError(f"page_stride: the pools' is {strides[0]}, got {page_stride}")
+    s = lib().pka_read_paged_kv_cache(
+        ctypes.byref(params), batch, at, ind, rows, ptr, idx, last, kpool, vpool,
+        int(page_stride), pshape[0], outs[0], outs[1], _here_stream(stream, dev))
+    if check and s:
+        _check(s, "pka_read_paged_kv_cache")
     return s
 
 

@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libpka.so")
 SOURCES = ["plan.cpp", "check.cpp", "decode.cu", "prefill.cu", "util.cu", "static_scratch.cu",
-           "rope.cu", "pages.cu"]
+           "rope.cu", "pages.cu", "kv4.cu", "decode4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,584 @@
+// Decode attention (one query row per request) over a cache held in 4 bits.
+//
+// The work list, the splits and the join of their pieces are the decode
+// kernel's (decode.cu); what differs is how a key's bytes become operands.
+// With origin z and step s of a key's group of elements and q the query,
+//   score = scale * sum over groups (s * (q . c) + z * sum(q)),
+//   o     = (sum p * s * c + sum p * z) / sum p,
+// so the codes c go to the tensor cores as they are and the words are applied
+// to scores and probabilities, one product a key and group instead of one an
+// element.
+//
+// A code becomes an f16 operand by one AND: four bits at the bottom of an f16
+// are the subnormal c * 2^-24, and at bits 4..7 16 c * 2^-24, exact and taken
+// at full rate by the MMA.  So a word of 8 codes takes one shift and four ANDs;
+// the 2^24 and the 16 are taken back in Q (K's products) and at the end (V's).
+// An OR with 1024's or 128's exponent would leave an offset of 1024 or 128 in
+// every product, whose cancellation costs the statistics 2^-17 or so.
+//   Q is scaled to f16 by a power of two per head that puts its largest element
+// in [2^14, 2^15): bf16 values down to 2^-28 of it stay exact.
+//   P goes to f16 with V's step in it, 11 bits against the 8 of bf16: p * s,
+// relative to the running maximum of log2(p) + log2(s) less 6, so it lies under
+// 2^15 (a maximum may be passed by 2^8 before the state is rescaled) and what
+// falls below f16's 2^-25 is under 2^-31 of the largest.
+//
+// Warps: each kv head of the CTA is served by several warps that take the item's
+// 32-key tiles in turn, so 16 warps work whatever the head count; their states
+// meet in shared memory at the end of an item.  Every warp brings its own tiles
+// in with cp.async, two stages ahead, and waits only for its own copies: there
+// is no producer, no barrier wait that could run out, and any page size, layout
+// and stride is one address a key.
+#include "decode_join.cuh"
+#include "pka_kv4.h"
+
+namespace pka {
+namespace {
+
+constexpr int kTile = 32;        // keys of a warp's step
+constexpr int kMaxWarps = 16;
+constexpr int kStages = 2;
+constexpr float kRescale = 8.0f;  // log2 units, as in decode.cu
+constexpr float kHeadroom = 6.0f;
+// log2 of a step, at least: below it p * s no longer counts against the other
+// keys, and p itself stays far from overflow
+constexpr float kLeastStep = -60.0f;
+
+template <int D, int GR>
+struct Shape {
+  static constexpr int G = D / GR;        // groups of a head
+  static constexpr int CH = D / 32;       // 16-byte chunks of a row of codes
+  static constexpr int ROW = D / 2;       // bytes of a row of codes
+  static constexpr int MT = D / 16;       // 16-row blocks of V^T
+  static constexpr int DL = GR / 8;       // elements of a group that a lane's V rows hold
+  static constexpr int CODES = kTile * ROW;
+  static constexpr int WORDS = kTile * G * 4;
+  static constexpr int STAGE = 2 * (CODES + WORDS);  // K codes, V codes, K words, V words
+  static constexpr int STATE = MT * 4 + 4 + 2 * G;   // floats of a lane's state
+  static constexpr int SLOT = STATE * 128;           // bytes of a warp's state
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// d += a . b for a 16x16 (row) and 16x8 (col) f16 fragment pair.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t float2_to_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Copy BYTES (4, 8 or 16) to shared memory, or zeros where `there` is false.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
+  const int n = there ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES),
+                 "r"(n)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+
+// The G words of a key.
+template <int G>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[G]) {
+  if constexpr (G == 1) {
+    w[0] = lds32(addr);
+  } else if constexpr (G == 2) {
+    const uint2 v = lds64(addr);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr));
+  }
+}
+
+__device__ __forceinline__ float step_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float origin_of(uint32_t w) {
+  return __uint_as_float(w & 0xffff0000u);
+}
+
+struct Decode4Args {
+  AttnArgs a;
+  int64_t code_bytes;  // of a page
+  int splits;          // warps of a kv head
+};
+
+// Rows are held as they lie in the page, 16-byte chunk j of key i at chunk
+// j ^ chunk_swap(i).  K's words are read by 8 keys (lane / 4) at a time and V's
+// by 4 keys (lane % 4), and both meet every bank once.
+template <int D>
+__device__ __forceinline__ int chunk_swap(int key) {
+  return D == 128 ? (key & 2) | (key >> 2 & 1) : key >> 2 & 1;
+}
+
+// The sum over the 8 lanes that hold one head's keys.
+__device__ __forceinline__ float sum_keys(float x) {
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  return x;
+}
+
+template <int D, int GR>
+__global__ void __launch_bounds__(32 * kMaxWarps, 1)
+    decode4_kernel(const __grid_constant__ Decode4Args p) {
+  using S = Shape<D, GR>;
+  constexpr int G = S::G, CH = S::CH, MT = S::MT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const AttnArgs& a = p.a;
+  const int i0 = a.cta_ptr[blockIdx.x], i1 = a.cta_ptr[blockIdx.x + 1];
+  if (i0 >= i1) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hpc = a.heads_per_cta, n_split = p.splits;
+  const int hl = warp % hpc, split = warp / hpc;
+  const int Hk = a.num_kv_heads, Hq = a.num_qo_heads, group = Hq / Hk;
+  const int P = a.page_size;
+  const int qd = lane & 3, grp = lane >> 2;
+  const float sc = a.scale_log2;
+  const uint32_t ring = smem_u32(smem) + warp * (kStages * S::STAGE);
+  // states that meet: floor(splits / 2) slots a head
+  float* const slots = reinterpret_cast<float*>(
+      smem + hpc * n_split * (kStages * S::STAGE) + hl * (n_split >> 1) * S::SLOT);
+
+  // ---- what this warp copies: its tiles of all items, one after another ----
+  const uint8_t* const kp = reinterpret_cast<const uint8_t*>(a.k);
+  const uint8_t* const vp = reinterpret_cast<const uint8_t*>(a.v);
+  // (unsigned: a key count may end right below 2^31)
+  uint32_t c_key = 0, c_end = 0;
+  int c_item = i0, c_head = 0, c_base = 0, c_page = 0;
+  auto next_tile = [&]() {  // to the next tile that exists, and its pages' ids
+    while (c_key >= c_end && c_item < i1) {
+      const PkaWorkItem* w = a.items + c_item++;
+      c_key = w->t0 + kTile * split;
+      c_end = w->t1;
+      c_head = w->kv_head0 + hl;
+      c_base = w->kv_base;
+    }
+    if (c_key < c_end)
+      c_page = a.kv_indices[c_base + min(c_key + lane, c_end - 1) / (uint32_t)P];
+  };
+  auto copy_tile = [&](int stage) {
+    if (c_key < c_end) {
+      const uint32_t at = ring + stage * S::STAGE;
+      const uint32_t slot = min(c_key + lane, c_end - 1) % (uint32_t)P;
+      const uint32_t idx = a.layout == PKA_NHD ? slot * Hk + c_head : (uint32_t)c_head * P + slot;
+      const int64_t page = (int64_t)c_page * a.page_stride;
+      const bool there = c_key + lane < c_end;
+      const int64_t words = page + p.code_bytes + (int64_t)idx * (4 * G);
+      copy_async<4 * G>(at + 2 * S::CODES + lane * (4 * G), kp + words, there);
+      copy_async<4 * G>(at + 2 * S::CODES + S::WORDS + lane * (4 * G), vp + words, there);
+      const int64_t row = page + (int64_t)idx * S::ROW;
+      const int ch = lane % CH;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int k = lane / CH + i * (32 / CH);
+        const int64_t from = __shfl_sync(0xffffffffu, row, k) + ch * 16;
+        const uint32_t to = at + k * S::ROW + ((ch ^ chunk_swap<D>(k)) << 4);
+        copy_async<16>(to, kp + from, c_key + k < c_end);
+        copy_async<16>(to + S::CODES, vp + from, c_key + k < c_end);
+      }
+      c_key += kTile * n_split;
+      next_tile();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  next_tile();
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) copy_tile(s);
+
+  // rows of the MMA's A fragments: row r of a 16-key block is key
+  // (r & 1) * 4 + (r & 7) / 2 (+ 8), so that V's lanes read keys t, t + 4, t + 8
+  // and t + 12 (t = lane % 4)
+  const int my_key = (grp & 1) * 4 + (grp >> 1);
+  const int k_swap = chunk_swap<D>(my_key);
+  const uint32_t k_lane = my_key * S::ROW + qd * 4;
+  // halves of a word: elements 0..3 and 4..7; groups of 32 give a lane one half
+  const uint32_t half_lo = S::DL == 4 && (grp & 1) ? 0x7632u : 0x5410u;
+
+  int stage = 0;
+  for (int ii = i0; ii < i1; ++ii) {
+    const PkaWorkItem w = a.items[ii];
+    const int head_base = (w.kv_head0 + hl) * group;
+    // Q^T fragments, head grp: elements 8 qd .. 8 qd + 7 of each 32-element
+    // chunk, in the order of K's operands, and the sums of q over the groups
+    uint32_t qf[2 * CH][2];
+    float cs[2], qs[G][2];
+    {
+      const bool real = grp < group;
+      const uint4* row = reinterpret_cast<const uint4*>(
+          a.q + ((int64_t)w.q_row0 * Hq + head_base + (real ? grp : 0)) * D);
+      float x[CH][8], most = 0.f, sum[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) sum[g] = 0.f;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        const uint4 v = real ? row[4 * j + qd] : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = bf16x2_to_float2(u[i]);
+          x[j][2 * i] = f.x;
+          x[j][2 * i + 1] = f.y;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          most = fmaxf(most, fabsf(x[j][i]));
+          sum[j * 32 / GR] += x[j][i];
+        }
+      }
+#pragma unroll
+      for (int off = 1; off < 4; off <<= 1) {
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+#pragma unroll
+        for (int g = 0; g < G; ++g) sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], off);
+      }
+      // 2^(14 - e) for the largest element's exponent e (kept from -100 on)
+      const int e = max((int)(__float_as_uint(most) >> 23) - 127, -100);
+      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+      const float down = ldexpf(sc, 24 - 14 + e);
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[j][i] * ((i & 1) ? up * 0.0625f : up);
+        qf[2 * j][0] = float2_to_f16x2(y[0], y[4]);
+        qf[2 * j][1] = float2_to_f16x2(y[1], y[5]);
+        qf[2 * j + 1][0] = float2_to_f16x2(y[2], y[6]);
+        qf[2 * j + 1][1] = float2_to_f16x2(y[3], y[7]);
+      }
+      // a lane's scores are of heads 2 qd and 2 qd + 1
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        cs[h] = __shfl_sync(0xffffffffu, down, (2 * qd + h) * 4);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          qs[g][h] = sc * __shfl_sync(0xffffffffu, sum[g], (2 * qd + h) * 4);
+      }
+    }
+    float acc[MT][4], zs[G][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) zs[g][0] = zs[g][1] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY};  // reference of the exponents (log2)
+    float l[2] = {0.f, 0.f};              // this lane's share of the sums
+    const int64_t mrow = ((int64_t)w.mask_hi << 32 | (uint32_t)w.mask_lo) +
+                         (int64_t)w.q_local0 * w.kv_len;
+
+    const uint32_t t1 = w.t1;
+    for (uint32_t a0 = w.t0 + kTile * split; a0 < t1; a0 += kTile * n_split) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();
+      const uint32_t at = ring + stage * S::STAGE;
+      // scores of keys my_key (+ 8) of both 16-key blocks, heads 2 qd and 2 qd + 1
+      float s[2][4];
+      float vstep[2][2][G], vorig[2][2][G];  // [block][key][group]
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        float sg[G][4];
+#pragma unroll
+        for (int g = 0; g < G; ++g) sg[g][0] = sg[g][1] = sg[g][2] = sg[g][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+          const uint32_t from = at + k_lane + b * 16 * S::ROW + ((j ^ k_swap) << 4);
+          const uint32_t w0 = lds32(from), w1 = lds32(from + 8 * S::ROW);
+          const uint32_t t0 = w0 >> 8, t1 = w1 >> 8;
+          float(&d)[4] = sg[j * 32 / GR];
+          mma16816(d, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u,
+                   qf[2 * j][0], qf[2 * j][1]);
+          mma16816(d, t0 & 0x000f000fu, t1 & 0x000f000fu, t0 & 0x00f000f0u, t1 & 0x00f000f0u,
+                   qf[2 * j + 1][0], qf[2 * j + 1][1]);
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int key = 16 * b + 8 * y + my_key;
+          uint32_t kw[G], vw[G];
+          lds_words<G>(at + 2 * S::CODES + key * (4 * G), kw);
+          lds_words<G>(at + 2 * S::CODES + S::WORDS + key * (4 * G), vw);
+          float d0 = 0.f, d1 = 0.f, z0 = 0.f, z1 = 0.f;
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const float ks = step_of(kw[g]), kz = origin_of(kw[g]);
+            d0 = fmaf(ks, sg[g][2 * y], d0);
+            d1 = fmaf(ks, sg[g][2 * y + 1], d1);
+            z0 = fmaf(kz, qs[g][0], z0);
+            z1 = fmaf(kz, qs[g][1], z1);
+          }
+          bool seen = a0 + key < t1;
+          if (a.mask_mode == PKA_MASK_CUSTOM && seen) {
+            const int64_t bit = mrow + a0 + key;
+            seen = (a.mask[bit >> 3] >> (bit & 7)) & 1;
+          }
+          s[b][2 * y] = seen ? fmaf(d0, cs[0], z0) : -INFINITY;
+          s[b][2 * y + 1] = seen ? fmaf(d1, cs[1], z1) : -INFINITY;
+          // an unseen key's words may hold anything: they become zeros
+          float most = 0.f;
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            vstep[b][y][g] = seen ? step_of(vw[g]) : 0.f;
+            vorig[b][y][g] = seen ? origin_of(vw[g]) : 0.f;
+            most = fmaxf(most, fabsf(vstep[b][y][g]));
+          }
+          const float up = fmaxf(lg2(most), kLeastStep);
+          top[0] = fmaxf(top[0], s[b][2 * y] + up);
+          top[1] = fmaxf(top[1], s[b][2 * y + 1] + up);
+        }
+      }
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], off));
+        top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], off));
+      }
+      float al[2] = {1.f, 1.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float want = top[h] - kHeadroom;
+        if (m[h] == -INFINITY) {
+          m[h] = want;
+        } else if (want > m[h] + kRescale) {
+          al[h] = ex2(m[h] - want);
+          m[h] = want;
+        }
+      }
+      if (al[0] != 1.f || al[1] != 1.f) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          l[h] *= al[h];
+#pragma unroll
+          for (int g = 0; g < G; ++g) zs[g][h] *= al[h];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            acc[mt][h] *= al[h];
+            acc[mt][2 + h] *= al[h];
+          }
+        }
+      }
+      // O^T += V^T . P^T, block by block
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = s[b][i] == -INFINITY ? 0.f : ex2(s[b][i] - m[i & 1]);
+        l[0] += e[0] + e[2];
+        l[1] += e[1] + e[3];
+        const uint32_t vat = at + S::CODES + (16 * b + qd) * S::ROW;
+        const int swap0 = chunk_swap<D>(qd), swap4 = chunk_swap<D>(qd + 4);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float s0 = vstep[b][0][g], s1 = vstep[b][1][g];
+          const float o0 = vorig[b][0][g], o1 = vorig[b][1][g];
+          zs[g][0] = fmaf(e[0], o0, fmaf(e[2], o1, zs[g][0]));
+          zs[g][1] = fmaf(e[1], o0, fmaf(e[3], o1, zs[g][1]));
+          const uint32_t pb0 = transpose8x8(float2_to_f16x2(e[0] * s0, e[1] * s0));
+          const uint32_t pb1 = transpose8x8(float2_to_f16x2(e[2] * s1, e[3] * s1));
+          // the lane's elements of keys t, t + 4, t + 8, t + 12 of this group
+          constexpr int WL = S::DL < 8 ? 1 : S::DL / 8;  // words
+          uint32_t v0[WL], v4[WL], v8[WL], v12[WL];
+          const int word = g * (GR / 8) + (grp * S::DL >> 3);  // of the row
+          const uint32_t c0 = vat + (((word >> 2) ^ swap0) << 4) + ((word & 3) << 2);
+          const uint32_t c4 = vat + 4 * S::ROW + (((word >> 2) ^ swap4) << 4) + ((word & 3) << 2);
+          if constexpr (WL == 2) {
+            const uint2 x0 = lds64(c0), x4 = lds64(c4), x8 = lds64(c0 + 8 * S::ROW),
+                        x12 = lds64(c4 + 8 * S::ROW);
+            v0[0] = x0.x, v0[1] = x0.y, v4[0] = x4.x, v4[1] = x4.y;
+            v8[0] = x8.x, v8[1] = x8.y, v12[0] = x12.x, v12[1] = x12.y;
+          } else {
+            v0[0] = lds32(c0), v4[0] = lds32(c4);
+            v8[0] = lds32(c0 + 8 * S::ROW), v12[0] = lds32(c4 + 8 * S::ROW);
+          }
+#pragma unroll
+          for (int q = 0; q < S::DL / 4; ++q) {  // four elements, two 16-row blocks
+            const uint32_t sel = S::DL == 4 ? half_lo : (q & 1) ? 0x7632u : 0x5410u;
+            const uint32_t x = __byte_perm(v0[q >> 1], v4[q >> 1], sel);
+            const uint32_t y = __byte_perm(v8[q >> 1], v12[q >> 1], sel);
+            const uint32_t x8 = x >> 8, y8 = y >> 8;
+            const int mt = (g * (S::DL / 4) + q) * 2;
+            mma16816(acc[mt], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u,
+                     pb0, pb1);
+            mma16816(acc[mt + 1], x8 & 0x000f000fu, x8 & 0x00f000f0u, y8 & 0x000f000fu,
+                     y8 & 0x00f000f0u, pb0, pb1);
+          }
+        }
+      }
+      __syncwarp();
+      copy_tile(stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+
+    // ---- the head's warps bring their states together, pair by pair ----
+    for (int n = n_split; n > 1;) {
+      const int half = (n + 1) >> 1;
+      float* const slot = slots + (split >= half ? split - half : split) * (S::SLOT / 4) + lane;
+      if (split >= half && split < n) {
+        int i = 0;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) slot[32 * i++] = acc[mt][x];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          slot[32 * i++] = m[h];
+          slot[32 * i++] = l[h];
+#pragma unroll
+          for (int g = 0; g < G; ++g) slot[32 * i++] = zs[g][h];
+        }
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(hl + 1), "r"(32 * n_split) : "memory");
+      if (split < n - half) {
+        const float* const tail = slot + 32 * 4 * MT;
+        float mine[2], other[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float om = tail[32 * (h * (2 + G))];
+          const float to = fmaxf(m[h], om);
+          mine[h] = m[h] == -INFINITY ? 0.f : ex2(m[h] - to);
+          other[h] = om == -INFINITY ? 0.f : ex2(om - to);
+          m[h] = to;
+          l[h] = l[h] * mine[h] + tail[32 * (h * (2 + G) + 1)] * other[h];
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+            zs[g][h] = zs[g][h] * mine[h] + tail[32 * (h * (2 + G) + 2 + g)] * other[h];
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            acc[mt][x] = acc[mt][x] * mine[x & 1] + slot[32 * (4 * mt + x)] * other[x & 1];
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(hl + 1), "r"(32 * n_split) : "memory");
+      n = half;
+    }
+    if (split) continue;
+
+    // ---- normalise and write: O and the LSE, or this piece's partial state ----
+    l[0] = sum_keys(l[0]);
+    l[1] = sum_keys(l[1]);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      zs[g][0] = sum_keys(zs[g][0]);
+      zs[g][1] = sum_keys(zs[g][1]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int head = head_base + 2 * qd + h;
+      if (2 * qd + h >= group) continue;
+      // a NaN among the words of a seen key makes the sums NaN, which is not "no key"
+      const bool none = l[h] == 0.f;
+      const float inv = none ? 0.f : 1.f / l[h];
+      const float even = inv * 16777216.f, odd = inv * 1048576.f;  // 2^24, 2^20
+      const float lse = none ? -INFINITY : m[h] + log2f(l[h]);
+      const int rec = w.out_rec + (head - w.kv_head0 * group);
+      uint16_t* orow = a.o + ((int64_t)w.q_row0 * Hq + head) * D;
+      float* prow = a.part_o + (int64_t)rec * D;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+#pragma unroll
+        for (int q = 0; q < S::DL / 4; ++q) {
+          const int mt = (g * (S::DL / 4) + q) * 2;
+          const float z = zs[g][h] * inv;
+          const float x0 = fmaf(acc[mt][h], even, z), x1 = fmaf(acc[mt][2 + h], odd, z);
+          const float x2 = fmaf(acc[mt + 1][h], even, z), x3 = fmaf(acc[mt + 1][2 + h], odd, z);
+          const int d = g * GR + grp * S::DL + 4 * q;
+          if (w.out_rec < 0)
+            *reinterpret_cast<uint2*>(orow + d) =
+                make_uint2(float2_to_bf16x2(x0, x1), float2_to_bf16x2(x2, x3));
+          else
+            *reinterpret_cast<float4*>(prow + d) = make_float4(x0, x1, x2, x3);
+        }
+      }
+      if (grp == 0) {
+        if (w.out_rec >= 0)
+          a.part_lse[rec] = lse;
+        else if (a.lse)
+          a.lse[(int64_t)w.q_row0 * Hq + head] = lse;
+      }
+    }
+    if (w.join >= 0 && a.joins) {
+      // count the piece in once its state is visible; the last one merges
+      PkaDecodeJoin* const jp = a.joins + w.join + hl;
+      __threadfence();
+      __syncwarp();
+      int last = 0;
+      if (lane == 0) last = atomicAdd(&jp->arrived, 1) == jp->nslots - 1;
+      if (__shfl_sync(0xffffffffu, last, 0)) {
+        __threadfence();
+        join_merge<D>(a, *jp, w.q_row0, head_base, group, lane);
+        __syncwarp();
+        if (lane == 0) jp->arrived = 0;  // re-armed for the next run
+      }
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <int D, int GR>
+cudaError_t launch_t(const AttnArgs& a, int num_ctas, cudaStream_t stream) {
+  using S = Shape<D, GR>;
+  Decode4Args p{};
+  p.a = a;
+  p.code_bytes = (int64_t)a.page_size * a.num_kv_heads * (D / 2);
+  const int hpc = a.heads_per_cta;
+  p.splits = kMaxWarps / hpc;
+  const int warps = hpc * p.splits;
+  const int smem = warps * kStages * S::STAGE + hpc * (p.splits / 2) * S::SLOT;
+  static_assert(kMaxWarps * kStages * S::STAGE + kMaxWarps / 2 * S::SLOT <= 227 * 1024,
+                "shared memory");
+  cudaError_t e = ensure_dynamic_smem<decode4_kernel<D, GR>>(smem);
+  if (e != cudaSuccess) return e;
+  decode4_kernel<D, GR><<<num_ctas, 32 * warps, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_decode4(const AttnArgs& a, int num_ctas, int head_dim, int group,
+                           cudaStream_t stream) {
+  if (head_dim == 128)
+    return group == 32   ? launch_t<128, 32>(a, num_ctas, stream)
+           : group == 64 ? launch_t<128, 64>(a, num_ctas, stream)
+                         : launch_t<128, 128>(a, num_ctas, stream);
+  return group == 32 ? launch_t<64, 32>(a, num_ctas, stream)
+                     : launch_t<64, 64>(a, num_ctas, stream);
+}
+
+}  // namespace pka

@@ -15,6 +15,7 @@
 
 #include "pka_cache.h"
 #include "pka_internal.h"
+#include "pka_kv4.h"
 
 namespace pka {
 namespace {
@@ -827,6 +828,9 @@ struct CopyArgs {
   int32_t layout;
   int32_t head_row;          // bytes of one head's row of a slot
   int32_t slot_row;          // bytes of all heads' rows of a slot
+  int32_t code_bytes;        // 4-bit pages: where the words start,
+  int32_t page_words;        // how many they are,
+  int32_t head_words;        // and of one head's row
   int32_t* err;
 };
 
@@ -838,6 +842,40 @@ __device__ __forceinline__ bool in_slots(const CopyArgs& a, uint32_t off, int sl
                             ? off / (uint32_t)a.slot_row
                             : off / (uint32_t)a.head_row % (uint32_t)a.page_size;
   return slot < (uint32_t)slots;
+}
+
+// Which 32-bit words of piece `off` of a 4-bit page belong to the first `slots`
+// slots: all or none of the codes' pieces, some of a piece of the words where a
+// slot (or the page) ends inside it.
+__device__ __forceinline__ uint32_t words_in_slots(const CopyArgs& a, uint32_t off, int slots) {
+  if (off < (uint32_t)a.code_bytes) return in_slots(a, off, slots) ? 15u : 0u;
+  uint32_t mask = 0;
+#pragma unroll
+  for (uint32_t i = 0; i < 4; ++i) {
+    const uint32_t word = (off - a.code_bytes) / 4 + i, row = word / (uint32_t)a.head_words;
+    const uint32_t slot = a.layout == PKA_NHD ? row / ((uint32_t)a.slot_row / a.head_row)
+                                              : row % (uint32_t)a.page_size;
+    mask |= (word < (uint32_t)a.page_words && slot < (uint32_t)slots ? 1u : 0u) << i;
+  }
+  return mask;
+}
+
+template <bool WORDS>
+__device__ __forceinline__ uint32_t piece_mask(const CopyArgs& a, uint32_t off, int slots) {
+  return WORDS ? words_in_slots(a, off, slots) : in_slots(a, off, slots) ? 15u : 0u;
+}
+
+template <bool WORDS>
+__device__ __forceinline__ void store_piece(uint8_t* to, const uint4& x, uint32_t mask) {
+  if (!WORDS || mask == 15u) {
+    *reinterpret_cast<uint4*>(to) = x;
+    return;
+  }
+  uint32_t* w = reinterpret_cast<uint32_t*>(to);
+  if (mask & 1u) w[0] = x.x;
+  if (mask & 2u) w[1] = x.y;
+  if (mask & 4u) w[2] = x.z;
+  if (mask & 8u) w[3] = x.w;
 }
 
 // Entry i of the list, or false for one that is skipped.
@@ -860,13 +898,15 @@ __device__ __forceinline__ bool copy_at(const CopyArgs& a, int64_t i, int64_t* f
 // that takes, each lane with its own list entries.  Bound by memory bandwidth:
 // 4,001 pages of 32 KB, K and V in four layers, take 310 us, 6.77 TB/s.  In us,
 // a stretch / SMALL: 60,000 pages of 64 B 18.9 / 5.7, of 1 KB 44.9 / 39.9, of
-// 2 KB 76.4 / 76.5, 20,000 of 8 KB 100.1 / 100.0.
-template <bool SMALL>
+// 2 KB 76.4 / 76.5, 20,000 of 8 KB 100.1 / 100.0.  WORDS: pages of 4-bit pools,
+// whose last pieces are copied word by word where a slot ends inside them.
+template <bool SMALL, bool WORDS>
 __global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
   constexpr int PIECES = 8, CHUNK = PIECES * 512;
   const int lane = threadIdx.x & 31;
   uint8_t* pool = (blockIdx.y & 1 ? a.v : a.k) + (blockIdx.y >> 1) * a.layer_bytes;
-  const uint32_t whole = (uint32_t)a.page_size * a.slot_row;
+  const uint32_t whole = WORDS ? ((uint32_t)a.code_bytes + a.page_words * 4u + 15u) & ~15u
+                               : (uint32_t)a.page_size * a.slot_row;
   const uint32_t chunks = (whole + CHUNK - 1) / CHUNK, pieces = whole / 16;
   int64_t n = a.max_copies;
   if (a.count) n = min(n, (int64_t)max(*a.count, 0));
@@ -877,6 +917,7 @@ __global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
     uint4 x[PIECES];
     if constexpr (SMALL) {
       int64_t put[PIECES];
+      uint32_t mask[PIECES];
       const int64_t at = w * (32 * PIECES) + lane;
       int64_t i = at <= UINT32_MAX ? (uint32_t)at / pieces : at / pieces;
       uint32_t piece = (uint32_t)(at - i * pieces);
@@ -885,7 +926,8 @@ __global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
         int64_t from, to;
         int slots;
         put[u] = -1;
-        if (i < n && copy_at(a, i, &from, &to, &slots, &bad) && in_slots(a, piece * 16, slots)) {
+        if (i < n && copy_at(a, i, &from, &to, &slots, &bad) &&
+            (mask[u] = piece_mask<WORDS>(a, piece * 16, slots))) {
           x[u] = *reinterpret_cast<const uint4*>(pool + from + piece * 16);
           put[u] = to + piece * 16;
         }
@@ -898,23 +940,23 @@ __global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
       }
 #pragma unroll
       for (int u = 0; u < PIECES; ++u)
-        if (put[u] >= 0) *reinterpret_cast<uint4*>(pool + put[u]) = x[u];
+        if (put[u] >= 0) store_piece<WORDS>(pool + put[u], x[u], mask[u]);
     } else {
       const int64_t i = w <= UINT32_MAX ? (uint32_t)w / chunks : w / chunks;
       const uint32_t off0 = (uint32_t)(w - i * chunks) * CHUNK + lane * 16;
       int64_t from, to;
       int slots;
       if (!copy_at(a, i, &from, &to, &slots, &bad)) continue;
-      bool take[PIECES];
+      uint32_t take[PIECES];
 #pragma unroll
       for (int u = 0; u < PIECES; ++u) {
         const uint32_t off = off0 + u * 512;
-        take[u] = off < whole && in_slots(a, off, slots);
+        take[u] = off < whole ? piece_mask<WORDS>(a, off, slots) : 0u;
         if (take[u]) x[u] = *reinterpret_cast<const uint4*>(pool + from + off);
       }
 #pragma unroll
       for (int u = 0; u < PIECES; ++u)
-        if (take[u]) *reinterpret_cast<uint4*>(pool + to + off0 + u * 512) = x[u];
+        if (take[u]) store_piece<WORDS>(pool + to + off0 + u * 512, x[u], take[u]);
     }
   }
   if (bad) note_error(a.err, PKA_ERR_METADATA);
@@ -1016,21 +1058,22 @@ pka_status pka_copy_pages(const pka_params* p, int32_t num_layers, void* k, void
   if (!pka::params_valid(p) || num_layers < 0 || max_copies < 0 || num_pool_pages < 0)
     return PKA_ERR_INVALID_ARG;
   if (p->head_dim != 64 && p->head_dim != 128) return PKA_ERR_UNSUPPORTED;
-  if (p->kv_ragged || num_layers > 32767) return PKA_ERR_UNSUPPORTED;
+  if (p->kv_ragged || num_layers > 32767 || !pka::kv4_supported(*p)) return PKA_ERR_UNSUPPORTED;
   if (num_layers == 0 || max_copies == 0) return PKA_OK;
   if (!k || !v || !src_d || !dst_d || page_stride <= 0) return PKA_ERR_INVALID_ARG;
   if (pka::unaligned(src_d) || pka::unaligned(dst_d) || pka::unaligned(slots_d) ||
       pka::unaligned(num_copies_d))
     return PKA_ERR_INVALID_ARG;
-  const bool f8 = p->kv_dtype == PKA_KV_FP8_E4M3;
-  const int item = f8 ? 1 : 2;
+  const int group = pka::kv4_group(p->kv_dtype);
+  const int item = p->kv_dtype == PKA_KV_BF16 ? 2 : 1;  // bytes of an element of a stride
   const uintptr_t mis = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
-  const int64_t whole16 = f8 ? 15 : 7;
+  const int64_t whole16 = pka::kv_stride_mask(p->kv_dtype);
   if ((mis & 15) || (page_stride & whole16)) return PKA_ERR_INVALID_ARG;
   if (num_layers > 1 && (layer_stride <= 0 || (layer_stride & whole16)))
     return PKA_ERR_INVALID_ARG;
   pka::CopyArgs a{};
-  const int64_t slot_row = (int64_t)p->num_kv_heads * p->head_dim * item;
+  const int head_row = group ? p->head_dim / 2 : p->head_dim * item;
+  const int64_t slot_row = (int64_t)p->num_kv_heads * head_row;
   if (slot_row > INT32_MAX / p->page_size) return PKA_ERR_UNSUPPORTED;  // a page of 2 GB
   a.k = static_cast<uint8_t*>(k);
   a.v = static_cast<uint8_t*>(v);
@@ -1044,20 +1087,32 @@ pka_status pka_copy_pages(const pka_params* p, int32_t num_layers, void* k, void
   a.max_copies = max_copies;
   a.page_size = p->page_size;
   a.layout = p->layout;
-  a.head_row = p->head_dim * item;
+  a.head_row = head_row;
   a.slot_row = (int32_t)slot_row;
   a.err = pka::device_error_word();
-  const int64_t page = p->page_size * slot_row;
+  int64_t page = p->page_size * slot_row;
+  if (group) {
+    a.code_bytes = (int32_t)page;
+    a.head_words = p->head_dim / group;
+    a.page_words = (int32_t)(pka::kv4_word_bytes(*p) / 4);
+    page += pka::kv4_word_bytes(*p);
+    if (page_stride < page) return PKA_ERR_INVALID_ARG;
+    page = (page + 15) & ~int64_t(15);
+  }
   const bool small = page < 2048;
   const int64_t units = small ? (max_copies * page + 4095) / 4096
                               : max_copies * ((page + 4095) / 4096);
   const int per_sm = 16 / (2 * num_layers) > 1 ? 16 / (2 * num_layers) : 1;
   const dim3 grid((unsigned)pka::blocks_for(units, 8, per_sm), (unsigned)(2 * num_layers));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (small)
-    pka::copy_kernel<true><<<grid, 256, 0, st>>>(a);
+  if (group && small)
+    pka::copy_kernel<true, true><<<grid, 256, 0, st>>>(a);
+  else if (group)
+    pka::copy_kernel<false, true><<<grid, 256, 0, st>>>(a);
+  else if (small)
+    pka::copy_kernel<true, false><<<grid, 256, 0, st>>>(a);
   else
-    pka::copy_kernel<false><<<grid, 256, 0, st>>>(a);
+    pka::copy_kernel<false, false><<<grid, 256, 0, st>>>(a);
   return pka::done(cudaGetLastError(), "page copy launch");
 }
 

@@ -1,0 +1,146 @@
+// K/V held in 4 bits: the page format and the launches that know it.
+//
+// A page of the K (or V) pool is one run of bytes:
+//   codes [P, Hk, D/2] (HND: [Hk, P, D/2]): element 2i of a head in the low
+//     half of byte i, element 2i + 1 in the high half;
+//   words [P, Hk, G] (HND: [Hk, P, G]): one 32-bit word for each of the G =
+//     D / group groups of a head, a bf16 step in the low half and a bf16 origin
+//     in the high half;
+// padded to a multiple of 16 bytes.  Code c stands for origin + step * c.
+// Codes and words lie apart so that both start on whole 16-byte pieces for
+// every head count: a row of 64 bytes with its word beside it would start on
+// multiples of 4.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pka.h"
+#include "pka_internal.h"
+
+namespace pka {
+
+// Elements of a group, or 0 for K/V in other types.
+inline int kv4_group(int kv_dtype) {
+  return kv_dtype == PKA_KV_INT4_G32    ? 32
+         : kv_dtype == PKA_KV_INT4_G64  ? 64
+         : kv_dtype == PKA_KV_INT4_G128 ? 128
+                                        : 0;
+}
+
+// Bytes of the codes and of the words of one page.
+inline int64_t kv4_code_bytes(const pka_params& p) {
+  return (int64_t)p.page_size * p.num_kv_heads * (p.head_dim / 2);
+}
+inline int64_t kv4_word_bytes(const pka_params& p) {
+  return (int64_t)p.page_size * p.num_kv_heads * (p.head_dim / kv4_group(p.kv_dtype)) * 4;
+}
+
+// Whether 4-bit parameters describe something built: paged K/V, groups of at
+// most a head, pages under 2 GB (a row's place in its page is 32 bits wide).
+inline bool kv4_supported(const pka_params& p) {
+  const int g = kv4_group(p.kv_dtype);
+  if (g == 0) return true;
+  if (g > p.head_dim || p.kv_ragged) return false;
+  return (int64_t)p.num_kv_heads * (p.head_dim / 2 + p.head_dim / g * 4) <=
+         (INT32_MAX - 15) / p.page_size;
+}
+
+// Largest calls of the kernels in kv4.cu: heads make the second grid axis,
+// rows the first.
+constexpr int kKvMaxHeads = 4096;
+constexpr int64_t kKvMaxRows = INT64_C(1) << 33;
+
+// Elements of 16 bytes in a pool, less one: what a stride in elements may not have set.
+inline int64_t kv_stride_mask(int kv_dtype) { return kv_dtype == PKA_KV_BF16 ? 7 : 15; }
+
+// Where the rows of a call lie in the pools.
+struct KvRows {
+  // rows of requests: row t of request r is position begin[r] + t (begin null: 0
+  // for a read, the request's last rows for an append)
+  int32_t batch;
+  const int32_t* begin;
+  const int32_t* row_indptr;
+  const int32_t* kv_indptr;
+  const int32_t* last_page_len;
+  int64_t num_pages;         // of the pools; INT64_MAX: page ids are trusted
+  // or rows of the plan's units (units not null)
+  const PkaDequantUnit* units;
+  int32_t num_units;
+  const int32_t* counts;     // graph mode: the plan's unit and row counts on the device
+  int64_t rows;
+  const int32_t* kv_indices;
+  int64_t page_stride;       // elements
+  int32_t page_size;
+  int32_t layout;
+  int32_t heads;
+  int32_t* err;
+};
+
+// bf16 rows [rows, heads, D] quantised into 4-bit pools.
+cudaError_t launch_append4(const KvRows& r, int head_dim, int group, const uint16_t* k_new,
+                           const uint16_t* v_new, uint8_t* k, uint8_t* v, cudaStream_t stream);
+// Rows of pools of any type to bf16 [rows, heads, D]; an output may be null.
+cudaError_t launch_read(const KvRows& r, int kv_dtype, int head_dim, float k_scale, float v_scale,
+                        const void* k, const void* v, uint16_t* k_out, uint16_t* v_out,
+                        cudaStream_t stream);
+// Decode rows over 4-bit pools.
+cudaError_t launch_decode4(const AttnArgs& a, int num_ctas, int head_dim, int group,
+                           cudaStream_t stream);
+
+#ifdef __CUDACC__
+// The step and origin of a group whose least and greatest elements are given,
+// and the reciprocal that the codes are made with (0: every code is 0).
+//   A step is the range's 15th and an origin the least element, each rounded to
+// bf16: 8 significant bits leave a step within 2^-9, a 33rd of a step over 15
+// codes, and 16 bits more a group would be spent on it.  A range that is not
+// finite (an infinity or NaN in the group) makes both NaN, so the group reads
+// back as NaN; a range too small for a normal bf16 step is held as its origin.
+struct Group4 {
+  uint32_t word;
+  float step, origin, inv;
+};
+
+__device__ __forceinline__ Group4 group4(float lo, float hi) {
+  Group4 g;
+  const float range = hi - lo;
+  if (!(fabsf(range) <= 3.402823466e38f)) {
+    g.word = 0x7fc07fc0u;
+    g.step = g.origin = g.inv = 0.f;
+    return g;
+  }
+  uint32_t s;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(s) : "f"(lo), "f"(__fdiv_rn(range, 15.f)));
+  if ((s & 0x7fffu) < 0x0080u) s &= 0xffff0000u;
+  g.word = s;
+  g.step = __uint_as_float(s << 16);
+  g.origin = __uint_as_float(s & 0xffff0000u);
+  g.inv = g.step > 0.f ? __frcp_rn(g.step) : 0.f;
+  return g;
+}
+
+// 8 codes of a group, element i in bits 4i.
+//   The quotient (x - origin) / step is the product with the reciprocal,
+// corrected by its residual: exact where the quotient is a float32, so ties
+// round to even as after a division, and elsewhere no quotient of 24-bit by
+// 8-bit numbers that matters lies near a tie.  The sum with 1.5 * 2^23 rounds
+// it; the code is then the low bits.
+__device__ __forceinline__ uint32_t codes4(const float (&x)[8], const Group4& g) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float d = x[i] - g.origin;
+    float q = d * g.inv;
+    q = fmaf(fmaf(-q, g.step, d), g.inv, q);
+    q = fminf(fmaxf(q, 0.f), 15.f);
+    w += __float_as_uint(q + 12582912.f) << (4 * i);
+  }
+  // each float's bits are 0x4b400000 + code: their sum, shifted, is taken off
+  constexpr uint32_t kBias = 0x4b400000u;
+  uint32_t off = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) off += kBias << (4 * i);
+  return w - off;
+}
+#endif
+
+}  // namespace pka

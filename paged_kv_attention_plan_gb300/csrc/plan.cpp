@@ -17,6 +17,7 @@
 
 #include "pka_cache.h"
 #include "pka_internal.h"
+#include "pka_kv4.h"
 
 using pka::AttnArgs;
 
@@ -112,7 +113,7 @@ bool params_ok(const pka_params* p) {
   if (p->split_mode == PKA_SPLIT_FIXED && p->fixed_split_pages < 1) return false;
   if (!p->kv_ragged && p->page_size < 1) return false;
   if (p->num_sms < 0) return false;
-  if (p->kv_dtype != PKA_KV_BF16 && p->kv_dtype != PKA_KV_FP8_E4M3) return false;
+  if (p->kv_dtype < PKA_KV_BF16 || p->kv_dtype > PKA_KV_INT4_G128) return false;
   if (!std::isfinite(p->k_scale) || !std::isfinite(p->v_scale)) return false;
   return true;
 }
@@ -124,8 +125,12 @@ pka_status check_supported(const pka_params* p) {
   if (g != 1 && g != 2 && g != 4 && g != 8) return PKA_ERR_UNSUPPORTED;
   if (p->head_dim != 64 && p->head_dim != 128) return PKA_ERR_UNSUPPORTED;
   if (p->graph_max_batch > 0 && p->split_mode == PKA_SPLIT_FIXED) return PKA_ERR_UNSUPPORTED;
+  if (!pka::kv4_supported(*p)) return PKA_ERR_UNSUPPORTED;
   return PKA_OK;
 }
+
+// e4m3 and 4-bit K/V: decode rows read the codes, other rows a bf16 scratch.
+bool has_codes(const pka_params* p) { return p->kv_dtype != PKA_KV_BF16; }
 
 bool graph_mode(const pka_params* p) { return p->graph_max_batch > 0; }
 
@@ -154,7 +159,7 @@ GraphCaps graph_caps(const pka_params* p, int num_sms) {
     c.joins = B * p->num_kv_heads;
     c.records = c.dec_items * hpc * g;
   }
-  if (p->kv_dtype == PKA_KV_FP8_E4M3 && p->graph_max_kv_tokens > 0) {
+  if (has_codes(p) && p->graph_max_kv_tokens > 0) {
     // one unit per request with qo_len >= 2; its keys count against the
     // declared K/V token capacity
     c.dequant_units = B;
@@ -221,23 +226,24 @@ pka_status derive(const pka_params* p, int32_t batch, const int32_t* qo, const i
   return PKA_OK;
 }
 
-// e4m3 K/V: decode rows read the codes; rows with qo_len >= 2 read a bf16
-// scratch decoded in run(), whose size depends on the batch: graph mode
+// e4m3 and 4-bit K/V: decode rows read the codes; rows with qo_len >= 2 read a
+// bf16 scratch decoded in run(), whose size depends on the batch: graph mode
 // (fixed workspaces) sizes it by graph_max_kv_tokens and refuses such rows
 // when that capacity is not declared.
 pka_status check_kv_dtype(const pka_params* p, const Batch& b) {
-  if (p->kv_dtype != PKA_KV_FP8_E4M3 || !graph_mode(p) || p->graph_max_kv_tokens > 0)
+  if (!has_codes(p) || !graph_mode(p) || p->graph_max_kv_tokens > 0)
     return PKA_OK;
   const int32_t tc_rows = p->decode_on_tensor_cores ? 1 : 2;  // rows the tensor-core kernel takes
   for (int32_t q : b.qo_len)
     if (q >= tc_rows) {
-      pka::set_last_error("graph mode over e4m3 pools with qo_len >= 2 rows needs graph_max_kv_tokens");
+      pka::set_last_error("graph mode over e4m3 or 4-bit pools with qo_len >= 2 rows needs "
+                          "graph_max_kv_tokens");
       return PKA_ERR_UNSUPPORTED;
     }
   return PKA_OK;
 }
 
-// e4m3 K/V: one dequant unit per request (or cascade node) that tensor-core
+// e4m3 and 4-bit K/V: one dequant unit per request (or cascade node) that tensor-core
 // items read, identified by its page-list start kv_base (distinct for every
 // node with pages), its scratch rows back to back in the order the items meet
 // them; the items' kv_base is rewritten to the node's first scratch row (the
@@ -675,7 +681,7 @@ pka_status plan_levels(pka_plan_t plan, const pka_params* p, const std::vector<B
   plan_decode(p, lv, num_sms, &L);
   plan_prefill(p, lv, num_sms, &L);
   if (cascade) build_slot_merges(&L, nnz, p->num_qo_heads);
-  if (p->kv_dtype == PKA_KV_FP8_E4M3 && !L.pre_items.empty()) plan_dequant(&L);
+  if (has_codes(p) && !L.pre_items.empty()) plan_dequant(&L);
   if (L.dequant_rows > INT32_MAX) return PKA_ERR_UNSUPPORTED;
   GraphCaps caps;
   if (graph) {
@@ -746,7 +752,7 @@ pka_status plan_levels(pka_plan_t plan, const pka_params* p, const std::vector<B
   size_t rec_o_al = (rec_o + 255) & ~size_t(255);
   info.float_ws_bytes =
       layout_records ? rec_o_al + (((size_t)layout_records * 4 + 255) & ~size_t(255)) : 0;
-  // e4m3 K/V: the bf16 K and V scratch follow the partial states
+  // e4m3 and 4-bit K/V: the bf16 K and V scratch follow the partial states
   info.float_ws_bytes += 2 * kv_scratch_bytes(p, scratch_rows);
   info.kv_scratch_rows = (int32_t)L.dequant_rows;
   info.num_requests = batch;
@@ -954,8 +960,12 @@ pka_status pka_run(pka_plan_t plan, const pka_params* p, const void* q, const vo
   const uintptr_t mis = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) |
                         reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(o);
   const bool fp8 = p->kv_dtype == PKA_KV_FP8_E4M3;
-  // page stride in elements: 16 bytes for bf16 (8 elements) or e4m3 (16)
-  if ((mis & 15) || (!p->kv_ragged && (page_stride & (fp8 ? 15 : 7)))) return PKA_ERR_INVALID_ARG;
+  const bool int4 = pka::kv4_group(p->kv_dtype) != 0;
+  // page stride in elements: 16 bytes for bf16 (8 elements), e4m3 or 4 bits (16)
+  if ((mis & 15) || (!p->kv_ragged && (page_stride & pka::kv_stride_mask(p->kv_dtype))))
+    return PKA_ERR_INVALID_ARG;
+  if (int4 && page_stride < pka::kv4_code_bytes(*p) + pka::kv4_word_bytes(*p))
+    return PKA_ERR_INVALID_ARG;
   if (p->mask_mode == PKA_MASK_CUSTOM && !mask) return PKA_ERR_INVALID_ARG;
   if (float_ws_bytes < plan->info.float_ws_bytes || (plan->info.float_ws_bytes && !float_ws))
     return PKA_ERR_WORKSPACE;
@@ -999,7 +1009,10 @@ pka_status pka_run(pka_plan_t plan, const pka_params* p, const void* q, const vo
     a.joins = h.off_decode_joins
                   ? reinterpret_cast<PkaDecodeJoin*>(plan->int_ws_d + h.off_decode_joins)
                   : nullptr;
-    cudaError_t e = pka::launch_decode(a, h.num_decode_ctas, p->head_dim, g, &plan->decode_maps, st);
+    cudaError_t e =
+        int4 ? pka::launch_decode4(a, h.num_decode_ctas, p->head_dim,
+                                   pka::kv4_group(p->kv_dtype), st)
+             : pka::launch_decode(a, h.num_decode_ctas, p->head_dim, g, &plan->decode_maps, st);
     if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   }
   if (graph || h.num_prefill_items > 0) {
@@ -1010,7 +1023,7 @@ pka_status pka_run(pka_plan_t plan, const pka_params* p, const void* q, const vo
     int64_t kv_rows = graph ? p->graph_max_kv_tokens : plan->info.total_kv;
     pka::AttnArgs pa = a;
     if (graph ? plan->dequant_capacity > 0 : h.num_dequant_units > 0) {
-      // e4m3 K/V: decode the keys of the tensor-core requests to bf16 in the
+      // e4m3 and 4-bit K/V: decode the keys of the tensor-core requests to bf16 in the
       // float workspace (after the partial states); the tensor-core kernel
       // then reads them as ragged K/V.  Graph mode lays the scratch out for
       // its capacity and launches on that fixed size; the dequant kernel
@@ -1023,11 +1036,28 @@ pka_status pka_run(pka_plan_t plan, const pka_params* p, const void* q, const vo
       uint16_t* sv = reinterpret_cast<uint16_t*>(base + kv_scratch_bytes(p, plan->scratch_capacity));
       const int32_t* counts =
           graph ? plan->int_ws_d + offsetof(PkaImageHeader, num_dequant_units) / 4 : nullptr;
-      cudaError_t e = pka::launch_dequant(
-          reinterpret_cast<const PkaDequantUnit*>(plan->int_ws_d + h.off_dequant_units),
-          graph ? plan->dequant_capacity : h.num_dequant_units,
-          graph ? plan->scratch_capacity : h.dequant_rows, counts, kv_indices, k, v, page_stride,
-          p->page_size, p->layout, p->kv_ragged, p->num_kv_heads, p->head_dim, sk, sv, st);
+      const auto* units =
+          reinterpret_cast<const PkaDequantUnit*>(plan->int_ws_d + h.off_dequant_units);
+      const int n_units = graph ? plan->dequant_capacity : h.num_dequant_units;
+      const int64_t n_rows = graph ? plan->scratch_capacity : h.dequant_rows;
+      cudaError_t e;
+      if (int4) {
+        pka::KvRows r{};
+        r.units = units;
+        r.num_units = n_units;
+        r.counts = counts;
+        r.rows = n_rows;
+        r.kv_indices = kv_indices;
+        r.page_stride = page_stride;
+        r.page_size = p->page_size;
+        r.layout = p->layout;
+        r.heads = p->num_kv_heads;
+        e = pka::launch_read(r, p->kv_dtype, p->head_dim, 1.f, 1.f, k, v, sk, sv, st);
+      } else {
+        e = pka::launch_dequant(units, n_units, n_rows, counts, kv_indices, k, v, page_stride,
+                                p->page_size, p->layout, p->kv_ragged, p->num_kv_heads,
+                                p->head_dim, sk, sv, st);
+      }
       if (e != cudaSuccess) return cuda_fail(e, "dequant launch");
       pa.k = sk;
       pa.v = sv;
@@ -1067,6 +1097,10 @@ pka_status pka_append_paged_kv_cache(const pka_params* p, int32_t batch, const v
   if (p->head_dim != 64 && p->head_dim != 128) return PKA_ERR_UNSUPPORTED;
 
   if (p->kv_ragged) return PKA_ERR_UNSUPPORTED;
+  const int group = pka::kv4_group(p->kv_dtype);
+  if (!pka::kv4_supported(*p)) return PKA_ERR_UNSUPPORTED;
+  if (group && (p->num_kv_heads > pka::kKvMaxHeads || nnz_new > pka::kKvMaxRows))
+    return PKA_ERR_UNSUPPORTED;
   if (nnz_new == 0 || batch == 0) return PKA_OK;
   if (!k_new || !v_new || !append_indptr || !kv_indptr || !kv_indices || !last_page_len || !k ||
       !v || page_stride <= 0)
@@ -1075,13 +1109,92 @@ pka_status pka_append_paged_kv_cache(const pka_params* p, int32_t batch, const v
   // stride of whole 16-byte units (8 bf16 or 16 e4m3 elements)
   const uintptr_t mis = reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new) |
                         reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
-  if ((mis & 15) || (page_stride & (p->kv_dtype == PKA_KV_FP8_E4M3 ? 15 : 7)))
-    return PKA_ERR_INVALID_ARG;
+  if ((mis & 15) || (page_stride & pka::kv_stride_mask(p->kv_dtype))) return PKA_ERR_INVALID_ARG;
+  if (group) {
+    for (const int32_t* x : {append_indptr, kv_indptr, kv_indices, last_page_len})
+      if (reinterpret_cast<uintptr_t>(x) & 3) return PKA_ERR_INVALID_ARG;
+    if (page_stride < pka::kv4_code_bytes(*p) + pka::kv4_word_bytes(*p)) return PKA_ERR_INVALID_ARG;
+    pka::KvRows r{};
+    r.batch = batch;
+    r.row_indptr = append_indptr;
+    r.kv_indptr = kv_indptr;
+    r.last_page_len = last_page_len;
+    r.num_pages = INT64_MAX;
+    r.rows = nnz_new;
+    r.kv_indices = kv_indices;
+    r.page_stride = page_stride;
+    r.page_size = p->page_size;
+    r.layout = p->layout;
+    r.heads = p->num_kv_heads;
+    r.err = pka::device_error_word();
+    cudaError_t e = pka::launch_append4(r, p->head_dim, group, static_cast<const uint16_t*>(k_new),
+                                        static_cast<const uint16_t*>(v_new),
+                                        static_cast<uint8_t*>(k), static_cast<uint8_t*>(v),
+                                        static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKA_OK : cuda_fail(e, "append launch");
+  }
   cudaError_t e = pka::launch_append(*p, batch, static_cast<const uint16_t*>(k_new),
                                      static_cast<const uint16_t*>(v_new), append_indptr, nnz_new,
                                      kv_indptr, kv_indices, last_page_len, k, v, page_stride,
                                      static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKA_OK : cuda_fail(e, "append launch");
+}
+
+pka_status pka_kv_page_bytes(const pka_params* p, int64_t* bytes) {
+  if (!params_ok(p) || !bytes) return PKA_ERR_INVALID_ARG;
+  if (p->kv_ragged || !pka::kv4_supported(*p)) return PKA_ERR_UNSUPPORTED;
+  if (p->head_dim != 64 && p->head_dim != 128) return PKA_ERR_UNSUPPORTED;
+  if (pka::kv4_group(p->kv_dtype)) {
+    *bytes = (pka::kv4_code_bytes(*p) + pka::kv4_word_bytes(*p) + 15) & ~int64_t(15);
+  } else {
+    *bytes = (int64_t)p->page_size * p->num_kv_heads * p->head_dim *
+             (p->kv_dtype == PKA_KV_FP8_E4M3 ? 1 : 2);
+  }
+  return PKA_OK;
+}
+
+pka_status pka_read_paged_kv_cache(const pka_params* p, int32_t batch, const int32_t* begin,
+                                   const int32_t* read_indptr, int64_t nnz,
+                                   const int32_t* kv_indptr, const int32_t* kv_indices,
+                                   const int32_t* last_page_len, const void* k, const void* v,
+                                   int64_t page_stride, int64_t num_pool_pages, void* k_out,
+                                   void* v_out, void* stream) {
+  if (!params_ok(p) || batch < 0 || nnz < 0 || num_pool_pages < 0) return PKA_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128) return PKA_ERR_UNSUPPORTED;
+  if (p->kv_ragged || !pka::kv4_supported(*p)) return PKA_ERR_UNSUPPORTED;
+  if (p->num_kv_heads > pka::kKvMaxHeads || nnz > pka::kKvMaxRows) return PKA_ERR_UNSUPPORTED;
+  if (nnz == 0 || batch == 0 || (!k_out && !v_out)) return PKA_OK;
+  if (!read_indptr || !kv_indptr || !kv_indices || !last_page_len || (k_out && !k) ||
+      (v_out && !v) || page_stride <= 0)
+    return PKA_ERR_INVALID_ARG;
+  for (const int32_t* x : {begin, read_indptr, kv_indptr, kv_indices, last_page_len})
+    if (reinterpret_cast<uintptr_t>(x) & 3) return PKA_ERR_INVALID_ARG;
+  uintptr_t mis = reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out);
+  if (k_out) mis |= reinterpret_cast<uintptr_t>(k);
+  if (v_out) mis |= reinterpret_cast<uintptr_t>(v);
+  if ((mis & 15) || (page_stride & pka::kv_stride_mask(p->kv_dtype))) return PKA_ERR_INVALID_ARG;
+  if (pka::kv4_group(p->kv_dtype) &&
+      page_stride < pka::kv4_code_bytes(*p) + pka::kv4_word_bytes(*p))
+    return PKA_ERR_INVALID_ARG;
+  pka::KvRows r{};
+  r.batch = batch;
+  r.begin = begin;
+  r.row_indptr = read_indptr;
+  r.kv_indptr = kv_indptr;
+  r.last_page_len = last_page_len;
+  r.num_pages = num_pool_pages;
+  r.rows = nnz;
+  r.kv_indices = kv_indices;
+  r.page_stride = page_stride;
+  r.page_size = p->page_size;
+  r.layout = p->layout;
+  r.heads = p->num_kv_heads;
+  r.err = pka::device_error_word();
+  cudaError_t e = pka::launch_read(
+      r, p->kv_dtype, p->head_dim, p->k_scale > 0.f ? p->k_scale : 1.f,
+      p->v_scale > 0.f ? p->v_scale : 1.f, k, v, static_cast<uint16_t*>(k_out),
+      static_cast<uint16_t*>(v_out), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKA_OK : cuda_fail(e, "read launch");
 }
 
 pka_status pka_merge_states(const float* v, const float* lse, const int32_t* indptr,

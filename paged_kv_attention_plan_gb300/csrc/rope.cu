@@ -14,6 +14,7 @@
 #include "pka_cache.h"
 #include "pka_device.cuh"
 #include "pka_internal.h"
+#include "pka_kv4.h"
 
 namespace pka {
 namespace {
@@ -24,6 +25,9 @@ enum RopeLayout {
   kAdjacent = 1,   // (x[2i], x[2i + 1])
   kScattered = 2,  // (x[i], x[i + R/2]), any other R: through shared memory
 };
+
+// What the pools hold.
+enum PoolType { kBf16 = 0, kE4m3 = 1, kInt4 = 2 };
 
 constexpr int kMaxHeads = 4096;            // of a row; keeps the second grid axis small
 constexpr int64_t kMaxRows = INT64_C(1) << 33;  // eight a block
@@ -56,6 +60,8 @@ struct RopeArgs {
   int layout;
   float k_scale, v_scale;    // e4m3 pools
   float k_inv, v_inv;        // pow2_reciprocal of these
+  int group;                 // 4-bit pools: elements of a group,
+  int64_t code_bytes;        // and where a page's words start
   int32_t* err;
   uint64_t turns[64];        // F_i
 };
@@ -106,6 +112,12 @@ __device__ __forceinline__ void round_turned(uint32_t& w, float lo, float hi, in
   w = turned > 1 ? y : (y & 0xffffu) | (w & 0xffff0000u);
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 __device__ __forceinline__ void to_shared(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -146,17 +158,20 @@ __device__ __forceinline__ void from_shared(const float* p, float (&x)[8]) {
 // 128 elements turned 46.6 / 42.4, 16,387 with 126 88.2 / 93.4, an append of
 // 9,216 with 40 50.6 / 46.3).
 // Into e4m3 pools both pieces are held as floats: three blocks, 80 registers
-// and 12 to 36 bytes spilled.
+// and 12 to 36 bytes spilled.  Into 4-bit pools the rotated floats of a step go
+// through shared memory, whatever the layout: a group's elements lie in pieces
+// of several lanes, and behind it a lane holds 16 elements in a row.
 constexpr int kInFlight = 2;
 
-template <int D, int L, bool APPEND, bool F8>
-__global__ void __launch_bounds__(256, F8 ? 3 : 4)
+template <int D, int L, bool APPEND, int POOL>
+__global__ void __launch_bounds__(256, POOL != kBf16 ? 3 : 4)
 rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr bool F8 = POOL == kE4m3, INT4 = POOL == kInt4;
   constexpr int UNITS = D / 16;      // lanes of a head
   constexpr int HPS = 32 / UNITS;    // heads of a step
   constexpr int K = 8 / HPS;         // pairs whose sine and cosine a lane computes
   constexpr int STRIDE = D + UNITS;  // floats of a head in shared memory
-  __shared__ __align__(16) float heads_in_shared[L == kScattered ? 8 * HPS * STRIDE : 4];
+  __shared__ __align__(16) float heads_in_shared[L == kScattered || INT4 ? 8 * HPS * STRIDE : 4];
   const int lane = threadIdx.x & 31;
   const int u = lane % UNITS, sub = lane / UNITS;
   const int rd = a.rotary_dim;
@@ -274,7 +289,7 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
       const bool is_v = APPEND && h >= k_end;
       const bool to_pool = APPEND && h >= a.q_heads;
       const bool store = h < h1 && !(to_pool && page < 0);
-      if (L != kScattered && !store) continue;
+      if (L != kScattered && !INT4 && !store) continue;
       float xa[8], xb[8];
       if constexpr (L == kScattered) {  // all lanes: the heads of a step meet the barriers together
         float* m = heads_in_shared + ((threadIdx.x >> 5) * HPS + sub) * STRIDE;
@@ -307,8 +322,8 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
           }
         }
         __syncwarp();  // read before the next step writes
-        if (!store) continue;
-      } else if (F8 || (L == kHalf && turning && !is_v)) {
+        if (!INT4 && !store) continue;
+      } else if (F8 || INT4 || (L == kHalf && turning && !is_v)) {
         unpack8(wa[t], xa);
         unpack8(wb[t], xb);
         if (!is_v) {
@@ -339,6 +354,42 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
           const float2 f = bf16x2_to_float2(w);
           if (turning >> j & 1)
             w = float2_to_bf16x2(f.x * c[j] - f.y * s[j], f.x * s[j] + f.y * c[j]);
+        }
+      }
+      if constexpr (INT4) {  // all lanes: the heads of a step meet the barriers together
+        float* m = heads_in_shared + ((threadIdx.x >> 5) * HPS + sub) * STRIDE;
+        to_shared(m + off_a, xa);
+        to_shared(m + off_a + apart, xb);
+        __syncwarp();
+        float y[2][8];
+        from_shared(m + 16 * u, y[0]);
+        from_shared(m + 16 * u + 8, y[1]);
+        __syncwarp();  // read before the next step writes
+        // least element and negated greatest, of the lane and then of its group
+        float lo = y[0][0], hi = -y[0][0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) {
+          lo = min_nan(lo, y[i >> 3][i & 7]);
+          hi = min_nan(hi, -y[i >> 3][i & 7]);
+        }
+        for (int off = 1; off < a.group / 16; off <<= 1) {
+          lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+          hi = min_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+        }
+        if (!store) continue;
+        if (to_pool) {
+          const Group4 g = group4(lo, -hi);
+          const int hh = h - (is_v ? k_end : a.q_heads);
+          const int64_t idx = a.layout == PKA_NHD ? (int64_t)slot * a.k_heads + hh
+                                                  : (int64_t)hh * a.page_size + slot;
+          uint8_t* p = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) +
+                       (int64_t)page * a.page_stride;
+          *reinterpret_cast<uint2*>(p + idx * (D / 2) + 8 * u) =
+              make_uint2(codes4(y[0], g), codes4(y[1], g));
+          if (u % (a.group / 16) == 0)
+            *reinterpret_cast<uint32_t*>(p + a.code_bytes +
+                                         (idx * (D / a.group) + u / (a.group / 16)) * 4) = g.word;
+          continue;
         }
       }
       // rotated elements are rounded once, to bf16 or to a code; the others keep their bits
@@ -380,7 +431,7 @@ int steps_per_part(int64_t rows, int steps) {
   return (steps + parts - 1) / parts;
 }
 
-template <int D, int L, bool APPEND, bool F8>
+template <int D, int L, bool APPEND, int POOL>
 cudaError_t launch(const RopeArgs& args, cudaStream_t stream) {
   constexpr int HPS = 512 / D;  // heads of a step
   RopeArgs a = args;
@@ -389,20 +440,20 @@ cudaError_t launch(const RopeArgs& args, cudaStream_t stream) {
   a.steps_per_part = steps_per_part(a.rows, steps);
   const int parts = (steps + a.steps_per_part - 1) / a.steps_per_part;
   const dim3 grid((unsigned)((a.rows + 7) / 8), (unsigned)parts);
-  rope_kernel<D, L, APPEND, F8><<<grid, 256, 0, stream>>>(a);
+  rope_kernel<D, L, APPEND, POOL><<<grid, 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
-template <bool APPEND, bool F8>
+template <bool APPEND, int POOL>
 cudaError_t launch_any(const RopeArgs& a, int head_dim, bool adjacent, cudaStream_t stream) {
   const int l = adjacent ? kAdjacent : a.rotary_dim % 16 == 0 ? kHalf : kScattered;
   if (head_dim == 128)
-    return l == kAdjacent ? launch<128, kAdjacent, APPEND, F8>(a, stream)
-           : l == kHalf   ? launch<128, kHalf, APPEND, F8>(a, stream)
-                          : launch<128, kScattered, APPEND, F8>(a, stream);
-  return l == kAdjacent ? launch<64, kAdjacent, APPEND, F8>(a, stream)
-         : l == kHalf   ? launch<64, kHalf, APPEND, F8>(a, stream)
-                        : launch<64, kScattered, APPEND, F8>(a, stream);
+    return l == kAdjacent ? launch<128, kAdjacent, APPEND, POOL>(a, stream)
+           : l == kHalf   ? launch<128, kHalf, APPEND, POOL>(a, stream)
+                          : launch<128, kScattered, APPEND, POOL>(a, stream);
+  return l == kAdjacent ? launch<64, kAdjacent, APPEND, POOL>(a, stream)
+         : l == kHalf   ? launch<64, kHalf, APPEND, POOL>(a, stream)
+                        : launch<64, kScattered, APPEND, POOL>(a, stream);
 }
 
 bool rope_valid(const pka_rope* r, int head_dim) {
@@ -517,7 +568,7 @@ pka_status pka_apply_rope(const pka_rope* rope, int32_t transpose, int32_t head_
   a.k_out_stride = k_out_row_stride;
   a.q_heads = q_heads;
   a.k_heads = k_heads;
-  const cudaError_t e = pka::launch_any<false, false>(a, head_dim, rope->interleaved != 0,
+  const cudaError_t e = pka::launch_any<false, pka::kBf16>(a, head_dim, rope->interleaved != 0,
                                                       static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKA_OK : pka::cuda_failure(e, "rope launch");
 }
@@ -531,7 +582,7 @@ pka_status pka_rope_append_paged_kv_cache(
   if (!pka::params_valid(p) || batch < 0 || nnz_new < 0 || num_pool_pages < 0)
     return PKA_ERR_INVALID_ARG;
   if (p->head_dim != 64 && p->head_dim != 128) return PKA_ERR_UNSUPPORTED;
-  if (p->kv_ragged) return PKA_ERR_UNSUPPORTED;
+  if (p->kv_ragged || !pka::kv4_supported(*p)) return PKA_ERR_UNSUPPORTED;
   if (p->num_qo_heads > pka::kMaxHeads || p->num_kv_heads > pka::kMaxHeads ||
       nnz_new > pka::kMaxRows)
     return PKA_ERR_UNSUPPORTED;
@@ -544,8 +595,11 @@ pka_status pka_rope_append_paged_kv_cache(
        {positions_d, append_indptr_d, kv_indptr_d, kv_indices_d, last_page_len_d})
     if (pka::unaligned(x)) return PKA_ERR_INVALID_ARG;
   const bool f8 = p->kv_dtype == PKA_KV_FP8_E4M3;
+  const int group = pka::kv4_group(p->kv_dtype);
   const uintptr_t mis = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
-  if ((mis & 15) || (page_stride & (f8 ? 15 : 7))) return PKA_ERR_INVALID_ARG;
+  if ((mis & 15) || (page_stride & pka::kv_stride_mask(p->kv_dtype))) return PKA_ERR_INVALID_ARG;
+  if (group && page_stride < pka::kv4_code_bytes(*p) + pka::kv4_word_bytes(*p))
+    return PKA_ERR_INVALID_ARG;
   const int d = p->head_dim, hk = p->num_kv_heads;
   const int64_t q_out_stride = (int64_t)p->num_qo_heads * d;
   if (!pka::rows_ok(k_new, k_row_stride, nnz_new, hk, d) ||
@@ -585,11 +639,14 @@ pka_status pka_rope_append_paged_kv_cache(
   a.v_scale = p->v_scale > 0.f ? p->v_scale : 1.f;
   a.k_inv = pka::pow2_reciprocal(a.k_scale);
   a.v_inv = pka::pow2_reciprocal(a.v_scale);
+  a.group = group;
+  a.code_bytes = pka::kv4_code_bytes(*p);
   a.err = pka::device_error_word();
   const bool adjacent = rope->interleaved != 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = f8 ? pka::launch_any<true, true>(a, d, adjacent, st)
-                           : pka::launch_any<true, false>(a, d, adjacent, st);
+  const cudaError_t e = group ? pka::launch_any<true, pka::kInt4>(a, d, adjacent, st)
+                        : f8  ? pka::launch_any<true, pka::kE4m3>(a, d, adjacent, st)
+                              : pka::launch_any<true, pka::kBf16>(a, d, adjacent, st);
   return e == cudaSuccess ? PKA_OK : pka::cuda_failure(e, "rope append launch");
 }
 
