@@ -103,10 +103,12 @@ typedef enum pka_mask_mode {
  * differences and quotients in float32); a group whose hi - lo is not finite
  * (NaN, infinities) is stored as NaN, and one whose step would be no normal
  * bf16 as its origin alone.  Decode rows read the codes and words without
- * rounding them; rows with qo_len >= 2 (and decode_on_tensor_cores) read a bf16
- * scratch as over e4m3 pools, each value rounded once more, to bf16.  Paged
- * K/V only (PKA_ERR_UNSUPPORTED for ragged, for a group above head_dim and for
- * pages of 2 GB); everything else as over e4m3 pools. */
+ * rounding them; rows with qo_len >= 2 (and decode_on_tensor_cores) read an f16
+ * scratch, each value rounded once more, to 11 bits (Q, too, is brought to f16,
+ * where its bf16 values are exact; both scaled by powers of two, so magnitudes
+ * are not limited).  Paged K/V only (PKA_ERR_UNSUPPORTED for ragged, for a group
+ * above head_dim, for pages of 2 GB and over 4096 kv heads); everything else as
+ * over e4m3 pools.  A group that is NaN makes the rows that see it NaN. */
 typedef enum pka_kv_dtype {
   PKA_KV_BF16 = 0,
   PKA_KV_FP8_E4M3 = 1,
@@ -173,7 +175,7 @@ typedef struct pka_plan_info {
   int32_t num_decode_joins;  /* split (decode row, kv head) pairs that the     */
                              /* decode kernel merges itself (their g qo heads  */
                              /* are among num_merge_tasks)                     */
-  int32_t kv_scratch_rows;   /* e4m3 and 4-bit K/V: bf16 rows decoded for the   */
+  int32_t kv_scratch_rows;   /* e4m3 and 4-bit K/V: rows decoded for the        */
                              /* tensor-core rows in the float workspace (else 0) */
   int32_t reserved[3];
 } pka_plan_info;

@@ -125,28 +125,23 @@ def request_rows(pool: Pool, kv_indptr, kv_indices, r, n) -> np.ndarray:
 
 
 def attention(q_bits, k_pool, v_pool, *, qo_indptr, kv_indptr, kv_indices, kv_lens, hq, hk,
-              mask="causal", mask_bool=None, sm_scale=None, rounded=False):
-    """(o, lse, a_k, a_v) float64: attention of q [rows, hq, D] (bf16 bits) over
-    4-bit pools; `rounded` rounds K's and V's values to bf16 first (a number: of so
-    many first keys).  a_k
-    [rows, hq] bounds the magnitudes that a score sums, in log2 units, and a_v
-    [rows, hq, D] those that an output sums, both by the parts (step * code and
-    origin) that the words keep apart."""
+              mask="causal", mask_bool=None, sm_scale=None):
+    """(o, lse, a_k, a_v, a_2) float64: attention of q [rows, hq, D] (bf16 bits)
+    over 4-bit pools.  a_k [rows, hq] bounds the magnitudes that a score sums, in
+    log2 units, and a_v [rows, hq, D] those that an output sums, both by the
+    parts (step * code and origin) that the words keep apart; a_2 [rows, hq] is
+    the largest root of the sum of squares of a score's products."""
     q = ref.bf16_bits_to_f64(q_bits)
     d, g = q.shape[-1], hq // hk
     scale = sm_scale or 1.0 / math.sqrt(d)
     o, a_v = np.zeros(q.shape), np.zeros(q.shape)
-    lse, a_k = np.full(q.shape[:2], -np.inf), np.zeros(q.shape[:2])
+    lse, a_k, a_2 = np.full(q.shape[:2], -np.inf), np.zeros(q.shape[:2]), np.zeros(q.shape[:2])
     at = 0
     k_parts, v_parts = _parts(k_pool), _parts(v_pool)
     for r, n in enumerate(kv_lens):
         n, q0, q1 = int(n), int(qo_indptr[r]), int(qo_indptr[r + 1])
-        k, v = (request_rows(p, kv_indptr, kv_indices, r, n) for p in (k_pool, v_pool))
-        for x in (k, v) if rounded else ():
-            first = x[:n if rounded is True else rounded]
-            first[:] = bf16_round(first.astype(np.float32))
-        part_k, part_v = (request_rows(p, kv_indptr, kv_indices, r, n)
-                          for p in (k_parts, v_parts))
+        k, v, part_k, part_v = (request_rows(p, kv_indptr, kv_indices, r, n)
+                                for p in (k_pool, v_pool, k_parts, v_parts))
         for i in range(q1 - q0):
             seen = np.ones(n, bool)
             if mask == "causal":
@@ -162,10 +157,12 @@ def attention(q_bits, k_pool, v_pool, *, qo_indptr, kv_indptr, kv_indices, kv_le
                 e = np.exp(s - top)
                 o[row, h] = e @ v[seen, kh] / e.sum()
                 lse[row, h] = (top + math.log(e.sum())) / math.log(2.0)
-                a_k[row, h] = scale / math.log(2.0) * (part_k[seen, kh] @ np.abs(q[row, h])).max()
+                log2 = scale / math.log(2.0)
+                a_k[row, h] = log2 * (part_k[seen, kh] @ np.abs(q[row, h])).max()
                 a_v[row, h] = e @ part_v[seen, kh] / e.sum()
+                a_2[row, h] = log2 * math.sqrt(((k[seen, kh] ** 2) @ (q[row, h] ** 2)).max())
         at += (q1 - q0) * n
-    return o, lse, a_k, a_v
+    return o, lse, a_k, a_v, a_2
 
 
 def _parts(pool: Pool) -> Pool:

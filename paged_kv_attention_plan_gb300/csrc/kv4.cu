@@ -1,6 +1,6 @@
-// K/V held in 4 bits: the append that quantises, and the read-back of cached
-// rows (of pools of every type), also as the bf16 scratch of the tensor-core
-// rows.  The page format and the rounding rules are in pka_kv4.h.
+// K/V held in 4 bits: the append that quantises, the read-back of cached rows
+// (of pools of every type), and the f16 rows of the tensor-core launch.  The
+// page format and the rounding rules are in pka_kv4.h.
 #include "pka_cache.h"
 #include "pka_device.cuh"
 #include "pka_kv4.h"
@@ -178,38 +178,13 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
   const int k_end = a.k_out ? hk : 0, heads = k_end + (a.v_out ? hk : 0);
   const int h0 = blockIdx.y * a.steps_per_part * HPS;
   const int h1 = min(heads, h0 + a.steps_per_part * HPS);
-  int64_t rows = t.rows;
-  int units = t.num_units;
-  if (t.counts) {  // this plan's counts, within what the launch was sized for
-    units = min(max(t.counts[0], 0), units);
-    rows = min((int64_t)max(t.counts[2], 0), rows);
-    if (units <= 0) return;
-  }
-  for (int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5); row < rows; row += gridDim.x * 8ll) {
-    Place p;
-    if (t.units) {
-      // the last unit that starts at or before the row
-      int lo = 0, n = units;
-      while (n > 1) {
-        const int step = (n + 31) >> 5;
-        const int at = lane * step;
-        const bool le = at < n && t.units[lo + at].dst_row0 <= row;
-        const int below = max(__popc(__ballot_sync(kAll, le)) - 1, 0);
-        lo += below * step;
-        n = min(step, n - below * step);
-      }
-      const PkaDequantUnit u = t.units[lo];
-      const uint32_t j = (uint32_t)(row - u.dst_row0), nth = j / (uint32_t)t.page_size;
-      p.page = t.kv_indices[u.kv_base + nth];
-      p.slot = (int)(j - nth * (uint32_t)t.page_size);
-    } else {
-      const int r = request_of(t, row, lane);
-      if (r < 0) break;
-      p = place_of(t, r, (t.begin ? t.begin[r] : 0ll) + (row - t.row_indptr[r]));
-      if (p.page < 0) {
-        if (lane == 0) note_error(t.err, PKA_ERR_METADATA);
-        continue;
-      }
+  for (int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5); row < t.rows; row += gridDim.x * 8ll) {
+    const int r = request_of(t, row, lane);
+    if (r < 0) break;
+    const Place p = place_of(t, r, (t.begin ? t.begin[r] : 0ll) + (row - t.row_indptr[r]));
+    if (p.page < 0) {
+      if (lane == 0) note_error(t.err, PKA_ERR_METADATA);
+      continue;
     }
     const int64_t page = (int64_t)p.page * t.page_stride * (KIND == 0 ? 2 : 1);
     for (int hb = h0; hb < h1; hb += kReadSteps * HPS) {
@@ -284,6 +259,190 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
   }
 }
 
+// ---------------------------------------------------------------------------
+// The f16 rows of a launch on the tensor cores (F16Stage), in three launches:
+// bounds of each kv head's largest magnitude from the words alone, then K and V
+// with their scales, and Q.  Bound by memory; 16 to 20 times as many bytes go
+// out as the words that are read twice.
+// ---------------------------------------------------------------------------
+
+// The rows of this plan: in graph mode what the device image says.
+__device__ __forceinline__ int64_t staged_rows(const KvRows& t, int* units) {
+  *units = t.num_units;
+  if (!t.counts) return t.rows;
+  *units = min(max(t.counts[0], 0), t.num_units);
+  return *units > 0 ? min((int64_t)max(t.counts[2], 0), t.rows) : 0;
+}
+
+// Page and slot of scratch row `row` (the last unit that starts at or before it).
+__device__ __forceinline__ Place unit_place(const KvRows& t, int units, int64_t row) {
+  int lo = 0, hi = units - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.units[mid].dst_row0 <= row) lo = mid; else hi = mid - 1;
+  }
+  const PkaDequantUnit u = t.units[lo];
+  const uint32_t j = (uint32_t)(row - u.dst_row0), nth = j / (uint32_t)t.page_size;
+  Place p;
+  p.page = t.kv_indices[u.kv_base + nth];
+  p.slot = (int)(j - nth * (uint32_t)t.page_size);
+  return p;
+}
+
+__device__ __forceinline__ float word_step(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float word_origin(uint32_t w) {
+  return __uint_as_float(w & 0xffff0000u);
+}
+
+// blockIdx.y is the kv head; a thread takes rows.
+template <int G>
+__global__ void __launch_bounds__(256)
+    range_kernel(const __grid_constant__ F16Stage a, const int64_t code_bytes) {
+  const KvRows& t = a.rows;
+  int units;
+  const int64_t rows = staged_rows(t, &units);
+  const int head = blockIdx.y;
+  float most[2] = {0.f, 0.f};
+  for (int64_t row = blockIdx.x * 256ll + threadIdx.x; row < rows; row += gridDim.x * 256ll) {
+    const Place p = unit_place(t, units, row);
+    const int64_t idx = t.layout == PKA_NHD ? (int64_t)p.slot * t.heads + head
+                                            : (int64_t)head * t.page_size + p.slot;
+    const int64_t at = (int64_t)p.page * t.page_stride + code_bytes + idx * (4 * G);
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>((kv ? a.v : a.k) + at);
+#pragma unroll
+      for (int g = 0; g < G; ++g)  // fmaxf passes a NaN group over
+        most[kv] = fmaxf(most[kv], fmaf(15.f, fabsf(word_step(w[g])), fabsf(word_origin(w[g]))));
+    }
+  }
+  __shared__ uint32_t block[2];
+  if (threadIdx.x < 2) block[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    const uint32_t m = __reduce_max_sync(kAll, __float_as_uint(most[kv]));
+    if ((threadIdx.x & 31) == 0 && m) atomicMax(&block[kv], m);
+  }
+  __syncthreads();
+  if (threadIdx.x < 2 && block[threadIdx.x])
+    atomicMax(a.kv_range + 2 * head + threadIdx.x, block[threadIdx.x]);
+}
+
+__device__ __forceinline__ uint32_t float2_to_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// 8 codes under a step and an origin -> f16.
+__device__ __forceinline__ uint4 codes_to_f16(uint32_t codes, float step, float origin) {
+  uint32_t out[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = codes >> (8 * i);
+    const float c0 = __uint_as_float((w & 15u) | 0x4b000000u) - 8388608.f;
+    const float c1 = __uint_as_float((w >> 4 & 15u) | 0x4b000000u) - 8388608.f;
+    out[i] = float2_to_f16x2(fmaf(step, c0, origin), fmaf(step, c1, origin));
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+constexpr int kStageSteps = 4;  // in flight
+
+// A warp takes a row or a part of its heads, 8 elements of K and of V a lane and
+// step.  A key whose V is NaN in a group gets zeros there and NaN in K instead:
+// the rows that see it become NaN, and the others, whose probability of it is 0,
+// do not (0 * NaN in the P V product would reach every row of a tile).  For the
+// same reason the up to 127 rows behind the last one that a tile may read, old
+// ones of another plan in graph mode, become zeros.
+template <int D, int GR>
+__global__ void __launch_bounds__(256)
+    stage_kernel(const __grid_constant__ F16Stage a, const int64_t code_bytes,
+                 const int steps_per_part) {
+  constexpr int LPH = D / 8, HPS = 32 / LPH, G = D / GR;
+  const int lane = threadIdx.x & 31;
+  const int sub = lane / LPH, piece = lane % LPH;
+  const KvRows& t = a.rows;
+  const int hk = t.heads;
+  const int h0 = blockIdx.y * steps_per_part * HPS;
+  const int h1 = min(hk, h0 + steps_per_part * HPS);
+  int units;
+  const int64_t rows = staged_rows(t, &units), end = min(rows + 127, t.rows);
+  for (int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5); row < end; row += gridDim.x * 8ll) {
+    uint4* const k16 = reinterpret_cast<uint4*>(a.k16 + row * hk * D) + piece;
+    uint4* const v16 = reinterpret_cast<uint4*>(a.v16 + row * hk * D) + piece;
+    if (row >= rows) {
+      for (int h = h0 + sub; h < h1; h += HPS)
+        k16[h * LPH] = v16[h * LPH] = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
+    const Place p = unit_place(t, units, row);
+    const int64_t page = (int64_t)p.page * t.page_stride;
+    for (int hb = h0; hb < h1; hb += kStageSteps * HPS) {
+      uint32_t kc[kStageSteps], vc[kStageSteps], kw[kStageSteps], vw[kStageSteps];
+#pragma unroll
+      for (int s = 0; s < kStageSteps; ++s) {
+        const int h = hb + s * HPS + sub;
+        if (h >= h1) continue;
+        const int64_t idx = t.layout == PKA_NHD ? (int64_t)p.slot * hk + h
+                                                : (int64_t)h * t.page_size + p.slot;
+        const int64_t c = page + idx * (D / 2) + piece * 4;
+        const int64_t w = page + code_bytes + (idx * G + piece / (GR / 8)) * 4;
+        kc[s] = *reinterpret_cast<const uint32_t*>(a.k + c);
+        vc[s] = *reinterpret_cast<const uint32_t*>(a.v + c);
+        kw[s] = *reinterpret_cast<const uint32_t*>(a.k + w);
+        vw[s] = *reinterpret_cast<const uint32_t*>(a.v + w);
+      }
+#pragma unroll
+      for (int s = 0; s < kStageSteps; ++s) {
+        const int h = hb + s * HPS + sub;
+        if (h >= h1) continue;
+        const float ku = f16_up(a.kv_range[2 * h]), vu = f16_up(a.kv_range[2 * h + 1]);
+        uint4 k = codes_to_f16(kc[s], word_step(kw[s]) * ku, word_origin(kw[s]) * ku);
+        uint4 v = codes_to_f16(vc[s], word_step(vw[s]) * vu, word_origin(vw[s]) * vu);
+        if (!(word_step(vw[s]) + word_origin(vw[s]) <= INFINITY)) {  // NaN
+          k = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
+          v = make_uint4(0u, 0u, 0u, 0u);
+        }
+        k16[h * LPH] = k;
+        v16[h * LPH] = v;
+      }
+    }
+  }
+}
+
+// Q: D / 8 lanes a (row, head), 8 elements a lane.
+template <int D>
+__global__ void __launch_bounds__(256) stage_q_kernel(const __grid_constant__ F16Stage a) {
+  constexpr int LPH = D / 8;
+  const int64_t total = a.q_rows * a.q_heads * LPH;
+  // whole warps: 32 is a multiple of LPH and the rounded-up lanes only shuffle
+  for (int64_t at = blockIdx.x * 256ll + threadIdx.x; at - (threadIdx.x & 31) < total;
+       at += gridDim.x * 256ll) {
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (at < total) x = reinterpret_cast<const uint4*>(a.q)[at];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float most = 0.f, f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = bf16x2_to_float2(w[i]);
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
+      most = fmaxf(most, fmaxf(fabsf(v.x), fabsf(v.y)));
+    }
+#pragma unroll
+    for (int off = 1; off < LPH; off <<= 1)
+      most = fmaxf(most, __shfl_xor_sync(kAll, most, off));
+    if (at >= total) continue;
+    const float up = f16_up(__float_as_uint(most));
+    reinterpret_cast<uint4*>(a.q16)[at] =
+        make_uint4(float2_to_f16x2(f[0] * up, f[1] * up), float2_to_f16x2(f[2] * up, f[3] * up),
+                   float2_to_f16x2(f[4] * up, f[5] * up), float2_to_f16x2(f[6] * up, f[7] * up));
+    if (at % LPH == 0) a.q_down[at / LPH] = f16_down(__float_as_uint(most));
+  }
+}
+
 // How many of a row's steps one warp takes: enough warps first (16 an SM), then
 // as many steps as are in flight at once.
 int steps_per_part(int64_t rows, int steps, int most) {
@@ -323,7 +482,39 @@ cudaError_t launch_append_t(const Append4Args& args, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+unsigned blocks_of(int64_t work, int per_block, int per_sm) {
+  const int sms = current_device_sms();
+  const int64_t most = (int64_t)per_sm * (sms > 0 ? sms : 1);
+  const int64_t b = (work + per_block - 1) / per_block;
+  return (unsigned)(b < 1 ? 1 : b > most ? most : b);
+}
+
+template <int D, int GR>
+cudaError_t launch_stage_t(const F16Stage& a, cudaStream_t stream) {
+  constexpr int HPS = 256 / D;
+  const KvRows& t = a.rows;
+  const int64_t code_bytes = (int64_t)t.page_size * t.heads * (D / 2);
+  cudaError_t e = cudaMemsetAsync(a.kv_range, 0, (size_t)t.heads * 2 * sizeof(uint32_t), stream);
+  if (e != cudaSuccess) return e;
+  const dim3 ranges(blocks_of(t.rows, 256, 8), (unsigned)t.heads);
+  range_kernel<D / GR><<<ranges, 256, 0, stream>>>(a, code_bytes);
+  const int steps = (t.heads + HPS - 1) / HPS;
+  const int per = steps_per_part(t.rows, steps, kStageSteps);
+  stage_kernel<D, GR><<<grid_of(t.rows, steps, per), 256, 0, stream>>>(a, code_bytes, per);
+  const int64_t q_work = a.q_rows * a.q_heads * (D / 8);
+  stage_q_kernel<D><<<blocks_of(q_work, 256, 32), 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
 }  // namespace
+
+cudaError_t launch_stage_f16(const F16Stage& s, int head_dim, int group, cudaStream_t stream) {
+  if (head_dim == 128)
+    return group == 32   ? launch_stage_t<128, 32>(s, stream)
+           : group == 64 ? launch_stage_t<128, 64>(s, stream)
+                         : launch_stage_t<128, 128>(s, stream);
+  return group == 32 ? launch_stage_t<64, 32>(s, stream) : launch_stage_t<64, 64>(s, stream);
+}
 
 cudaError_t launch_append4(const KvRows& r, int head_dim, int group, const uint16_t* k_new,
                            const uint16_t* v_new, uint8_t* k, uint8_t* v, cudaStream_t stream) {

@@ -35,20 +35,20 @@ inline int64_t kv4_word_bytes(const pka_params& p) {
   return (int64_t)p.page_size * p.num_kv_heads * (p.head_dim / kv4_group(p.kv_dtype)) * 4;
 }
 
+// Largest calls of the kernels in kv4.cu: heads make the second grid axis,
+// rows the first.
+constexpr int kKvMaxHeads = 4096;
+constexpr int64_t kKvMaxRows = INT64_C(1) << 33;
+
 // Whether 4-bit parameters describe something built: paged K/V, groups of at
 // most a head, pages under 2 GB (a row's place in its page is 32 bits wide).
 inline bool kv4_supported(const pka_params& p) {
   const int g = kv4_group(p.kv_dtype);
   if (g == 0) return true;
-  if (g > p.head_dim || p.kv_ragged) return false;
+  if (g > p.head_dim || p.kv_ragged || p.num_kv_heads > kKvMaxHeads) return false;
   return (int64_t)p.num_kv_heads * (p.head_dim / 2 + p.head_dim / g * 4) <=
          (INT32_MAX - 15) / p.page_size;
 }
-
-// Largest calls of the kernels in kv4.cu: heads make the second grid axis,
-// rows the first.
-constexpr int kKvMaxHeads = 4096;
-constexpr int64_t kKvMaxRows = INT64_C(1) << 33;
 
 // Elements of 16 bytes in a pool, less one: what a stride in elements may not have set.
 inline int64_t kv_stride_mask(int kv_dtype) { return kv_dtype == PKA_KV_BF16 ? 7 : 15; }
@@ -79,15 +79,53 @@ struct KvRows {
 // bf16 rows [rows, heads, D] quantised into 4-bit pools.
 cudaError_t launch_append4(const KvRows& r, int head_dim, int group, const uint16_t* k_new,
                            const uint16_t* v_new, uint8_t* k, uint8_t* v, cudaStream_t stream);
-// Rows of pools of any type to bf16 [rows, heads, D]; an output may be null.
+// Rows of requests in pools of any type to bf16 [rows, heads, D]; an output may be null.
 cudaError_t launch_read(const KvRows& r, int kv_dtype, int head_dim, float k_scale, float v_scale,
                         const void* k, const void* v, uint16_t* k_out, uint16_t* v_out,
                         cudaStream_t stream);
+// The rows of a launch on the tensor cores, staged in f16 from 4-bit pools and
+// bf16 queries: 11 bits where bf16 would round origin + step * code to 8.  Each
+// of Q's heads and each kv head of K and of V is scaled by the power of two that
+// brings its largest element into [2^14, 2^15), so no magnitude leaves f16's
+// range: an element keeps 11 bits down to 2^-28 of the largest.
+struct F16Scales {
+  const float* q_down;       // [rows, Hq]: what Q's rows are to be multiplied by
+  const uint32_t* kv_range;  // [Hk][K, V]: bits of a bound of the largest magnitude
+};
+struct F16Stage {
+  KvRows rows;               // units; rows: of the scratch (its capacity in graph mode)
+  const uint8_t* k;
+  const uint8_t* v;
+  uint16_t* k16;             // [rows, Hk, D]
+  uint16_t* v16;
+  const uint16_t* q;         // [q_rows, Hq, D] bf16
+  uint16_t* q16;
+  float* q_down;
+  int64_t q_rows;
+  int q_heads;
+  uint32_t* kv_range;
+};
+cudaError_t launch_stage_f16(const F16Stage& s, int head_dim, int group, cudaStream_t stream);
+cudaError_t launch_prefill_f16(const AttnArgs& a, const F16Scales& scales, int num_ctas,
+                               int head_dim, int group, int nnz_q, int64_t total_kv,
+                               MapCache* cache, cudaStream_t stream);
 // Decode rows over 4-bit pools.
 cudaError_t launch_decode4(const AttnArgs& a, int num_ctas, int head_dim, int group,
                            cudaStream_t stream);
 
 #ifdef __CUDACC__
+// 2^(14 - e) and 2^(e - 14) for the exponent e of a float given by its bits
+// (kept from -100 on, so that both are normal).
+__device__ __forceinline__ int f16_exponent(uint32_t bits) {
+  return max((int)(bits >> 23) - 127, -100);
+}
+__device__ __forceinline__ float f16_up(uint32_t bits) {
+  return __uint_as_float((uint32_t)(127 + 14 - f16_exponent(bits)) << 23);
+}
+__device__ __forceinline__ float f16_down(uint32_t bits) {
+  return __uint_as_float((uint32_t)(127 - 14 + f16_exponent(bits)) << 23);
+}
+
 // The step and origin of a group whose least and greatest elements are given,
 // and the reciprocal that the codes are made with (0: every code is 0).
 //   A step is the range's 15th and an origin the least element, each rounded to

@@ -129,7 +129,7 @@ pka_status check_supported(const pka_params* p) {
   return PKA_OK;
 }
 
-// e4m3 and 4-bit K/V: decode rows read the codes, other rows a bf16 scratch.
+// e4m3 and 4-bit K/V: decode rows read the codes, other rows a 16-bit scratch.
 bool has_codes(const pka_params* p) { return p->kv_dtype != PKA_KV_BF16; }
 
 bool graph_mode(const pka_params* p) { return p->graph_max_batch > 0; }
@@ -227,7 +227,7 @@ pka_status derive(const pka_params* p, int32_t batch, const int32_t* qo, const i
 }
 
 // e4m3 and 4-bit K/V: decode rows read the codes; rows with qo_len >= 2 read a
-// bf16 scratch decoded in run(), whose size depends on the batch: graph mode
+// 16-bit scratch decoded in run(), whose size depends on the batch: graph mode
 // (fixed workspaces) sizes it by graph_max_kv_tokens and refuses such rows
 // when that capacity is not declared.
 pka_status check_kv_dtype(const pka_params* p, const Batch& b) {
@@ -638,6 +638,18 @@ size_t kv_scratch_bytes(const pka_params* p, int64_t rows) {
   return (b + 255) & ~size_t(255);
 }
 
+// What 4-bit K/V stage besides K and V for `rows` query rows: Q in f16 [rows, Hq,
+// D], its scales [rows, Hq], and a bound of K's and V's magnitudes per kv head;
+// each part rounded up to 256 bytes.
+struct Kv4Staging {
+  size_t rows, down, range;
+};
+Kv4Staging kv4_staging(const pka_params* p, int64_t rows) {
+  const size_t heads = (size_t)rows * p->num_qo_heads;
+  auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
+  return {up(heads * p->head_dim * 2), up(heads * 4), up((size_t)p->num_kv_heads * 8)};
+}
+
 }  // namespace
 
 void pka::set_last_error(const char* msg) {
@@ -752,8 +764,13 @@ pka_status plan_levels(pka_plan_t plan, const pka_params* p, const std::vector<B
   size_t rec_o_al = (rec_o + 255) & ~size_t(255);
   info.float_ws_bytes =
       layout_records ? rec_o_al + (((size_t)layout_records * 4 + 255) & ~size_t(255)) : 0;
-  // e4m3 and 4-bit K/V: the bf16 K and V scratch follow the partial states
+  // e4m3 and 4-bit K/V: the 16-bit K and V scratch follow the partial states,
+  // and for 4-bit K/V the staged rows of Q and the scales
   info.float_ws_bytes += 2 * kv_scratch_bytes(p, scratch_rows);
+  if (pka::kv4_group(p->kv_dtype) && scratch_rows > 0) {
+    const Kv4Staging q = kv4_staging(p, graph ? p->graph_max_qo_rows : nnz);
+    info.float_ws_bytes += q.rows + q.down + q.range;
+  }
   info.kv_scratch_rows = (int32_t)L.dequant_rows;
   info.num_requests = batch;
   info.nnz_qo = nnz;
@@ -1022,8 +1039,9 @@ pka_status pka_run(pka_plan_t plan, const pka_params* p, const void* q, const vo
     const int rows = graph ? p->graph_max_qo_rows : plan->info.nnz_qo;
     int64_t kv_rows = graph ? p->graph_max_kv_tokens : plan->info.total_kv;
     pka::AttnArgs pa = a;
+    pka::F16Scales scales{};
     if (graph ? plan->dequant_capacity > 0 : h.num_dequant_units > 0) {
-      // e4m3 and 4-bit K/V: decode the keys of the tensor-core requests to bf16 in the
+      // e4m3 and 4-bit K/V: decode the keys of the tensor-core requests to 16 bits in the
       // float workspace (after the partial states); the tensor-core kernel
       // then reads them as ragged K/V.  Graph mode lays the scratch out for
       // its capacity and launches on that fixed size; the dequant kernel
@@ -1042,17 +1060,32 @@ pka_status pka_run(pka_plan_t plan, const pka_params* p, const void* q, const vo
       const int64_t n_rows = graph ? plan->scratch_capacity : h.dequant_rows;
       cudaError_t e;
       if (int4) {
-        pka::KvRows r{};
-        r.units = units;
-        r.num_units = n_units;
-        r.counts = counts;
-        r.rows = n_rows;
-        r.kv_indices = kv_indices;
-        r.page_stride = page_stride;
-        r.page_size = p->page_size;
-        r.layout = p->layout;
-        r.heads = p->num_kv_heads;
-        e = pka::launch_read(r, p->kv_dtype, p->head_dim, 1.f, 1.f, k, v, sk, sv, st);
+        const Kv4Staging size = kv4_staging(p, rows);
+        char* q16 = reinterpret_cast<char*>(sv) + kv_scratch_bytes(p, plan->scratch_capacity);
+        pka::F16Stage f{};
+        f.rows.units = units;
+        f.rows.num_units = n_units;
+        f.rows.counts = counts;
+        f.rows.rows = n_rows;
+        f.rows.kv_indices = kv_indices;
+        f.rows.page_stride = page_stride;
+        f.rows.page_size = p->page_size;
+        f.rows.layout = p->layout;
+        f.rows.heads = p->num_kv_heads;
+        f.k = static_cast<const uint8_t*>(k);
+        f.v = static_cast<const uint8_t*>(v);
+        f.k16 = sk;
+        f.v16 = sv;
+        f.q = a.q;
+        f.q16 = reinterpret_cast<uint16_t*>(q16);
+        f.q_down = reinterpret_cast<float*>(q16 + size.rows);
+        f.q_rows = rows;
+        f.q_heads = p->num_qo_heads;
+        f.kv_range = reinterpret_cast<uint32_t*>(q16 + size.rows + size.down);
+        e = pka::launch_stage_f16(f, p->head_dim, pka::kv4_group(p->kv_dtype), st);
+        pa.q = f.q16;
+        scales.q_down = f.q_down;
+        scales.kv_range = f.kv_range;
       } else {
         e = pka::launch_dequant(units, n_units, n_rows, counts, kv_indices, k, v, page_stride,
                                 p->page_size, p->layout, p->kv_ragged, p->num_kv_heads,
@@ -1066,8 +1099,12 @@ pka_status pka_run(pka_plan_t plan, const pka_params* p, const void* q, const vo
       pa.kv_fp8 = 0;
       kv_rows = plan->scratch_capacity;
     }
-    cudaError_t e = pka::launch_prefill(pa, h.num_prefill_ctas, p->head_dim, g, rows, kv_rows,
-                                         &plan->prefill_maps, st);
+    cudaError_t e =
+        scales.q_down
+            ? pka::launch_prefill_f16(pa, scales, h.num_prefill_ctas, p->head_dim, g, rows,
+                                      kv_rows, &plan->prefill_maps, st)
+            : pka::launch_prefill(pa, h.num_prefill_ctas, p->head_dim, g, rows, kv_rows,
+                                  &plan->prefill_maps, st);
     if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
   }
   if (graph ? plan->merge_capacity > 0 : h.num_merge_tasks > 0) {

@@ -22,6 +22,10 @@
 // alternates between them, so one tile's MMAs overlap the other tile's
 // softmax.  P stays in tensor memory (it overwrites the first half of its S
 // tile) and feeds the P V product as the A operand.
+//
+// F16 (4-bit pools): Q, K and V come as f16 rows staged from the cache, scaled
+// by powers of two, and P is f16; the scales are taken back per row (Q's) and
+// per kv head (K's in the scores, V's in the output).
 #include <cudaTypedefs.h>
 
 #include <cmath>
@@ -29,6 +33,7 @@
 #include <mutex>
 
 #include "pka_internal.h"
+#include "pka_kv4.h"
 #include "tc_device.cuh"
 
 namespace pka {
@@ -60,6 +65,7 @@ struct PrefillParams {
   int group;
   int gather;              // 1: rows outside whole-page boxes come by TMA gather4
   int64_t rows_per_page;   // page_stride / D: rows of the 2-D view per page
+  F16Scales f16;           // F16 only
 };
 
 struct Bars {
@@ -74,6 +80,12 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ uint32_t float2_to_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -283,7 +295,7 @@ __device__ __forceinline__ void st_global_v8(void* p, uint32_t a0, uint32_t a1, 
                : "memory");
 }
 
-template <int D>
+template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams pp) {
   constexpr int NB = D / 64;
@@ -416,8 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // same loop run by lane 0 alone under a branch issued the MMAs about 20%
     // slower on the append-prefill workload.)
     {
-      constexpr uint32_t idS = tc::idesc_bf16_f32(BM, BN, false, false);
-      constexpr uint32_t idO = tc::idesc_bf16_f32(BM, D, false, true);
+      constexpr uint32_t idS = F16 ? tc::idesc_f16_f32(BM, BN, false, false)
+                                   : tc::idesc_bf16_f32(BM, BN, false, false);
+      constexpr uint32_t idO = F16 ? tc::idesc_f16_f32(BM, D, false, true)
+                                   : tc::idesc_bf16_f32(BM, D, false, true);
       uint32_t kv_it = 0, q_uses = 0;
       uint32_t uses0 = 0, uses1 = 0, o_uses0 = 0, o_uses1 = 0;  // per query tile
       const bool custom = a.mask_mode == PKA_MASK_CUSTOM;
@@ -515,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + x * 128 + lane_off;
     const uint32_t tO = tmem + 256 + x * 128 + lane_off;
     const int i_tok = x * TQ + row / G, g = row % G;
-    const float sc = a.scale_log2;
+    float sc = a.scale_log2;
     uint32_t uses = 0;
     for (int ii = i0; ii < i1 && !warp_any(&abort_flag); ++ii) {
       const PkaWorkItem w = a.items[ii];
@@ -526,6 +540,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int klim_first = w.kv_len - w.qo_len + w.q_local0 + x * TQ;
       const int64_t mrow = ((int64_t)w.mask_hi << 32 | (uint32_t)w.mask_lo) + (int64_t)i * w.kv_len;
       const int mm = (w.flags & PKA_ITEM_ALL_VISIBLE) ? (int)PKA_MASK_NONE : a.mask_mode;
+      if constexpr (F16) {
+        sc = a.scale_log2 * f16_down(pp.f16.kv_range[2 * w.kv_head0]);
+        if (i_tok < w.q_count)
+          sc *= pp.f16.q_down[(int64_t)(w.q_row0 + i_tok) * a.num_qo_heads + w.kv_head0 * G + g];
+        sc = fmaxf(sc, 1.17549435e-38f);  // a masked -inf times 0 would be NaN
+      }
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       for (int k = 0; k < n; ++k) {
@@ -605,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float p0 = ex2(t2.x);
             const float p1 = ex2(t2.y);
             sum2[(j >> 1) & 1] = __fadd2_rn(sum2[(j >> 1) & 1], make_float2(p0, p1));
-            r[c][j / 2] = float2_to_bf16x2(p0, p1);
+            r[c][j / 2] = F16 ? float2_to_f16x2(p0, p1) : float2_to_bf16x2(p0, p1);
           }
           tc::tmem_st16(tS + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(&r[c][0]));
         }
@@ -633,8 +653,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---------------- epilogue
       const bool store = i_tok < w.q_count;
-      const bool any = l > 0.f;
-      const float inv = any ? a.v_scale / l : 0.f;  // V's scale (1 for bf16 K/V)
+      const bool any = F16 ? l != 0.f : l > 0.f;  // F16: NaN is not "no key"
+      // V's scale (1 for bf16 K/V)
+      const float v_scale = F16 ? f16_down(pp.f16.kv_range[2 * w.kv_head0 + 1]) : a.v_scale;
+      const float inv = any ? v_scale / l : 0.f;
       const int head = w.kv_head0 * G + g;
       uint16_t* odst = a.o + ((int64_t)(w.q_row0 + i_tok) * a.num_qo_heads + head) * D;
       const int rec = w.out_rec + i_tok * G + g;
@@ -820,7 +842,7 @@ int encode_maps(Maps& maps, const AttnArgs& a, int G, int nnz_q, int64_t total_k
   return pp_gather;
 }
 
-template <int D>
+template <int D, bool F16>
 cudaError_t launch_t(PrefillParams pp, int num_ctas, int nnz_q, int64_t total_kv,
                      MapCache* cache, cudaStream_t stream) {
   const AttnArgs& a = pp.a;
@@ -847,11 +869,11 @@ cudaError_t launch_t(PrefillParams pp, int num_ctas, int nnz_q, int64_t total_kv
   // At least 120 KiB, so that one CTA (and its 512 TMEM columns) owns each SM.
   size_t smem = 1024 + (size_t)(2 + Ring<D>::K + Ring<D>::V) * NB * BLK;
   if (smem < 120 * 1024) smem = 120 * 1024;
-  cudaError_t e = ensure_dynamic_smem<prefill_kernel<D>>((int)smem);
+  cudaError_t e = ensure_dynamic_smem<prefill_kernel<D, F16>>((int)smem);
   if (e != cudaSuccess) return e;
   pp.gather = pp_gather;
   pp.rows_per_page = pp_gather ? a.page_stride / D : 0;
-  prefill_kernel<D><<<num_ctas, kThreads, smem, stream>>>(maps, pp);
+  prefill_kernel<D, F16><<<num_ctas, kThreads, smem, stream>>>(maps, pp);
   return cudaGetLastError();
 }
 
@@ -859,12 +881,24 @@ cudaError_t launch_t(PrefillParams pp, int num_ctas, int nnz_q, int64_t total_kv
 
 cudaError_t launch_prefill(const AttnArgs& a0, int num_ctas, int head_dim, int group,
                            int nnz_q, int64_t total_kv, MapCache* cache, cudaStream_t stream) {
-  PrefillParams pp;
+  PrefillParams pp{};
   pp.a = a0;
   pp.a.err = device_error_word();
   pp.group = group;
-  if (head_dim == 128) return launch_t<128>(pp, num_ctas, nnz_q, total_kv, cache, stream);
-  return launch_t<64>(pp, num_ctas, nnz_q, total_kv, cache, stream);
+  if (head_dim == 128) return launch_t<128, false>(pp, num_ctas, nnz_q, total_kv, cache, stream);
+  return launch_t<64, false>(pp, num_ctas, nnz_q, total_kv, cache, stream);
+}
+
+cudaError_t launch_prefill_f16(const AttnArgs& a0, const F16Scales& scales, int num_ctas,
+                               int head_dim, int group, int nnz_q, int64_t total_kv,
+                               MapCache* cache, cudaStream_t stream) {
+  PrefillParams pp{};
+  pp.a = a0;
+  pp.a.err = device_error_word();
+  pp.group = group;
+  pp.f16 = scales;
+  if (head_dim == 128) return launch_t<128, true>(pp, num_ctas, nnz_q, total_kv, cache, stream);
+  return launch_t<64, true>(pp, num_ctas, nnz_q, total_kv, cache, stream);
 }
 
 }  // namespace pka

@@ -80,26 +80,29 @@ def test_pool_round_trip(layout, dim, group):
 
 
 def test_reference_attention_against_softmax():
-    """The reference equals the plain attention reference on the pools' values in bf16."""
+    """The reference equals the plain attention reference on the pools' values,
+    where these are bf16 numbers (steps of 1/2, origins of multiples of 1/2)."""
     from oracle import ref
     from inputs import workloads as W
     rng = np.random.default_rng(1)
     b = W.make_paged_batch(3, [3, 1, 4], [6, 2, 9], page_size=4, hq=4, hk=2, d=64)
     kp, vp = (kv4.Pool.empty(b.k_pool.shape[0], 4, 2, 64, 32, "NHD") for _ in range(2))
     for p in (kp, vp):
-        kv4.fill(p, b.kv_indptr, b.kv_indices, b.kv_lens,
-                 [rng.standard_normal((int(n), 2, 64)) for n in b.kv_lens])
+        x = [rng.integers(0, 16, (int(n), 2, 64)) / 2 - 4 for n in b.kv_lens]
+        for rows in x:
+            rows[..., 0::32], rows[..., 1::32] = -4, 3.5  # a range of 15 half steps
+        kv4.fill(p, b.kv_indptr, b.kv_indices, b.kv_lens, x)
+    kw = dict(qo_indptr=b.qo_indptr, kv_indptr=b.kv_indptr, kv_indices=b.kv_indices)
     vals = []
     for p in (kp, vp):
         x = np.stack([[p.read(i, s) for s in range(4)] for i in range(p.data.shape[0])])
-        vals.append((kv4.bf16_round(x.astype(np.float32)).view(np.uint32) >> 16).astype(np.uint16))
-    o2, lse2 = ref.batch_attention(b.q, *vals, qo_indptr=b.qo_indptr, kv_indptr=b.kv_indptr,
-                                   kv_indices=b.kv_indices, last_page_len=b.last_page_len,
-                                   page_size=4, num_qo_heads=4, num_kv_heads=2)
-    r, lr, _, _ = kv4.attention(b.q, kp, vp, qo_indptr=b.qo_indptr, kv_indptr=b.kv_indptr,
-                                kv_indices=b.kv_indices, kv_lens=b.kv_lens, hq=4, hk=2,
-                                rounded=True)
-    assert np.abs(r - o2).max() < 1e-12 and np.abs(lr - lse2).max() < 1e-12
+        vals.append((x.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16))
+        assert np.array_equal(ref.bf16_bits_to_f64(vals[-1]), x)
+    want = ref.batch_attention(b.q, *vals, last_page_len=b.last_page_len, page_size=4,
+                               num_qo_heads=4, num_kv_heads=2, **kw)
+    got = kv4.attention(b.q, kp, vp, kv_lens=b.kv_lens, hq=4, hk=2, **kw)
+    for x, y in zip(got, want):
+        assert np.abs(x - y).max() < 1e-12
 
 
 # ---------------------------------------------------------------------------
@@ -173,7 +176,11 @@ def test_plans_decode_rows_apart_and_others_over_a_scratch(kv):
     got, want = (_plan(pka.make_params(8, 2, 128, 4, kv_dtype=t, num_sms=152), qo, ptr, last)
                  for t in (kv, "e4m3"))
     assert got[0] == want[0] == OK
-    assert got[1].as_dict() == want[1].as_dict() and got[1].kv_scratch_rows == 8
+    a, b = got[1].as_dict(), want[1].as_dict()
+    # beside the keys: 5 rows of Q in f16, their scales, and a word a kv head and pool
+    staged = 5 * 8 * 128 * 2 + 256 + 256
+    assert a.pop("float_ws_bytes") == b.pop("float_ws_bytes") + staged
+    assert a == b and a["kv_scratch_rows"] == 8
     assert got[2] == want[2]
 
 
