@@ -69,6 +69,12 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // d += a . b for a 16x16 (row) and 16x8 (col) f16 fragment pair.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -137,6 +143,13 @@ __device__ __forceinline__ float origin_of(uint32_t w) {
   return __uint_as_float(w & 0xffff0000u);
 }
 
+struct Yes {
+  static constexpr bool value = true;
+};
+struct No {
+  static constexpr bool value = false;
+};
+
 struct Decode4Args {
   AttnArgs a;
   int64_t code_bytes;  // of a page
@@ -151,18 +164,26 @@ __device__ __forceinline__ int chunk_swap(int key) {
   return D == 128 ? (key & 2) | (key >> 2 & 1) : key >> 2 & 1;
 }
 
-// The sum over the 8 lanes that hold one head's keys.
+// The sum over the lanes that hold one head's keys.
+template <bool HALF>
 __device__ __forceinline__ float sum_keys(float x) {
 #pragma unroll
-  for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  for (int off = HALF ? 2 : 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
   return x;
 }
 
-template <int D, int GR>
+// HALF (at most 4 qo heads a kv head): Q's columns 4..7 repeat columns 0..3, so
+// every lane has scores of its heads for both 16-key blocks of a tile, and lanes
+// 0, 1 of a quad go on with the first block, lanes 2, 3 with the second: half the
+// exponentials, words and products a tile.  P^T then holds the blocks in columns
+// 0..3 and 4..7; each block's V takes its own columns (the others as zeros), and
+// the two halves of O meet at the end.
+template <int D, int GR, bool HALF>
 __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     decode4_kernel(const __grid_constant__ Decode4Args p) {
   using S = Shape<D, GR>;
   constexpr int G = S::G, CH = S::CH, MT = S::MT;
+  constexpr int NB = HALF ? 1 : 2;  // blocks of a tile whose scores a lane keeps
   extern __shared__ __align__(128) uint8_t smem[];
   const AttnArgs& a = p.a;
   const int i0 = a.cta_ptr[blockIdx.x], i1 = a.cta_ptr[blockIdx.x + 1];
@@ -170,9 +191,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hpc = a.heads_per_cta, n_split = p.splits;
   const int hl = warp % hpc, split = warp / hpc;
-  const int Hk = a.num_kv_heads, Hq = a.num_qo_heads, group = Hq / Hk;
-  const int P = a.page_size;
+  const int Hq = a.num_qo_heads, group = Hq / a.num_kv_heads;
   const int qd = lane & 3, grp = lane >> 2;
+  const int h0 = HALF ? (2 * qd) & 3 : 2 * qd;  // the lane's heads: h0, h0 + 1
+  const int my_block = HALF ? qd >> 1 : 0;
   const float sc = a.scale_log2;
   const uint32_t ring = smem_u32(smem) + warp * (kStages * S::STAGE);
   // states that meet: floor(splits / 2) slots a head
@@ -182,30 +204,38 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
   // ---- what this warp copies: its tiles of all items, one after another ----
   const uint8_t* const kp = reinterpret_cast<const uint8_t*>(a.k);
   const uint8_t* const vp = reinterpret_cast<const uint8_t*>(a.v);
-  // (unsigned: a key count may end right below 2^31)
-  uint32_t c_key = 0, c_end = 0;
-  int c_item = i0, c_head = 0, c_base = 0, c_page = 0;
-  auto next_tile = [&]() {  // to the next tile that exists, and its pages' ids
+  // Lane i follows key c_key + i through the table: its page's index, slot and id.
+  // (Unsigned: a key count may end right below 2^31.)
+  const uint32_t P = a.page_size, stride = kTile * n_split;
+  const uint32_t step_pages = stride / P, step_slots = stride % P;
+  const uint32_t per_slot = a.layout == PKA_NHD ? a.num_kv_heads : 1;
+  const uint32_t per_head = a.layout == PKA_NHD ? 1 : P;
+  uint32_t c_key = 0, c_end = 0, c_pi = 0, c_last = 0, c_slot = 0, c_row0 = 0;
+  int c_item = i0;
+  const int32_t* c_table = nullptr;
+  int32_t c_page = 0;
+  auto next_item = [&]() {  // to the next item that has a tile for this warp
     while (c_key >= c_end && c_item < i1) {
       const PkaWorkItem* w = a.items + c_item++;
       c_key = w->t0 + kTile * split;
       c_end = w->t1;
-      c_head = w->kv_head0 + hl;
-      c_base = w->kv_base;
+      c_row0 = (uint32_t)(w->kv_head0 + hl) * per_head;
+      c_table = a.kv_indices + w->kv_base;
+      c_pi = (c_key + lane) / P;
+      c_slot = (c_key + lane) - c_pi * P;
+      c_last = (c_end - 1) / P;
     }
-    if (c_key < c_end)
-      c_page = a.kv_indices[c_base + min(c_key + lane, c_end - 1) / (uint32_t)P];
+    if (c_key < c_end) c_page = c_table[min(c_pi, c_last)];
   };
   auto copy_tile = [&](int stage) {
     if (c_key < c_end) {
       const uint32_t at = ring + stage * S::STAGE;
-      const uint32_t slot = min(c_key + lane, c_end - 1) % (uint32_t)P;
-      const uint32_t idx = a.layout == PKA_NHD ? slot * Hk + c_head : (uint32_t)c_head * P + slot;
+      const uint32_t idx = c_slot * per_slot + c_row0;
       const int64_t page = (int64_t)c_page * a.page_stride;
-      const bool there = c_key + lane < c_end;
+      const uint32_t left = c_end - c_key;
       const int64_t words = page + p.code_bytes + (int64_t)idx * (4 * G);
-      copy_async<4 * G>(at + 2 * S::CODES + lane * (4 * G), kp + words, there);
-      copy_async<4 * G>(at + 2 * S::CODES + S::WORDS + lane * (4 * G), vp + words, there);
+      copy_async<4 * G>(at + 2 * S::CODES + lane * (4 * G), kp + words, lane < left);
+      copy_async<4 * G>(at + 2 * S::CODES + S::WORDS + lane * (4 * G), vp + words, lane < left);
       const int64_t row = page + (int64_t)idx * S::ROW;
       const int ch = lane % CH;
 #pragma unroll
@@ -213,15 +243,21 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
         const int k = lane / CH + i * (32 / CH);
         const int64_t from = __shfl_sync(0xffffffffu, row, k) + ch * 16;
         const uint32_t to = at + k * S::ROW + ((ch ^ chunk_swap<D>(k)) << 4);
-        copy_async<16>(to, kp + from, c_key + k < c_end);
-        copy_async<16>(to + S::CODES, vp + from, c_key + k < c_end);
+        copy_async<16>(to, kp + from, k < left);
+        copy_async<16>(to + S::CODES, vp + from, k < left);
       }
-      c_key += kTile * n_split;
-      next_tile();
+      c_key += stride;
+      c_pi += step_pages;
+      c_slot += step_slots;
+      if (c_slot >= P) {
+        c_slot -= P;
+        ++c_pi;
+      }
+      next_item();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  next_tile();
+  next_item();
 #pragma unroll
   for (int s = 0; s < kStages; ++s) copy_tile(s);
 
@@ -238,14 +274,15 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
   for (int ii = i0; ii < i1; ++ii) {
     const PkaWorkItem w = a.items[ii];
     const int head_base = (w.kv_head0 + hl) * group;
-    // Q^T fragments, head grp: elements 8 qd .. 8 qd + 7 of each 32-element
+    // Q^T fragments of column grp: elements 8 qd .. 8 qd + 7 of each 32-element
     // chunk, in the order of K's operands, and the sums of q over the groups
     uint32_t qf[2 * CH][2];
     float cs[2], qs[G][2];
     {
-      const bool real = grp < group;
+      const int col = HALF ? grp & 3 : grp;
+      const bool real = col < group;
       const uint4* row = reinterpret_cast<const uint4*>(
-          a.q + ((int64_t)w.q_row0 * Hq + head_base + (real ? grp : 0)) * D);
+          a.q + ((int64_t)w.q_row0 * Hq + head_base + (real ? col : 0)) * D);
       float x[CH][8], most = 0.f, sum[G];
 #pragma unroll
       for (int g = 0; g < G; ++g) sum[g] = 0.f;
@@ -271,10 +308,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
 #pragma unroll
         for (int g = 0; g < G; ++g) sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], off);
       }
-      // 2^(14 - e) for the largest element's exponent e (kept from -100 on)
-      const int e = max((int)(__float_as_uint(most) >> 23) - 127, -100);
-      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-      const float down = ldexpf(sc, 24 - 14 + e);
+      const float up = f16_up(__float_as_uint(most));
+      const float down = f16_down(__float_as_uint(most)) * (16777216.f * sc);
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
         float y[8];
@@ -285,13 +320,12 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
         qf[2 * j + 1][0] = float2_to_f16x2(y[2], y[6]);
         qf[2 * j + 1][1] = float2_to_f16x2(y[3], y[7]);
       }
-      // a lane's scores are of heads 2 qd and 2 qd + 1
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        cs[h] = __shfl_sync(0xffffffffu, down, (2 * qd + h) * 4);
+        cs[h] = __shfl_sync(0xffffffffu, down, (h0 + h) * 4);
 #pragma unroll
         for (int g = 0; g < G; ++g)
-          qs[g][h] = sc * __shfl_sync(0xffffffffu, sum[g], (2 * qd + h) * 4);
+          qs[g][h] = sc * __shfl_sync(0xffffffffu, sum[g], (h0 + h) * 4);
       }
     }
     float acc[MT][4], zs[G][2];
@@ -303,35 +337,50 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     float l[2] = {0.f, 0.f};              // this lane's share of the sums
     const int64_t mrow = ((int64_t)w.mask_hi << 32 | (uint32_t)w.mask_lo) +
                          (int64_t)w.q_local0 * w.kv_len;
-
     const uint32_t t1 = w.t1;
-    for (uint32_t a0 = w.t0 + kTile * split; a0 < t1; a0 += kTile * n_split) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-      __syncwarp();
+
+    // One tile of keys a0 .. a0 + 31.  ALL: every key is there and seen.
+    auto tile = [&](auto all, uint32_t a0) {
+      constexpr bool ALL = decltype(all)::value;
       const uint32_t at = ring + stage * S::STAGE;
-      // scores of keys my_key (+ 8) of both 16-key blocks, heads 2 qd and 2 qd + 1
-      float s[2][4];
-      float vstep[2][2][G], vorig[2][2][G];  // [block][key][group]
-      float top[2] = {-INFINITY, -INFINITY};
+      // q . c per group, of keys my_key and my_key + 8 of the lane's blocks
+      float sg[NB][G][4];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        float sg[G][4];
+      for (int g = 0; g < G; ++g) {
+        float d[2][4];
 #pragma unroll
-        for (int g = 0; g < G; ++g) sg[g][0] = sg[g][1] = sg[g][2] = sg[g][3] = 0.f;
+        for (int b = 0; b < 2; ++b) {
+          d[b][0] = d[b][1] = d[b][2] = d[b][3] = 0.f;
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-          const uint32_t from = at + k_lane + b * 16 * S::ROW + ((j ^ k_swap) << 4);
-          const uint32_t w0 = lds32(from), w1 = lds32(from + 8 * S::ROW);
-          const uint32_t t0 = w0 >> 8, t1 = w1 >> 8;
-          float(&d)[4] = sg[j * 32 / GR];
-          mma16816(d, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u,
-                   qf[2 * j][0], qf[2 * j][1]);
-          mma16816(d, t0 & 0x000f000fu, t1 & 0x000f000fu, t0 & 0x00f000f0u, t1 & 0x00f000f0u,
-                   qf[2 * j + 1][0], qf[2 * j + 1][1]);
+          for (int j = g * (GR / 32); j < (g + 1) * (GR / 32); ++j) {
+            const uint32_t from = at + k_lane + b * 16 * S::ROW + ((j ^ k_swap) << 4);
+            const uint32_t w0 = lds32(from), w1 = lds32(from + 8 * S::ROW);
+            const uint32_t u0 = w0 >> 8, u1 = w1 >> 8;
+            mma16816(d[b], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u,
+                     w1 & 0x00f000f0u, qf[2 * j][0], qf[2 * j][1]);
+            mma16816(d[b], u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u,
+                     u1 & 0x00f000f0u, qf[2 * j + 1][0], qf[2 * j + 1][1]);
+          }
         }
 #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (HALF) {
+            sg[0][g][i] = my_block ? d[1][i] : d[0][i];
+          } else {
+            sg[0][g][i] = d[0][i];
+            sg[NB - 1][g][i] = d[1][i];
+          }
+        }
+      }
+      float s[NB][4];                             // scores: [key 0, key 1] x [head 0, head 1]
+      float vstep[NB][2][G], vorig[NB][2][G];
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float up[2];
+#pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const int key = 16 * b + 8 * y + my_key;
+          const int key = 16 * (HALF ? my_block : b) + 8 * y + my_key;
           uint32_t kw[G], vw[G];
           lds_words<G>(at + 2 * S::CODES + key * (4 * G), kw);
           lds_words<G>(at + 2 * S::CODES + S::WORDS + key * (4 * G), vw);
@@ -339,79 +388,99 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
 #pragma unroll
           for (int g = 0; g < G; ++g) {
             const float ks = step_of(kw[g]), kz = origin_of(kw[g]);
-            d0 = fmaf(ks, sg[g][2 * y], d0);
-            d1 = fmaf(ks, sg[g][2 * y + 1], d1);
+            d0 = fmaf(ks, sg[b][g][2 * y], d0);
+            d1 = fmaf(ks, sg[b][g][2 * y + 1], d1);
             z0 = fmaf(kz, qs[g][0], z0);
             z1 = fmaf(kz, qs[g][1], z1);
           }
-          bool seen = a0 + key < t1;
-          if (a.mask_mode == PKA_MASK_CUSTOM && seen) {
-            const int64_t bit = mrow + a0 + key;
-            seen = (a.mask[bit >> 3] >> (bit & 7)) & 1;
-          }
-          s[b][2 * y] = seen ? fmaf(d0, cs[0], z0) : -INFINITY;
-          s[b][2 * y + 1] = seen ? fmaf(d1, cs[1], z1) : -INFINITY;
-          // an unseen key's words may hold anything: they become zeros
+          s[b][2 * y] = fmaf(d0, cs[0], z0);
+          s[b][2 * y + 1] = fmaf(d1, cs[1], z1);
           float most = 0.f;
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            vstep[b][y][g] = seen ? step_of(vw[g]) : 0.f;
-            vorig[b][y][g] = seen ? origin_of(vw[g]) : 0.f;
-            most = fmaxf(most, fabsf(vstep[b][y][g]));
+            vstep[b][y][g] = step_of(vw[g]);
+            vorig[b][y][g] = origin_of(vw[g]);
           }
-          const float up = fmaxf(lg2(most), kLeastStep);
-          top[0] = fmaxf(top[0], s[b][2 * y] + up);
-          top[1] = fmaxf(top[1], s[b][2 * y + 1] + up);
+          if constexpr (!ALL) {
+            bool seen = a0 + key < t1;
+            if (a.mask_mode == PKA_MASK_CUSTOM && seen) {
+              const int64_t bit = mrow + a0 + key;
+              seen = (a.mask[bit >> 3] >> (bit & 7)) & 1;
+            }
+            if (!seen) {  // its words may hold anything
+              s[b][2 * y] = s[b][2 * y + 1] = -INFINITY;
+#pragma unroll
+              for (int g = 0; g < G; ++g) vstep[b][y][g] = vorig[b][y][g] = 0.f;
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < G; ++g) most = fmaxf(most, fabsf(vstep[b][y][g]));
+          up[y] = fmaxf(lg2(most), kLeastStep);
         }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          top[h] = max3(top[h], s[b][h] + up[0], s[b][2 + h] + up[1]);
       }
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
+      for (int off = HALF ? 2 : 4; off < 32; off <<= 1) {
         top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], off));
         top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], off));
       }
-      float al[2] = {1.f, 1.f};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float want = top[h] - kHeadroom;
-        if (m[h] == -INFINITY) {
-          m[h] = want;
-        } else if (want > m[h] + kRescale) {
-          al[h] = ex2(m[h] - want);
-          m[h] = want;
-        }
-      }
-      if (al[0] != 1.f || al[1] != 1.f) {
+      // the first tile with a key (m = -inf) or a maximum well past the reference:
+      // the state is rescaled, the same in all lanes of a column
+      if (top[0] - kHeadroom > m[0] + kRescale || top[1] - kHeadroom > m[1] + kRescale) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          l[h] *= al[h];
+          const float want = top[h] - kHeadroom;
+          if (!(want > m[h] + kRescale)) continue;
+          const float al = ex2(m[h] - want);  // 0 while m is -inf
+          m[h] = want;
+          l[h] *= al;
 #pragma unroll
-          for (int g = 0; g < G; ++g) zs[g][h] *= al[h];
+          for (int g = 0; g < G; ++g) zs[g][h] *= al;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            acc[mt][h] *= al[h];
-            acc[mt][2 + h] *= al[h];
+            acc[mt][h] *= al;
+            acc[mt][2 + h] *= al;
           }
         }
       }
-      // O^T += V^T . P^T, block by block
+      // O^T += V^T . P^T
+      float e[NB][4];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        float e[4];
+      for (int b = 0; b < NB; ++b) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = s[b][i] == -INFINITY ? 0.f : ex2(s[b][i] - m[i & 1]);
-        l[0] += e[0] + e[2];
-        l[1] += e[1] + e[3];
-        const uint32_t vat = at + S::CODES + (16 * b + qd) * S::ROW;
-        const int swap0 = chunk_swap<D>(qd), swap4 = chunk_swap<D>(qd + 4);
+        for (int i = 0; i < 4; ++i) {
+          e[b][i] = ex2(s[b][i] - m[i & 1]);
+          if constexpr (!ALL) e[b][i] = s[b][i] == -INFINITY ? 0.f : e[b][i];  // not -inf + inf
+        }
+        l[0] += e[b][0] + e[b][2];
+        l[1] += e[b][1] + e[b][3];
+      }
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
+      for (int g = 0; g < G; ++g) {
+        uint32_t pb[2][2];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
           const float s0 = vstep[b][0][g], s1 = vstep[b][1][g];
           const float o0 = vorig[b][0][g], o1 = vorig[b][1][g];
-          zs[g][0] = fmaf(e[0], o0, fmaf(e[2], o1, zs[g][0]));
-          zs[g][1] = fmaf(e[1], o0, fmaf(e[3], o1, zs[g][1]));
-          const uint32_t pb0 = transpose8x8(float2_to_f16x2(e[0] * s0, e[1] * s0));
-          const uint32_t pb1 = transpose8x8(float2_to_f16x2(e[2] * s1, e[3] * s1));
+          zs[g][0] = fmaf(e[b][0], o0, fmaf(e[b][2], o1, zs[g][0]));
+          zs[g][1] = fmaf(e[b][1], o0, fmaf(e[b][3], o1, zs[g][1]));
+          pb[b][0] = transpose8x8(float2_to_f16x2(e[b][0] * s0, e[b][1] * s0));
+          pb[b][1] = transpose8x8(float2_to_f16x2(e[b][2] * s1, e[b][3] * s1));
+        }
+        if constexpr (HALF) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            pb[1][y] = grp < 4 ? 0u : pb[0][y];
+            pb[0][y] = grp < 4 ? pb[0][y] : 0u;
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
           // the lane's elements of keys t, t + 4, t + 8, t + 12 of this group
+          const uint32_t vat = at + S::CODES + (16 * b + qd) * S::ROW;
+          const int swap0 = chunk_swap<D>(qd), swap4 = chunk_swap<D>(qd + 4);
           constexpr int WL = S::DL < 8 ? 1 : S::DL / 8;  // words
           uint32_t v0[WL], v4[WL], v8[WL], v12[WL];
           const int word = g * (GR / 8) + (grp * S::DL >> 3);  // of the row
@@ -434,12 +503,21 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
             const uint32_t x8 = x >> 8, y8 = y >> 8;
             const int mt = (g * (S::DL / 4) + q) * 2;
             mma16816(acc[mt], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u,
-                     pb0, pb1);
+                     pb[b][0], pb[b][1]);
             mma16816(acc[mt + 1], x8 & 0x000f000fu, x8 & 0x00f000f0u, y8 & 0x000f000fu,
-                     y8 & 0x00f000f0u, pb0, pb1);
+                     y8 & 0x00f000f0u, pb[b][0], pb[b][1]);
           }
         }
       }
+    };
+    const uint32_t all_end = a.mask_mode == PKA_MASK_CUSTOM ? 0u : t1;
+    for (uint32_t a0 = w.t0 + kTile * split; a0 < t1; a0 += stride) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();
+      if (a0 + kTile <= all_end)
+        tile(Yes{}, a0);
+      else
+        tile(No{}, a0);
       __syncwarp();
       copy_tile(stage);
       stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -491,17 +569,22 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     if (split) continue;
 
     // ---- normalise and write: O and the LSE, or this piece's partial state ----
-    l[0] = sum_keys(l[0]);
-    l[1] = sum_keys(l[1]);
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      zs[g][0] = sum_keys(zs[g][0]);
-      zs[g][1] = sum_keys(zs[g][1]);
+    for (int h = 0; h < 2; ++h) {
+      l[h] = sum_keys<HALF>(l[h]);
+#pragma unroll
+      for (int g = 0; g < G; ++g) zs[g][h] = sum_keys<HALF>(zs[g][h]);
+    }
+    if constexpr (HALF) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[mt][i] += __shfl_xor_sync(0xffffffffu, acc[mt][i], 2);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int head = head_base + 2 * qd + h;
-      if (2 * qd + h >= group) continue;
+      const int head = head_base + h0 + h;
+      if (h0 + h >= group || my_block) continue;
       // a NaN among the words of a seen key makes the sums NaN, which is not "no key"
       const bool none = l[h] == 0.f;
       const float inv = none ? 0.f : 1.f / l[h];
@@ -551,7 +634,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <int D, int GR>
+template <int D, int GR, bool HALF>
 cudaError_t launch_t(const AttnArgs& a, int num_ctas, cudaStream_t stream) {
   using S = Shape<D, GR>;
   Decode4Args p{};
@@ -563,22 +646,29 @@ cudaError_t launch_t(const AttnArgs& a, int num_ctas, cudaStream_t stream) {
   const int smem = warps * kStages * S::STAGE + hpc * (p.splits / 2) * S::SLOT;
   static_assert(kMaxWarps * kStages * S::STAGE + kMaxWarps / 2 * S::SLOT <= 227 * 1024,
                 "shared memory");
-  cudaError_t e = ensure_dynamic_smem<decode4_kernel<D, GR>>(smem);
+  cudaError_t e = ensure_dynamic_smem<decode4_kernel<D, GR, HALF>>(smem);
   if (e != cudaSuccess) return e;
-  decode4_kernel<D, GR><<<num_ctas, 32 * warps, smem, stream>>>(p);
+  decode4_kernel<D, GR, HALF><<<num_ctas, 32 * warps, smem, stream>>>(p);
   return cudaGetLastError();
+}
+
+template <int D, int GR>
+cudaError_t launch_any(const AttnArgs& a, int num_ctas, bool half, cudaStream_t stream) {
+  return half ? launch_t<D, GR, true>(a, num_ctas, stream)
+              : launch_t<D, GR, false>(a, num_ctas, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_decode4(const AttnArgs& a, int num_ctas, int head_dim, int group,
                            cudaStream_t stream) {
+  const bool half = a.num_qo_heads <= 4 * a.num_kv_heads;
   if (head_dim == 128)
-    return group == 32   ? launch_t<128, 32>(a, num_ctas, stream)
-           : group == 64 ? launch_t<128, 64>(a, num_ctas, stream)
-                         : launch_t<128, 128>(a, num_ctas, stream);
-  return group == 32 ? launch_t<64, 32>(a, num_ctas, stream)
-                     : launch_t<64, 64>(a, num_ctas, stream);
+    return group == 32   ? launch_any<128, 32>(a, num_ctas, half, stream)
+           : group == 64 ? launch_any<128, 64>(a, num_ctas, half, stream)
+                         : launch_any<128, 128>(a, num_ctas, half, stream);
+  return group == 32 ? launch_any<64, 32>(a, num_ctas, half, stream)
+                     : launch_any<64, 64>(a, num_ctas, half, stream);
 }
 
 }  // namespace pka

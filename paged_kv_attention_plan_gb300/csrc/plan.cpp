@@ -443,6 +443,10 @@ void plan_decode(const pka_params* p, const std::vector<Batch>& lv, int num_sms,
     chunk = (int64_t)p->fixed_split_pages * (p->kv_ragged ? 1 : p->page_size);
   } else if (p->split_mode == PKA_SPLIT_AUTO) {
     int64_t target = (total + num_sms - 1) / num_sms;
+    // A CTA closes up to 15 keys short of its share.  A CTA more than SMs costs
+    // little where two share an SM; over 4-bit pools one fills it (153 CTAs took
+    // 61 us for 64 requests, 152 take 41), so its share covers the 15.
+    if (pka::kv4_group(p->kv_dtype)) target += pka::kDecodeTileTokens - 1;
     target = (target + pka::kDecodeTileTokens - 1) / pka::kDecodeTileTokens * pka::kDecodeTileTokens;
     chunk = std::max<int64_t>(target, kMinDecodeChunk);
   }
