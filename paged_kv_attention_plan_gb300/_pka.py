@@ -192,6 +192,8 @@ def _int32_host(a, name):
 def _dev(t, name, dtype):
     if t is None:
         return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -204,15 +206,16 @@ def _dev(t, name, dtype):
 def _dev_pool(t, name, params=None):
     """K/V pool: the last three dims contiguous; pages may be strided (5-D view).
     bf16, or uint8 e4m3 codes or 4-bit pages [pages, bytes] when the params say so."""
+    if params is not None and params.kv_dtype >= PKA_KV_INT4_G32 and \
+            isinstance(t, torch.Tensor) and t.dtype is torch.uint8 and t.is_cuda:
+        _int4_pages(t, name, params)
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     want = (torch.uint8 if params is not None and params.kv_dtype != PKA_KV_BF16
             else torch.bfloat16)
     if t.dtype != want:
         raise TypeError(f"{name} must be {want}, got {t.dtype}")
-    if params is not None and params.kv_dtype >= PKA_KV_INT4_G32:
-        _int4_pages(t, name, params)
-        return t.data_ptr()
     if t.dim() >= 3 and (t.stride(-1) != 1 or t.stride(-2) != t.shape[-1]
                          or t.stride(-3) != t.shape[-1] * t.shape[-2]):
         raise ValueError(f"{name}: the last three dims must be contiguous")
@@ -221,9 +224,9 @@ def _dev_pool(t, name, params=None):
 
 def _int4_pages(t, name, params):
     """4-bit pages: [.., pages, bytes], the bytes of a page (pka_kv_page_bytes) contiguous."""
-    size = _page_bytes(params)
-    if t.dim() < 2 or t.shape[-1] != size or t.stride(-1) != 1 or \
-            (t.shape[-2] > 1 and t.stride(-2) < size):
+    size, shape, strides = _page_bytes(params), t.shape, t.stride()
+    if len(shape) < 2 or shape[-1] != size or strides[-1] != 1 or \
+            (shape[-2] > 1 and strides[-2] < size):
         raise ValueError(f"{name} must be [.., pages, {size}] with each page contiguous, got "
                          f"{tuple(t.shape)} with strides {t.stride()}")
 
@@ -313,7 +316,7 @@ def _here_stream(stream, dev) -> int:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 

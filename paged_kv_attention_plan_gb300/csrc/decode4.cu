@@ -28,7 +28,7 @@
 // in with cp.async, two stages ahead, and waits only for its own copies: there
 // is no producer, no barrier wait that could run out, and any page size, layout
 // and stride is one address a key.
-#include "decode_join.cuh"
+#include "pka_device.cuh"
 #include "pka_kv4.h"
 
 namespace pka {
@@ -172,6 +172,78 @@ __device__ __forceinline__ float sum_keys(float x) {
   return x;
 }
 
+// Merge the pieces of a split (request, kv head) for its qo heads first, first +
+// step, ...: with b_k the pieces' base-2 statistics, m = max b_k and s = sum
+// 2^(b_k - m), o = sum (2^(b_k - m) / s) o_k and lse = m + log2 s; pieces with b_k
+// = -inf carry no weight, and if all are empty o = 0 and lse = -inf.  Lane k takes
+// the statistics of pieces k, k + 32, ..; then the rows come in, 16 in flight,
+// from other SMs through L2 (.cg).
+template <int D>
+__device__ __noinline__ void join_heads(const AttnArgs& a, const PkaDecodeJoin j, int row,
+                                        int head0, int group, int first, int step, int lane) {
+  constexpr int PER = D / 32, R = 16;
+  for (int h = first; h < group; h += step) {
+    auto stat = [&](int k) {
+      return k < j.nslots ? __ldcg(a.part_lse + j.rec_first + (int64_t)k * j.rec_stride + h)
+                          : -INFINITY;
+    };
+    float b0 = stat(lane), m = b0;
+    for (int k = lane + 32; k < j.nslots; k += 32) m = fmaxf(m, stat(k));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const float shift = m == -INFINITY ? 0.f : m;
+    float sum = exp2f(b0 - shift);
+    for (int k = lane + 32; k < j.nslots; k += 32) sum += exp2f(stat(k) - shift);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    const bool none = sum == 0.f;
+    const float inv = none ? 0.f : 1.f / sum;
+    float acc[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    for (int base = 0; base < j.nslots; base += 32) {
+      const float b = base ? stat(base + lane) : b0;
+      const float weight = exp2f(b - shift) * inv;
+      const int n = min(32, j.nslots - base);
+      for (int k0 = 0; k0 < n; k0 += R) {
+        float x[R][PER];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+#pragma unroll
+          for (int e = 0; e < PER; ++e) x[q][e] = 0.f;
+          const float* src = a.part_o + lane * PER +
+                             (j.rec_first + (int64_t)(base + k0 + q) * j.rec_stride + h) * D;
+          if (k0 + q < n) {
+            if constexpr (PER == 4) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+              x[q][0] = v.x, x[q][1] = v.y, x[q][2] = v.z, x[q][3] = v.w;
+            } else {
+              const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+              x[q][0] = v.x, x[q][1] = v.y;
+            }
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+          const float w = __shfl_sync(0xffffffffu, weight, (k0 + q) & 31);
+          // a piece without keys holds zeros; one past the last carries none
+          if (k0 + q < n)
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, x[q][e], acc[e]);
+        }
+      }
+    }
+    const int64_t out = (int64_t)row * a.num_qo_heads + head0 + h;
+    uint16_t* dst = a.o + out * D + lane * PER;
+    if constexpr (PER == 4)
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(float2_to_bf16x2(acc[0], acc[1]), float2_to_bf16x2(acc[2], acc[3]));
+    else
+      *reinterpret_cast<uint32_t*>(dst) = float2_to_bf16x2(acc[0], acc[1]);
+    if (lane == 0 && a.lse) a.lse[out] = none ? -INFINITY : shift + log2f(sum);
+  }
+}
+
 // HALF (at most 4 qo heads a kv head): Q's columns 4..7 repeat columns 0..3, so
 // every lane has scores of its heads for both 16-key blocks of a tile, and lanes
 // 0, 1 of a quad go on with the first block, lanes 2, 3 with the second: half the
@@ -185,6 +257,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
   constexpr int G = S::G, CH = S::CH, MT = S::MT;
   constexpr int NB = HALF ? 1 : 2;  // blocks of a tile whose scores a lane keeps
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int merging[8];  // per kv head of the CTA
   const AttnArgs& a = p.a;
   const int i0 = a.cta_ptr[blockIdx.x], i1 = a.cta_ptr[blockIdx.x + 1];
   if (i0 >= i1) return;
@@ -221,6 +294,13 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
       c_end = w->t1;
       c_row0 = (uint32_t)(w->kv_head0 + hl) * per_head;
       c_table = a.kv_indices + w->kv_base;
+      // the item's queries, ahead of their use
+      const int lines = (group * D * 2 + 127) / 128;
+      if (lane < lines)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(
+            reinterpret_cast<const uint8_t*>(
+                a.q + ((int64_t)w->q_row0 * Hq + (w->kv_head0 + hl) * group) * D) +
+            lane * 128));
       c_pi = (c_key + lane) / P;
       c_slot = (c_key + lane) - c_pi * P;
       c_last = (c_end - 1) / P;
@@ -523,11 +603,13 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 
-    // ---- the head's warps bring their states together, pair by pair ----
+    // ---- the head's warps bring their states together, pair by pair; which warp
+    // ends an item goes round, so that the others are at the next one meanwhile ----
+    const int turn = (ii - i0) % n_split, rank = split >= turn ? split - turn : split - turn + n_split;
     for (int n = n_split; n > 1;) {
       const int half = (n + 1) >> 1;
-      float* const slot = slots + (split >= half ? split - half : split) * (S::SLOT / 4) + lane;
-      if (split >= half && split < n) {
+      float* const slot = slots + (rank >= half ? rank - half : rank) * (S::SLOT / 4) + lane;
+      if (rank >= half && rank < n) {
         int i = 0;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -542,7 +624,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
         }
       }
       asm volatile("bar.sync %0, %1;" ::"r"(hl + 1), "r"(32 * n_split) : "memory");
-      if (split < n - half) {
+      if (rank < n - half) {
         const float* const tail = slot + 32 * 4 * MT;
         float mine[2], other[2];
 #pragma unroll
@@ -566,7 +648,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
       asm volatile("bar.sync %0, %1;" ::"r"(hl + 1), "r"(32 * n_split) : "memory");
       n = half;
     }
-    if (split) continue;
+    if (rank == 0) {
 
     // ---- normalise and write: O and the LSE, or this piece's partial state ----
 #pragma unroll
@@ -616,18 +698,32 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
           a.lse[(int64_t)w.q_row0 * Hq + head] = lse;
       }
     }
+    }  // rank 0
     if (w.join >= 0 && a.joins) {
-      // count the piece in once its state is visible; the last one merges
+      // count the piece in once its state is visible; the last one merges: for a
+      // CTA's last item all warps of the head, before it the one that ended the item
       PkaDecodeJoin* const jp = a.joins + w.join + hl;
-      __threadfence();
-      __syncwarp();
+      const bool together = ii + 1 == i1 && n_split > 1;
       int last = 0;
-      if (lane == 0) last = atomicAdd(&jp->arrived, 1) == jp->nslots - 1;
-      if (__shfl_sync(0xffffffffu, last, 0)) {
+      if (rank == 0) {
         __threadfence();
-        join_merge<D>(a, *jp, w.q_row0, head_base, group, lane);
         __syncwarp();
-        if (lane == 0) jp->arrived = 0;  // re-armed for the next run
+        if (lane == 0) last = atomicAdd(&jp->arrived, 1) == jp->nslots - 1;
+        if (together && lane == 0) merging[hl] = last;
+        last = __shfl_sync(0xffffffffu, last, 0);
+      }
+      if (together) {
+        asm volatile("bar.sync %0, %1;" ::"r"(hl + 1), "r"(32 * n_split) : "memory");
+        last = merging[hl];
+      }
+      if (last) {
+        __threadfence();
+        join_heads<D>(a, *jp, w.q_row0, head_base, group, together ? rank : 0,
+                      together ? n_split : 1, lane);
+        __syncwarp();
+        if (together)  // every warp has read the fixed fields
+          asm volatile("bar.sync %0, %1;" ::"r"(hl + 1), "r"(32 * n_split) : "memory");
+        if (rank == 0 && lane == 0) jp->arrived = 0;  // re-armed for the next run
       }
     }
   }

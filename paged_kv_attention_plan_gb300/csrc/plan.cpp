@@ -88,6 +88,8 @@ struct pka_plan_s {
 namespace {
 
 constexpr int kMinDecodeChunk = 64;
+// 4-bit pools: what starting and ending an item takes, in keys (3 us at 25 ns a key)
+constexpr int kItemCost4 = 112;
 
 thread_local char g_last_error[256] = "";
 
@@ -415,6 +417,18 @@ void order_split_pieces(PlanLists* L) {
   }
 }
 
+// How many of a unit's `left` keys go to a CTA whose share of `chunk` keys holds
+// `load`, where an item costs `over` keys besides its own; 0: the CTA is full.
+// Cuts inside a request fall on 16-key tile boundaries, so that whole pages stay
+// in one tile of the decode kernel.
+int64_t take_keys(int64_t left, int64_t chunk, int64_t load, int64_t over) {
+  const int64_t room = chunk - load - over;
+  if (left <= room) return left;
+  return room < pka::kDecodeTileTokens
+             ? 0
+             : room / pka::kDecodeTileTokens * pka::kDecodeTileTokens;
+}
+
 // Decode rows (qo_len == 1): units are (request, block of kv heads); with
 // split AUTO the keys of all units are dealt out in equal shares to one
 // persistent CTA per SM (a unit may span CTAs, a CTA may hold several units).
@@ -438,19 +452,41 @@ void plan_decode(const pka_params* p, const std::vector<Batch>& lv, int num_sms,
     }
   }
   if (units.empty()) return;
-  int64_t chunk = 0;
+  int64_t chunk = 0, over = 0;  // keys of a CTA's share, and what an item adds to its own
   if (p->split_mode == PKA_SPLIT_FIXED) {
     chunk = (int64_t)p->fixed_split_pages * (p->kv_ragged ? 1 : p->page_size);
   } else if (p->split_mode == PKA_SPLIT_AUTO) {
     int64_t target = (total + num_sms - 1) / num_sms;
-    // A CTA closes up to 15 keys short of its share.  A CTA more than SMs costs
-    // little where two share an SM; over 4-bit pools one fills it (153 CTAs took
-    // 61 us for 64 requests, 152 take 41), so its share covers the 15.
-    if (pka::kv4_group(p->kv_dtype)) target += pka::kDecodeTileTokens - 1;
     target = (target + pka::kDecodeTileTokens - 1) / pka::kDecodeTileTokens * pka::kDecodeTileTokens;
     chunk = std::max<int64_t>(target, kMinDecodeChunk);
+    if (pka::kv4_group(p->kv_dtype)) {
+      // An item costs a CTA kItemCost4 keys besides its own, and no more CTAs than
+      // SMs: one fills an SM there (shared memory), so that the next starts after it.
+      over = kItemCost4;
+      auto ctas = [&](int64_t share) {
+        int64_t n = 0, load = 0;
+        for (const Unit& u : units) {
+          int64_t left = u.K;
+          do {
+            const int64_t take = take_keys(left, share, load, over);
+            if (take == 0) {
+              ++n;
+              load = 0;
+              continue;
+            }
+            left -= take;
+            load += take + over;
+          } while (left > 0);
+        }
+        return n + (load > 0);
+      };
+      target = (total + over * (int64_t)units.size() + num_sms - 1) / num_sms;
+      chunk = std::max<int64_t>((target + 15) / 16 * 16, kMinDecodeChunk + over);
+      for (int64_t step = 16; ctas(chunk) > num_sms; chunk += step, step += step / 2 / 16 * 16) {
+      }
+    }
   }
-  L->decode_chunk = (int)chunk;
+  L->decode_chunk = (int)std::min<int64_t>(chunk, INT32_MAX);
   auto& items = L->dec_items;
   std::vector<int> pieces;  // items of the current unit (reused: the planner runs every step)
   pieces.reserve(64);
@@ -479,21 +515,16 @@ void plan_decode(const pka_params* p, const std::vector<Batch>& lv, int num_sms,
     pieces.clear();
     int64_t t = 0;
     do {
-      // Cuts inside a request fall on 16-key tile boundaries, so that whole
-      // pages stay in one tile of the decode kernel.
-      int64_t take = u.K - t;
-      if (take > chunk - load) {
-        take = (chunk - load) / pka::kDecodeTileTokens * pka::kDecodeTileTokens;
-        if (take == 0) {  // no room for a whole tile: close this CTA
-          L->dec_cta_ptr.push_back((int)items.size());
-          load = 0;
-          continue;
-        }
+      const int64_t take = take_keys(u.K - t, chunk, load, over);
+      if (take == 0) {  // no room for a whole tile: close this CTA
+        L->dec_cta_ptr.push_back((int)items.size());
+        load = 0;
+        continue;
       }
       pieces.push_back((int)items.size());
       items.push_back(make_item(lv[u.l], u.r, u.hg * hpc, hpc, 0, 1, (int)t, (int)(t + take)));
       t += take;
-      load += take;
+      load += take + over;
       if (load >= chunk) {
         L->dec_cta_ptr.push_back((int)items.size());
         load = 0;

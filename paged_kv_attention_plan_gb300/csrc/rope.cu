@@ -289,7 +289,7 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
       const bool is_v = APPEND && h >= k_end;
       const bool to_pool = APPEND && h >= a.q_heads;
       const bool store = h < h1 && !(to_pool && page < 0);
-      if (L != kScattered && !INT4 && !store) continue;
+      if (L != kScattered && !store && !(INT4 && hb + (t + 1) * HPS > a.q_heads)) continue;
       float xa[8], xb[8];
       if constexpr (L == kScattered) {  // all lanes: the heads of a step meet the barriers together
         float* m = heads_in_shared + ((threadIdx.x >> 5) * HPS + sub) * STRIDE;
@@ -322,7 +322,7 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
           }
         }
         __syncwarp();  // read before the next step writes
-        if (!INT4 && !store) continue;
+        if (!store && !(INT4 && hb + (t + 1) * HPS > a.q_heads)) continue;
       } else if (F8 || INT4 || (L == kHalf && turning && !is_v)) {
         unpack8(wa[t], xa);
         unpack8(wb[t], xb);
@@ -356,7 +356,8 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
             w = float2_to_bf16x2(f.x * c[j] - f.y * s[j], f.x * s[j] + f.y * c[j]);
         }
       }
-      if constexpr (INT4) {  // all lanes: the heads of a step meet the barriers together
+      // a step of q heads alone keeps off shared memory
+      if (INT4 && hb + (t + 1) * HPS > a.q_heads) {  // the same for all lanes
         float* m = heads_in_shared + ((threadIdx.x >> 5) * HPS + sub) * STRIDE;
         to_shared(m + off_a, xa);
         to_shared(m + off_a + apart, xb);

@@ -180,8 +180,36 @@ def test_plans_decode_rows_apart_and_others_over_a_scratch(kv):
     # beside the keys: 5 rows of Q in f16, their scales, and a word a kv head and pool
     staged = 5 * 8 * 128 * 2 + 256 + 256
     assert a.pop("float_ws_bytes") == b.pop("float_ws_bytes") + staged
+    # a decode CTA's share counts what its items cost besides their keys
+    assert a.pop("decode_chunk_tokens") >= b.pop("decode_chunk_tokens")
+    for x in (a, b):
+        for k in ("num_decode_ctas", "int_ws_bytes"):
+            x.pop(k)
     assert a == b and a["kv_scratch_rows"] == 8
-    assert got[2] == want[2]
+    for k in ("prefill_items", "merges", "joins"):
+        assert got[2][k] == want[2][k]
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_decode_plans_fill_the_sms_once(seed):
+    """Over 4-bit pools no plan has more decode CTAs than SMs, whatever the lengths,
+    every key is covered once, and CTAs of many short requests close early."""
+    from inputs import workloads as W
+    from tests.test_host_abi import check_coverage
+    rng = np.random.default_rng(seed)
+    n = int(rng.integers(1, 400))
+    kv = rng.integers(1, [2, 40, 3000, 20000][seed % 4], n)
+    hq, hk = [(32, 8), (8, 1), (28, 7), (64, 16)][seed // 3]
+    b = W.make_paged_batch(seed, np.ones(n, np.int32), kv, page_size=16, hq=hq, hk=hk, d=128,
+                           is_decode=True, with_payload=False)
+    p = pka.make_params(hq, hk, 128, 16, kv_dtype="int4_g64", num_sms=152)
+    s, info, plan = _plan(p, b.qo_indptr, b.kv_indptr, b.last_page_len)
+    assert s == OK and info.num_decode_ctas <= 152
+    check_coverage(plan, b, hq, hk, True, info)
+    ptr = plan["decode_cta_ptr"]
+    per = [ptr[i + 1] - ptr[i] for i in range(len(ptr) - 1)]
+    if seed % 4 == 0:  # single keys: dealt evenly
+        assert max(per) <= -(-len(plan["decode_items"]) // 152) + 1
 
 
 @pytest.mark.parametrize("kv", INT4)
