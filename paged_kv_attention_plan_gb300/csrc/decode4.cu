@@ -176,71 +176,95 @@ __device__ __forceinline__ float sum_keys(float x) {
 // step, ...: with b_k the pieces' base-2 statistics, m = max b_k and s = sum
 // 2^(b_k - m), o = sum (2^(b_k - m) / s) o_k and lse = m + log2 s; pieces with b_k
 // = -inf carry no weight, and if all are empty o = 0 and lse = -inf.  Lane k takes
-// the statistics of pieces k, k + 32, ..; then the rows come in, 16 in flight,
-// from other SMs through L2 (.cg).
+// the statistics of pieces k, k + 32, ..; then the rows come in, from other SMs
+// through L2 (.cg).  Two heads at a time, 8 rows of each in flight: the call is a
+// chain of such round trips at the end of the kernel.
 template <int D>
 __device__ __noinline__ void join_heads(const AttnArgs& a, const PkaDecodeJoin j, int row,
                                         int head0, int group, int first, int step, int lane) {
-  constexpr int PER = D / 32, R = 16;
-  for (int h = first; h < group; h += step) {
-    auto stat = [&](int k) {
+  constexpr int PER = D / 32, R = 4;
+  for (int h0 = first; h0 < group; h0 += 2 * step) {
+    const int heads[2] = {h0, h0 + step < group ? h0 + step : h0};
+    auto stat = [&](int k, int h) {
       return k < j.nslots ? __ldcg(a.part_lse + j.rec_first + (int64_t)k * j.rec_stride + h)
                           : -INFINITY;
     };
-    float b0 = stat(lane), m = b0;
-    for (int k = lane + 32; k < j.nslots; k += 32) m = fmaxf(m, stat(k));
+    float b0[2], m[2], sum[2], acc[2][PER];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    const float shift = m == -INFINITY ? 0.f : m;
-    float sum = exp2f(b0 - shift);
-    for (int k = lane + 32; k < j.nslots; k += 32) sum += exp2f(stat(k) - shift);
+    for (int i = 0; i < 2; ++i) m[i] = b0[i] = stat(lane, heads[i]);
+    for (int k = lane + 32; k < j.nslots; k += 32)
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const bool none = sum == 0.f;
-    const float inv = none ? 0.f : 1.f / sum;
-    float acc[PER];
+      for (int i = 0; i < 2; ++i) m[i] = fmaxf(m[i], stat(k, heads[i]));
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1)
+        m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], off));
+      if (m[i] == -INFINITY) m[i] = 0.f;
+      sum[i] = exp2f(b0[i] - m[i]);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[i][e] = 0.f;
+    }
     for (int base = 0; base < j.nslots; base += 32) {
-      const float b = base ? stat(base + lane) : b0;
-      const float weight = exp2f(b - shift) * inv;
+      float weight[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        weight[i] = exp2f((base ? stat(base + lane, heads[i]) : b0[i]) - m[i]);
+        if (base) sum[i] += weight[i];
+      }
       const int n = min(32, j.nslots - base);
       for (int k0 = 0; k0 < n; k0 += R) {
-        float x[R][PER];
+        float x[2][R][PER];
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
+        for (int i = 0; i < 2; ++i) {
 #pragma unroll
-          for (int e = 0; e < PER; ++e) x[q][e] = 0.f;
-          const float* src = a.part_o + lane * PER +
-                             (j.rec_first + (int64_t)(base + k0 + q) * j.rec_stride + h) * D;
-          if (k0 + q < n) {
-            if constexpr (PER == 4) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-              x[q][0] = v.x, x[q][1] = v.y, x[q][2] = v.z, x[q][3] = v.w;
-            } else {
-              const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-              x[q][0] = v.x, x[q][1] = v.y;
+          for (int q = 0; q < R; ++q) {
+#pragma unroll
+            for (int e = 0; e < PER; ++e) x[i][q][e] = 0.f;
+            const float* src =
+                a.part_o + lane * PER +
+                (j.rec_first + (int64_t)(base + k0 + q) * j.rec_stride + heads[i]) * D;
+            if (k0 + q < n) {
+              if constexpr (PER == 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+                x[i][q][0] = v.x, x[i][q][1] = v.y, x[i][q][2] = v.z, x[i][q][3] = v.w;
+              } else {
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+                x[i][q][0] = v.x, x[i][q][1] = v.y;
+              }
             }
           }
         }
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-          const float w = __shfl_sync(0xffffffffu, weight, (k0 + q) & 31);
-          // a piece without keys holds zeros; one past the last carries none
-          if (k0 + q < n)
+        for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, x[q][e], acc[e]);
+          for (int q = 0; q < R; ++q) {  // past the last piece: weight 0 of zeros
+            const float w = __shfl_sync(0xffffffffu, weight[i], (k0 + q) & 31);
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[i][e] = fmaf(w, x[i][q][e], acc[i][e]);
+          }
         }
       }
     }
-    const int64_t out = (int64_t)row * a.num_qo_heads + head0 + h;
-    uint16_t* dst = a.o + out * D + lane * PER;
-    if constexpr (PER == 4)
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2(float2_to_bf16x2(acc[0], acc[1]), float2_to_bf16x2(acc[2], acc[3]));
-    else
-      *reinterpret_cast<uint32_t*>(dst) = float2_to_bf16x2(acc[0], acc[1]);
-    if (lane == 0 && a.lse) a.lse[out] = none ? -INFINITY : shift + log2f(sum);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1)
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], off);
+      if (i && heads[1] == heads[0]) continue;
+      const bool none = sum[i] == 0.f;
+      const float inv = none ? 0.f : 1.f / sum[i];
+      const int64_t out = (int64_t)row * a.num_qo_heads + head0 + heads[i];
+      uint16_t* dst = a.o + out * D + lane * PER;
+      if constexpr (PER == 4)
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(float2_to_bf16x2(acc[i][0] * inv, acc[i][1] * inv),
+                       float2_to_bf16x2(acc[i][2] * inv, acc[i][3] * inv));
+      else
+        *reinterpret_cast<uint32_t*>(dst) =
+            float2_to_bf16x2(acc[i][0] * inv, acc[i][1] * inv);
+      if (lane == 0 && a.lse) a.lse[out] = none ? -INFINITY : m[i] + log2f(sum[i]);
+    }
   }
 }
 

@@ -170,7 +170,9 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int UNITS = D / 16;      // lanes of a head
   constexpr int HPS = 32 / UNITS;    // heads of a step
   constexpr int K = 8 / HPS;         // pairs whose sine and cosine a lane computes
-  constexpr int STRIDE = D + UNITS;  // floats of a head in shared memory
+  // floats of a head in shared memory; 4-bit pools read it back 16 in a row, four
+  // floats of padding apart so that the lanes of a head meet different banks
+  constexpr int STRIDE = INT4 ? D + 4 * UNITS : D + UNITS;
   __shared__ __align__(16) float heads_in_shared[L == kScattered || INT4 ? 8 * HPS * STRIDE : 4];
   const int lane = threadIdx.x & 31;
   const int u = lane % UNITS, sub = lane / UNITS;
@@ -359,12 +361,13 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
       // a step of q heads alone keeps off shared memory
       if (INT4 && hb + (t + 1) * HPS > a.q_heads) {  // the same for all lanes
         float* m = heads_in_shared + ((threadIdx.x >> 5) * HPS + sub) * STRIDE;
-        to_shared(m + off_a, xa);
-        to_shared(m + off_a + apart, xb);
+        const int off_b = off_a + apart;
+        to_shared(m + off_a + (off_a >> 4) * 4, xa);
+        to_shared(m + off_b + (off_b >> 4) * 4, xb);
         __syncwarp();
         float y[2][8];
-        from_shared(m + 16 * u, y[0]);
-        from_shared(m + 16 * u + 8, y[1]);
+        from_shared(m + 20 * u, y[0]);
+        from_shared(m + 20 * u + 8, y[1]);
         __syncwarp();  // read before the next step writes
         // least element and negated greatest, of the lane and then of its group
         float lo = y[0][0], hi = -y[0][0];
