@@ -39,9 +39,9 @@ constexpr int kMaxWarps = 16;
 constexpr int kStages = 2;
 constexpr float kRescale = 8.0f;  // log2 units, as in decode.cu
 constexpr float kHeadroom = 6.0f;
-// log2 of a step, at least: below it p * s no longer counts against the other
-// keys, and p itself stays far from overflow
-constexpr float kLeastStep = -60.0f;
+// Added to a key's largest step: below it p * s no longer counts against the
+// other keys, and p itself stays far from overflow.
+constexpr float kLeastStep = 0x1p-60f;
 
 template <int D, int GR>
 struct Shape {
@@ -153,6 +153,7 @@ struct No {
 struct Decode4Args {
   AttnArgs a;
   int64_t code_bytes;  // of a page
+  int64_t v_from_k;    // V's pool, seen from K's
   int splits;          // warps of a kv head
 };
 
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
 
   // ---- what this warp copies: its tiles of all items, one after another ----
   const uint8_t* const kp = reinterpret_cast<const uint8_t*>(a.k);
-  const uint8_t* const vp = reinterpret_cast<const uint8_t*>(a.v);
+  const uint8_t* const k_chunk = kp + lane % CH * 16;
   // Lane i follows key c_key + i through the table: its page's index, slot and id.
   // (Unsigned: a key count may end right below 2^31.)
   const uint32_t P = a.page_size, stride = kTile * n_split;
@@ -318,13 +319,6 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
       c_end = w->t1;
       c_row0 = (uint32_t)(w->kv_head0 + hl) * per_head;
       c_table = a.kv_indices + w->kv_base;
-      // the item's queries, ahead of their use
-      const int lines = (group * D * 2 + 127) / 128;
-      if (lane < lines)
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(
-            reinterpret_cast<const uint8_t*>(
-                a.q + ((int64_t)w->q_row0 * Hq + (w->kv_head0 + hl) * group) * D) +
-            lane * 128));
       c_pi = (c_key + lane) / P;
       c_slot = (c_key + lane) - c_pi * P;
       c_last = (c_end - 1) / P;
@@ -339,16 +333,17 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
       const uint32_t left = c_end - c_key;
       const int64_t words = page + p.code_bytes + (int64_t)idx * (4 * G);
       copy_async<4 * G>(at + 2 * S::CODES + lane * (4 * G), kp + words, lane < left);
-      copy_async<4 * G>(at + 2 * S::CODES + S::WORDS + lane * (4 * G), vp + words, lane < left);
+      copy_async<4 * G>(at + 2 * S::CODES + S::WORDS + lane * (4 * G), kp + words + p.v_from_k,
+                        lane < left);
       const int64_t row = page + (int64_t)idx * S::ROW;
       const int ch = lane % CH;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int k = lane / CH + i * (32 / CH);
-        const int64_t from = __shfl_sync(0xffffffffu, row, k) + ch * 16;
+        const uint8_t* from = k_chunk + __shfl_sync(0xffffffffu, row, k);
         const uint32_t to = at + k * S::ROW + ((ch ^ chunk_swap<D>(k)) << 4);
-        copy_async<16>(to, kp + from, k < left);
-        copy_async<16>(to + S::CODES, vp + from, k < left);
+        copy_async<16>(to, from, k < left);
+        copy_async<16>(to + S::CODES, from + p.v_from_k, k < left);
       }
       c_key += stride;
       c_pi += step_pages;
@@ -519,7 +514,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
           }
 #pragma unroll
           for (int g = 0; g < G; ++g) most = fmaxf(most, fabsf(vstep[b][y][g]));
-          up[y] = fmaxf(lg2(most), kLeastStep);
+          up[y] = lg2(most + kLeastStep);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -760,6 +755,7 @@ cudaError_t launch_t(const AttnArgs& a, int num_ctas, cudaStream_t stream) {
   Decode4Args p{};
   p.a = a;
   p.code_bytes = (int64_t)a.page_size * a.num_kv_heads * (D / 2);
+  p.v_from_k = reinterpret_cast<intptr_t>(a.v) - reinterpret_cast<intptr_t>(a.k);
   const int hpc = a.heads_per_cta;
   p.splits = kMaxWarps / hpc;
   const int warps = hpc * p.splits;

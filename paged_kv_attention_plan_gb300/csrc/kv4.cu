@@ -39,6 +39,38 @@ __device__ __forceinline__ int request_of(const KvRows& a, int64_t row, int lane
   return warp_find(a.row_indptr, a.batch, row, lane);
 }
 
+// Where the rows of a slot lie in a page: `row` bytes a head, at slot * per_slot +
+// head * per_head.
+struct Rows {
+  int64_t per_slot, per_head;
+  __device__ __forceinline__ Rows(const KvRows& t, int row)
+      : per_slot(t.layout == PKA_NHD ? (int64_t)t.heads * row : row),
+        per_head(t.layout == PKA_NHD ? row : (int64_t)t.page_size * row) {}
+};
+
+__device__ __forceinline__ float word_step(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float word_origin(uint32_t w) {
+  return __uint_as_float(w & 0xffff0000u);
+}
+
+// origin + step * c of the 8 codes c of a word, each pair as (even, odd).  A code
+// becomes the float 2^23 + c by one byte permutation, and c by a subtraction;
+// step * c is exact (8 by 4 bits), so the sum is rounded once.
+__device__ __forceinline__ void values4(uint32_t codes, float step, float origin,
+                                        float2 (&out)[4]) {
+  const uint32_t even = codes & 0x0f0f0f0fu, odd = codes >> 4 & 0x0f0f0f0fu;
+  const float2 s = make_float2(step, step), z = make_float2(origin, origin);
+  const float2 less = make_float2(-8388608.f, -8388608.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t sel = 0x7540u + i;  // code i, 0, 0, 0x4b
+    const float2 c = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(even, 0x4b000000u, sel)),
+                                            __uint_as_float(__byte_perm(odd, 0x4b000000u, sel))),
+                                less);
+    out[i] = __ffma2_rn(s, c, z);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Append.  A warp takes a row, or a part of its heads (K's, then V's, as one
 // list), in steps of 256 elements: 8 a lane, four steps in flight.  The lanes
@@ -77,6 +109,7 @@ __global__ void __launch_bounds__(256) append4_kernel(const __grid_constant__ Ap
   const int sub = lane / LPH, piece = lane % LPH;
   const KvRows& t = a.rows;
   const int hk = t.heads, heads = 2 * hk;
+  const Rows codes(t, D / 2), words(t, 4 * G);
   const int h0 = blockIdx.y * a.steps_per_part * HPS;
   const int h1 = min(heads, h0 + a.steps_per_part * HPS);
   for (int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5); row < t.rows; row += gridDim.x * 8ll) {
@@ -105,6 +138,8 @@ __global__ void __launch_bounds__(256) append4_kernel(const __grid_constant__ Ap
       continue;
     }
     const int64_t page = (int64_t)p.page * t.page_stride;
+    const int64_t code_at = page + p.slot * codes.per_slot + piece * 4;
+    const int64_t word_at = page + a.code_bytes + p.slot * words.per_slot + piece / LPG * 4;
     for (int hb = h0;;) {
 #pragma unroll
       for (int s = 0; s < kAppendSteps; ++s) {
@@ -130,12 +165,10 @@ __global__ void __launch_bounds__(256) append4_kernel(const __grid_constant__ Ap
         }
         const bool is_v = h >= hk;
         const int hh = is_v ? h - hk : h;
-        const int64_t idx = t.layout == PKA_NHD ? (int64_t)p.slot * hk + hh
-                                                : (int64_t)hh * t.page_size + p.slot;
-        uint8_t* pool = (is_v ? a.v : a.k) + page;
-        *reinterpret_cast<uint32_t*>(pool + idx * (D / 2) + piece * 4) = codes4(f, g);
+        uint8_t* pool = is_v ? a.v : a.k;
+        *reinterpret_cast<uint32_t*>(pool + code_at + hh * codes.per_head) = codes4(f, g);
         if (piece % LPG == 0)
-          *reinterpret_cast<uint32_t*>(pool + a.code_bytes + (idx * G + piece / LPG) * 4) = g.word;
+          *reinterpret_cast<uint32_t*>(pool + word_at + hh * words.per_head) = g.word;
       }
       hb += kAppendSteps * HPS;
       if (hb >= h1) break;
@@ -174,6 +207,7 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
   const int sub = lane / LPH, piece = lane % LPH;
   const KvRows& t = a.rows;
   const int hk = t.heads;
+  const Rows codes(t, LPH * IN), words(t, 4 * G);
   // the outputs asked for, as one list of heads
   const int k_end = a.k_out ? hk : 0, heads = k_end + (a.v_out ? hk : 0);
   const int h0 = blockIdx.y * a.steps_per_part * HPS;
@@ -187,6 +221,9 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
       continue;
     }
     const int64_t page = (int64_t)p.page * t.page_stride * (KIND == 0 ? 2 : 1);
+    const int64_t code_at = page + p.slot * codes.per_slot + piece * IN;
+    const int64_t word_at =
+        page + a.code_bytes + p.slot * words.per_slot + piece / (KIND > 1 ? KIND / 8 : 1) * 4;
     for (int hb = h0; hb < h1; hb += kReadSteps * HPS) {
       uint4 x[kReadSteps];
 #pragma unroll
@@ -194,10 +231,8 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
         const int h = hb + s * HPS + sub;
         if (h >= h1) continue;
         const int hh = h < k_end ? h : h - k_end;
-        const int64_t idx = t.layout == PKA_NHD ? (int64_t)p.slot * hk + hh
-                                                : (int64_t)hh * t.page_size + p.slot;
-        const uint8_t* pool = (h < k_end ? a.k : a.v) + page;
-        const uint8_t* src = pool + (idx * LPH + piece) * IN;
+        const uint8_t* pool = h < k_end ? a.k : a.v;
+        const uint8_t* src = pool + code_at + hh * codes.per_head;
         if constexpr (KIND == 0) {
           x[s] = *reinterpret_cast<const uint4*>(src);
         } else if constexpr (KIND == 1) {
@@ -206,8 +241,7 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
           x[s].y = c.y;
         } else {
           x[s].x = *reinterpret_cast<const uint32_t*>(src);
-          x[s].y = *reinterpret_cast<const uint32_t*>(pool + a.code_bytes +
-                                                      (idx * G + piece / (KIND / 8)) * 4);
+          x[s].y = *reinterpret_cast<const uint32_t*>(pool + word_at + hh * words.per_head);
         }
       }
 #pragma unroll
@@ -238,31 +272,23 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
             out[i] = float2_to_bf16x2(lo * scale, hi * scale);
           }
         } else {
-          const float step = __uint_as_float(x[s].y << 16);
-          const float origin = __uint_as_float(x[s].y & 0xffff0000u);
+          float2 v[4];
+          values4(x[s].x, word_step(x[s].y), word_origin(x[s].y), v);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // the code as a float: 2^23 + c less 2^23
-            const uint32_t w = x[s].x >> (8 * i);
-            const float c0 = __uint_as_float((w & 15u) | 0x4b000000u) - 8388608.f;
-            const float c1 = __uint_as_float((w >> 4 & 15u) | 0x4b000000u) - 8388608.f;
-            // step * c is exact (8 by 4 bits), so this rounds twice: the sum to
-            // float32 and the result to bf16
-            out[i] = float2_to_bf16x2(fmaf(step, c0, origin), fmaf(step, c1, origin));
-          }
+          for (int i = 0; i < 4; ++i) out[i] = float2_to_bf16x2(v[i].x, v[i].y);
         }
         uint16_t* dst = (is_k ? a.k_out : a.v_out) +
                         (row * hk + (is_k ? h : h - k_end)) * (int64_t)D + piece * 8;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+        __stcs(reinterpret_cast<uint4*>(dst), make_uint4(out[0], out[1], out[2], out[3]));
       }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// The f16 rows of a launch on the tensor cores (F16Stage), in three launches:
-// bounds of each kv head's largest magnitude from the words alone, then K and V
-// with their scales, and Q.  Bound by memory; 16 to 20 times as many bytes go
+// The f16 rows of a launch on the tensor cores (F16Stage), in two launches: Q
+// and, from the words alone, bounds of each kv head's largest magnitude, then K
+// and V with their scales.  Bound by memory; 16 to 20 times as many bytes go
 // out as the words that are read twice.
 // ---------------------------------------------------------------------------
 
@@ -289,21 +315,15 @@ __device__ __forceinline__ Place unit_place(const KvRows& t, int units, int64_t 
   return p;
 }
 
-__device__ __forceinline__ float word_step(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float word_origin(uint32_t w) {
-  return __uint_as_float(w & 0xffff0000u);
-}
-
-// blockIdx.y is the kv head; a thread takes rows.
+// The bounds of one kv head: block `block_id` of `blocks` takes its rows.
 template <int G>
-__global__ void __launch_bounds__(256)
-    range_kernel(const __grid_constant__ F16Stage a, const int64_t code_bytes) {
+__device__ __forceinline__ void range_of_words(const F16Stage& a, int64_t code_bytes, int head,
+                                               unsigned block_id, unsigned blocks) {
   const KvRows& t = a.rows;
   int units;
   const int64_t rows = staged_rows(t, &units);
-  const int head = blockIdx.y;
   float most[2] = {0.f, 0.f};
-  for (int64_t row = blockIdx.x * 256ll + threadIdx.x; row < rows; row += gridDim.x * 256ll) {
+  for (int64_t row = block_id * 256ll + threadIdx.x; row < rows; row += blocks * 256ll) {
     const Place p = unit_place(t, units, row);
     const int64_t idx = t.layout == PKA_NHD ? (int64_t)p.slot * t.heads + head
                                             : (int64_t)head * t.page_size + p.slot;
@@ -337,15 +357,10 @@ __device__ __forceinline__ uint32_t float2_to_f16x2(float a, float b) {
 
 // 8 codes under a step and an origin -> f16.
 __device__ __forceinline__ uint4 codes_to_f16(uint32_t codes, float step, float origin) {
-  uint32_t out[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = codes >> (8 * i);
-    const float c0 = __uint_as_float((w & 15u) | 0x4b000000u) - 8388608.f;
-    const float c1 = __uint_as_float((w >> 4 & 15u) | 0x4b000000u) - 8388608.f;
-    out[i] = float2_to_f16x2(fmaf(step, c0, origin), fmaf(step, c1, origin));
-  }
-  return make_uint4(out[0], out[1], out[2], out[3]);
+  float2 v[4];
+  values4(codes, step, origin, v);
+  return make_uint4(float2_to_f16x2(v[0].x, v[0].y), float2_to_f16x2(v[1].x, v[1].y),
+                    float2_to_f16x2(v[2].x, v[2].y), float2_to_f16x2(v[3].x, v[3].y));
 }
 
 constexpr int kStageSteps = 4;  // in flight
@@ -365,6 +380,7 @@ __global__ void __launch_bounds__(256)
   const int sub = lane / LPH, piece = lane % LPH;
   const KvRows& t = a.rows;
   const int hk = t.heads;
+  const Rows codes(t, D / 2), words(t, 4 * G);
   const int h0 = blockIdx.y * steps_per_part * HPS;
   const int h1 = min(hk, h0 + steps_per_part * HPS);
   int units;
@@ -379,16 +395,15 @@ __global__ void __launch_bounds__(256)
     }
     const Place p = unit_place(t, units, row);
     const int64_t page = (int64_t)p.page * t.page_stride;
+    const int64_t code_at = page + p.slot * codes.per_slot + piece * 4;
+    const int64_t word_at = page + code_bytes + p.slot * words.per_slot + piece / (GR / 8) * 4;
     for (int hb = h0; hb < h1; hb += kStageSteps * HPS) {
       uint32_t kc[kStageSteps], vc[kStageSteps], kw[kStageSteps], vw[kStageSteps];
 #pragma unroll
       for (int s = 0; s < kStageSteps; ++s) {
         const int h = hb + s * HPS + sub;
         if (h >= h1) continue;
-        const int64_t idx = t.layout == PKA_NHD ? (int64_t)p.slot * hk + h
-                                                : (int64_t)h * t.page_size + p.slot;
-        const int64_t c = page + idx * (D / 2) + piece * 4;
-        const int64_t w = page + code_bytes + (idx * G + piece / (GR / 8)) * 4;
+        const int64_t c = code_at + h * codes.per_head, w = word_at + h * words.per_head;
         kc[s] = *reinterpret_cast<const uint32_t*>(a.k + c);
         vc[s] = *reinterpret_cast<const uint32_t*>(a.v + c);
         kw[s] = *reinterpret_cast<const uint32_t*>(a.k + w);
@@ -412,14 +427,22 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Q: D / 8 lanes a (row, head), 8 elements a lane.
-template <int D>
-__global__ void __launch_bounds__(256) stage_q_kernel(const __grid_constant__ F16Stage a) {
+// The first word_blocks blocks take the words, kv head by kv head; the others Q: D
+// / 8 lanes a (row, head), 8 elements a lane.
+template <int D, int G>
+__global__ void __launch_bounds__(256)
+    stage_q_kernel(const __grid_constant__ F16Stage a, const int64_t code_bytes,
+                   const unsigned word_blocks) {
   constexpr int LPH = D / 8;
-  const int64_t total = a.q_rows * a.q_heads * LPH;
+  if (blockIdx.x < word_blocks) {
+    const unsigned heads = a.rows.heads;
+    range_of_words<G>(a, code_bytes, blockIdx.x % heads, blockIdx.x / heads, word_blocks / heads);
+    return;
+  }
+  const int64_t total = a.q_rows * a.q_heads * LPH, turn = (gridDim.x - word_blocks) * 256ll;
   // whole warps: 32 is a multiple of LPH and the rounded-up lanes only shuffle
-  for (int64_t at = blockIdx.x * 256ll + threadIdx.x; at - (threadIdx.x & 31) < total;
-       at += gridDim.x * 256ll) {
+  for (int64_t at = (blockIdx.x - word_blocks) * 256ll + threadIdx.x;
+       at - (threadIdx.x & 31) < total; at += turn) {
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
     if (at < total) x = reinterpret_cast<const uint4*>(a.q)[at];
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -496,13 +519,14 @@ cudaError_t launch_stage_t(const F16Stage& a, cudaStream_t stream) {
   const int64_t code_bytes = (int64_t)t.page_size * t.heads * (D / 2);
   cudaError_t e = cudaMemsetAsync(a.kv_range, 0, (size_t)t.heads * 2 * sizeof(uint32_t), stream);
   if (e != cudaSuccess) return e;
-  const dim3 ranges(blocks_of(t.rows, 256, 8), (unsigned)t.heads);
-  range_kernel<D / GR><<<ranges, 256, 0, stream>>>(a, code_bytes);
+  // the words of all heads beside Q's rows: neither waits for the other
+  const unsigned word_blocks = blocks_of(t.rows, 256, 1) * (unsigned)t.heads;
+  const unsigned q_blocks = blocks_of(a.q_rows * a.q_heads * (D / 8), 256, 32);
+  stage_q_kernel<D, D / GR>
+      <<<word_blocks + q_blocks, 256, 0, stream>>>(a, code_bytes, word_blocks);
   const int steps = (t.heads + HPS - 1) / HPS;
   const int per = steps_per_part(t.rows, steps, kStageSteps);
   stage_kernel<D, GR><<<grid_of(t.rows, steps, per), 256, 0, stream>>>(a, code_bytes, per);
-  const int64_t q_work = a.q_rows * a.q_heads * (D / 8);
-  stage_q_kernel<D><<<blocks_of(q_work, 256, 32), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
