@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(256) append4_kernel(const __grid_constant__ Ap
         const bool is_v = h >= hk;
         const int hh = is_v ? h - hk : h;
         uint8_t* pool = is_v ? a.v : a.k;
-        *reinterpret_cast<uint32_t*>(pool + code_at + hh * codes.per_head) = codes4(f, g);
+        *reinterpret_cast<uint32_t*>(pool + code_at + hh * codes.per_head) = codes4<false>(f, g);
         if (piece % LPG == 0)
           *reinterpret_cast<uint32_t*>(pool + word_at + hh * words.per_head) = g.word;
       }

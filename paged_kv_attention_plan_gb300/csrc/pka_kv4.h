@@ -146,31 +146,44 @@ __device__ __forceinline__ Group4 group4(float lo, float hi) {
     g.step = g.origin = g.inv = 0.f;
     return g;
   }
+  // range / 15: the product with 1 / 15 corrected by its residual, exact where the
+  // quotient is a float32, so that it rounds to bf16 as the quotient does
+  const float fifteenth = 1.f / 15.f, near = range * fifteenth;
+  const float step = fmaf(fmaf(-near, 15.f, range), fifteenth, near);
   uint32_t s;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(s) : "f"(lo), "f"(__fdiv_rn(range, 15.f)));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(s) : "f"(lo), "f"(step));
   if ((s & 0x7fffu) < 0x0080u) s &= 0xffff0000u;
   g.word = s;
   g.step = __uint_as_float(s << 16);
   g.origin = __uint_as_float(s & 0xffff0000u);
-  g.inv = g.step > 0.f ? __frcp_rn(g.step) : 0.f;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g.inv) : "f"(g.step));
+  if (!(g.step > 0.f)) g.inv = 0.f;
   return g;
 }
 
 // 8 codes of a group, element i in bits 4i.
-//   The quotient (x - origin) / step is the product with the reciprocal,
-// corrected by its residual: exact where the quotient is a float32, so ties
-// round to even as after a division, and elsewhere no quotient of 24-bit by
-// 8-bit numbers that matters lies near a tie.  The sum with 1.5 * 2^23 rounds
-// it; the code is then the low bits.
+//   The quotient (x - origin) / step is the product with an approximate
+// reciprocal, corrected by its residual: exact where the quotient is a float32,
+// so ties round to even as after a division, and elsewhere no quotient of 24-bit
+// by 8-bit numbers that matters lies near a tie.  The sum with 1.5 * 2^23 rounds
+// it; the code is then the low bits.  CLAMP: the origin may lie off the least
+// element (which is no bf16), and quotients outside 0 .. 15.
+template <bool CLAMP>
 __device__ __forceinline__ uint32_t codes4(const float (&x)[8], const Group4& g) {
+  const float2 less = make_float2(-g.origin, -g.origin), inv = make_float2(g.inv, g.inv);
+  const float2 minus = make_float2(-g.step, -g.step), round = make_float2(12582912.f, 12582912.f);
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float d = x[i] - g.origin;
-    float q = d * g.inv;
-    q = fmaf(fmaf(-q, g.step, d), g.inv, q);
-    q = fminf(fmaxf(q, 0.f), 15.f);
-    w += __float_as_uint(q + 12582912.f) << (4 * i);
+  for (int i = 0; i < 8; i += 2) {
+    const float2 d = __fadd2_rn(make_float2(x[i], x[i + 1]), less);
+    float2 q = __fmul2_rn(d, inv);
+    q = __ffma2_rn(__ffma2_rn(q, minus, d), inv, q);
+    if constexpr (CLAMP) {
+      q.x = fminf(fmaxf(q.x, 0.f), 15.f);
+      q.y = fminf(fmaxf(q.y, 0.f), 15.f);
+    }
+    q = __fadd2_rn(q, round);
+    w += (__float_as_uint(q.x) << (4 * i)) + (__float_as_uint(q.y) << (4 * i + 4));
   }
   // each float's bits are 0x4b400000 + code: their sum, shifted, is taken off
   constexpr uint32_t kBias = 0x4b400000u;

@@ -389,7 +389,7 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
           uint8_t* p = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) +
                        (int64_t)page * a.page_stride;
           *reinterpret_cast<uint2*>(p + idx * (D / 2) + 8 * u) =
-              make_uint2(codes4(y[0], g), codes4(y[1], g));
+              make_uint2(codes4<true>(y[0], g), codes4<true>(y[1], g));
           if (u % (a.group / 16) == 0)
             *reinterpret_cast<uint32_t*>(p + a.code_bytes +
                                          (idx * (D / a.group) + u / (a.group / 16)) * 4) = g.word;
