@@ -434,6 +434,40 @@ def test_decode_steps_of_all_sizes():
         _assert_decode(o, lse, b.want())
 
 
+@pytest.mark.parametrize("hq,hk", [(4, 1), (8, 1)])
+def test_long_flat_rows_keep_their_precision(hq, hk):
+    """160,000 keys of near equal weight in one piece: the output, the mean of as many
+    values, is 400 times smaller than they.  Its own rounding to bf16 is 2^-8 / sqrt(3)
+    of it (rms, at most), P's to f16 2^-11 / sqrt(3) of step * code (rms 2.9 values)
+    a key, independently, 0.0009 of it; 313 tiles a warp round sums of at most a
+    hundredth of the values' own by 2^-23, 0.0002 of it."""
+    n = 160000
+    rng = np.random.default_rng(60)
+    params = pka.make_params(hq, hk, 128, 64, kv_dtype="int4_g128")
+    size, pages = pka.pka_kv_page_bytes(params), n // 64
+    pools = [torch.zeros(pages, size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    g = torch.Generator(device="cuda").manual_seed(6)
+    rows = [torch.randn(n, hk, 128, generator=g, device="cuda").to(torch.bfloat16)
+            for _ in range(2)]
+    ptr, idx = np.array([0, pages], np.int32), rng.permutation(pages).astype(np.int32)
+    last = np.array([64], np.int32)
+    pka.pka_append_paged_kv_cache(params, *rows, i32([0, n]), i32(ptr), i32(idx), i32(last),
+                                  *pools, size)
+    q = W.normal_bf16_bits(rng, (1, hq, 128))
+    q = (kv4.bf16_round((ref.bf16_bits_to_f64(q) / 64).astype(np.float32)).view(np.uint32)
+         >> 16).astype(np.uint16)
+    attn = pka.BatchAttention()
+    attn.plan(None, ptr, last, num_qo_heads=hq, num_kv_heads=hk, head_dim=128, page_size=64,
+              split_mode="off", kv_dtype="int4_g128")
+    o, _ = attn.run(bf16(q), *pools, i32(idx))
+    torch.cuda.synchronize()
+    kp, vp = (kv4.Pool(p.cpu().numpy(), 64, hk, 128, 128, "NHD") for p in pools)
+    want = kv4.attention(q, kp, vp, qo_indptr=[0, 1], kv_indptr=ptr, kv_indices=idx, kv_lens=[n],
+                         hq=hq, hk=hk)[0]
+    rel = np.sqrt(((f64(o) - want) ** 2).mean() / (want ** 2).mean())
+    assert rel <= 2.0 ** -8 / np.sqrt(3) + 0.0009 + 0.0002
+
+
 def test_decode_zero_query_and_queries_of_zeros_and_one_value():
     b = Batch(11, [50, 20], page=16, hq=8, hk=2, group=64)
     b.q[0] = 0
