@@ -108,7 +108,8 @@ typedef enum pka_mask_mode {
  * where its bf16 values are exact; both scaled by powers of two, so magnitudes
  * are not limited).  Paged K/V only (PKA_ERR_UNSUPPORTED for ragged, for a group
  * above head_dim, for pages of 2 GB and over 4096 kv heads); everything else as
- * over e4m3 pools.  A group that is NaN makes the rows that see it NaN. */
+ * over e4m3 pools.  A NaN group of a key that a row sees makes the row NaN (a
+ * decode row: of V, its own elements of it). */
 typedef enum pka_kv_dtype {
   PKA_KV_BF16 = 0,
   PKA_KV_FP8_E4M3 = 1,

@@ -82,6 +82,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// tc::idesc_bf16_f32 with f16 A and B (format 0).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn, bool b_mn) {
+  return tc::idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
 __device__ __forceinline__ uint32_t float2_to_f16x2(float a, float b) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
@@ -428,9 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // same loop run by lane 0 alone under a branch issued the MMAs about 20%
     // slower on the append-prefill workload.)
     {
-      constexpr uint32_t idS = F16 ? tc::idesc_f16_f32(BM, BN, false, false)
+      constexpr uint32_t idS = F16 ? idesc_f16_f32(BM, BN, false, false)
                                    : tc::idesc_bf16_f32(BM, BN, false, false);
-      constexpr uint32_t idO = F16 ? tc::idesc_f16_f32(BM, D, false, true)
+      constexpr uint32_t idO = F16 ? idesc_f16_f32(BM, D, false, true)
                                    : tc::idesc_bf16_f32(BM, D, false, true);
       uint32_t kv_it = 0, q_uses = 0;
       uint32_t uses0 = 0, uses1 = 0, o_uses0 = 0, o_uses1 = 0;  // per query tile
