@@ -10,15 +10,18 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
-// A row's place in the pools; page < 0: nowhere.
+// A row's place in the pools.
 struct Place {
-  int32_t page;
+  int32_t page;  // or one of these
   int32_t slot;
 };
+constexpr int32_t kBad = -1;   // outside its request's keys, or a page id out of range
+constexpr int32_t kNone = -2;  // a row of no request
+constexpr int32_t kZero = -3;  // a row of the scratch behind the last: zeros
 
-// The logical position `pos` of request r, looked up in its table.
+// The place of logical position `pos` of request r.
 __device__ __forceinline__ Place place_of(const KvRows& a, int r, int64_t pos) {
-  Place p{-1, 0};
+  Place p{kBad, 0};
   const int kv0 = a.kv_indptr[r], pages = a.kv_indptr[r + 1] - kv0;
   const int64_t kv_len = (int64_t)(pages - 1) * a.page_size + a.last_page_len[r];
   if (pos < 0 || pos >= kv_len) return p;
@@ -26,25 +29,75 @@ __device__ __forceinline__ Place place_of(const KvRows& a, int r, int64_t pos) {
                                         : pos / a.page_size;
   p.page = a.kv_indices[kv0 + nth];
   p.slot = (int)(pos - nth * a.page_size);
-  if (p.page >= a.num_pages) p.page = -1;
+  if (p.page < 0 || p.page >= a.num_pages) p.page = kBad;
   return p;
 }
 
-// The request of row `row` of a batch, or -1 for a row of none.  A decode
-// step's rows are one a request, so row r is tried as request r's first.
-__device__ __forceinline__ int request_of(const KvRows& a, int64_t row, int lane) {
+// The place of row `row` of a batch: a read's rows count from `begin`, an
+// append's are its request's last.  A decode step's rows are one a request, so
+// row r is tried as request r's first.
+__device__ __forceinline__ Place row_place(const KvRows& a, int64_t row, bool append) {
+  int r = (int)min(row, (int64_t)a.batch - 1);
+  if (row < a.row_indptr[r] || row >= a.row_indptr[r + 1]) {
+    if (row >= a.row_indptr[a.batch]) return Place{kNone, 0};
+    int hi = a.batch - 1;  // the last request that starts at or before the row
+    r = 0;
+    while (r < hi) {
+      const int mid = (int)(((int64_t)r + hi + 1) >> 1);
+      if (a.row_indptr[mid] <= row) r = mid; else hi = mid - 1;
+    }
+  }
+  int64_t pos = row - a.row_indptr[r];
+  if (append) {
+    const int pages = a.kv_indptr[r + 1] - a.kv_indptr[r];
+    pos += (int64_t)(pages - 1) * a.page_size + a.last_page_len[r] -
+           (a.row_indptr[r + 1] - a.row_indptr[r]);
+  } else if (a.begin) {
+    pos += a.begin[r];
+  }
+  return place_of(a, r, pos);
+}
+
+// The request of row `row`, or -1 for a row of none, found by a whole warp.
+__device__ __forceinline__ int warp_request(const KvRows& a, int64_t row, int lane) {
   const int guess = (int)min(row, (int64_t)a.batch - 1);
   if (row >= a.row_indptr[guess] && row < a.row_indptr[guess + 1]) return guess;
   if (row >= a.row_indptr[a.batch]) return -1;
   return warp_find(a.row_indptr, a.batch, row, lane);
 }
 
+// How a call's rows are dealt to warps: a step is 256 elements of a row (8 a lane,
+// one to four heads); a warp keeps one step, so that what its lanes' heads need is
+// worked out once, and walks `rows` rows at a time, kAhead of them in flight.  Its
+// lanes look up the places of all these rows at once, since a look-up is a chain of
+// four or more dependent loads.
+struct Deal {
+  int steps;  // of a row
+  int rows;
+};
+constexpr int kAhead = 4;
+
+struct Walk {
+  int step;
+  int64_t row0, turn;  // the warp's first rows, and how far it goes on
+  bool any;
+  __device__ __forceinline__ Walk(const Deal& d) {
+    const uint32_t warps = gridDim.x * 8, groups = warps / d.steps;
+    const uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5), group = w / d.steps;
+    step = (int)(w - group * d.steps);
+    row0 = (int64_t)group * d.rows;
+    turn = (int64_t)groups * d.rows;
+    any = group < groups;
+  }
+};
+
 // Where the rows of a slot lie in a page: `row` bytes a head, at slot * per_slot +
 // head * per_head.
 struct Rows {
-  int64_t per_slot, per_head;
+  int32_t per_slot;
+  int64_t per_head;
   __device__ __forceinline__ Rows(const KvRows& t, int row)
-      : per_slot(t.layout == PKA_NHD ? (int64_t)t.heads * row : row),
+      : per_slot(t.layout == PKA_NHD ? t.heads * row : row),
         per_head(t.layout == PKA_NHD ? row : (int64_t)t.page_size * row) {}
 };
 
@@ -72,13 +125,12 @@ __device__ __forceinline__ void values4(uint32_t codes, float step, float origin
 }
 
 // ---------------------------------------------------------------------------
-// Append.  A warp takes a row, or a part of its heads (K's, then V's, as one
-// list), in steps of 256 elements: 8 a lane, four steps in flight.  The lanes
-// of a group exchange its least and greatest element (exact in bf16, both in
-// one word: the least and the negated greatest under one minimum), then every
-// lane makes its 8 codes, one 32-bit store.
-//   Bound by memory on long appends; on a decode step by the dependent look-ups
-// of request, page and slot.
+// Append.  A row's steps are K's heads, then V's.  The lanes of a group exchange
+// its least and greatest element (exact in bf16, both in one word: the least and
+// the negated greatest under one minimum), then every lane makes its 8 codes, one
+// 32-bit store.
+//   Bound by instructions on long appends, and by the dependent look-ups of
+// request, page and slot on a decode step.
 // ---------------------------------------------------------------------------
 
 struct Append4Args {
@@ -88,7 +140,7 @@ struct Append4Args {
   uint8_t* k;
   uint8_t* v;
   int64_t code_bytes;  // of a page
-  int steps_per_part;
+  Deal deal;
 };
 
 __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
@@ -97,8 +149,6 @@ __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
   return r;
 }
 
-constexpr int kAppendSteps = 4;  // in flight
-
 template <int D, int GR>
 __global__ void __launch_bounds__(256) append4_kernel(const __grid_constant__ Append4Args a) {
   constexpr int LPH = D / 8;      // lanes of a head
@@ -106,46 +156,42 @@ __global__ void __launch_bounds__(256) append4_kernel(const __grid_constant__ Ap
   constexpr int LPG = GR / 8;     // lanes of a group
   constexpr int G = D / GR;
   const int lane = threadIdx.x & 31;
-  const int sub = lane / LPH, piece = lane % LPH;
+  const int piece = lane % LPH;
   const KvRows& t = a.rows;
-  const int hk = t.heads, heads = 2 * hk;
+  const Walk walk(a.deal);
+  if (!walk.any) return;
+  const int hk = t.heads, h = walk.step * HPS + lane / LPH;
+  const bool have = h < 2 * hk, is_v = h >= hk;
+  const int hh = !have ? 0 : is_v ? h - hk : h;
   const Rows codes(t, D / 2), words(t, 4 * G);
-  const int h0 = blockIdx.y * a.steps_per_part * HPS;
-  const int h1 = min(heads, h0 + a.steps_per_part * HPS);
-  for (int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5); row < t.rows; row += gridDim.x * 8ll) {
-    const int64_t at = row * hk * D + piece * 8;
-    uint4 x[kAppendSteps];
-    auto load = [&](int hb) {
+  const uint16_t* const src = (is_v ? a.v_new : a.k_new) + hh * D + piece * 8;
+  uint8_t* const pool = is_v ? a.v : a.k;
+  uint8_t* const code_pool = pool + hh * codes.per_head + piece * 4;
+  uint8_t* const word_pool = pool + a.code_bytes + hh * words.per_head + piece / LPG * 4;
+  const int64_t row_elems = (int64_t)hk * D;
+  for (int64_t row0 = walk.row0; row0 < t.rows; row0 += walk.turn) {
+    const int n = (int)min((int64_t)a.deal.rows, t.rows - row0);
+    uint4 x[kAhead];
+    auto load = [&](int i0) {
 #pragma unroll
-      for (int s = 0; s < kAppendSteps; ++s) {
-        const int h = hb + s * HPS + sub;
-        x[s] = make_uint4(0u, 0u, 0u, 0u);
-        if (h >= h1) continue;
-        const uint16_t* src = h < hk ? a.k_new + at + (int64_t)h * D
-                                     : a.v_new + at + (int64_t)(h - hk) * D;
-        x[s] = *reinterpret_cast<const uint4*>(src);
+      for (int u = 0; u < kAhead; ++u) {
+        x[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (have && i0 + u < n)
+          x[u] = *reinterpret_cast<const uint4*>(src + (row0 + i0 + u) * row_elems);
       }
     };
-    load(h0);
-    const int r = request_of(t, row, lane);
-    if (r < 0) break;  // this row and those behind it belong to no request
-    const int first = t.row_indptr[r], n = t.row_indptr[r + 1] - first;
-    const int kv0 = t.kv_indptr[r], pages = t.kv_indptr[r + 1] - kv0;
-    const int64_t kv_len = (int64_t)(pages - 1) * t.page_size + t.last_page_len[r];
-    const Place p = place_of(t, r, kv_len - n + (row - first));
-    if (p.page < 0) {
-      if (lane == 0) note_error(t.err, PKA_ERR_METADATA);
-      continue;
-    }
-    const int64_t page = (int64_t)p.page * t.page_stride;
-    const int64_t code_at = page + p.slot * codes.per_slot + piece * 4;
-    const int64_t word_at = page + a.code_bytes + p.slot * words.per_slot + piece / LPG * 4;
-    for (int hb = h0;;) {
+    load(0);  // before the look-ups, which take longer
+    Place mine{kNone, 0};
+    if (lane < n) mine = row_place(t, row0 + lane, true);
+    if (mine.page == kBad) note_error(t.err, PKA_ERR_METADATA);
+    for (int i0 = 0;;) {
 #pragma unroll
-      for (int s = 0; s < kAppendSteps; ++s) {
-        const int h = hb + s * HPS + sub;
+      for (int u = 0; u < kAhead; ++u) {
+        if (i0 + u >= n) break;
+        const int32_t page = __shfl_sync(kAll, mine.page, i0 + u);
+        const int32_t slot = __shfl_sync(kAll, mine.slot, i0 + u);
         // {least, -greatest} of the lane's 8 elements, then of its group
-        const uint32_t w[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
         const uint32_t lo = min2_nan(min2_nan(w[0], w[1]), min2_nan(w[2], w[3]));
         const uint32_t hi = min2_nan(min2_nan(w[0] ^ 0x80008000u, w[1] ^ 0x80008000u),
                                      min2_nan(w[2] ^ 0x80008000u, w[3] ^ 0x80008000u));
@@ -153,7 +199,7 @@ __global__ void __launch_bounds__(256) append4_kernel(const __grid_constant__ Ap
 #pragma unroll
         for (int off = 1; off < LPG; off <<= 1)
           both = min2_nan(both, __shfl_xor_sync(kAll, both, off));
-        if (h >= h1) continue;
+        if (!have || page < 0) continue;
         const Group4 g = group4(__uint_as_float(both << 16),
                                 -__uint_as_float(both & 0xffff0000u));
         float f[8];
@@ -163,25 +209,27 @@ __global__ void __launch_bounds__(256) append4_kernel(const __grid_constant__ Ap
           f[2 * i] = v.x;
           f[2 * i + 1] = v.y;
         }
-        const bool is_v = h >= hk;
-        const int hh = is_v ? h - hk : h;
-        uint8_t* pool = is_v ? a.v : a.k;
-        *reinterpret_cast<uint32_t*>(pool + code_at + hh * codes.per_head) = codes4<false>(f, g);
+        const int64_t at = (int64_t)page * t.page_stride;
+        *reinterpret_cast<uint32_t*>(code_pool + at + (int64_t)slot * codes.per_slot) =
+            codes4<false>(f, g);
         if (piece % LPG == 0)
-          *reinterpret_cast<uint32_t*>(pool + word_at + hh * words.per_head) = g.word;
+          *reinterpret_cast<uint32_t*>(word_pool + at + (int64_t)slot * words.per_slot) = g.word;
       }
-      hb += kAppendSteps * HPS;
-      if (hb >= h1) break;
-      load(hb);
+      i0 += kAhead;
+      if (i0 >= n) break;
+      load(i0);
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Read-back.  A warp takes a row or a part of its heads as above, 8 elements a
-// lane and step (4 bytes of codes, 8 of e4m3, 16 of bf16 in; 16 out), eight
-// steps in flight.  Bound by memory: the rows go out in 2 bytes an element
-// whatever they came in.
+// Read-back.  A row's steps are the heads of the outputs asked for, K's first; a
+// lane takes 4 bytes of codes, 8 of e4m3 or 16 of bf16 a step and writes 16.  Here
+// a warp takes a row (or a part of its steps), eight steps in flight, and looks it
+// up alone: bound by the rows that go out, in 2 bytes an element whatever they came
+// in, it is faster where a warp writes K's and V's whole rows (walking rows as
+// above, 40,800 rows of 8 heads of 128: 40.9 us for 39.9 out of 4-bit pools, 53.8
+// for 43.7 out of e4m3 ones).
 // ---------------------------------------------------------------------------
 
 struct ReadArgs {
@@ -213,8 +261,8 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
   const int h0 = blockIdx.y * a.steps_per_part * HPS;
   const int h1 = min(heads, h0 + a.steps_per_part * HPS);
   for (int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5); row < t.rows; row += gridDim.x * 8ll) {
-    const int r = request_of(t, row, lane);
-    if (r < 0) break;
+    const int r = warp_request(t, row, lane);
+    if (r < 0) break;  // this row and those behind it belong to no request
     const Place p = place_of(t, r, (t.begin ? t.begin[r] : 0ll) + (row - t.row_indptr[r]));
     if (p.page < 0) {
       if (lane == 0) note_error(t.err, PKA_ERR_METADATA);
@@ -363,65 +411,63 @@ __device__ __forceinline__ uint4 codes_to_f16(uint32_t codes, float step, float 
                     float2_to_f16x2(v[2].x, v[2].y), float2_to_f16x2(v[3].x, v[3].y));
 }
 
-constexpr int kStageSteps = 4;  // in flight
-
-// A warp takes a row or a part of its heads, 8 elements of K and of V a lane and
-// step.  A key whose V is NaN in a group gets zeros there and NaN in K instead:
-// the rows that see it become NaN, and the others, whose probability of it is 0,
-// do not (0 * NaN in the P V product would reach every row of a tile).  For the
-// same reason the up to 127 rows behind the last one that a tile may read, old
-// ones of another plan in graph mode, become zeros.
+// A warp's rows as above, K and V of a head together.  A key whose V is NaN in a
+// group gets zeros there and NaN in K instead: the rows that see it become NaN, and
+// the others, whose probability of it is 0, do not (0 * NaN in the P V product
+// would reach every row of a tile).  For the same reason the up to 127 rows behind
+// the last one that a tile may read, old ones of another plan in graph mode, become
+// zeros.
 template <int D, int GR>
 __global__ void __launch_bounds__(256)
-    stage_kernel(const __grid_constant__ F16Stage a, const int64_t code_bytes,
-                 const int steps_per_part) {
-  constexpr int LPH = D / 8, HPS = 32 / LPH, G = D / GR;
+    stage_kernel(const __grid_constant__ F16Stage a, const int64_t code_bytes, const Deal deal) {
+  constexpr int LPH = D / 8, HPS = 32 / LPH, G = D / GR, LPG = GR / 8;
   const int lane = threadIdx.x & 31;
-  const int sub = lane / LPH, piece = lane % LPH;
+  const int piece = lane % LPH;
   const KvRows& t = a.rows;
-  const int hk = t.heads;
+  const Walk walk(deal);
+  if (!walk.any) return;
+  const int hk = t.heads, h = walk.step * HPS + lane / LPH;
+  const bool have = h < hk;
+  const int hh = have ? h : 0;
   const Rows codes(t, D / 2), words(t, 4 * G);
-  const int h0 = blockIdx.y * steps_per_part * HPS;
-  const int h1 = min(hk, h0 + steps_per_part * HPS);
+  const int64_t code_off = hh * codes.per_head + piece * 4;
+  const int64_t word_off = code_bytes + hh * words.per_head + piece / LPG * 4;
+  const float ku = f16_up(a.kv_range[2 * hh]), vu = f16_up(a.kv_range[2 * hh + 1]);
+  const int64_t row_elems = (int64_t)hk * D, out_off = hh * D + piece * 8;
   int units;
   const int64_t rows = staged_rows(t, &units), end = min(rows + 127, t.rows);
-  for (int64_t row = blockIdx.x * 8ll + (threadIdx.x >> 5); row < end; row += gridDim.x * 8ll) {
-    uint4* const k16 = reinterpret_cast<uint4*>(a.k16 + row * hk * D) + piece;
-    uint4* const v16 = reinterpret_cast<uint4*>(a.v16 + row * hk * D) + piece;
-    if (row >= rows) {
-      for (int h = h0 + sub; h < h1; h += HPS)
-        k16[h * LPH] = v16[h * LPH] = make_uint4(0u, 0u, 0u, 0u);
-      continue;
-    }
-    const Place p = unit_place(t, units, row);
-    const int64_t page = (int64_t)p.page * t.page_stride;
-    const int64_t code_at = page + p.slot * codes.per_slot + piece * 4;
-    const int64_t word_at = page + code_bytes + p.slot * words.per_slot + piece / (GR / 8) * 4;
-    for (int hb = h0; hb < h1; hb += kStageSteps * HPS) {
-      uint32_t kc[kStageSteps], vc[kStageSteps], kw[kStageSteps], vw[kStageSteps];
+  for (int64_t row0 = walk.row0; row0 < end; row0 += walk.turn) {
+    const int n = (int)min((int64_t)deal.rows, end - row0);
+    Place mine{kZero, 0};
+    if (lane < n && row0 + lane < rows) mine = unit_place(t, units, row0 + lane);
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+      uint32_t kc[kAhead], vc[kAhead], kw[kAhead], vw[kAhead];
 #pragma unroll
-      for (int s = 0; s < kStageSteps; ++s) {
-        const int h = hb + s * HPS + sub;
-        if (h >= h1) continue;
-        const int64_t c = code_at + h * codes.per_head, w = word_at + h * words.per_head;
-        kc[s] = *reinterpret_cast<const uint32_t*>(a.k + c);
-        vc[s] = *reinterpret_cast<const uint32_t*>(a.v + c);
-        kw[s] = *reinterpret_cast<const uint32_t*>(a.k + w);
-        vw[s] = *reinterpret_cast<const uint32_t*>(a.v + w);
+      for (int u = 0; u < kAhead; ++u) {
+        const int32_t page = __shfl_sync(kAll, mine.page, (i0 + u) & 31);
+        const int32_t slot = __shfl_sync(kAll, mine.slot, (i0 + u) & 31);
+        kc[u] = vc[u] = kw[u] = vw[u] = 0u;  // zeros under a step and an origin of 0
+        if (!have || i0 + u >= n || page == kZero) continue;
+        const int64_t at = (int64_t)page * t.page_stride;
+        const int64_t c = at + (int64_t)slot * codes.per_slot + code_off;
+        const int64_t w = at + (int64_t)slot * words.per_slot + word_off;
+        kc[u] = *reinterpret_cast<const uint32_t*>(a.k + c);
+        vc[u] = *reinterpret_cast<const uint32_t*>(a.v + c);
+        kw[u] = *reinterpret_cast<const uint32_t*>(a.k + w);
+        vw[u] = *reinterpret_cast<const uint32_t*>(a.v + w);
       }
 #pragma unroll
-      for (int s = 0; s < kStageSteps; ++s) {
-        const int h = hb + s * HPS + sub;
-        if (h >= h1) continue;
-        const float ku = f16_up(a.kv_range[2 * h]), vu = f16_up(a.kv_range[2 * h + 1]);
-        uint4 k = codes_to_f16(kc[s], word_step(kw[s]) * ku, word_origin(kw[s]) * ku);
-        uint4 v = codes_to_f16(vc[s], word_step(vw[s]) * vu, word_origin(vw[s]) * vu);
-        if (!(word_step(vw[s]) + word_origin(vw[s]) <= INFINITY)) {  // NaN
+      for (int u = 0; u < kAhead; ++u) {
+        if (!have || i0 + u >= n) continue;
+        uint4 k = codes_to_f16(kc[u], word_step(kw[u]) * ku, word_origin(kw[u]) * ku);
+        uint4 v = codes_to_f16(vc[u], word_step(vw[u]) * vu, word_origin(vw[u]) * vu);
+        if (!(word_step(vw[u]) + word_origin(vw[u]) <= INFINITY)) {  // NaN
           k = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
           v = make_uint4(0u, 0u, 0u, 0u);
         }
-        k16[h * LPH] = k;
-        v16[h * LPH] = v;
+        const int64_t at = (row0 + i0 + u) * row_elems + out_off;
+        *reinterpret_cast<uint4*>(a.k16 + at) = k;
+        *reinterpret_cast<uint4*>(a.v16 + at) = v;
       }
     }
   }
@@ -466,22 +512,21 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// How many of a row's steps one warp takes: enough warps first (16 an SM), then
-// as many steps as are in flight at once.
-int steps_per_part(int64_t rows, int steps, int most) {
+// Rows a warp takes at a time: up to 16, as many as leave 24 warps an SM (an
+// append of 9,101 rows of 8 heads of 128 with its read-back, in us: at most four
+// rows 28.1, eight 24.4, sixteen 22.4, thirty-two 23.0).
+Deal deal_of(int64_t rows, int steps) {
   const int sms = current_device_sms();
-  const int64_t warps = 16 * (int64_t)(sms > 0 ? sms : 1);
-  const int64_t per = (rows * steps + warps - 1) / warps;
-  const int n = per < 1 ? 1 : per > most ? most : (int)per;
-  const int parts = (steps + n - 1) / n;
-  return (steps + parts - 1) / parts;
+  const int64_t per = rows * steps / (24 * (int64_t)(sms > 0 ? sms : 1));
+  const int n = per < 1 ? 1 : per > 16 ? 16 : (int)per;
+  return {steps, n < kAhead ? n : n / kAhead * kAhead};
 }
 
-dim3 grid_of(int64_t rows, int steps, int per_part) {
-  const int parts = (steps + per_part - 1) / per_part;
-  const int64_t blocks = (rows + 7) / 8;
-  const int64_t most = (int64_t)1 << 24;
-  return dim3((unsigned)(blocks < 1 ? 1 : blocks > most ? most : blocks), (unsigned)parts);
+// Whole turns of all steps, at most 2^20 blocks.
+unsigned blocks_of(int64_t rows, const Deal& d) {
+  const int64_t groups = (rows + d.rows - 1) / d.rows;
+  const int64_t blocks = (groups * d.steps + 7) / 8, most = (int64_t)1 << 20;
+  return (unsigned)(blocks < 1 ? 1 : blocks > most ? most : blocks);
 }
 
 template <int D, int KIND>
@@ -490,8 +535,17 @@ cudaError_t launch_read_t(const ReadArgs& args, cudaStream_t stream) {
   constexpr int HPS = 256 / D;
   const int heads = a.rows.heads * ((a.k_out ? 1 : 0) + (a.v_out ? 1 : 0));
   const int steps = (heads + HPS - 1) / HPS;
-  a.steps_per_part = steps_per_part(a.rows.rows, steps, kReadSteps);
-  read_kernel<D, KIND><<<grid_of(a.rows.rows, steps, a.steps_per_part), 256, 0, stream>>>(a);
+  // enough warps first (16 an SM, for which a row is split), then whole rows
+  const int sms = current_device_sms();
+  const int64_t warps = 16 * (int64_t)(sms > 0 ? sms : 1), rows = a.rows.rows;
+  const int64_t per = (rows * steps + warps - 1) / warps;
+  int parts = per >= kReadSteps ? 1 : (steps + (int)per - 1) / (int)per;
+  if (parts == 1) parts = (steps + kReadSteps - 1) / kReadSteps;
+  a.steps_per_part = (steps + parts - 1) / parts;
+  const int64_t blocks = (rows + 7) / 8, most = (int64_t)1 << 24;
+  const dim3 grid((unsigned)(blocks > most ? most : blocks),
+                  (unsigned)((steps + a.steps_per_part - 1) / a.steps_per_part));
+  read_kernel<D, KIND><<<grid, 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -500,8 +554,8 @@ cudaError_t launch_append_t(const Append4Args& args, cudaStream_t stream) {
   Append4Args a = args;
   constexpr int HPS = 256 / D;
   const int steps = (2 * a.rows.heads + HPS - 1) / HPS;
-  a.steps_per_part = steps_per_part(a.rows.rows, steps, 2 * kAppendSteps);
-  append4_kernel<D, GR><<<grid_of(a.rows.rows, steps, a.steps_per_part), 256, 0, stream>>>(a);
+  a.deal = deal_of(a.rows.rows, steps);
+  append4_kernel<D, GR><<<blocks_of(a.rows.rows, a.deal), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -525,8 +579,8 @@ cudaError_t launch_stage_t(const F16Stage& a, cudaStream_t stream) {
   stage_q_kernel<D, D / GR>
       <<<word_blocks + q_blocks, 256, 0, stream>>>(a, code_bytes, word_blocks);
   const int steps = (t.heads + HPS - 1) / HPS;
-  const int per = steps_per_part(t.rows, steps, kStageSteps);
-  stage_kernel<D, GR><<<grid_of(t.rows, steps, per), 256, 0, stream>>>(a, code_bytes, per);
+  const Deal d = deal_of(t.rows, steps);
+  stage_kernel<D, GR><<<blocks_of(t.rows, d), 256, 0, stream>>>(a, code_bytes, d);
   return cudaGetLastError();
 }
 
