@@ -791,6 +791,99 @@ def test_graph_replayed_over_plans(rows):
         _assert_staged(o, lse, b.want(), rows=more)
 
 
+@pytest.mark.parametrize("hk", [24, 33])
+@pytest.mark.parametrize("d,group", SHAPES)
+def test_many_heads(d, group, hk):
+    """More heads than a warp's lanes take in one go, in pages a stride apart: append,
+    read, decode."""
+    rng = np.random.default_rng(hk)
+    kv = np.array([37, 3, 64])
+    ptr, idx, last, pages = W.build_page_table(rng, kv, 16, pool_pages=9)
+    ind = np.concatenate([[0], np.cumsum(kv)]).astype(np.int32)
+    n = int(ind[-1])
+    params = pka.make_params(hk, hk, d, 16, "HND", kv_dtype=_name(group))
+    size = pka.pka_kv_page_bytes(params)
+    both = torch.full((pages, 3, size), 0x5A, dtype=torch.uint8, device="cuda")
+    kp, vp = both[:, 0], both[:, 2]
+    k, v = (W.normal_bf16_bits(rng, (n, hk, d)) for _ in range(2))
+    table = (i32(ptr), i32(idx), i32(last))
+    pka.pka_append_paged_kv_cache(params, bf16(k), bf16(v), i32(ind), *table, kp, vp, kp.stride(0))
+    outs = [torch.zeros(n, hk, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    pka.pka_read_paged_kv_cache(params, None, i32(ind), *table, kp, vp, kp.stride(0), *outs)
+    q = W.normal_bf16_bits(rng, (3, hk, d))
+    attn = pka.BatchAttention()
+    attn.plan(None, ptr, last, num_qo_heads=hk, num_kv_heads=hk, head_dim=d, page_size=16,
+              layout="HND", kv_dtype=_name(group))
+    o, lse = attn.run(bf16(q), kp, vp, i32(idx))
+    torch.cuda.synchronize()
+    assert (both[:, 1] == 0x5A).all() and pka.pka_get_device_error() == 0
+    pools = [kv4.Pool.empty(pages, 16, hk, d, group, "HND", fill=0x5A) for _ in range(2)]
+    for p, x, got, out in zip(pools, (k, v), (kp, vp), outs):
+        p.data[:] = _appended(p, ref.bf16_bits_to_f64(x), ind, ptr, idx, last)
+        assert np.array_equal(got.cpu().numpy(), p.data)
+        rows = np.concatenate([kv4.request_rows(p, ptr, idx, r, int(m)) for r, m in enumerate(kv)])
+        assert np.array_equal(f64(out), kv4.bf16_round(rows.astype(np.float32)).astype(float))
+    _assert_decode(f64(o), f64(lse), kv4.attention(q, *pools, qo_indptr=np.arange(4),
+                                                   kv_indptr=ptr, kv_indices=idx, kv_lens=kv,
+                                                   hq=hk, hk=hk))
+
+
+@pytest.mark.parametrize("hq,hk", [(8, 2), (8, 1)])
+def test_many_short_requests(hq, hk):
+    rng = np.random.default_rng(70)
+    b = Batch(70, rng.integers(1, 6, 700), page=4, hq=hq, hk=hk, d=64, group=64)
+    o, lse, info = b.run()
+    assert info.num_decode_ctas <= 152
+    _assert_decode(o, lse, b.want())
+
+
+def test_captured_step_replayed():
+    """Append, attention and read-back captured once and replayed over new rows: each
+    replay's bytes and outputs are the eager calls'."""
+    page, hq, hk, d = 16, 8, 2, 128
+    rng = np.random.default_rng(80)
+    params = pka.make_params(hq, hk, d, page, kv_dtype="int4_g32")
+    size = pka.pka_kv_page_bytes(params)
+    kv = np.array([50, 17])
+    ptr, idx, last, pages = W.build_page_table(rng, kv, page, pool_pages=8)
+    table = (i32(ptr), i32(idx), i32(last))
+    ind, begin = i32([0, 1, 2]), i32(kv - 1)
+    pools = torch.zeros(pages, 2, size, dtype=torch.uint8, device="cuda")
+    q, o = (torch.zeros(2, hq, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lse = torch.zeros(2, hq, device="cuda")
+    x, y, ko, vo = (torch.zeros(2, hk, d, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    attn = pka.BatchAttention()
+    attn.plan(None, ptr, last, num_qo_heads=hq, num_kv_heads=hk, head_dim=d, page_size=page,
+              kv_dtype="int4_g32")
+    ids = i32(idx)
+
+    def step(stream=None):
+        k, v = pools[:, 0], pools[:, 1]
+        pka.pka_append_paged_kv_cache(params, x, y, ind, *table, k, v, k.stride(0), stream=stream)
+        attn.run(q, k, v, ids, out=o, lse=lse, stream=stream)
+        pka.pka_read_paged_kv_cache(params, begin, ind, *table, k, v, k.stride(0), ko, vo,
+                                    stream=stream)
+    step()
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        step(stream)
+    for i in range(3):
+        for t, h in ((q, hq), (x, hk), (y, hk)):
+            t.copy_(bf16(W.normal_bf16_bits(rng, (2, h, d))))
+        pools.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (pools, o, lse, ko, vo)]
+        pools.zero_()
+        step()
+        torch.cuda.synchronize()
+        for a, b in zip(got, (pools, o, lse, ko, vo)):
+            assert torch.equal(a, b)
+        assert got[0].any() and pka.pka_get_device_error() == 0
+
+
 # ---------------------------------------------------------------------------
 # Pages of 4-bit pools
 # ---------------------------------------------------------------------------
