@@ -32,6 +32,16 @@
 // in with cp.async, two stages ahead, and waits only for its own copies: there
 // is no producer, no barrier wait that could run out, and any page size, layout
 // and stride is one address a key.
+//   A CTA fills an SM (16 warps of 128 registers), at most one is launched on each.
+//
+// What bounds it: long rows run at 6.6 TB/s with groups of 128 of a head of 128
+// (25 ns a key of 8 heads on an SM), 6.2 with 64 and 5.2 with 32, where two or four
+// words a key instead of one are applied to the scores; D = 64 at 4.7, pages of one
+// key at 4.8.  Groups of 128 are bound by memory, the others by the warps' chains of
+// MMA, shuffle and exponential (issue slots 40 to 62% used, 16 warps).  An item's
+// start and end are 3 us, the kernel's about 10: the first copies, four look-ups
+// deep, and at the end the states' meeting, the write, the count and the join, each
+// a round trip.
 #include "pka_device.cuh"
 #include "pka_kv4.h"
 
@@ -40,6 +50,8 @@ namespace {
 
 constexpr int kTile = 32;        // keys of a warp's step
 constexpr int kMaxWarps = 16;
+// Tiles a warp has on their way.  More do not help: 37 requests over a token pool of
+// heads of 64 take 28.1 us with two, 28.4 with three, 28.8 with four.
 constexpr int kStages = 2;
 constexpr float kRescale = 8.0f;  // log2 units, as in decode.cu
 constexpr float kHeadroom = 6.0f;
@@ -182,8 +194,9 @@ __device__ __forceinline__ float sum_keys(float x) {
 // 2^(b_k - m), o = sum (2^(b_k - m) / s) o_k and lse = m + log2 s; pieces with b_k
 // = -inf carry no weight, and if all are empty o = 0 and lse = -inf.  Lane k takes
 // the statistics of pieces k, k + 32, ..; then the rows come in, from other SMs
-// through L2 (.cg).  Two heads at a time, 8 rows of each in flight: the call is a
-// chain of such round trips at the end of the kernel.
+// through L2 (.cg).  Two heads at a time, R rows of each in flight: the call is a
+// chain of such round trips at the end of the kernel.  With R = 8 it is shorter, but
+// its registers are taken from the main loop's (64 requests 45.6 us, 40.5 with 4).
 template <int D>
 __device__ __noinline__ void join_heads(const AttnArgs& a, const PkaDecodeJoin j, int row,
                                         int head0, int group, int first, int step, int lane) {
@@ -278,7 +291,8 @@ __device__ __noinline__ void join_heads(const AttnArgs& a, const PkaDecodeJoin j
 // 0, 1 of a quad go on with the first block, lanes 2, 3 with the second: half the
 // exponentials, words and products a tile.  P^T then holds the blocks in columns
 // 0..3 and 4..7; each block's V takes its own columns (the others as zeros), and
-// the two halves of O meet at the end.
+// the two halves of O meet at the end.  With 4 qo heads a kv head: 8 requests of
+// 32K to 128K keys 138.8 us (148.0 without), 64 of 512 to 4096 40.6 (41.8).
 template <int D, int GR, bool HALF>
 __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     decode4_kernel(const __grid_constant__ Decode4Args p) {
@@ -628,7 +642,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
 
     // ---- the head's warps bring their states together, pair by pair; which warp
     // ends an item goes round, so that the others are at the next one meanwhile ----
-    const int turn = (ii - i0) % n_split, rank = split >= turn ? split - turn : split - turn + n_split;
+    const int turn = (ii - i0) % n_split;
+    const int rank = split >= turn ? split - turn : split - turn + n_split;
     for (int n = n_split; n > 1;) {
       const int half = (n + 1) >> 1;
       float* const slot = slots + (rank >= half ? rank - half : rank) * (S::SLOT / 4) + lane;

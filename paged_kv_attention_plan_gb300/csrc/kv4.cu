@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(256) append4_kernel(const __grid_constant__ Ap
 // a warp takes a row (or a part of its steps), eight steps in flight, and looks it
 // up alone: bound by the rows that go out, in 2 bytes an element whatever they came
 // in, it is faster where a warp writes K's and V's whole rows (walking rows as
-// above, 40,800 rows of 8 heads of 128: 40.9 us for 39.9 out of 4-bit pools, 53.8
+// above, 40,710 rows of 8 heads of 128: 40.9 us for 39.9 out of 4-bit pools, 53.8
 // for 43.7 out of e4m3 ones).
 // ---------------------------------------------------------------------------
 

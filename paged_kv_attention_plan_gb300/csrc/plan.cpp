@@ -88,7 +88,9 @@ struct pka_plan_s {
 namespace {
 
 constexpr int kMinDecodeChunk = 64;
-// 4-bit pools: what starting and ending an item takes, in keys (3 us at 25 ns a key)
+// 4-bit pools: what starting and ending an item takes, in keys (3 us at 25 ns a key).
+// A token pool of 37 requests: 31.3 us with 0, 29.4 with 56, 28.3 with 112, 28.1 with
+// 224; 64 requests of 512 to 4096 keys 42.0, 41.2, 40.6 and 40.5.
 constexpr int kItemCost4 = 112;
 
 thread_local char g_last_error[256] = "";
