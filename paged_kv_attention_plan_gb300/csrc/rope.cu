@@ -24,10 +24,11 @@ enum RopeLayout {
   kHalf = 0,       // (x[i], x[i + R/2]), R/2 a multiple of 8: whole 16-byte pieces
   kAdjacent = 1,   // (x[2i], x[2i + 1])
   kScattered = 2,  // (x[i], x[i + R/2]), any other R: through shared memory
+  kPartOfHalf = 3,  // kHalf with R < D, where a lane's pieces lie elsewhere: 4-bit pools
 };
 
-// What the pools hold.
-enum PoolType { kBf16 = 0, kE4m3 = 1, kInt4 = 2 };
+// What the pools hold; any other number: 4 bits in groups of so many.
+enum PoolType { kBf16 = 0, kE4m3 = 1 };
 
 constexpr int kMaxHeads = 4096;            // of a row; keeps the second grid axis small
 constexpr int64_t kMaxRows = INT64_C(1) << 33;  // eight a block
@@ -60,8 +61,7 @@ struct RopeArgs {
   int layout;
   float k_scale, v_scale;    // e4m3 pools
   float k_inv, v_inv;        // pow2_reciprocal of these
-  int group;                 // 4-bit pools: elements of a group,
-  int64_t code_bytes;        // and where a page's words start
+  int64_t code_bytes;        // 4-bit pools: where a page's words start
   int32_t* err;
   uint64_t turns[64];        // F_i
 };
@@ -118,6 +118,20 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return r;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The least of 8 numbers, or of their negatives; NaN where one is.
+template <bool NEGATED>
+__device__ __forceinline__ float least8(const float (&x)[8]) {
+  auto at = [&](int i) { return NEGATED ? -x[i] : x[i]; };
+  const float a = min_nan(at(0), at(1), at(2)), b = min_nan(at(3), at(4), at(5));
+  return min_nan(min_nan(at(6), at(7), a), b);
+}
+
 __device__ __forceinline__ void to_shared(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -158,22 +172,30 @@ __device__ __forceinline__ void from_shared(const float* p, float (&x)[8]) {
 // 128 elements turned 46.6 / 42.4, 16,387 with 126 88.2 / 93.4, an append of
 // 9,216 with 40 50.6 / 46.3).
 // Into e4m3 pools both pieces are held as floats: three blocks, 80 registers
-// and 12 to 36 bytes spilled.  Into 4-bit pools the rotated floats of a step go
-// through shared memory, whatever the layout: a group's elements lie in pieces
-// of several lanes, and behind it a lane holds 16 elements in a row.
+// and 12 to 36 bytes spilled.
+//   Into 4-bit pools as well.  A lane's pieces are elements 8u .. and D/2 + 8u .. of
+// a head, so a group is a power of two of lanes; only half layouts that rotate a part
+// of a head (kPartOfHalf) hand their floats on through shared memory, 16 in a row to
+// a lane.  Bound by instructions: 9,101 rows of 48 heads of 128 with the read-back of
+// what they wrote take 52.8 us with groups of a head, 55 with smaller ones, 59.4 where
+// half of each head rotates (through shared memory for all: 61.3, 60.5 and 59.6;
+// group sizes known at run time only: 64.1; four blocks an SM 59.4, two 62).
 constexpr int kInFlight = 2;
 
 template <int D, int L, bool APPEND, int POOL>
 __global__ void __launch_bounds__(256, POOL != kBf16 ? 3 : 4)
 rope_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr bool F8 = POOL == kE4m3, INT4 = POOL == kInt4;
+  constexpr bool F8 = POOL == kE4m3, INT4 = POOL > kE4m3;
+  constexpr int GR = POOL;  // elements of a group (4-bit pools)
+  constexpr bool HALF = L == kHalf || L == kPartOfHalf;
   constexpr int UNITS = D / 16;      // lanes of a head
   constexpr int HPS = 32 / UNITS;    // heads of a step
   constexpr int K = 8 / HPS;         // pairs whose sine and cosine a lane computes
-  // floats of a head in shared memory; 4-bit pools read it back 16 in a row, four
+  // floats of a head in shared memory; kPartOfHalf reads it back 16 in a row, four
   // floats of padding apart so that the lanes of a head meet different banks
-  constexpr int STRIDE = INT4 ? D + 4 * UNITS : D + UNITS;
-  __shared__ __align__(16) float heads_in_shared[L == kScattered || INT4 ? 8 * HPS * STRIDE : 4];
+  constexpr int STRIDE = L == kPartOfHalf ? D + 4 * UNITS : D + UNITS;
+  constexpr bool SHARED = L == kScattered || L == kPartOfHalf;
+  __shared__ __align__(16) float heads_in_shared[SHARED ? 8 * HPS * STRIDE : 4];
   const int lane = threadIdx.x & 31;
   const int u = lane % UNITS, sub = lane / UNITS;
   const int rd = a.rotary_dim;
@@ -184,13 +206,13 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
   // where the lane's pieces lie in a head (B `apart` elements behind A), and
   // which of its pairs rotate
   int off_a = 8 * u, apart = D / 2;
-  if (L == kHalf) {
+  if (HALF) {
     const int t = u - rd / 16;
     if (t >= 0) off_a = rd + 16 * t;
     apart = t < 0 ? rd / 2 : 8;
   }
   auto pair_of = [&](int j) {
-    return L == kHalf ? 8 * u + j
+    return HALF ? 8 * u + j
            : L == kScattered ? u + UNITS * j
                              : j < 4 ? 4 * u + j : D / 4 + 4 * u + j - 4;
   };
@@ -284,6 +306,12 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
   const int64_t in_pool = (int64_t)page * a.page_stride +
                           (int64_t)slot * (a.layout == PKA_NHD ? a.k_heads * D : D) + off_a;
 
+  // 4-bit pools: the page's bytes, the row's place among the page's (slot, head) and a
+  // head's step there (a page is under 2 GB)
+  const int64_t pool_page = (int64_t)page * a.page_stride;
+  const int pool_slot = a.layout == PKA_NHD ? slot * a.k_heads : slot;
+  const int pool_head = a.layout == PKA_NHD ? 1 : a.page_size;
+
   for (int hb = h0;;) {
 #pragma unroll
     for (int t = 0; t < kInFlight; ++t) {
@@ -325,23 +353,24 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
         }
         __syncwarp();  // read before the next step writes
         if (!store && !(INT4 && hb + (t + 1) * HPS > a.q_heads)) continue;
-      } else if (F8 || INT4 || (L == kHalf && turning && !is_v)) {
+      } else if (F8 || INT4 || (HALF && turning && !is_v)) {
         unpack8(wa[t], xa);
         unpack8(wb[t], xb);
         if (!is_v) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             // pair j: (A[j], B[j]), or adjacent elements of A (j < 4) or of B
-            float& x = L == kHalf ? xa[j] : j < 4 ? xa[2 * j] : xb[2 * (j - 4)];
-            float& y = L == kHalf ? xb[j] : j < 4 ? xa[2 * j + 1] : xb[2 * (j - 4) + 1];
-            if (L == kHalf ? turning != 0 : (turning >> j & 1) != 0) {
+            float& x = HALF ? xa[j] : j < 4 ? xa[2 * j] : xb[2 * (j - 4)];
+            float& y = HALF ? xb[j] : j < 4 ? xa[2 * j + 1] : xb[2 * (j - 4) + 1];
+            if (HALF ? turning != 0 : (turning >> j & 1) != 0) {
               const float z = x * c[j] - y * s[j];
               y = x * s[j] + y * c[j];
               x = z;
-              if (L == kAdjacent) (j < 4 ? wa[t][j & 3] : wb[t][j & 3]) = float2_to_bf16x2(x, y);
+              if (L == kAdjacent && !(INT4 && to_pool))
+                (j < 4 ? wa[t][j & 3] : wb[t][j & 3]) = float2_to_bf16x2(x, y);
             }
           }
-          if (L == kHalf && turning) {
+          if (HALF && turning && !(INT4 && to_pool)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               wa[t][i] = float2_to_bf16x2(xa[2 * i], xa[2 * i + 1]);
@@ -358,42 +387,57 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
             w = float2_to_bf16x2(f.x * c[j] - f.y * s[j], f.x * s[j] + f.y * c[j]);
         }
       }
-      // a step of q heads alone keeps off shared memory
-      if (INT4 && hb + (t + 1) * HPS > a.q_heads) {  // the same for all lanes
-        float* m = heads_in_shared + ((threadIdx.x >> 5) * HPS + sub) * STRIDE;
-        const int off_b = off_a + apart;
-        to_shared(m + off_a + (off_a >> 4) * 4, xa);
-        to_shared(m + off_b + (off_b >> 4) * 4, xb);
-        __syncwarp();
-        float y[2][8];
-        from_shared(m + 20 * u, y[0]);
-        from_shared(m + 20 * u + 8, y[1]);
-        __syncwarp();  // read before the next step writes
-        // least element and negated greatest, of the lane and then of its group
-        float lo = y[0][0], hi = -y[0][0];
+      // 4-bit pools: a group is pieces 8u .. and D/2 + 8u .. of all the head's lanes, or
+      // one of the two of GR / 8 lanes.  A step of q heads alone has none.
+      if constexpr (INT4) {
+        if (hb + (t + 1) * HPS > a.q_heads) {  // the same for all lanes
+          constexpr bool ROW = L == kPartOfHalf;  // its pieces now, through shared memory
+          if constexpr (ROW) {
+            float* m = heads_in_shared + ((threadIdx.x >> 5) * HPS + sub) * STRIDE;
+            to_shared(m + off_a + (off_a >> 4) * 4, xa);
+            to_shared(m + off_a + apart + ((off_a + apart) >> 4) * 4, xb);
+            __syncwarp();
+            from_shared(m + 20 * u, xa);
+            from_shared(m + 20 * u + 8, xb);
+            __syncwarp();  // read before the next step writes
+          }
+          constexpr int N = ROW || GR == D ? 1 : 2;  // groups that a lane is in
+          constexpr int LANES = ROW ? GR / 16 : GR == D ? UNITS : GR / 8;
+          const int at_head = pool_slot + (h - (is_v ? k_end : a.q_heads)) * pool_head;
+          uint8_t* const p = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) + pool_page;
+          uint8_t* const codes = p + at_head * (D / 2) + (ROW ? 8 : 4) * u;
+          uint8_t* const words = p + a.code_bytes + (at_head * (D / GR) + u / LANES) * 4;
+          // least elements and negated greatest, of the lane and then of its groups
+          float lo[2] = {least8<false>(xa), least8<false>(xb)};
+          float hi[2] = {least8<true>(xa), least8<true>(xb)};
+          if constexpr (N == 1) {
+            lo[0] = min_nan(lo[0], lo[1]);
+            hi[0] = min_nan(hi[0], hi[1]);
+          }
 #pragma unroll
-        for (int i = 1; i < 16; ++i) {
-          lo = min_nan(lo, y[i >> 3][i & 7]);
-          hi = min_nan(hi, -y[i >> 3][i & 7]);
-        }
-        for (int off = 1; off < a.group / 16; off <<= 1) {
-          lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-          hi = min_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-        }
-        if (!store) continue;
-        if (to_pool) {
-          const Group4 g = group4(lo, -hi);
-          const int hh = h - (is_v ? k_end : a.q_heads);
-          const int64_t idx = a.layout == PKA_NHD ? (int64_t)slot * a.k_heads + hh
-                                                  : (int64_t)hh * a.page_size + slot;
-          uint8_t* p = static_cast<uint8_t*>(is_v ? a.v_pool : a.k_pool) +
-                       (int64_t)page * a.page_stride;
-          *reinterpret_cast<uint2*>(p + idx * (D / 2) + 8 * u) =
-              make_uint2(codes4<true>(y[0], g), codes4<true>(y[1], g));
-          if (u % (a.group / 16) == 0)
-            *reinterpret_cast<uint32_t*>(p + a.code_bytes +
-                                         (idx * (D / a.group) + u / (a.group / 16)) * 4) = g.word;
-          continue;
+          for (int off = 1; off < LANES; off <<= 1) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              lo[i] = min_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], off));
+              hi[i] = min_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], off));
+            }
+          }
+          if (to_pool && store) {
+            const Group4 g = group4(lo[0], -hi[0]);
+            const Group4 gb = N == 1 ? g : group4(lo[1], -hi[1]);
+            const uint32_t ca = codes4<true>(xa, g), cb = codes4<true>(xb, gb);
+            if constexpr (ROW) {
+              *reinterpret_cast<uint2*>(codes) = make_uint2(ca, cb);
+            } else {
+              *reinterpret_cast<uint32_t*>(codes) = ca;
+              *reinterpret_cast<uint32_t*>(codes + D / 4) = cb;
+            }
+            if (u % LANES == 0) {
+              *reinterpret_cast<uint32_t*>(words) = g.word;
+              if constexpr (N == 2) *reinterpret_cast<uint32_t*>(words + D / GR * 2) = gb.word;
+            }
+          }
+          if (to_pool || !store) continue;
         }
       }
       // rotated elements are rounded once, to bf16 or to a code; the others keep their bits
@@ -448,16 +492,24 @@ cudaError_t launch(const RopeArgs& args, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+template <int D, bool APPEND, int POOL>
+cudaError_t launch_layout(const RopeArgs& a, int l, cudaStream_t stream) {
+  if constexpr (POOL > kE4m3)
+    if (l == kPartOfHalf) return launch<D, kPartOfHalf, APPEND, POOL>(a, stream);
+  return l == kAdjacent ? launch<D, kAdjacent, APPEND, POOL>(a, stream)
+         : l == kHalf   ? launch<D, kHalf, APPEND, POOL>(a, stream)
+                        : launch<D, kScattered, APPEND, POOL>(a, stream);
+}
+
 template <bool APPEND, int POOL>
 cudaError_t launch_any(const RopeArgs& a, int head_dim, bool adjacent, cudaStream_t stream) {
-  const int l = adjacent ? kAdjacent : a.rotary_dim % 16 == 0 ? kHalf : kScattered;
-  if (head_dim == 128)
-    return l == kAdjacent ? launch<128, kAdjacent, APPEND, POOL>(a, stream)
-           : l == kHalf   ? launch<128, kHalf, APPEND, POOL>(a, stream)
-                          : launch<128, kScattered, APPEND, POOL>(a, stream);
-  return l == kAdjacent ? launch<64, kAdjacent, APPEND, POOL>(a, stream)
-         : l == kHalf   ? launch<64, kHalf, APPEND, POOL>(a, stream)
-                        : launch<64, kScattered, APPEND, POOL>(a, stream);
+  const int l = adjacent                                        ? kAdjacent
+                : a.rotary_dim % 16                             ? kScattered
+                : POOL > kE4m3 && a.rotary_dim < head_dim       ? kPartOfHalf
+                                                                : kHalf;
+  if (head_dim == 128) return launch_layout<128, APPEND, POOL>(a, l, stream);
+  if constexpr (POOL <= 64) return launch_layout<64, APPEND, POOL>(a, l, stream);
+  return cudaErrorInvalidValue;  // a group of more than a head
 }
 
 bool rope_valid(const pka_rope* r, int head_dim) {
@@ -643,14 +695,15 @@ pka_status pka_rope_append_paged_kv_cache(
   a.v_scale = p->v_scale > 0.f ? p->v_scale : 1.f;
   a.k_inv = pka::pow2_reciprocal(a.k_scale);
   a.v_inv = pka::pow2_reciprocal(a.v_scale);
-  a.group = group;
   a.code_bytes = pka::kv4_code_bytes(*p);
   a.err = pka::device_error_word();
   const bool adjacent = rope->interleaved != 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = group ? pka::launch_any<true, pka::kInt4>(a, d, adjacent, st)
-                        : f8  ? pka::launch_any<true, pka::kE4m3>(a, d, adjacent, st)
-                              : pka::launch_any<true, pka::kBf16>(a, d, adjacent, st);
+  const cudaError_t e = group == 32    ? pka::launch_any<true, 32>(a, d, adjacent, st)
+                        : group == 64  ? pka::launch_any<true, 64>(a, d, adjacent, st)
+                        : group == 128 ? pka::launch_any<true, 128>(a, d, adjacent, st)
+                        : f8           ? pka::launch_any<true, pka::kE4m3>(a, d, adjacent, st)
+                                       : pka::launch_any<true, pka::kBf16>(a, d, adjacent, st);
   return e == cudaSuccess ? PKA_OK : pka::cuda_failure(e, "rope append launch");
 }
 
