@@ -420,14 +420,15 @@ void order_split_pieces(PlanLists* L) {
 }
 
 // How many of a unit's `left` keys go to a CTA whose share of `chunk` keys holds
-// `load`, where an item costs `over` keys besides its own; 0: the CTA is full.
+// `load`, where an item costs `over` keys besides its own; -1: the CTA is full.  (A
+// request without keys takes its 0 keys: its row is written like any other.)
 // Cuts inside a request fall on 16-key tile boundaries, so that whole pages stay
 // in one tile of the decode kernel.
 int64_t take_keys(int64_t left, int64_t chunk, int64_t load, int64_t over) {
   const int64_t room = chunk - load - over;
   if (left <= room) return left;
   return room < pka::kDecodeTileTokens
-             ? 0
+             ? -1
              : room / pka::kDecodeTileTokens * pka::kDecodeTileTokens;
 }
 
@@ -469,16 +470,17 @@ void plan_decode(const pka_params* p, const std::vector<Batch>& lv, int num_sms,
         int64_t n = 0, load = 0;
         for (const Unit& u : units) {
           int64_t left = u.K;
-          do {
+          for (;;) {
             const int64_t take = take_keys(left, share, load, over);
-            if (take == 0) {
+            if (take < 0) {
               ++n;
               load = 0;
               continue;
             }
             left -= take;
             load += take + over;
-          } while (left > 0);
+            if (left == 0) break;
+          }
         }
         return n + (load > 0);
       };
@@ -516,9 +518,9 @@ void plan_decode(const pka_params* p, const std::vector<Batch>& lv, int num_sms,
   for (const Unit& u : units) {
     pieces.clear();
     int64_t t = 0;
-    do {
+    for (;;) {
       const int64_t take = take_keys(u.K - t, chunk, load, over);
-      if (take == 0) {  // no room for a whole tile: close this CTA
+      if (take < 0) {  // no room for a whole tile: close this CTA
         L->dec_cta_ptr.push_back((int)items.size());
         load = 0;
         continue;
@@ -531,7 +533,8 @@ void plan_decode(const pka_params* p, const std::vector<Batch>& lv, int num_sms,
         L->dec_cta_ptr.push_back((int)items.size());
         load = 0;
       }
-    } while (t < u.K);
+      if (t == u.K) break;
+    }
     assign_records(L, items, pieces, lv[u.l].q_row0[u.r], 1, u.hg * hpc * g, hpc * g, hpc);
   }
   if (L->dec_cta_ptr.back() != (int)items.size()) L->dec_cta_ptr.push_back((int)items.size());

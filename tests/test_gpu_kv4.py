@@ -979,3 +979,46 @@ def test_a_step_with_everything_together():
     tol = np.repeat(step, group, -1) * (0.5 + 15 * 2.0 ** -8) + 2.0 ** -7 * (np.abs(vals) + 5)
     assert np.all(np.abs(f64(back[1][:42]) - vals) <= tol)
     assert torch.equal(back[0][:41], back[0][42:83])
+
+
+@pytest.mark.parametrize("interleaved,rotary", [(False, 16), (False, 48), (True, 34)])
+@pytest.mark.parametrize("d,group", SHAPES)
+def test_rope_append_of_part_of_a_head(d, group, interleaved, rotary):
+    """Half layouts whose pieces do not lie where a lane's codes do, and adjacent pairs of
+    which a lane turns some."""
+    test_rope_append(d, group, interleaved, rotary)
+
+
+@pytest.mark.parametrize("rotary,interleaved", [(0, False), (32, False), (10, False), (0, True)])
+@pytest.mark.parametrize("d,group", SHAPES)
+def test_rope_append_layouts_agree(d, group, rotary, interleaved):
+    """The same rows into NHD and HND pools read back as the same values; many rows, so that
+    a warp takes several steps of one."""
+    hq, hk, page, kv = 9, 5, 16, [700, 3, 1200]
+    rng = np.random.default_rng(rotary + d)
+    ptr, idx, last, pages = W.build_page_table(rng, np.asarray(kv), page)
+    ind = i32(np.concatenate([[0], np.cumsum(kv)]))
+    table = (i32(ptr), i32(idx), i32(last))
+    n = sum(kv)
+    q, k, v = (bf16(W.normal_bf16_bits(rng, (n, h, d))) for h in (hq, hk, hk))
+    rope = pka.make_rope(rotary or d, interleaved=interleaved)
+    q_outs, reads = [], []
+    for layout in ("NHD", "HND"):
+        params = pka.make_params(hq, hk, d, page, layout, kv_dtype=_name(group))
+        pools = torch.zeros(pages, 2, pka.pka_kv_page_bytes(params), dtype=torch.uint8,
+                            device="cuda")
+        kp, vp = pools[:, 0], pools[:, 1]
+        q_outs.append(torch.empty_like(q))
+        pka.pka_rope_append_paged_kv_cache(params, rope, q, q_outs[-1], k, v, ind, *table, kp, vp,
+                                           kp.stride(0))
+        reads.append([torch.empty_like(k) for _ in range(2)])
+        pka.pka_read_paged_kv_cache(params, None, ind, *table, kp, vp, kp.stride(0), *reads[-1])
+    torch.cuda.synchronize()
+    assert pka.pka_get_device_error() == 0 and torch.equal(*q_outs)
+    for a, b in zip(*reads):
+        assert torch.equal(a, b)
+    # V is not rotated: off by half a step and the roundings of its words at most
+    x = f64(v)
+    _, step, _ = kv4.quantize(x.astype(np.float32), group)
+    tol = np.repeat(step, group, -1) * (0.5 + 15 * 2.0 ** -8) + 2.0 ** -7 * (np.abs(x) + 5)
+    assert np.all(np.abs(f64(reads[0][1]) - x) <= tol)

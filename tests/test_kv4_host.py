@@ -212,6 +212,32 @@ def test_decode_plans_fill_the_sms_once(seed):
         assert max(per) <= -(-len(plan["decode_items"]) // 152) + 1
 
 
+@pytest.mark.parametrize("lens", [(1, 33, 0, 250), (0,), (0, 0, 5000, 0), (64, 0, 64)])
+def test_rows_without_keys_are_planned(lens):
+    """A decode row whose request has no keys is an item of none, which writes its zeros;
+    ragged K/V, where lengths of 0 are allowed."""
+    n = len(lens)
+    p = pka.make_params(16, 4, 128, 1, mask_mode="none", kv_ragged=True, num_sms=152)
+    kv = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    s, info, plan = _plan(p, np.arange(n + 1, dtype=np.int32), kv, None)
+    assert s == OK
+    keys = {r: 0 for r in range(n)}
+    for w in plan["decode_items"]:
+        keys[w["q_row0"]] += w["t1"] - w["t0"]
+    assert {w["q_row0"] for w in plan["decode_items"]} == set(range(n))
+    assert [keys[r] for r in range(n)] == list(lens)
+    assert plan["decode_cta_ptr"][-1] == len(plan["decode_items"])
+
+
+@pytest.mark.parametrize("kv", INT4)
+def test_paged_requests_without_pages(kv):
+    """Paged requests hold at least one key: refused, as for bf16 pools."""
+    qo, ptr, last = _i32(0, 1, 2, 3), _i32(0, 2, 2, 5), _i32(4, 0, 1)
+    for t in (kv, "bf16"):
+        assert _plan(pka.make_params(8, 2, 128, 4, kv_dtype=t, num_sms=152), qo, ptr,
+                     last)[0] not in (OK, UNSUPPORTED)
+
+
 @pytest.mark.parametrize("kv", INT4)
 def test_graph_mode_needs_the_scratch_capacity(kv):
     kw = dict(kv_dtype=kv, graph_max_batch=4, graph_max_qo_rows=16, num_sms=152)
