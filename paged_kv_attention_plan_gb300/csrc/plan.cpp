@@ -1072,7 +1072,8 @@ pka_status pka_run(pka_plan_t plan, const pka_params* p, const void* q, const vo
              : pka::launch_decode(a, h.num_decode_ctas, p->head_dim, g, &plan->decode_maps, st);
     if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   }
-  if (graph || h.num_prefill_items > 0) {
+  // a graph over 4-bit pools that declared no scratch has decode rows alone
+  if (graph ? !int4 || plan->dequant_capacity > 0 : h.num_prefill_items > 0) {
     a.cta_ptr = plan->int_ws_d + h.off_prefill_cta_ptr;
     a.items = reinterpret_cast<const PkaWorkItem*>(plan->int_ws_d + h.off_prefill_items);
     // the Q (and ragged K/V) tensor maps span the buffers' declared rows

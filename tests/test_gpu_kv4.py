@@ -791,6 +791,40 @@ def test_graph_replayed_over_plans(rows):
         _assert_staged(o, lse, b.want(), rows=more)
 
 
+def test_graph_of_decode_rows_alone():
+    """Without graph_max_kv_tokens a graph serves decode batches; others are refused."""
+    cap = dict(graph_max_batch=5, graph_max_qo_rows=5)
+    attn, stream, graph = pka.BatchAttention(), torch.cuda.Stream(), None
+    for i, n in enumerate([5, 2, 4]):
+        b = Batch(60 + i, np.random.default_rng(i).integers(1, 900, n), page=16, hq=16, hk=2,
+                  layout="HND")
+        with torch.cuda.stream(stream):
+            if graph is None:
+                size = b.k.data.shape[1]
+                k, v = (torch.zeros(400, size, dtype=torch.uint8, device="cuda") for _ in range(2))
+                q, o = (torch.zeros(5, 16, 128, dtype=torch.bfloat16, device="cuda")
+                        for _ in range(2))
+                lse, idx = torch.zeros(5, 16, device="cuda"), i32(np.zeros(400, np.int32))
+            k[:len(b.k.data)], v[:len(b.k.data)] = _dev(b.k), _dev(b.v)
+            idx[:len(b.kv_indices)] = i32(b.kv_indices)
+            q[:n] = bf16(b.q)
+            stream.synchronize()
+            pka.pka_plan_wait(attn.handle)
+            attn.plan(b.qo_indptr, b.kv_indptr, b.last, stream=stream, **b.params(**cap))
+            if graph is None:
+                attn.run(q, k, v, idx, out=o, lse=lse, stream=stream)
+                stream.synchronize()
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph, stream=stream):
+                    attn.run(q, k, v, idx, out=o, lse=lse, stream=stream)
+            graph.replay()
+            stream.synchronize()
+        assert pka.pka_get_device_error() == 0
+        _assert_decode(f64(o[:n]), f64(lse[:n]), b.want())
+    with pytest.raises(pka.PkaError):
+        attn.plan(np.array([0, 2], np.int32), b.kv_indptr[:2], b.last[:1], **b.params(**cap))
+
+
 @pytest.mark.parametrize("hk", [24, 33])
 @pytest.mark.parametrize("d,group", SHAPES)
 def test_many_heads(d, group, hk):
