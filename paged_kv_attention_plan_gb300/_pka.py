@@ -268,6 +268,25 @@ def _here_rows(t, name, dev, rows, heads, dim):
             f"{_shape(rows, heads, dim)} with the heads of a row contiguous")
 
 
+def _here_table(indptr, name, kv_indptr, kv_indices, last_page_len, dev):
+    """Pointers of a batch's rows and page table, all checked by one expression: a call of
+    a few microseconds makes it."""
+    try:
+        if indptr.dtype is _I32 and kv_indptr.dtype is _I32 and kv_indices.dtype is _I32 \
+                and last_page_len.dtype is _I32 and indptr.get_device() == dev \
+                and kv_indptr.get_device() == dev and kv_indices.get_device() == dev \
+                and last_page_len.get_device() == dev and indptr.is_contiguous() \
+                and kv_indptr.is_contiguous() and kv_indices.is_contiguous() \
+                and last_page_len.is_contiguous():
+            return (indptr.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(),
+                    last_page_len.data_ptr())
+    except AttributeError:
+        pass
+    return (_here(indptr, name, _I32, dev), _here(kv_indptr, "kv_indptr", _I32, dev),
+            _here(kv_indices, "kv_indices", _I32, dev),
+            _here(last_page_len, "last_page_len", _I32, dev))
+
+
 def _shape(*dims):
     return "[" + ", ".join(map(str, dims)) + "]"
 
@@ -487,6 +506,18 @@ def pka_run_static_scratch(handle, params, q, k, v, page_stride, kv_indices, pac
 
 def pka_append_paged_kv_cache(params, k_new, v_new, append_indptr, kv_indptr, kv_indices,
                               last_page_len, k, v, page_stride, stream=None, check=True) -> int:
+    if params.kv_dtype >= PKA_KV_INT4_G32:
+        dev = torch.cuda.current_device()
+        kn, vn = _here(k_new, "k_new", _BF16, dev), _here(v_new, "v_new", _BF16, dev)
+        app, ptr, idx, last = _here_table(append_indptr, "append_indptr", kv_indptr, kv_indices,
+                                          last_page_len, dev)
+        kpool, vpool = _here_pools(k, v, params, dev)[:2]
+        s = lib().pka_append_paged_kv_cache(
+            ctypes.byref(params), append_indptr.numel() - 1, kn, vn, app, k_new.shape[0], ptr, idx,
+            last, kpool, vpool, int(page_stride), _here_stream(stream, dev))
+        if check and s:
+            _check(s, "pka_append_paged_kv_cache")
+        return s
     bf16, i32 = torch.bfloat16, torch.int32
     s = lib().pka_append_paged_kv_cache(
         ctypes.byref(params), append_indptr.numel() - 1, _dev(k_new, "k_new", bf16),
@@ -496,7 +527,7 @@ def pka_append_paged_kv_cache(params, k_new, v_new, append_indptr, kv_indptr, kv
         _dev_pool(v, "v", params),
         int(page_stride),
         _stream(stream))
-    if check:
+    if check and s:
         _check(s, "pka_append_paged_kv_cache")
     return s
 
@@ -527,22 +558,22 @@ def pka_read_paged_kv_cache(params, begin, read_indptr, kv_indptr, kv_indices, l
     if not isinstance(some, torch.Tensor) or some.dim() != 3:
         raise ValueError("k_out and v_out must be [rows, num_kv_heads, head_dim], one of them "
                          "given")
-    rows, batch = some.shape[0], read_indptr.numel() - 1
-    shape = (rows, params.num_kv_heads, params.head_dim)
-    outs = []
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None and isinstance(t, torch.Tensor) and t.shape != shape:
-            raise ValueError(f"{name} must be {_shape(*shape)}, got {tuple(t.shape)}")
-        outs.append(None if t is None else _here(t, name, _BF16, dev))
+    shape = some.shape
+    rows, batch = shape[0], read_indptr.numel() - 1
+    if shape[1] != params.num_kv_heads or shape[2] != params.head_dim or \
+            (isinstance(v_out, torch.Tensor) and v_out.shape != shape):
+        want = _shape(rows, params.num_kv_heads, params.head_dim)
+        raise ValueError(f"k_out and v_out must be {want}, got " + " and ".join(
+            str(tuple(t.shape)) for t in (k_out, v_out) if isinstance(t, torch.Tensor)))
+    k_to = None if k_out is None else _here(k_out, "k_out", _BF16, dev)
+    v_to = None if v_out is None else _here(v_out, "v_out", _BF16, dev)
     at = None
     if begin is not None:
         at = _here(begin, "begin", _I32, dev)
         if begin.numel() != batch:
             raise ValueError(f"begin: {batch} values, got {begin.numel()}")
-    ind = _here(read_indptr, "read_indptr", _I32, dev)
-    ptr = _here(kv_indptr, "kv_indptr", _I32, dev)
-    idx = _here(kv_indices, "kv_indices", _I32, dev)
-    last = _here(last_page_len, "last_page_len", _I32, dev)
+    ind, ptr, idx, last = _here_table(read_indptr, "read_indptr", kv_indptr, kv_indices,
+                                      last_page_len, dev)
     if kv_indptr.numel() != batch + 1 or last_page_len.numel() != batch:
         raise ValueError("kv_indptr and last_page_len must describe read_indptr's requests")
     kpool, vpool, pshape, strides = _here_pools(k, v, params, dev)
@@ -552,7 +583,7 @@ def pka_read_paged_kv_cache(params, begin, read_indptr, kv_indptr, kv_indices, l
         raise ValueError(f"page_stride: the pools' is {strides[0]}, got {page_stride}")
     s = lib().pka_read_paged_kv_cache(
         ctypes.byref(params), batch, at, ind, rows, ptr, idx, last, kpool, vpool,
-        int(page_stride), pshape[0], outs[0], outs[1], _here_stream(stream, dev))
+        int(page_stride), pshape[0], k_to, v_to, _here_stream(stream, dev))
     if check and s:
         _check(s, "pka_read_paged_kv_cache")
     return s
@@ -619,10 +650,8 @@ def pka_rope_append_paged_kv_cache(params, rope, q, q_out, k_new, v_new, append_
         pos = _here(positions, "positions", _I32, dev)
         if positions.numel() != rows:
             raise ValueError(f"positions: {rows} values, got {positions.numel()}")
-    app = _here(append_indptr, "append_indptr", _I32, dev)
-    ptr = _here(kv_indptr, "kv_indptr", _I32, dev)
-    idx = _here(kv_indices, "kv_indices", _I32, dev)
-    last = _here(last_page_len, "last_page_len", _I32, dev)
+    app, ptr, idx, last = _here_table(append_indptr, "append_indptr", kv_indptr, kv_indices,
+                                      last_page_len, dev)
     if kv_indptr.numel() != batch + 1 or last_page_len.numel() != batch:
         raise ValueError("kv_indptr and last_page_len must describe append_indptr's requests")
     kpool, vpool, shape, strides = _here_pools(k, v, params, dev)
