@@ -269,9 +269,10 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
       continue;
     }
     const int64_t page = (int64_t)p.page * t.page_stride * (KIND == 0 ? 2 : 1);
-    const int64_t code_at = page + p.slot * codes.per_slot + piece * IN;
-    const int64_t word_at =
-        page + a.code_bytes + p.slot * words.per_slot + piece / (KIND > 1 ? KIND / 8 : 1) * 4;
+    // 64 bits: pages of bf16 and e4m3 pools may be larger than 2 GB
+    const int64_t code_at = page + (int64_t)p.slot * codes.per_slot + piece * IN;
+    const int64_t word_at = page + a.code_bytes + (int64_t)p.slot * words.per_slot +
+                            piece / (KIND > 1 ? KIND / 8 : 1) * 4;
     for (int hb = h0; hb < h1; hb += kReadSteps * HPS) {
       uint4 x[kReadSteps];
 #pragma unroll

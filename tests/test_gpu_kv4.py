@@ -335,6 +335,40 @@ def test_read_other_types(kv, scales, layout, d):
             assert np.array_equal(f64(o), kv4.bf16_round(v).astype(np.float64))
 
 
+@pytest.mark.parametrize("kv,layout,hk,bytes_a_slot", [
+    ("bf16", "NHD", 32, 8192), ("bf16", "HND", 1, 256), ("e4m3", "NHD", 32, 4096),
+    ("e4m3", "HND", 1, 128)])
+def test_read_of_pages_over_2_gb(kv, layout, hk, bytes_a_slot):
+    """One page a request, past 2 GB: a row's place in it does not fit 32 bits."""
+    d, page = 128, (1 << 31) // bytes_a_slot + 70
+    shape = (1, page, hk, d) if layout == "NHD" else (1, hk, page, d)
+    pool = torch.zeros(shape, dtype=torch.bfloat16 if kv == "bf16" else torch.uint8, device="cuda")
+    by_slot = pool if layout == "NHD" else pool.transpose(1, 2)
+    begin = np.array([0, page // 2 - 1, page - 70 - 2, page - 3], np.int32)
+    g = torch.Generator(device="cuda").manual_seed(hk)
+    want = []
+    for s in begin:
+        if kv == "bf16":
+            rows = torch.randn(3, hk, d, generator=g, device="cuda").to(torch.bfloat16)
+            by_slot[0, s:s + 3] = rows
+        else:
+            codes = torch.randint(0, 127, (3, hk, d), generator=g, device="cuda",
+                                  dtype=torch.uint8)
+            by_slot[0, s:s + 3] = codes
+            rows = codes.view(torch.float8_e4m3fn).float().to(torch.bfloat16)
+        want.append(rows)
+    params = pka.make_params(hk, hk, d, page, layout, kv_dtype=kv)
+    n = len(begin)
+    outs = [torch.zeros(3 * n, hk, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    pka.pka_read_paged_kv_cache(params, i32(begin), i32(3 * np.arange(n + 1)), i32(np.arange(n + 1)),
+                                i32(np.zeros(n)), i32(np.full(n, page)), pool, pool,
+                                pool.stride(0), *outs)
+    torch.cuda.synchronize()
+    assert pka.pka_get_device_error() == 0
+    for o in outs:
+        assert torch.equal(o, torch.cat(want))
+
+
 def test_read_steps_around_bad_rows():
     """Positions outside a request's keys and page ids outside the pool are left
     and noted; the other rows come back."""
