@@ -509,12 +509,23 @@ def pka_append_paged_kv_cache(params, k_new, v_new, append_indptr, kv_indptr, kv
     if params.kv_dtype >= PKA_KV_INT4_G32:
         dev = torch.cuda.current_device()
         kn, vn = _here(k_new, "k_new", _BF16, dev), _here(v_new, "v_new", _BF16, dev)
+        shape, batch = k_new.shape, append_indptr.numel() - 1
+        if shape != v_new.shape or shape[1:] != (params.num_kv_heads, params.head_dim):
+            want = _shape("rows", params.num_kv_heads, params.head_dim)
+            raise ValueError(f"k_new and v_new must both be {want}, got {tuple(shape)} and "
+                             f"{tuple(v_new.shape)}")
         app, ptr, idx, last = _here_table(append_indptr, "append_indptr", kv_indptr, kv_indices,
                                           last_page_len, dev)
-        kpool, vpool = _here_pools(k, v, params, dev)[:2]
+        if kv_indptr.numel() != batch + 1 or last_page_len.numel() != batch:
+            raise ValueError("kv_indptr and last_page_len must describe append_indptr's requests")
+        kpool, vpool, pshape, strides = _here_pools(k, v, params, dev)
+        if len(pshape) != 4:
+            raise ValueError("k and v must be pools [pages, ...]")
+        if page_stride != strides[0] and pshape[0] > 1:
+            raise ValueError(f"page_stride: the pools' is {strides[0]}, got {page_stride}")
         s = lib().pka_append_paged_kv_cache(
-            ctypes.byref(params), append_indptr.numel() - 1, kn, vn, app, k_new.shape[0], ptr, idx,
-            last, kpool, vpool, int(page_stride), _here_stream(stream, dev))
+            ctypes.byref(params), batch, kn, vn, app, shape[0], ptr, idx, last, kpool, vpool,
+            int(page_stride), _here_stream(stream, dev))
         if check and s:
             _check(s, "pka_append_paged_kv_cache")
         return s

@@ -339,3 +339,41 @@ def test_binding_refuses_tensors_off_the_device(p4):
     with pytest.raises(ValueError):
         _pka._int4_pages(torch.zeros(3, 1088, dtype=torch.uint8)[:, ::2], "k", p4)
     _pka._int4_pages(torch.zeros(3, 2, 544, dtype=torch.uint8)[:, 1], "k", p4)
+
+
+def test_append_binding_refuses_rows_tables_and_strides_that_do_not_fit(monkeypatch):
+    """Rows of K and V alike, tables of one batch, and the pools' own stride: the kernel
+    reads V by K's row count and trusts the table.  (Checked on host tensors, with the
+    library's entry replaced.)"""
+    calls = []
+
+    class Library:
+        @staticmethod
+        def pka_append_paged_kv_cache(*args):
+            calls.append(args)
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # host tensors' device
+    monkeypatch.setattr(_pka, "lib", lambda: Library)
+    p = pka.make_params(8, 2, 128, 4, kv_dtype="int4_g128")
+    pools = torch.zeros(5, 2, 544, dtype=torch.uint8)
+    rows = torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    table = [torch.tensor(x, dtype=torch.int32) for x in ([0, 1, 3], [0, 1, 2], [0, 1], [1, 2])]
+
+    def append(k_new=rows, v_new=rows, table=table, k=pools[:, 0], v=pools[:, 1], stride=1088):
+        return pka.pka_append_paged_kv_cache(p, k_new, v_new, *table, k, v, stride, stream=0)
+
+    assert append() == 0 and append(k=pools[:1, 0], v=pools[:1, 1], stride=544) == 0
+    assert len(calls) == 2
+    longer = torch.zeros(4, 2, 128, dtype=torch.bfloat16)
+    for kw in (dict(v_new=rows[:2]), dict(k_new=longer), dict(k_new=longer[:3, :1].contiguous()),
+               dict(k_new=longer[..., :64].contiguous(), v_new=longer[..., :64].contiguous()),
+               dict(k_new=rows.view(3, 256), v_new=rows.view(3, 256)),
+               dict(table=[table[0], table[1][:2]] + table[2:]),
+               dict(table=table[:3] + [table[3][:1]]),
+               dict(stride=544), dict(stride=2176), dict(stride=0),
+               dict(k=pools, v=pools, stride=1088), dict(k=pools, v=pools, stride=544),
+               dict(v=pools[:, 1].contiguous())):
+        with pytest.raises(ValueError):
+            append(**kw)
+    assert len(calls) == 2
