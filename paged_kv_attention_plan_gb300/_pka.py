@@ -223,12 +223,27 @@ def _dev_pool(t, name, params=None):
 
 
 def _int4_pages(t, name, params):
-    """4-bit pages: [.., pages, bytes], the bytes of a page (pka_kv_page_bytes) contiguous."""
+    """4-bit pages: [pages, bytes], the bytes of a page (pka_kv_page_bytes) contiguous."""
     size, shape, strides = _page_bytes(params), t.shape, t.stride()
-    if len(shape) < 2 or shape[-1] != size or strides[-1] != 1 or \
-            (shape[-2] > 1 and strides[-2] < size):
-        raise ValueError(f"{name} must be [.., pages, {size}] with each page contiguous, got "
+    if len(shape) != 2 or shape[1] != size or strides[1] != 1 or \
+            (shape[0] > 1 and strides[0] < size):
+        raise ValueError(f"{name} must be [pages, {size}] with each page contiguous, got "
                          f"{tuple(t.shape)} with strides {t.stride()}")
+
+
+def _run_pools(k, v, params, page_stride):
+    """Pointers of the K and V that a run reads; page_stride is 4-bit pools' own."""
+    kp, vp = _dev_pool(k, "k", params), _dev_pool(v, "v", params)
+    if params.kv_dtype >= PKA_KV_INT4_G32:
+        _int4_strides(k, v, page_stride)
+    return kp, vp
+
+
+def _int4_strides(k, v, page_stride):
+    for t, name in ((k, "k"), (v, "v")):
+        if t.shape[0] > 1 and t.stride(0) != page_stride:
+            raise ValueError(f"{name}: its pages are {t.stride(0)} apart, page_stride is "
+                             f"{page_stride}")
 
 
 # The checks of the operators around the cache: their calls are a few
@@ -478,8 +493,8 @@ def pka_run(handle, params, q, k, v, page_stride, kv_indices, packed_mask, o, ls
             stream=None, check=True) -> int:
     bf16 = torch.bfloat16
     fws = float_ws.numel() * float_ws.element_size() if float_ws is not None else 0
-    s = lib().pka_run(handle, ctypes.byref(params), _dev(q, "q", bf16),
-                      _dev_pool(k, "k", params), _dev_pool(v, "v", params), int(page_stride),
+    kp, vp = _run_pools(k, v, params, page_stride)
+    s = lib().pka_run(handle, ctypes.byref(params), _dev(q, "q", bf16), kp, vp, int(page_stride),
                       _dev(kv_indices, "kv_indices", torch.int32),
                       _dev(packed_mask, "packed_mask", torch.uint8), _dev(o, "o", bf16),
                       _dev(lse, "lse", torch.float32), _ptr(float_ws), fws, _stream(stream))
@@ -493,10 +508,10 @@ def pka_run_static_scratch(handle, params, q, k, v, page_stride, kv_indices, pac
     """pka_run with the split-KV scratch in the library's static device array
     (no workspace from the caller; see include/pka.h)."""
     bf16 = torch.bfloat16
+    kp, vp = _run_pools(k, v, params, page_stride)
     s = lib().pka_run_static_scratch(
-        handle, ctypes.byref(params), _dev(q, "q", bf16), _dev_pool(k, "k", params),
-        _dev_pool(v, "v", params),
-        int(page_stride), _dev(kv_indices, "kv_indices", torch.int32),
+        handle, ctypes.byref(params), _dev(q, "q", bf16), kp, vp, int(page_stride),
+        _dev(kv_indices, "kv_indices", torch.int32),
         _dev(packed_mask, "packed_mask", torch.uint8), _dev(o, "o", bf16),
         _dev(lse, "lse", torch.float32), _stream(stream))
     if check:

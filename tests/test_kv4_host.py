@@ -377,3 +377,19 @@ def test_append_binding_refuses_rows_tables_and_strides_that_do_not_fit(monkeypa
         with pytest.raises(ValueError):
             append(**kw)
     assert len(calls) == 2
+
+
+def test_runs_refuse_pools_of_several_layers_and_strides_of_their_own(p4):
+    """A run takes one layer's pages, K's and V's the same stride apart: a pool of all
+    layers would be read a layer apart."""
+    pools = torch.zeros(3, 5, 2, 544, dtype=torch.uint8)  # layers, pages, K and V
+    for t in (pools, pools[:, :, 0], pools[0], pools[0, 0, 0]):
+        with pytest.raises(ValueError):
+            _pka._int4_pages(t, "k", p4)
+    k, v = pools[0, :, 0], pools[0, :, 1]
+    _pka._int4_pages(k, "k", p4)
+    _pka._int4_strides(k, v, 1088)
+    _pka._int4_strides(k[:1], v[:1], 544)  # one page: its stride leads nowhere
+    for kk, vv, stride in ((k, v, 544), (k, v.contiguous(), 1088), (k.contiguous(), v, 544)):
+        with pytest.raises(ValueError):
+            _pka._int4_strides(kk, vv, stride)
