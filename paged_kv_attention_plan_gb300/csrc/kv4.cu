@@ -106,6 +106,11 @@ __device__ __forceinline__ float word_origin(uint32_t w) {
   return __uint_as_float(w & 0xffff0000u);
 }
 
+// The largest magnitude under a word: that of code 0 or of code 15.
+__device__ __forceinline__ float word_bound(uint32_t w) {
+  return fmaxf(fabsf(word_origin(w)), fabsf(fmaf(15.f, word_step(w), word_origin(w))));
+}
+
 // origin + step * c of the 8 codes c of a word, each pair as (even, odd).  A code
 // becomes the float 2^23 + c by one byte permutation, and c by a subtraction;
 // step * c is exact (8 by 4 bits), so the sum is rounded once.
@@ -336,8 +341,8 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
 
 // ---------------------------------------------------------------------------
 // The f16 rows of a launch on the tensor cores (F16Stage), in two launches: Q
-// and, from the words alone, bounds of each kv head's largest magnitude, then K
-// and V with their scales.  Bound by memory; 16 to 20 times as many bytes go
+// and, from the words alone, bounds of the largest magnitude in each kv head of
+// each unit, then K and V with their scales.  Bound by memory; 16 to 20 times as many bytes go
 // out as the words that are read twice.
 // ---------------------------------------------------------------------------
 
@@ -349,13 +354,15 @@ __device__ __forceinline__ int64_t staged_rows(const KvRows& t, int* units) {
   return *units > 0 ? min((int64_t)max(t.counts[2], 0), t.rows) : 0;
 }
 
-// Page and slot of scratch row `row` (the last unit that starts at or before it).
-__device__ __forceinline__ Place unit_place(const KvRows& t, int units, int64_t row) {
+// Page and slot of scratch row `row`, and its unit (the last that starts at or before it).
+__device__ __forceinline__ Place unit_place(const KvRows& t, int units, int64_t row,
+                                            int* unit) {
   int lo = 0, hi = units - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (t.units[mid].dst_row0 <= row) lo = mid; else hi = mid - 1;
   }
+  *unit = lo;
   const PkaDequantUnit u = t.units[lo];
   const uint32_t j = (uint32_t)(row - u.dst_row0), nth = j / (uint32_t)t.page_size;
   Place p;
@@ -364,38 +371,41 @@ __device__ __forceinline__ Place unit_place(const KvRows& t, int units, int64_t 
   return p;
 }
 
-// The bounds of one kv head: block `block_id` of `blocks` takes its rows.
+// The bounds of one kv head in all units: block `block_id` of `blocks` takes its rows.
+// Lanes whose rows are of one unit add to its bounds together.
 template <int G>
 __device__ __forceinline__ void range_of_words(const F16Stage& a, int64_t code_bytes, int head,
                                                unsigned block_id, unsigned blocks) {
   const KvRows& t = a.rows;
   int units;
   const int64_t rows = staged_rows(t, &units);
-  float most[2] = {0.f, 0.f};
-  for (int64_t row = block_id * 256ll + threadIdx.x; row < rows; row += blocks * 256ll) {
-    const Place p = unit_place(t, units, row);
-    const int64_t idx = t.layout == PKA_NHD ? (int64_t)p.slot * t.heads + head
-                                            : (int64_t)head * t.page_size + p.slot;
-    const int64_t at = (int64_t)p.page * t.page_stride + code_bytes + idx * (4 * G);
+  const int lane = threadIdx.x & 31;
+  for (int64_t row0 = block_id * 256ll + (threadIdx.x & ~31); row0 < rows;
+       row0 += blocks * 256ll) {
+    float most[2] = {0.f, 0.f};
+    int unit = -1;
+    if (row0 + lane < rows) {
+      const Place p = unit_place(t, units, row0 + lane, &unit);
+      const int64_t idx = t.layout == PKA_NHD ? (int64_t)p.slot * t.heads + head
+                                              : (int64_t)head * t.page_size + p.slot;
+      const int64_t at = (int64_t)p.page * t.page_stride + code_bytes + idx * (4 * G);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>((kv ? a.v : a.k) + at);
+#pragma unroll
+        for (int g = 0; g < G; ++g)  // fmaxf passes a NaN group over
+          most[kv] = fmaxf(most[kv], word_bound(w[g]));
+      }
+    }
+    const unsigned with = __match_any_sync(kAll, unit);
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      const uint32_t* w = reinterpret_cast<const uint32_t*>((kv ? a.v : a.k) + at);
-#pragma unroll
-      for (int g = 0; g < G; ++g)  // fmaxf passes a NaN group over
-        most[kv] = fmaxf(most[kv], fmaf(15.f, fabsf(word_step(w[g])), fabsf(word_origin(w[g]))));
+      const uint32_t m = __reduce_max_sync(with, __float_as_uint(most[kv]));
+      if (m && lane == __ffs(with) - 1)  // lanes of no row have 0
+        atomicMax(reinterpret_cast<uint32_t*>(a.kv_range + (int64_t)unit * t.heads + head) + kv,
+                  m);
     }
   }
-  __shared__ uint32_t block[2];
-  if (threadIdx.x < 2) block[threadIdx.x] = 0;
-  __syncthreads();
-#pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    const uint32_t m = __reduce_max_sync(kAll, __float_as_uint(most[kv]));
-    if ((threadIdx.x & 31) == 0 && m) atomicMax(&block[kv], m);
-  }
-  __syncthreads();
-  if (threadIdx.x < 2 && block[threadIdx.x])
-    atomicMax(a.kv_range + 2 * head + threadIdx.x, block[threadIdx.x]);
 }
 
 __device__ __forceinline__ uint32_t float2_to_f16x2(float a, float b) {
@@ -433,14 +443,16 @@ __global__ void __launch_bounds__(256)
   const Rows codes(t, D / 2), words(t, 4 * G);
   const int64_t code_off = hh * codes.per_head + piece * 4;
   const int64_t word_off = code_bytes + hh * words.per_head + piece / LPG * 4;
-  const float ku = f16_up(a.kv_range[2 * hh]), vu = f16_up(a.kv_range[2 * hh + 1]);
+  float ku = 0.f, vu = 0.f;  // the scales of the lane's head in unit `scaled`
+  int scaled = -1;
   const int64_t row_elems = (int64_t)hk * D, out_off = hh * D + piece * 8;
   int units;
   const int64_t rows = staged_rows(t, &units), end = min(rows + 127, t.rows);
   for (int64_t row0 = walk.row0; row0 < end; row0 += walk.turn) {
     const int n = (int)min((int64_t)deal.rows, end - row0);
     Place mine{kZero, 0};
-    if (lane < n && row0 + lane < rows) mine = unit_place(t, units, row0 + lane);
+    int my_unit = 0;
+    if (lane < n && row0 + lane < rows) mine = unit_place(t, units, row0 + lane, &my_unit);
     for (int i0 = 0; i0 < n; i0 += kAhead) {
       uint32_t kc[kAhead], vc[kAhead], kw[kAhead], vw[kAhead];
 #pragma unroll
@@ -459,7 +471,14 @@ __global__ void __launch_bounds__(256)
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
+        const int unit = __shfl_sync(kAll, my_unit, (i0 + u) & 31);
         if (!have || i0 + u >= n) continue;
+        if (unit != scaled) {
+          const uint2 bound = a.kv_range[(int64_t)unit * hk + hh];
+          ku = f16_up(bound.x);
+          vu = f16_up(bound.y);
+          scaled = unit;
+        }
         uint4 k = codes_to_f16(kc[u], word_step(kw[u]) * ku, word_origin(kw[u]) * ku);
         uint4 v = codes_to_f16(vc[u], word_step(vw[u]) * vu, word_origin(vw[u]) * vu);
         if (!(word_step(vw[u]) + word_origin(vw[u]) <= INFINITY)) {  // NaN
@@ -572,7 +591,8 @@ cudaError_t launch_stage_t(const F16Stage& a, cudaStream_t stream) {
   constexpr int HPS = 256 / D;
   const KvRows& t = a.rows;
   const int64_t code_bytes = (int64_t)t.page_size * t.heads * (D / 2);
-  cudaError_t e = cudaMemsetAsync(a.kv_range, 0, (size_t)t.heads * 2 * sizeof(uint32_t), stream);
+  cudaError_t e = cudaMemsetAsync(
+      a.kv_range, 0, (size_t)t.num_units * t.heads * sizeof(*a.kv_range), stream);
   if (e != cudaSuccess) return e;
   // the words of all heads beside Q's rows: neither waits for the other
   const unsigned word_blocks = blocks_of(t.rows, 256, 1) * (unsigned)t.heads;

@@ -85,12 +85,13 @@ cudaError_t launch_read(const KvRows& r, int kv_dtype, int head_dim, float k_sca
                         cudaStream_t stream);
 // The rows of a launch on the tensor cores, staged in f16 from 4-bit pools and
 // bf16 queries: 11 bits where bf16 would round origin + step * code to 8.  Each
-// of Q's heads and each kv head of K and of V is scaled by the power of two that
-// brings its largest element into [2^14, 2^15), so no magnitude leaves f16's
-// range: an element keeps 11 bits down to 2^-28 of the largest.
+// of Q's heads, and each kv head of K and of V of a unit (a request's or a cascade
+// node's keys), is scaled by the power of two that brings its largest element into
+// [2^14, 2^15), so no magnitude leaves f16's range: an element keeps 11 bits down to
+// 2^-28 of the largest.  A launch reads no other unit's scales with a unit's keys.
 struct F16Scales {
-  const float* q_down;       // [rows, Hq]: what Q's rows are to be multiplied by
-  const uint32_t* kv_range;  // [Hk][K, V]: bits of a bound of the largest magnitude
+  const float* q_down;    // [rows, Hq]: what Q's rows are to be multiplied by
+  const uint2* kv_range;  // [units, Hk]: bits of a bound of K's and V's largest magnitude
 };
 struct F16Stage {
   KvRows rows;               // units; rows: of the scratch (its capacity in graph mode)
@@ -103,7 +104,7 @@ struct F16Stage {
   float* q_down;
   int64_t q_rows;
   int q_heads;
-  uint32_t* kv_range;
+  uint2* kv_range;           // [rows.num_units, Hk]
 };
 cudaError_t launch_stage_f16(const F16Stage& s, int head_dim, int group, cudaStream_t stream);
 cudaError_t launch_prefill_f16(const AttnArgs& a, const F16Scales& scales, int num_ctas,

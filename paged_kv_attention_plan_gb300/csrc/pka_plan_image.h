@@ -53,7 +53,8 @@ struct PkaWorkItem {
   int32_t mask_lo;     // mask_indptr[req] (bit offset), low/high words
   int32_t mask_hi;
   int32_t flags;
-  int32_t join;        // decode piece of a split: first PkaDecodeJoin of its unit, else -1
+  int32_t join;        // decode piece of a split: first PkaDecodeJoin of its unit; tensor-core
+                       // item over e4m3 or 4-bit K/V: its PkaDequantUnit; else -1
 };
 
 // One (query row, qo head) whose partial states are merged after a split.

@@ -44,7 +44,7 @@ struct PlanLists {
   std::vector<int32_t> merge_slots;
   // e4m3 K/V: requests whose keys are decoded to bf16 for the tensor-core rows
   std::vector<PkaDequantUnit> dequant;
-  std::unordered_map<int32_t, int32_t> dequant_row0;  // node page-list start -> first scratch row
+  std::unordered_map<int32_t, int32_t> dequant_unit;  // node page-list start -> its unit
   int64_t dequant_rows = 0;
 
   void reset(bool is_cascade) {
@@ -78,7 +78,7 @@ struct pka_plan_s {
   int device = -1;
   int32_t layout_records = 0;  // partial records the float workspace is laid out for
   int32_t merge_capacity = 0;  // graph mode: merge tasks the image has room for
-  int32_t dequant_capacity = 0;      // graph mode: dequant units the image has room for
+  int32_t dequant_capacity = 0;      // dequant units the image has room for
   int64_t scratch_capacity = 0;      // rows the float workspace's bf16 K/V scratch is laid out for
   PlanLists lists;             // the planner's lists, reused by every plan
   pka::MapCache decode_maps{};   // tensor maps of the last run's launches
@@ -253,15 +253,16 @@ pka_status check_kv_dtype(const pka_params* p, const Batch& b) {
 // them; the items' kv_base is rewritten to the node's first scratch row (the
 // kernel then reads the scratch as ragged K/V).
 void plan_dequant(PlanLists* L) {
-  L->dequant_row0.clear();
+  L->dequant_unit.clear();
   for (PkaWorkItem& w : L->pre_items) {
-    auto it = L->dequant_row0.find(w.kv_base);
-    if (it == L->dequant_row0.end()) {
-      it = L->dequant_row0.emplace(w.kv_base, (int32_t)L->dequant_rows).first;
+    auto it = L->dequant_unit.find(w.kv_base);
+    if (it == L->dequant_unit.end()) {
+      it = L->dequant_unit.emplace(w.kv_base, (int32_t)L->dequant.size()).first;
       L->dequant.push_back({w.kv_base, w.kv_len, (int32_t)L->dequant_rows, 0});
       L->dequant_rows += w.kv_len;
     }
-    w.kv_base = it->second;
+    w.join = it->second;
+    w.kv_base = L->dequant[it->second].dst_row0;
   }
 }
 
@@ -678,16 +679,17 @@ size_t kv_scratch_bytes(const pka_params* p, int64_t rows) {
   return (b + 255) & ~size_t(255);
 }
 
-// What 4-bit K/V stage besides K and V for `rows` query rows: Q in f16 [rows, Hq,
-// D], its scales [rows, Hq], and a bound of K's and V's magnitudes per kv head;
-// each part rounded up to 256 bytes.
+// What 4-bit K/V stage besides K and V for `rows` query rows and the keys of `units`
+// requests: Q in f16 [rows, Hq, D], its scales [rows, Hq], and bounds of K's and V's
+// magnitudes [units, Hk]; each part rounded up to 256 bytes.
 struct Kv4Staging {
   size_t rows, down, range;
 };
-Kv4Staging kv4_staging(const pka_params* p, int64_t rows) {
+Kv4Staging kv4_staging(const pka_params* p, int64_t rows, int64_t units) {
   const size_t heads = (size_t)rows * p->num_qo_heads;
   auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
-  return {up(heads * p->head_dim * 2), up(heads * 4), up((size_t)p->num_kv_heads * 8)};
+  return {up(heads * p->head_dim * 2), up(heads * 4),
+          up((size_t)units * p->num_kv_heads * 8)};
 }
 
 }  // namespace
@@ -808,7 +810,7 @@ pka_status plan_levels(pka_plan_t plan, const pka_params* p, const std::vector<B
   // and for 4-bit K/V the staged rows of Q and the scales
   info.float_ws_bytes += 2 * kv_scratch_bytes(p, scratch_rows);
   if (pka::kv4_group(p->kv_dtype) && scratch_rows > 0) {
-    const Kv4Staging q = kv4_staging(p, graph ? p->graph_max_qo_rows : nnz);
+    const Kv4Staging q = kv4_staging(p, graph ? p->graph_max_qo_rows : nnz, n_dequant);
     info.float_ws_bytes += q.rows + q.down + q.range;
   }
   info.kv_scratch_rows = (int32_t)L.dequant_rows;
@@ -1101,7 +1103,7 @@ pka_status pka_run(pka_plan_t plan, const pka_params* p, const void* q, const vo
       const int64_t n_rows = graph ? plan->scratch_capacity : h.dequant_rows;
       cudaError_t e;
       if (int4) {
-        const Kv4Staging size = kv4_staging(p, rows);
+        const Kv4Staging size = kv4_staging(p, rows, plan->dequant_capacity);
         char* q16 = reinterpret_cast<char*>(sv) + kv_scratch_bytes(p, plan->scratch_capacity);
         pka::F16Stage f{};
         f.rows.units = units;
@@ -1122,7 +1124,7 @@ pka_status pka_run(pka_plan_t plan, const pka_params* p, const void* q, const vo
         f.q_down = reinterpret_cast<float*>(q16 + size.rows);
         f.q_rows = rows;
         f.q_heads = p->num_qo_heads;
-        f.kv_range = reinterpret_cast<uint32_t*>(q16 + size.rows + size.down);
+        f.kv_range = reinterpret_cast<uint2*>(q16 + size.rows + size.down);
         e = pka::launch_stage_f16(f, p->head_dim, pka::kv4_group(p->kv_dtype), st);
         pa.q = f.q16;
         scales.q_down = f.q_down;

@@ -24,8 +24,8 @@
 // tile) and feeds the P V product as the A operand.
 //
 // F16 (4-bit pools): Q, K and V come as f16 rows staged from the cache, scaled
-// by powers of two, and P is f16; the scales are taken back per row (Q's) and
-// per kv head (K's in the scores, V's in the output).
+// by powers of two, and P is f16; the scales are taken back per row (Q's) and per
+// item (K's in the scores, V's in the output).
 #include <cudaTypedefs.h>
 
 #include <cmath>
@@ -545,8 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int klim_first = w.kv_len - w.qo_len + w.q_local0 + x * TQ;
       const int64_t mrow = ((int64_t)w.mask_hi << 32 | (uint32_t)w.mask_lo) + (int64_t)i * w.kv_len;
       const int mm = (w.flags & PKA_ITEM_ALL_VISIBLE) ? (int)PKA_MASK_NONE : a.mask_mode;
+      uint2 bound = make_uint2(0u, 0u);  // F16: of the K and V that this item reads
       if constexpr (F16) {
-        sc = a.scale_log2 * f16_down(pp.f16.kv_range[2 * w.kv_head0]);
+        bound = pp.f16.kv_range[(int64_t)w.join * a.num_kv_heads + w.kv_head0];
+        sc = a.scale_log2 * f16_down(bound.x);
         if (i_tok < w.q_count)
           sc *= pp.f16.q_down[(int64_t)(w.q_row0 + i_tok) * a.num_qo_heads + w.kv_head0 * G + g];
         sc = fmaxf(sc, 1.17549435e-38f);  // a masked -inf times 0 would be NaN
@@ -660,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool store = i_tok < w.q_count;
       const bool any = F16 ? l != 0.f : l > 0.f;  // F16: NaN is not "no key"
       // V's scale (1 for bf16 K/V)
-      const float v_scale = F16 ? f16_down(pp.f16.kv_range[2 * w.kv_head0 + 1]) : a.v_scale;
+      const float v_scale = F16 ? f16_down(bound.y) : a.v_scale;
       const float inv = any ? v_scale / l : 0.f;
       const int head = w.kv_head0 * G + g;
       uint16_t* odst = a.o + ((int64_t)(w.q_row0 + i_tok) * a.num_qo_heads + head) * D;

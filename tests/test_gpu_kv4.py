@@ -682,6 +682,40 @@ def test_staged_magnitudes(k_size, v_size, q_size):
     _assert_staged(o, lse, want)
 
 
+@pytest.mark.parametrize("apart", [2.0 ** 45, 2.0 ** 60])
+@pytest.mark.parametrize("rows", [(40, 7), (2, 1)])
+def test_staged_requests_of_unlike_magnitudes(apart, rows):
+    """Requests of one launch whose K and V are 2^45 or 2^60 apart, the large one first, in
+    the middle and last: each has the bits that it has alone."""
+    kv = [90, 70, 129]
+    for large in range(3):
+        size = [apart if r == large else 1.0 for r in range(3)]
+        b = Batch(26, kv, qo_lens=[rows[0], rows[1], 3], page=4, hq=8, hk=2, d=64, group=32)
+        rng = np.random.default_rng(8)
+        x = ref.bf16_bits_to_f64(b.q)
+        for r in range(3):
+            x[b.qo_indptr[r]:b.qo_indptr[r + 1]] /= size[r]
+        b.q = (kv4.bf16_round(x.astype(np.float32)).view(np.uint32) >> 16).astype(np.uint16)
+        for pool in (b.k, b.v):
+            kv4.fill(pool, b.kv_indptr, b.kv_indices, b.kv_lens,
+                     [s * rng.standard_normal((n, 2, 64)) for s, n in zip(size, kv)])
+        kw = dict(decode_on_tensor_cores=True)
+        o, lse, info = b.run(**kw)
+        assert info.kv_scratch_rows == sum(kv)
+        _assert_staged(o, lse, b.want())
+        for r in range(3):
+            q0, q1 = b.qo_indptr[r], b.qo_indptr[r + 1]
+            p0, p1 = b.kv_indptr[r], b.kv_indptr[r + 1]
+            attn = pka.BatchAttention()
+            attn.plan(np.array([0, q1 - q0], np.int32), np.array([0, p1 - p0], np.int32),
+                      b.last[r:r + 1], **b.params(mask_mode="causal", **kw))
+            alone, alone_lse = attn.run(bf16(b.q[q0:q1]), _dev(b.k), _dev(b.v),
+                                        i32(b.kv_indices[p0:p1]))
+            torch.cuda.synchronize()
+            assert np.array_equal(f64(alone), o[q0:q1])
+            assert np.array_equal(f64(alone_lse), lse[q0:q1])
+
+
 def test_custom_masks_of_several_rows():
     """Masks of several rows; what they hide may be NaN, in K and in V."""
     qo, kv = [3, 1, 9], [40, 20, 33]

@@ -238,6 +238,29 @@ def test_paged_requests_without_pages(kv):
                      last)[0] not in (OK, UNSUPPORTED)
 
 
+@pytest.mark.parametrize("kv", INT4 + ["e4m3"])
+def test_items_over_a_scratch_name_their_unit(kv):
+    """An item of the tensor cores knows whose keys it reads: 4-bit pools keep the scales
+    of the staged rows by request and kv head, so that requests share none."""
+    n = 60
+    qo = np.concatenate([[0], np.cumsum(1 + np.arange(n) % 3)]).astype(np.int32)
+    ptr = np.concatenate([[0], np.cumsum(1 + np.arange(n) % 5)]).astype(np.int32)
+    last = np.full(n, 4, np.int32)
+    s, info, plan = _plan(pka.make_params(8, 2, 128, 4, kv_dtype=kv, num_sms=152), qo, ptr, last)
+    assert s == OK
+    units = plan["dequant_units"]
+    assert len(units) == 40 and len({w["join"] for w in plan["prefill_items"]}) == 40
+    for w in plan["prefill_items"]:
+        u = units[w["join"]]
+        assert u["dst_row0"] == w["kv_base"] and u["kv_base"] == ptr[w["req"]]
+        assert u["kv_len"] == w["kv_len"]
+    if kv != "e4m3":  # beside e4m3's: staged Q, its scales, and two bounds a unit and kv head
+        want = _plan(pka.make_params(8, 2, 128, 4, kv_dtype="e4m3", num_sms=152), qo, ptr, last)
+        rows = int(qo[-1])
+        more = rows * 8 * 128 * 2 + rows * 8 * 4 + 40 * 2 * 8
+        assert info.float_ws_bytes >= want[1].float_ws_bytes + more
+
+
 @pytest.mark.parametrize("kv", INT4)
 def test_graph_mode_needs_the_scratch_capacity(kv):
     kw = dict(kv_dtype=kv, graph_max_batch=4, graph_max_qo_rows=16, num_sms=152)
