@@ -109,7 +109,9 @@ typedef enum pka_mask_mode {
  * are not limited).  Paged K/V only (PKA_ERR_UNSUPPORTED for ragged, for a group
  * above head_dim, for pages of 2 GB and over 4096 kv heads); everything else as
  * over e4m3 pools.  A NaN group of a key that a row sees makes the row NaN (a
- * decode row: of V, its own elements of it). */
+ * decode row: of V, its own elements of it), and so do groups of V whose words
+ * hold other values that are not finite (a decode row: infinite or NaN); rows
+ * that do not see the key are not touched by it. */
 typedef enum pka_kv_dtype {
   PKA_KV_BF16 = 0,
   PKA_KV_FP8_E4M3 = 1,

@@ -106,9 +106,11 @@ __device__ __forceinline__ float word_origin(uint32_t w) {
   return __uint_as_float(w & 0xffff0000u);
 }
 
-// The largest magnitude under a word: that of code 0 or of code 15.
+// The largest magnitude under a word, that of code 0 or of code 15; infinity where one
+// of them is not finite.
 __device__ __forceinline__ float word_bound(uint32_t w) {
-  return fmaxf(fabsf(word_origin(w)), fabsf(fmaf(15.f, word_step(w), word_origin(w))));
+  const float a = fabsf(word_origin(w)), b = fabsf(fmaf(15.f, word_step(w), word_origin(w)));
+  return a < INFINITY && b < INFINITY ? fmaxf(a, b) : INFINITY;
 }
 
 // origin + step * c of the 8 codes c of a word, each pair as (even, odd).  A code
@@ -393,8 +395,10 @@ __device__ __forceinline__ void range_of_words(const F16Stage& a, int64_t code_b
       for (int kv = 0; kv < 2; ++kv) {
         const uint32_t* w = reinterpret_cast<const uint32_t*>((kv ? a.v : a.k) + at);
 #pragma unroll
-        for (int g = 0; g < G; ++g)  // fmaxf passes a NaN group over
-          most[kv] = fmaxf(most[kv], word_bound(w[g]));
+        for (int g = 0; g < G; ++g) {
+          const float b = word_bound(w[g]);
+          most[kv] = fmaxf(most[kv], b < INFINITY ? b : 0.f);
+        }
       }
     }
     const unsigned with = __match_any_sync(kAll, unit);
@@ -422,8 +426,8 @@ __device__ __forceinline__ uint4 codes_to_f16(uint32_t codes, float step, float 
                     float2_to_f16x2(v[2].x, v[2].y), float2_to_f16x2(v[3].x, v[3].y));
 }
 
-// A warp's rows as above, K and V of a head together.  A key whose V is NaN in a
-// group gets zeros there and NaN in K instead: the rows that see it become NaN, and
+// A warp's rows as above, K and V of a head together.  A key whose V is not finite in
+// a group gets zeros there and NaN in K instead: the rows that see it become NaN, and
 // the others, whose probability of it is 0, do not (0 * NaN in the P V product
 // would reach every row of a tile).  For the same reason the up to 127 rows behind
 // the last one that a tile may read, old ones of another plan in graph mode, become
@@ -481,7 +485,7 @@ __global__ void __launch_bounds__(256)
         }
         uint4 k = codes_to_f16(kc[u], word_step(kw[u]) * ku, word_origin(kw[u]) * ku);
         uint4 v = codes_to_f16(vc[u], word_step(vw[u]) * vu, word_origin(vw[u]) * vu);
-        if (!(word_step(vw[u]) + word_origin(vw[u]) <= INFINITY)) {  // NaN
+        if (!(word_bound(vw[u]) < INFINITY)) {
           k = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
           v = make_uint4(0u, 0u, 0u, 0u);
         }

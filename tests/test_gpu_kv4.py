@@ -761,6 +761,55 @@ def test_staged_nan_group_shows(which):
     _assert_staged(o[10:20, 2:], lse[10:20, 2:], tuple(x[10:20, 2:] for x in other))
 
 
+def _set_word(pool, page, slot, head, group, step, origin):
+    """A word of the pool from the bits of its step and origin."""
+    n = pool.D // pool.g
+    at = pool.P * pool.H * (pool.D // 2) + (pool._row(slot, head) * n + group) * 4
+    pool.data[page, at:at + 4] = np.array([step, origin], np.uint16).view(np.uint8)
+
+
+INF, LARGE = 0x7F80, 0x7F7F  # bits of bf16 infinity and of its largest number
+
+
+@pytest.mark.parametrize("step,origin", [(0, INF), (0, INF | 0x8000), (INF, 0), (INF, INF | 0x8000),
+                                         (LARGE, LARGE), (0x7FC0, 0), (0x3F80, 0x7FC0)])
+def test_words_that_are_not_finite(step, origin):
+    """Infinite words (or whose 16th value is past float32), in V's and in K's groups: the
+    rows that see one are not finite, the rows that do not, by their causal end or in
+    another request, keep their values."""
+    qo, kv = [20, 30, 1], [60, 40, 25]
+    for hidden in (True, False):
+        b, clean = (Batch(27, kv, qo_lens=qo, page=4, hq=4, hk=2, d=128, group=64)
+                    for _ in range(2))
+        j, r = (59, 0) if hidden else (50, 0)  # seen by the last row alone, or from row 10 on
+        for pool in (b.v,) if hidden else (b.k, b.v):
+            _set_word(pool, int(b.kv_indices[b.kv_indptr[r] + j // 4]), j % 4, 0, 1, step, origin)
+        want = clean.want()
+        o, lse, _ = b.run()
+        first = 19 if hidden else 10
+        _assert_staged(o, lse, want, rows=list(range(first)) + list(range(20, 50)))
+        _assert_decode(o, lse, want, rows=[50])
+        assert np.isfinite(o[first:20, 2:]).all()
+        assert not np.isfinite(o[first:20, :2, 64:]).any()
+
+
+def test_infinite_words_behind_a_mask():
+    """A mask's hidden keys may be infinite in V, for staged rows and for decode rows."""
+    qo, kv = [5, 1], [40, 30]
+    b, clean = (Batch(28, kv, qo_lens=qo, page=4, hq=8, hk=2, d=64, group=32) for _ in range(2))
+    masks = [np.ones((a, c), bool) for a, c in zip(qo, kv)]
+    for r, j in ((0, 7), (0, 39), (1, 3)):
+        masks[r][:, j] = False
+        for h in range(2):
+            _set_word(b.v, int(b.kv_indices[b.kv_indptr[r] + j // 4]), j % 4, h, 1, 0, INF)
+    flat = np.concatenate([m.reshape(-1) for m in masks])
+    packed = torch.from_numpy(np.packbits(flat, bitorder="little")).cuda()
+    want = clean.want(mask="custom", mask_bool=flat)
+    o, lse, _ = b.run(mask=packed, mask_mode="custom")
+    _assert_staged(o, lse, want, rows=list(range(5)))
+    _assert_decode(o, lse, want, rows=[5])
+
+
 def test_decode_on_tensor_cores():
     b = Batch(22, [90, 1, 400], page=16, hq=8, hk=2, group=64)
     o, lse, info = b.run(decode_on_tensor_cores=True)
