@@ -105,8 +105,11 @@ typedef enum pka_mask_mode {
  * bf16 as its origin alone.  Decode rows read the codes and words without
  * rounding them; rows with qo_len >= 2 (and decode_on_tensor_cores) read an f16
  * scratch, each value rounded once more, to 11 bits (Q, too, is brought to f16,
- * where its bf16 values are exact; both scaled by powers of two, so magnitudes
- * are not limited).  Paged K/V only (PKA_ERR_UNSUPPORTED for ragged, for a group
+ * where its bf16 values are exact; Q is scaled by a power of two for each head of
+ * a row, K and V for each kv head of a request, whose values below 2^-28 of its
+ * largest have an error of 2^-39 of that).  A kv head of a request some of whose
+ * groups of K or of V, seen or not, have their largest values more than 2^16
+ * apart is read from a bf16 scratch, 8 bits of whatever magnitude.  Paged K/V only (PKA_ERR_UNSUPPORTED for ragged, for a group
  * above head_dim, for pages of 2 GB and over 4096 kv heads); everything else as
  * over e4m3 pools.  A NaN group of a key that a row sees makes the row NaN (a
  * decode row: of V, its own elements of it), and so do groups of V whose words

@@ -107,10 +107,11 @@ __device__ __forceinline__ float word_origin(uint32_t w) {
 }
 
 // The largest magnitude under a word, that of code 0 or of code 15; infinity where one
-// of them is not finite.
+// of them is not finite or would not be in bf16.
 __device__ __forceinline__ float word_bound(uint32_t w) {
   const float a = fabsf(word_origin(w)), b = fabsf(fmaf(15.f, word_step(w), word_origin(w)));
-  return a < INFINITY && b < INFINITY ? fmaxf(a, b) : INFINITY;
+  constexpr float kPastBf16 = 0x1.ffp127f;
+  return a < kPastBf16 && b < kPastBf16 ? fmaxf(a, b) : INFINITY;
 }
 
 // origin + step * c of the 8 codes c of a word, each pair as (even, odd).  A code
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadA
 // ---------------------------------------------------------------------------
 // The f16 rows of a launch on the tensor cores (F16Stage), in two launches: Q
 // and, from the words alone, bounds of the largest magnitude in each kv head of
-// each unit, then K and V with their scales.  Bound by memory; 16 to 20 times as many bytes go
+// each unit, and of the smallest of its groups, then K and V with their scales.  Bound by memory; 16 to 20 times as many bytes go
 // out as the words that are read twice.
 // ---------------------------------------------------------------------------
 
@@ -373,8 +374,9 @@ __device__ __forceinline__ Place unit_place(const KvRows& t, int units, int64_t 
   return p;
 }
 
-// The bounds of one kv head in all units: block `block_id` of `blocks` takes its rows.
-// Lanes whose rows are of one unit add to its bounds together.
+// The bounds of one kv head in all units: block `block_id` of `blocks` takes its rows,
+// 256 rows at a time, most often of one unit: then the block adds to its bounds at
+// once, otherwise each warp for the lanes of a unit.
 template <int G>
 __device__ __forceinline__ void range_of_words(const F16Stage& a, int64_t code_bytes, int head,
                                                unsigned block_id, unsigned blocks) {
@@ -382,12 +384,14 @@ __device__ __forceinline__ void range_of_words(const F16Stage& a, int64_t code_b
   int units;
   const int64_t rows = staged_rows(t, &units);
   const int lane = threadIdx.x & 31;
-  for (int64_t row0 = block_id * 256ll + (threadIdx.x & ~31); row0 < rows;
-       row0 += blocks * 256ll) {
-    float most[2] = {0.f, 0.f};
+  __shared__ uint32_t of_block[4];
+  __shared__ int block_unit;
+  for (int64_t row0 = block_id * 256ll; row0 < rows; row0 += blocks * 256ll) {
+    const int64_t row = row0 + threadIdx.x;
+    uint32_t most[4] = {0u, 0u, 0u, 0u};  // as in Kv4Range
     int unit = -1;
-    if (row0 + lane < rows) {
-      const Place p = unit_place(t, units, row0 + lane, &unit);
+    if (row < rows) {
+      const Place p = unit_place(t, units, row, &unit);
       const int64_t idx = t.layout == PKA_NHD ? (int64_t)p.slot * t.heads + head
                                               : (int64_t)head * t.page_size + p.slot;
       const int64_t at = (int64_t)p.page * t.page_stride + code_bytes + idx * (4 * G);
@@ -397,18 +401,28 @@ __device__ __forceinline__ void range_of_words(const F16Stage& a, int64_t code_b
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           const float b = word_bound(w[g]);
-          most[kv] = fmaxf(most[kv], b < INFINITY ? b : 0.f);
+          if (!(b > 0.f && b < INFINITY)) continue;
+          most[kv] = max(most[kv], __float_as_uint(b));
+          most[2 + kv] = max(most[2 + kv], ~__float_as_uint(b));
         }
       }
     }
-    const unsigned with = __match_any_sync(kAll, unit);
+    if (threadIdx.x == 0) block_unit = unit;
+    if (threadIdx.x < 4) of_block[threadIdx.x] = 0;
+    __syncthreads();
+    const bool one = __syncthreads_and(unit == block_unit || unit < 0);
+    const unsigned with = one ? kAll : __match_any_sync(kAll, unit);
+    uint32_t* const range =
+        reinterpret_cast<uint32_t*>(a.kv_range + (int64_t)max(unit, 0) * t.heads + head);
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint32_t m = __reduce_max_sync(with, __float_as_uint(most[kv]));
-      if (m && lane == __ffs(with) - 1)  // lanes of no row have 0
-        atomicMax(reinterpret_cast<uint32_t*>(a.kv_range + (int64_t)unit * t.heads + head) + kv,
-                  m);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t m = __reduce_max_sync(with, most[i]);  // 0 of lanes without a row
+      if (m && lane == __ffs(with) - 1) atomicMax(one ? of_block + i : range + i, m);
     }
+    __syncthreads();
+    if (one && threadIdx.x < 4 && of_block[threadIdx.x])
+      atomicMax(range + threadIdx.x, of_block[threadIdx.x]);
+    __syncthreads();
   }
 }
 
@@ -418,10 +432,14 @@ __device__ __forceinline__ uint32_t float2_to_f16x2(float a, float b) {
   return r;
 }
 
-// 8 codes under a step and an origin -> f16.
-__device__ __forceinline__ uint4 codes_to_f16(uint32_t codes, float step, float origin) {
+// 8 codes under a step and an origin -> f16, or bf16.
+__device__ __forceinline__ uint4 codes_to_16(uint32_t codes, float step, float origin,
+                                             bool bf16) {
   float2 v[4];
   values4(codes, step, origin, v);
+  if (bf16)
+    return make_uint4(float2_to_bf16x2(v[0].x, v[0].y), float2_to_bf16x2(v[1].x, v[1].y),
+                      float2_to_bf16x2(v[2].x, v[2].y), float2_to_bf16x2(v[3].x, v[3].y));
   return make_uint4(float2_to_f16x2(v[0].x, v[0].y), float2_to_f16x2(v[1].x, v[1].y),
                     float2_to_f16x2(v[2].x, v[2].y), float2_to_f16x2(v[3].x, v[3].y));
 }
@@ -448,6 +466,7 @@ __global__ void __launch_bounds__(256)
   const int64_t code_off = hh * codes.per_head + piece * 4;
   const int64_t word_off = code_bytes + hh * words.per_head + piece / LPG * 4;
   float ku = 0.f, vu = 0.f;  // the scales of the lane's head in unit `scaled`
+  bool wide = false;
   int scaled = -1;
   const int64_t row_elems = (int64_t)hk * D, out_off = hh * D + piece * 8;
   int units;
@@ -478,15 +497,16 @@ __global__ void __launch_bounds__(256)
         const int unit = __shfl_sync(kAll, my_unit, (i0 + u) & 31);
         if (!have || i0 + u >= n) continue;
         if (unit != scaled) {
-          const uint2 bound = a.kv_range[(int64_t)unit * hk + hh];
-          ku = f16_up(bound.x);
-          vu = f16_up(bound.y);
+          const Kv4Range r = a.kv_range[(int64_t)unit * hk + hh];
+          wide = f16_too_wide(r);
+          ku = wide ? 1.f : f16_up(r.x);
+          vu = wide ? 1.f : f16_up(r.y);
           scaled = unit;
         }
-        uint4 k = codes_to_f16(kc[u], word_step(kw[u]) * ku, word_origin(kw[u]) * ku);
-        uint4 v = codes_to_f16(vc[u], word_step(vw[u]) * vu, word_origin(vw[u]) * vu);
+        uint4 k = codes_to_16(kc[u], word_step(kw[u]) * ku, word_origin(kw[u]) * ku, wide);
+        uint4 v = codes_to_16(vc[u], word_step(vw[u]) * vu, word_origin(vw[u]) * vu, wide);
         if (!(word_bound(vw[u]) < INFINITY)) {
-          k = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
+          k = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);  // NaN in both
           v = make_uint4(0u, 0u, 0u, 0u);
         }
         const int64_t at = (row0 + i0 + u) * row_elems + out_off;

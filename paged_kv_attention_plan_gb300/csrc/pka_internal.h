@@ -61,7 +61,7 @@ struct MergeArgs {
 // buffer address, a stride, a shape) differs from the cached key.
 struct MapCache {
   static constexpr int kKeyWords = 16;
-  static constexpr int kMaps = 5;
+  static constexpr int kMaps = 6;
   uint64_t key[kKeyWords];
   int valid;
   int aux;  // a launch setting derived with the maps

@@ -89,9 +89,19 @@ cudaError_t launch_read(const KvRows& r, int kv_dtype, int head_dim, float k_sca
 // node's keys), is scaled by the power of two that brings its largest element into
 // [2^14, 2^15), so no magnitude leaves f16's range: an element keeps 11 bits down to
 // 2^-28 of the largest.  A launch reads no other unit's scales with a unit's keys.
+//   Where a kv head of a unit holds groups (of any of its keys, seen or not) whose
+// largest elements lie more than 2^kF16Span apart, its rows are staged in bf16
+// instead, unscaled, and Q and P are bf16 with them: 8 bits, at any magnitude, so that
+// a row does not lose what it sees to a key that is hidden from it or has no weight.
+// 16 leaves every group its 11 bits for elements down to 2^-12 of its largest.
+constexpr uint32_t kF16Span = 16;
+// Bits of the largest of a kv head's groups of K (x) and of V (y), and the complement
+// of the bits of the smallest that is not 0 (z, w); all 0 where there is none.
+typedef uint4 Kv4Range;
 struct F16Scales {
-  const float* q_down;    // [rows, Hq]: what Q's rows are to be multiplied by
-  const uint2* kv_range;  // [units, Hk]: bits of a bound of K's and V's largest magnitude
+  const float* q_down;       // [rows, Hq]: what Q's rows are to be multiplied by
+  const Kv4Range* kv_range;  // [units, Hk]
+  const uint16_t* q;         // bf16 Q
 };
 struct F16Stage {
   KvRows rows;               // units; rows: of the scratch (its capacity in graph mode)
@@ -104,12 +114,12 @@ struct F16Stage {
   float* q_down;
   int64_t q_rows;
   int q_heads;
-  uint2* kv_range;           // [rows.num_units, Hk]
+  Kv4Range* kv_range;        // [rows.num_units, Hk]
 };
 cudaError_t launch_stage_f16(const F16Stage& s, int head_dim, int group, cudaStream_t stream);
-cudaError_t launch_prefill_f16(const AttnArgs& a, const F16Scales& scales, int num_ctas,
-                               int head_dim, int group, int nnz_q, int64_t total_kv,
-                               MapCache* cache, cudaStream_t stream);
+cudaError_t launch_prefill_staged(const AttnArgs& a, const F16Scales& scales, int num_ctas,
+                                  int head_dim, int group, int nnz_q, int64_t total_kv,
+                                  MapCache* cache, cudaStream_t stream);
 // Decode rows over 4-bit pools.
 cudaError_t launch_decode4(const AttnArgs& a, int num_ctas, int head_dim, int group,
                            cudaStream_t stream);
@@ -125,6 +135,11 @@ __device__ __forceinline__ float f16_up(uint32_t bits) {
 }
 __device__ __forceinline__ float f16_down(uint32_t bits) {
   return __uint_as_float((uint32_t)(127 - 14 + f16_exponent(bits)) << 23);
+}
+
+// Whether a kv head's rows are staged in bf16.
+__device__ __forceinline__ bool f16_too_wide(const Kv4Range& r) {
+  return (r.x >> 23) > kF16Span + (~r.z >> 23) || (r.y >> 23) > kF16Span + (~r.w >> 23);
 }
 
 // The step and origin of a group whose least and greatest elements are given,

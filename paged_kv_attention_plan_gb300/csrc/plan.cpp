@@ -689,7 +689,7 @@ Kv4Staging kv4_staging(const pka_params* p, int64_t rows, int64_t units) {
   const size_t heads = (size_t)rows * p->num_qo_heads;
   auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
   return {up(heads * p->head_dim * 2), up(heads * 4),
-          up((size_t)units * p->num_kv_heads * 8)};
+          up((size_t)units * p->num_kv_heads * sizeof(pka::Kv4Range))};
 }
 
 }  // namespace
@@ -1104,7 +1104,7 @@ pka_status pka_run(pka_plan_t plan, const pka_params* p, const void* q, const vo
       cudaError_t e;
       if (int4) {
         const Kv4Staging size = kv4_staging(p, rows, plan->dequant_capacity);
-        char* q16 = reinterpret_cast<char*>(sv) + kv_scratch_bytes(p, plan->scratch_capacity);
+        char* staged = reinterpret_cast<char*>(sv) + kv_scratch_bytes(p, plan->scratch_capacity);
         pka::F16Stage f{};
         f.rows.units = units;
         f.rows.num_units = n_units;
@@ -1120,15 +1120,16 @@ pka_status pka_run(pka_plan_t plan, const pka_params* p, const void* q, const vo
         f.k16 = sk;
         f.v16 = sv;
         f.q = a.q;
-        f.q16 = reinterpret_cast<uint16_t*>(q16);
-        f.q_down = reinterpret_cast<float*>(q16 + size.rows);
+        f.q16 = reinterpret_cast<uint16_t*>(staged);
+        f.q_down = reinterpret_cast<float*>(staged + size.rows);
         f.q_rows = rows;
         f.q_heads = p->num_qo_heads;
-        f.kv_range = reinterpret_cast<uint2*>(q16 + size.rows + size.down);
+        f.kv_range = reinterpret_cast<pka::Kv4Range*>(staged + size.rows + size.down);
         e = pka::launch_stage_f16(f, p->head_dim, pka::kv4_group(p->kv_dtype), st);
         pa.q = f.q16;
         scales.q_down = f.q_down;
         scales.kv_range = f.kv_range;
+        scales.q = a.q;
       } else {
         e = pka::launch_dequant(units, n_units, n_rows, counts, kv_indices, k, v, page_stride,
                                 p->page_size, p->layout, p->kv_ragged, p->num_kv_heads,
@@ -1144,8 +1145,8 @@ pka_status pka_run(pka_plan_t plan, const pka_params* p, const void* q, const vo
     }
     cudaError_t e =
         scales.q_down
-            ? pka::launch_prefill_f16(pa, scales, h.num_prefill_ctas, p->head_dim, g, rows,
-                                      kv_rows, &plan->prefill_maps, st)
+            ? pka::launch_prefill_staged(pa, scales, h.num_prefill_ctas, p->head_dim, g, rows,
+                                         kv_rows, &plan->prefill_maps, st)
             : pka::launch_prefill(pa, h.num_prefill_ctas, p->head_dim, g, rows, kv_rows,
                                   &plan->prefill_maps, st);
     if (e != cudaSuccess) return cuda_fail(e, "prefill launch");

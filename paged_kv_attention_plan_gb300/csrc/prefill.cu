@@ -23,9 +23,13 @@
 // softmax.  P stays in tensor memory (it overwrites the first half of its S
 // tile) and feeds the P V product as the A operand.
 //
-// F16 (4-bit pools): Q, K and V come as f16 rows staged from the cache, scaled
-// by powers of two, and P is f16; the scales are taken back per row (Q's) and per
-// item (K's in the scores, V's in the output).
+// 4-bit pools: K and V come as rows staged from the cache.  Items staged in f16
+// (kStagedF16): Q, K and V are f16, scaled by powers of two, and P is f16; the
+// scales are taken back per row (Q's) and per item (K's in the scores, V's in the
+// output).  A CTA's items staged in bf16 (f16_too_wide), most often none, follow in
+// a pass of their own (kStagedBf16): a type decided item by item in one pass costs
+// the f16 items 5 to 10% (append-prefill 429 or 442 us, 404 without; the other pass
+// as a launch of its own 415).
 #include <cudaTypedefs.h>
 
 #include <cmath>
@@ -58,14 +62,18 @@ struct Maps {
   CUtensorMap kv_v;
   CUtensorMap row_k;  // paged: the pool as 2-D rows of D elements, box {64, 1} (row gathers)
   CUtensorMap row_v;
+  CUtensorMap q_bf16;  // staged items: Q as it came, like q
 };
+
+// What the items of a pass read.
+enum { kBf16, kStagedF16, kStagedBf16 };
 
 struct PrefillParams {
   AttnArgs a;
   int group;
   int gather;              // 1: rows outside whole-page boxes come by TMA gather4
   int64_t rows_per_page;   // page_stride / D: rows of the 2-D view per page
-  F16Scales f16;           // F16 only
+  F16Scales f16;           // staged items only
 };
 
 struct Bars {
@@ -300,64 +308,27 @@ __device__ __forceinline__ void st_global_v8(void* p, uint32_t a0, uint32_t a1, 
                : "memory");
 }
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads, 1)
-    prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams pp) {
-  constexpr int NB = D / 64;
-  const AttnArgs& a = pp.a;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  constexpr int KS = Ring<D>::K, VS = Ring<D>::V;
-  uint8_t* sQ = smem;                // 2 tiles x NB blocks
-  uint8_t* sK = sQ + 2 * NB * BLK;   // KS x NB blocks
-  uint8_t* sV = sK + KS * NB * BLK;  // VS x NB blocks
-  __shared__ Bars bars;
-  __shared__ uint32_t tmem_base_sh;
-  __shared__ volatile int abort_flag;
+// The magnitudes of the staged rows that an item reads, and whether pass KIND leaves
+// the item out.
+__device__ __forceinline__ Kv4Range item_range(const PrefillParams& pp, const PkaWorkItem& w) {
+  return pp.f16.kv_range[(int64_t)w.join * pp.a.num_kv_heads + w.kv_head0];
+}
+template <int KIND>
+__device__ __forceinline__ bool left_out(const PrefillParams& pp, const PkaWorkItem& w) {
+  return KIND != kBf16 && f16_too_wide(item_range(pp, w)) != (KIND == kStagedBf16);
+}
 
+// One pass over the CTA's items, all warps in their roles.
+template <int D, int KIND>
+__device__ __forceinline__ void attend(const Maps& maps, const PrefillParams& pp, Bars& bars,
+                                       volatile int& abort_flag, uint8_t* sQ, uint8_t* sK,
+                                       uint8_t* sV, uint32_t tmem, int i0, int i1) {
+  constexpr bool F16 = KIND == kStagedF16;
+  constexpr int NB = D / 64, KS = Ring<D>::K, VS = Ring<D>::V;
+  const AttnArgs& a = pp.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int i0 = a.cta_ptr[blockIdx.x], i1 = a.cta_ptr[blockIdx.x + 1];
-  if (i0 >= i1) return;  // an empty CTA of a fixed (graph mode) grid: no TMEM, no barriers
   const int G = pp.group;
   const int TQ = BM / G;  // query tokens of one 128-row tile
-
-  // Zero the K/V stages once: rows of a partial tile that no load writes must
-  // hold finite values (P is 0 there, and 0 * NaN would poison O).
-  for (int x = threadIdx.x; x < (KS + VS) * NB * (int)BLK / 16; x += kThreads)
-    reinterpret_cast<uint4*>(sK)[x] = make_uint4(0, 0, 0, 0);
-  tc::fence_proxy_async_smem();
-  if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&bars.q_full), 1);
-    mbar_init(smem_u32(&bars.q_empty), 1);
-    for (int s = 0; s < KS; ++s) {
-      mbar_init(smem_u32(&bars.k_full[s]), 33);  // TMA expect_tx + 32 producer lanes
-      mbar_init(smem_u32(&bars.k_empty[s]), 1);
-    }
-    for (int s = 0; s < VS; ++s) {
-      mbar_init(smem_u32(&bars.v_full[s]), 33);
-      mbar_init(smem_u32(&bars.v_empty[s]), 1);
-    }
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(smem_u32(&bars.s_full[x]), 1);
-      mbar_init(smem_u32(&bars.p_full[x]), BM);
-      mbar_init(smem_u32(&bars.o_done[x]), 1);
-      mbar_init(smem_u32(&bars.o_free[x]), BM);
-    }
-    abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 9) {
-    tc::tmem_alloc(smem_u32(&tmem_base_sh), 512);
-    tc::tmem_relinquish();
-  }
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = tmem_base_sh;
-  // TMEM columns: S of tile x at [128x, 128x + 128) (P, bf16, reuses its first
-  // 64 columns), O of tile x at [256 + 128x, 256 + 128x + D).
-
   if (warp == 8 || warp == 10) {
     // ------------------------------------------------------------ producers
     // warp 8: Q tiles and the K ring; warp 10: the V ring.
@@ -368,15 +339,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* ring = kq ? sK : sV;
     const CUtensorMap* map = kq ? &maps.kv_k : &maps.kv_v;
     const uint16_t* pool = kq ? a.k : a.v;
+    const CUtensorMap* q_map = KIND == kStagedBf16 ? &maps.q_bf16 : &maps.q;
     if (lane == 0) {
-      if (kq) tc::prefetch_tmap(&maps.q);
+      if (kq) tc::prefetch_tmap(q_map);
       tc::prefetch_tmap(map);
     }
     uint32_t it = 0, q_uses = 0;
     for (int ii = i0; ii < i1 && !warp_any(&abort_flag); ++ii) {
       const PkaWorkItem w = a.items[ii];
       const int n = num_tiles(w);
-      if (n == 0) continue;
+      if (n == 0 || left_out<KIND>(pp, w)) continue;
       if (kq) {
         const bool two = w.q_count > TQ;
         if (q_uses > 0 && !mbar_wait_warp(smem_u32(&bars.q_empty), (q_uses - 1) & 1)) {
@@ -388,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < (two ? 2 : 1); ++x)
 #pragma unroll
             for (int c = 0; c < NB; ++c)
-              tc::tma_load_3d(smem_u32(sQ + (x * NB + c) * BLK), &maps.q, c * 64, w.kv_head0 * G,
+              tc::tma_load_3d(smem_u32(sQ + (x * NB + c) * BLK), q_map, c * 64, w.kv_head0 * G,
                               w.q_row0 + x * TQ, smem_u32(&bars.q_full));
         }
         ++q_uses;
@@ -469,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int ii = i0; ii < i1 && ok && !warp_any(&abort_flag); ++ii) {
         const PkaWorkItem w = a.items[ii];
         const int n = num_tiles(w);
-        if (n == 0) continue;
+        if (n == 0 || left_out<KIND>(pp, w)) continue;
         const int nx = w.q_count > TQ ? 2 : 1;
         ok = mbar_wait_warp(smem_u32(&bars.q_full), q_uses & 1);
         ++q_uses;
@@ -539,16 +511,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int ii = i0; ii < i1 && !warp_any(&abort_flag); ++ii) {
       const PkaWorkItem w = a.items[ii];
       if (x == 1 && w.q_count <= TQ) continue;  // no second tile in this item
+      if (left_out<KIND>(pp, w)) continue;
       const int n = num_tiles(w);
       const int i = w.q_local0 + i_tok;              // query index inside the request
       const int klim = w.kv_len - w.qo_len + i;      // causal: keys <= klim are visible
       const int klim_first = w.kv_len - w.qo_len + w.q_local0 + x * TQ;
       const int64_t mrow = ((int64_t)w.mask_hi << 32 | (uint32_t)w.mask_lo) + (int64_t)i * w.kv_len;
       const int mm = (w.flags & PKA_ITEM_ALL_VISIBLE) ? (int)PKA_MASK_NONE : a.mask_mode;
-      uint2 bound = make_uint2(0u, 0u);  // F16: of the K and V that this item reads
+      float v_scale = a.v_scale;  // V's scale (1 for bf16 K/V)
       if constexpr (F16) {
-        bound = pp.f16.kv_range[(int64_t)w.join * a.num_kv_heads + w.kv_head0];
-        sc = a.scale_log2 * f16_down(bound.x);
+        const Kv4Range range = item_range(pp, w);
+        v_scale = f16_down(range.y);
+        sc = a.scale_log2 * f16_down(range.x);
         if (i_tok < w.q_count)
           sc *= pp.f16.q_down[(int64_t)(w.q_row0 + i_tok) * a.num_qo_heads + w.kv_head0 * G + g];
         sc = fmaxf(sc, 1.17549435e-38f);  // a masked -inf times 0 would be NaN
@@ -660,9 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---------------- epilogue
       const bool store = i_tok < w.q_count;
-      const bool any = F16 ? l != 0.f : l > 0.f;  // F16: NaN is not "no key"
-      // V's scale (1 for bf16 K/V)
-      const float v_scale = F16 ? f16_down(bound.y) : a.v_scale;
+      const bool any = KIND == kBf16 ? l > 0.f : l != 0.f;  // staged: NaN is not "no key"
       const float inv = any ? v_scale / l : 0.f;
       const int head = w.kv_head0 * G + g;
       uint16_t* odst = a.o + ((int64_t)(w.q_row0 + i_tok) * a.num_qo_heads + head) * D;
@@ -753,6 +725,80 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+}
+
+template <int D, bool STAGED>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_kernel(const __grid_constant__ Maps maps, const PrefillParams pp) {
+  constexpr int NB = D / 64;
+  const AttnArgs& a = pp.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  constexpr int KS = Ring<D>::K, VS = Ring<D>::V;
+  uint8_t* sQ = smem;                // 2 tiles x NB blocks
+  uint8_t* sK = sQ + 2 * NB * BLK;   // KS x NB blocks
+  uint8_t* sV = sK + KS * NB * BLK;  // VS x NB blocks
+  constexpr int PASSES = STAGED ? 2 : 1;
+  __shared__ Bars bars[PASSES];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ volatile int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i0 = a.cta_ptr[blockIdx.x], i1 = a.cta_ptr[blockIdx.x + 1];
+  if (i0 >= i1) return;  // an empty CTA of a fixed (graph mode) grid: no TMEM, no barriers
+
+  // Zero the K/V stages once: rows of a partial tile that no load writes must
+  // hold finite values (P is 0 there, and 0 * NaN would poison O).
+  for (int x = threadIdx.x; x < (KS + VS) * NB * (int)BLK / 16; x += kThreads)
+    reinterpret_cast<uint4*>(sK)[x] = make_uint4(0, 0, 0, 0);
+  tc::fence_proxy_async_smem();
+  if (threadIdx.x == 0) {
+    for (Bars& b : bars) {
+      mbar_init(smem_u32(&b.q_full), 1);
+      mbar_init(smem_u32(&b.q_empty), 1);
+      for (int s = 0; s < KS; ++s) {
+        mbar_init(smem_u32(&b.k_full[s]), 33);  // TMA expect_tx + 32 producer lanes
+        mbar_init(smem_u32(&b.k_empty[s]), 1);
+      }
+      for (int s = 0; s < VS; ++s) {
+        mbar_init(smem_u32(&b.v_full[s]), 33);
+        mbar_init(smem_u32(&b.v_empty[s]), 1);
+      }
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(smem_u32(&b.s_full[x]), 1);
+        mbar_init(smem_u32(&b.p_full[x]), BM);
+        mbar_init(smem_u32(&b.o_done[x]), 1);
+        mbar_init(smem_u32(&b.o_free[x]), BM);
+      }
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tc::tmem_alloc(smem_u32(&tmem_base_sh), 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_base_sh;
+  // TMEM columns: S of tile x at [128x, 128x + 128) (P, bf16, reuses its first
+  // 64 columns), O of tile x at [256 + 128x, 256 + 128x + D).
+
+  if constexpr (STAGED) {
+    attend<D, kStagedF16>(maps, pp, bars[0], abort_flag, sQ, sK, sV, tmem, i0, i1);
+    bool any = false;
+    for (int ii = i0 + lane; ii < i1; ii += 32) any |= !left_out<kStagedBf16>(pp, a.items[ii]);
+    if (__any_sync(0xffffffffu, any)) {  // the same in all warps
+      tc::fence_before_sync();
+      __syncthreads();
+      tc::fence_after_sync();
+      attend<D, kStagedBf16>(maps, pp, bars[1], abort_flag, sQ, sK, sV, tmem, i0, i1);
+    }
+  } else {
+    attend<D, kBf16>(maps, pp, bars[0], abort_flag, sQ, sK, sV, tmem, i0, i1);
+  }
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 9) {
@@ -799,7 +845,8 @@ bool encode(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
 // Encode the launch's tensor maps; returns whether the row maps for gather4
 // were made (0 / 1), or -1 on failure.
 template <int D>
-int encode_maps(Maps& maps, const AttnArgs& a, int G, int nnz_q, int64_t total_kv) {
+int encode_maps(Maps& maps, const AttnArgs& a, const uint16_t* q_bf16, int G, int nnz_q,
+                int64_t total_kv) {
   int pp_gather = 0;
   const uint64_t Hq = a.num_qo_heads, Hk = a.num_kv_heads;
   std::memset(&maps, 0, sizeof(maps));
@@ -808,6 +855,7 @@ int encode_maps(Maps& maps, const AttnArgs& a, int G, int nnz_q, int64_t total_k
     const uint64_t str[2] = {(uint64_t)D * 2, Hq * D * 2};
     const uint32_t box[3] = {64, (uint32_t)G, (uint32_t)(BM / G)};
     if (!encode(&maps.q, a.q, 3, dims, str, box)) return -1;
+    if (q_bf16 && !encode(&maps.q_bf16, q_bf16, 3, dims, str, box)) return -1;
   }
   if (a.kv_ragged) {
     const uint64_t dims[3] = {(uint64_t)D, Hk, (uint64_t)(total_kv > 0 ? total_kv : 1)};
@@ -849,7 +897,7 @@ int encode_maps(Maps& maps, const AttnArgs& a, int G, int nnz_q, int64_t total_k
   return pp_gather;
 }
 
-template <int D, bool F16>
+template <int D, bool STAGED>
 cudaError_t launch_t(PrefillParams pp, int num_ctas, int nnz_q, int64_t total_kv,
                      MapCache* cache, cudaStream_t stream) {
   const AttnArgs& a = pp.a;
@@ -862,13 +910,13 @@ cudaError_t launch_t(PrefillParams pp, int num_ctas, int nnz_q, int64_t total_kv
       reinterpret_cast<uintptr_t>(a.v), (uint64_t)a.page_stride, (uint64_t)a.page_size,
       (uint64_t)a.layout, (uint64_t)a.kv_ragged, (uint64_t)a.num_qo_heads,
       (uint64_t)a.num_kv_heads, (uint64_t)pp.group, (uint64_t)nnz_q, (uint64_t)total_kv,
-      (uint64_t)D, 0, 0, 0};
+      (uint64_t)D, reinterpret_cast<uintptr_t>(pp.f16.q), 0, 0};
   int pp_gather;
   if (cache && cache->hit(key)) {
     std::memcpy(&maps, cache->maps, sizeof(maps));
     pp_gather = cache->aux;
   } else {
-    pp_gather = encode_maps<D>(maps, a, pp.group, nnz_q, total_kv);
+    pp_gather = encode_maps<D>(maps, a, pp.f16.q, pp.group, nnz_q, total_kv);
     if (pp_gather < 0) return cudaErrorInvalidValue;
     if (cache) cache->store(key, &maps, sizeof(maps), pp_gather);
   }
@@ -876,11 +924,11 @@ cudaError_t launch_t(PrefillParams pp, int num_ctas, int nnz_q, int64_t total_kv
   // At least 120 KiB, so that one CTA (and its 512 TMEM columns) owns each SM.
   size_t smem = 1024 + (size_t)(2 + Ring<D>::K + Ring<D>::V) * NB * BLK;
   if (smem < 120 * 1024) smem = 120 * 1024;
-  cudaError_t e = ensure_dynamic_smem<prefill_kernel<D, F16>>((int)smem);
+  cudaError_t e = ensure_dynamic_smem<prefill_kernel<D, STAGED>>((int)smem);
   if (e != cudaSuccess) return e;
   pp.gather = pp_gather;
   pp.rows_per_page = pp_gather ? a.page_stride / D : 0;
-  prefill_kernel<D, F16><<<num_ctas, kThreads, smem, stream>>>(maps, pp);
+  prefill_kernel<D, STAGED><<<num_ctas, kThreads, smem, stream>>>(maps, pp);
   return cudaGetLastError();
 }
 
@@ -896,9 +944,9 @@ cudaError_t launch_prefill(const AttnArgs& a0, int num_ctas, int head_dim, int g
   return launch_t<64, false>(pp, num_ctas, nnz_q, total_kv, cache, stream);
 }
 
-cudaError_t launch_prefill_f16(const AttnArgs& a0, const F16Scales& scales, int num_ctas,
-                               int head_dim, int group, int nnz_q, int64_t total_kv,
-                               MapCache* cache, cudaStream_t stream) {
+cudaError_t launch_prefill_staged(const AttnArgs& a0, const F16Scales& scales, int num_ctas,
+                                  int head_dim, int group, int nnz_q, int64_t total_kv,
+                                  MapCache* cache, cudaStream_t stream) {
   PrefillParams pp{};
   pp.a = a0;
   pp.a.err = device_error_word();

@@ -28,7 +28,9 @@ A score's 128 roundings are independent of one another and of the sign, so
 their sum has a standard deviation of at most 2^-11 / sqrt(3) times the root of
 the sum of squares of its products (A2), and six of these are 3.5 2^-11 A2,
 which takes the place of the first term above: s = 3.5 2^-11 A2 + 2^-19 A,
-r = 2 ln2 s + 2^-20.  V's own rounding adds 2^-11 V to P's.
+r = 2 ln2 s + 2^-20.  V's own rounding adds 2^-11 V to P's.  Where a request's
+groups of a kv head are more than 2^16 apart, its rows, P and V round to bf16,
+half a step 2^-8: 2^-8 in the places of 2^-11.
 """
 import numpy as np
 import pytest
@@ -101,13 +103,13 @@ class Batch:
                              kv_lens=self.kv_lens, hq=self.hq, hk=self.hk, **kw)
 
 
-def _assert_decode(o, lse, want, rows=None, staged=False):
+def _assert_decode(o, lse, want, rows=None, staged=False, half=2.0 ** -11):
     ow, lw, a_k, a_v, a_2 = want if rows is None else tuple(x[rows] for x in want)
     if rows is not None:
         o, lse = o[rows], lse[rows]
-    score = 2.0 ** -19 * a_k + (3.5 * 2.0 ** -11 * a_2 if staged else 0)
+    score = 2.0 ** -19 * a_k + (3.5 * half * a_2 if staged else 0)
     r = 2 * np.log(2) * score[..., None] + 2.0 ** -20
-    tol = (2 * r + (2 if staged else 1) * 2.0 ** -11 + 2.0 ** -13) * a_v + 2.0 ** -8 * np.abs(ow)
+    tol = (2 * r + (2 if staged else 1) * half + 2.0 ** -13) * a_v + 2.0 ** -8 * np.abs(ow)
     assert np.all(np.isfinite(o)) and np.all(np.abs(o - ow) <= tol)
     fin = np.isfinite(lw)
     assert np.array_equal(fin, np.isfinite(lse)) and np.all(lse[~fin] == -np.inf)
@@ -117,6 +119,10 @@ def _assert_decode(o, lse, want, rows=None, staged=False):
 
 def _assert_staged(o, lse, want, rows=None):
     _assert_decode(o, lse, want, rows, staged=True)
+
+
+def _assert_wide(o, lse, want, rows=None):
+    _assert_decode(o, lse, want, rows, staged=True, half=2.0 ** -8)
 
 
 # ---------------------------------------------------------------------------
@@ -761,6 +767,76 @@ def test_staged_nan_group_shows(which):
     _assert_staged(o[10:20, 2:], lse[10:20, 2:], tuple(x[10:20, 2:] for x in other))
 
 
+@pytest.mark.parametrize("apart", [2.0 ** 13, 2.0 ** 18, 2.0 ** 24, 2.0 ** 40, 2.0 ** 100])
+@pytest.mark.parametrize("which", ["k", "v", "both"])
+def test_staged_keys_behind_a_mask_of_any_size(apart, which):
+    """Finite keys that a mask hides, the request's last ones (behind most rows' causal
+    ends, too) and one in the middle, far larger than those that are seen."""
+    qo, kv = [6, 1, 9], [140, 60, 33]
+    b = Batch(29, kv, qo_lens=qo, page=4, hq=8, hk=2, d=64, group=32)
+    rng = np.random.default_rng(9)
+    masks = [rng.random((a, c)) < 0.7 for a, c in zip(qo, kv)]
+    masks[2][4] = False  # a row that sees nothing
+    hide = [(0, 7), (0, 138), (0, 139), (1, 30), (2, 0), (2, 32)]
+    for r, j in hide:
+        masks[r][:, j] = False
+        for pool in {"k": (b.k,), "v": (b.v,), "both": (b.k, b.v)}[which]:
+            pool.write(int(b.kv_indices[b.kv_indptr[r] + j // 4]), j % 4,
+                       (apart * rng.standard_normal((2, 64))).astype(np.float32))
+    flat = np.concatenate([m.reshape(-1) for m in masks])
+    packed = torch.from_numpy(np.packbits(flat, bitorder="little")).cuda()
+    o, lse, _ = b.run(mask=packed, mask_mode="custom")
+    want = b.want(mask="custom", mask_bool=flat)
+    check = _assert_staged if apart < 2.0 ** 16 else _assert_wide
+    check(o, lse, want, rows=[0, 1, 2, 3, 4, 5] + list(range(7, 16)))
+    _assert_decode(o, lse, want, rows=[6])
+    assert not o[11].any() and np.all(lse[11] == -np.inf)
+
+
+def test_staged_keys_behind_the_causal_end_of_any_size():
+    """Chunks over a prefix, the last key of each request 2^60 of the others: the rows
+    before the last do not see it."""
+    qo, kv = [130, 5, 300], [300, 77, 300]
+    b = Batch(30, kv, qo_lens=qo, page=16, hq=8, hk=2, d=128, group=64)
+    rng = np.random.default_rng(10)
+    for r, n in enumerate(kv):
+        for pool in (b.k, b.v):
+            pool.write(int(b.kv_indices[b.kv_indptr[r] + (n - 1) // 16]), (n - 1) % 16,
+                       (2.0 ** 60 * rng.standard_normal((2, 128))).astype(np.float32))
+    o, lse, _ = b.run()
+    last = set(int(x) - 1 for x in b.qo_indptr[1:])
+    _assert_wide(o, lse, b.want(), rows=[i for i in range(435) if i not in last])
+
+
+@pytest.mark.parametrize("apart", [2.0 ** -13, 2.0 ** -19, 2.0 ** -30, 2.0 ** -60])
+def test_staged_groups_of_unlike_magnitudes(apart):
+    """V's groups of one head, and the keys of one request, far apart in size and all seen:
+    each output within the bits of what it sums."""
+    b = Batch(31, [150, 90], qo_lens=[20, 4], page=4, hq=8, hk=2, d=128, group=32)
+    rng = np.random.default_rng(11)
+    sizes = np.repeat([1.0, apart, apart ** 0.5, apart], 32)
+    rows = [rng.standard_normal((n, 2, 128)) * sizes for n in (150, 90)]
+    rows[1][::3, :, 32:64] *= 0  # groups of zeros are of no size
+    kv4.fill(b.v, b.kv_indptr, b.kv_indices, b.kv_lens, rows)
+    o, lse, _ = b.run()
+    (_assert_staged if apart > 2.0 ** -16 else _assert_wide)(o, lse, b.want())
+
+
+def test_staged_keys_of_all_sizes():
+    """V's keys from none over 2^-100 to 2^12 within a request, as decode rows take them."""
+    for order in (1, -1):
+        b = Batch(10, [260], qo_lens=[200], page=4, hq=4, hk=2, d=64, group=32)
+        rng = np.random.default_rng(3)
+        size = 2.0 ** np.linspace(-100, 12, 260)[::order]
+        for j in range(260):
+            row = rng.standard_normal((2, 64)) * size[j]
+            if j % 7 == 0:
+                row = np.full((2, 64), size[j])
+            b.v.write(int(b.kv_indices[j // 4]), j % 4, row.astype(np.float32))
+        o, lse, _ = b.run()
+        _assert_wide(o, lse, b.want())
+
+
 def _set_word(pool, page, slot, head, group, step, origin):
     """A word of the pool from the bits of its step and origin."""
     n = pool.D // pool.g
@@ -906,6 +982,42 @@ def test_graph_replayed_over_plans(rows):
         more = [i for i in range(len(b.q)) if i not in one]
         _assert_decode(o, lse, b.want(), rows=one)
         _assert_staged(o, lse, b.want(), rows=more)
+
+
+def test_graph_replayed_over_magnitudes():
+    """A captured run takes what the pools hold when it is replayed: groups alike (f16 rows),
+    then one request's far apart (its rows in bf16, the others' in f16), then alike again."""
+    kv, qo = [150, 40, 77], [9, 3, 1]
+    b = Batch(33, kv, qo_lens=qo, page=8, hq=8, hk=2, d=64, group=32)
+    attn, stream = pka.BatchAttention(), torch.cuda.Stream()
+    cap = dict(graph_max_batch=4, graph_max_qo_rows=20, graph_max_kv_tokens=400)
+    q, k, v, idx = bf16(b.q), _dev(b.k), _dev(b.v), i32(b.kv_indices)
+    q = torch.cat([q, torch.zeros(7, 8, 64, dtype=torch.bfloat16, device="cuda")])
+    o, lse = torch.empty_like(q), torch.empty(20, 8, device="cuda")
+    torch.cuda.synchronize()
+    attn.plan(b.qo_indptr, b.kv_indptr, b.last, stream=stream, mask_mode="causal",
+              **b.params(**cap))
+    attn.run(q, k, v, idx, out=o, lse=lse, stream=stream)
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        attn.run(q, k, v, idx, out=o, lse=lse, stream=stream)
+    rng = np.random.default_rng(12)
+    for apart in (1.0, 2.0 ** 40, 1.0):
+        sizes = np.repeat([1.0, apart], 32)
+        rows = [rng.standard_normal((n, 2, 64)) * (sizes if r == 0 else 1.0)
+                for r, n in enumerate(kv)]
+        kv4.fill(b.v, b.kv_indptr, b.kv_indices, b.kv_lens, rows)
+        v.copy_(_dev(b.v))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            graph.replay()
+        stream.synchronize()
+        want, got = b.want(), (f64(o[:13]), f64(lse[:13]))
+        (_assert_wide if apart > 1 else _assert_staged)(*got, want, rows=list(range(9)))
+        _assert_staged(*got, want, rows=[9, 10, 11])
+        _assert_decode(*got, want, rows=[12])
+    assert pka.pka_get_device_error() == 0
 
 
 def test_graph_of_decode_rows_alone():
