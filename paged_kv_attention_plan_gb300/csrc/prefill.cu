@@ -55,6 +55,12 @@ constexpr uint32_t BLK = 16384;       // one [128 rows x 128 B] swizzled block
 // softmax warpgroups 0-1, Q+K producer warp 8, MMA warp 9, V producer warp 10
 constexpr int kThreads = 352;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O only when the max grows by > 2^8
+// P in f16: the reference of the exponents lies this far below the running maximum, and
+// O is rescaled when that grows by more than 2^4, so P stays under 2^15 and has its 11
+// bits down to 2^-25 of the largest probability, where many keys of a long row may lie
+// (below, an error of 2^-36 of it).
+constexpr float kF16Headroom = 11.0f;
+constexpr float kF16RescaleThreshold = 4.0f;
 
 struct Maps {
   CUtensorMap q;     // 3-D {D, Hq, nnz_q}, box {64, g, 128/g}
@@ -579,11 +585,12 @@ __device__ __forceinline__ void attend(const Maps& maps, const PrefillParams& pp
           for (int j = 0; j < 32; j += 2)
             mxa[(j >> 1) & 3] =
                 max3(mxa[(j >> 1) & 3], __uint_as_float(r[c][j]), __uint_as_float(r[c][j + 1]));
-        const float mx = fmaxf(fmaxf(mxa[0], mxa[1]), fmaxf(mxa[2], mxa[3])) * sc;
+        float mx = fmaxf(fmaxf(mxa[0], mxa[1]), fmaxf(mxa[2], mxa[3])) * sc;
+        if constexpr (F16) mx -= kF16Headroom;
         float alpha = 1.f;
         if (m == -INFINITY) {
           m = mx;
-        } else if (mx > m + kRescaleThreshold) {
+        } else if (mx > m + (F16 ? kF16RescaleThreshold : kRescaleThreshold)) {
           alpha = exp2f(m - mx);
           m = mx;
         }

@@ -30,7 +30,9 @@ the sum of squares of its products (A2), and six of these are 3.5 2^-11 A2,
 which takes the place of the first term above: s = 3.5 2^-11 A2 + 2^-19 A,
 r = 2 ln2 s + 2^-20.  V's own rounding adds 2^-11 V to P's.  Where a request's
 groups of a kv head are more than 2^16 apart, its rows, P and V round to bf16,
-half a step 2^-8: 2^-8 in the places of 2^-11.
+half a step 2^-8: 2^-8 in the places of 2^-11.  P in f16 has 11 bits down to 2^-25 of
+the largest probability; below, half its last step is 2^-25 where the largest is at
+least 2^11: an output sums errors of 2^-36 of each |v| more.
 """
 import numpy as np
 import pytest
@@ -884,6 +886,42 @@ def test_infinite_words_behind_a_mask():
     o, lse, _ = b.run(mask=packed, mask_mode="custom")
     _assert_staged(o, lse, want, rows=list(range(5)))
     _assert_decode(o, lse, want, rows=[5])
+
+
+@pytest.mark.parametrize("below", [14.0, 20.0, 24.6, 25.2, 27.0, 31.0])
+def test_staged_long_tails(below):
+    """131,072 keys of one weight, 2^-14 to 2^-31 of the first key's, whose V is 0: the output
+    is all theirs, and none of it may be lost in P's rounding."""
+    n, hq, hk, d = 131073, 4, 1, 64
+    params = pka.make_params(hq, hk, d, 64, kv_dtype="int4_g32")
+    size, pages = pka.pka_kv_page_bytes(params), -(-n // 64)
+    pools = [torch.zeros(pages, size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    g = torch.Generator(device="cuda").manual_seed(7)
+    sign = torch.where(torch.arange(d, device="cuda") % 2 == 0, 1.0, -1.0)
+    k = torch.zeros(n, hk, d, device="cuda")
+    k[0] = sign * (below / (d ** 0.5 * np.log2(np.e)))  # q . k / sqrt(d) in log2 units
+    v = torch.rand(n, hk, d, generator=g, device="cuda") + 0.5
+    v[0] = 0
+    ptr, idx = np.array([0, pages], np.int32), np.arange(pages, dtype=np.int32)
+    last = np.array([n - (pages - 1) * 64], np.int32)
+    pka.pka_append_paged_kv_cache(params, k.to(torch.bfloat16), v.to(torch.bfloat16), i32([0, n]),
+                                  i32(ptr), i32(idx), i32(last), *pools, size)
+    q = sign.expand(2, hq, d).contiguous().to(torch.bfloat16)
+    attn = pka.BatchAttention()
+    attn.plan(np.array([0, 2], np.int32), ptr, last, num_qo_heads=hq, num_kv_heads=hk, head_dim=d,
+              page_size=64, mask_mode="none", kv_dtype="int4_g32")
+    o, lse = attn.run(q, *pools, i32(idx))
+    torch.cuda.synchronize()
+    kp, vp = (kv4.Pool(p.cpu().numpy(), 64, hk, d, 32, "NHD") for p in pools)
+    want = kv4.attention(bits_of(q), kp, vp, qo_indptr=[0, 2], kv_indptr=ptr, kv_indices=idx,
+                         kv_lens=[n], hq=hq, hk=hk, mask="none")
+    # the scores: 64 products of one size, exact in K's bits but for its rounding to f16, which
+    # moves all of them as one: 2^-11 of the score
+    shift = 2.0 ** -11 * below
+    assert np.abs(f64(lse) - want[1]).max() <= shift + 2.0 ** -17
+    tail = 2.0 ** -36 * 1.5 * (n - 1)
+    tol = (2 * np.log(2) * 2 * shift + 2 * 2.0 ** -11 + 2.0 ** -13 + 2.0 ** -8) * want[0] + tail
+    assert np.all(np.abs(f64(o) - want[0]) <= tol)
 
 
 def test_decode_on_tensor_cores():
