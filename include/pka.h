@@ -103,7 +103,8 @@ typedef enum pka_mask_mode {
  * differences and quotients in float32); a group whose hi - lo is not finite
  * (NaN, infinities) is stored as NaN, and one whose step would be no normal
  * bf16 as its origin alone.  Decode rows read the codes and words without
- * rounding them; rows with qo_len >= 2 (and decode_on_tensor_cores) read an f16
+ * rounding them (a key's weight times V's step is rounded to 11 bits, on a scale
+ * of each group's own); rows with qo_len >= 2 (and decode_on_tensor_cores) read an f16
  * scratch, each value rounded once more, to 11 bits (Q, too, is brought to f16,
  * where its bf16 values are exact; Q is scaled by a power of two for each head of
  * a row, K and V for each kv head of a request, whose values below 2^-28 of its

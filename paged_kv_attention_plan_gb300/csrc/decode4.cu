@@ -16,15 +16,17 @@
 // An OR with 1024's or 128's exponent would leave an offset of 1024 or 128 in
 // every product, whose cancellation costs the statistics 2^-17 or so.
 //   Q is scaled to f16 by a power of two per head that puts its largest element
-// in [2^14, 2^15): bf16 values down to 2^-28 of it stay exact.
+// in [2^14, 2^15): bf16 values down to 2^-27 of it stay exact.
 //   The second 8 keys of each 16 take V's codes from above, as 15 - c under -P and
 // an origin of z + 15 s: an output's sum then runs up by as much as down.  With c
 // alone all its terms are positive, it grows with the keys, and so does what each
 // MMA cuts off of it: 2% of an output that is the mean of 160,000 values.
-//   P goes to f16 with V's step in it, 11 bits against the 8 of bf16: p * s,
-// relative to the running maximum of log2(p) + log2(s) less 6, so it lies under
-// 2^15 (a maximum may be passed by 2^8 before the state is rescaled) and what
-// falls below f16's 2^-25 is under 2^-31 of the largest.
+//   P goes to f16 with V's step in it, 11 bits against the 8 of bf16: p * s times a
+// power of two of its own for each head and group, which puts the largest p * s seen
+// at 2^11 (a larger one may pass it by 2^4 before the state is rescaled).  So the 11
+// bits reach down to 2^-25 of the largest p * s of the group, however the groups of a
+// head and the keys differ in size (one power of two for all groups of a head took 6%
+// of outputs whose group's steps were 2^-24 of another's).
 //
 // Warps: each kv head of the CTA is served by several warps that take the item's
 // 32-key tiles in turn, so 16 warps work whatever the head count; their states
@@ -55,11 +57,16 @@ constexpr int kMaxWarps = 16;
 // Tiles a warp has on their way.  More do not help: 37 requests over a token pool of
 // heads of 64 take 28.1 us with two, 28.4 with three, 28.8 with four.
 constexpr int kStages = 2;
-constexpr float kRescale = 8.0f;  // log2 units, as in decode.cu
-constexpr float kHeadroom = 6.0f;
-// Added to a key's largest step: below it p * s no longer counts against the
-// other keys, and p itself stays far from overflow.
-constexpr float kLeastStep = 0x1p-60f;
+// p is 2^-kBelow at the running maximum: its products with values up to 2^115 and
+// their sums over a row stay finite.  The state is rescaled when the maximum grows by
+// more than 2^kRescale (as in decode.cu).
+constexpr float kBelow = 12.0f;
+constexpr float kRescale = 8.0f;
+// The largest P after a rescaling, and the largest that goes on without one (f16 bits).
+constexpr int kHeadroom = 11;
+constexpr uint32_t kMostP = 0x7800u;  // 2^15
+// Steps below it count as it for their group's power of two, which stays finite.
+constexpr float kLeastStep = 0x1p-100f;
 
 template <int D, int GR>
 struct Shape {
@@ -91,6 +98,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// The larger of each half; NaN only of two.
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// 2^n for a whole n up to 127; 0 below -126.
+__device__ __forceinline__ float pow2(float n) {
+  return n < -126.f ? 0.f : __uint_as_float((uint32_t)((int)n + 127) << 23);
+}
+// 1 / w for a power of two w in [2^-126, 2^126].
+__device__ __forceinline__ float pow2_inverse(float w) {
+  return __uint_as_float(0x7f000000u - __float_as_uint(w));
+}
+// Keeps 2^-n, and 2^24 2^n, normal numbers.
+__device__ __forceinline__ float clamp_log(float n) { return fminf(fmaxf(n, -126.f), 100.f); }
+__device__ __forceinline__ float pow2_log(float w) {
+  return (float)((int)(__float_as_uint(w) >> 23) - 127);
 }
 
 // d += a . b for a 16x16 (row) and 16x8 (col) f16 fragment pair.
@@ -183,7 +211,18 @@ __device__ __forceinline__ int chunk_swap(int key) {
   return D == 128 ? (key & 2) | (key >> 2 & 1) : key >> 2 & 1;
 }
 
-// The sum over the lanes that hold one head's keys.
+// The largest and the sum over the lanes that hold one head's keys.
+template <bool HALF, int N>
+__device__ __forceinline__ void max_keys(float2 (&x)[N]) {
+#pragma unroll
+  for (int off = HALF ? 2 : 4; off < 32; off <<= 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      x[i].x = fmaxf(x[i].x, __shfl_xor_sync(0xffffffffu, x[i].x, off));
+      x[i].y = fmaxf(x[i].y, __shfl_xor_sync(0xffffffffu, x[i].y, off));
+    }
+  }
+}
 template <bool HALF>
 __device__ __forceinline__ float sum_keys(float x) {
 #pragma unroll
@@ -396,7 +435,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     // Q^T fragments of column grp: elements 8 qd .. 8 qd + 7 of each 32-element
     // chunk, in the order of K's operands, and the sums of q over the groups
     uint32_t qf[2 * CH][2];
-    float cs[2], qs[G][2];
+    float2 cs, qs[G];
     {
       const int col = HALF ? grp & 3 : grp;
       const bool real = col < group;
@@ -439,154 +478,242 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
         qf[2 * j + 1][0] = float2_to_f16x2(y[2], y[6]);
         qf[2 * j + 1][1] = float2_to_f16x2(y[3], y[7]);
       }
+      // the sums in the units of q . c: Q's scale and the codes' 2^-24
+      auto of_heads = [&](float x) {
+        return make_float2(__shfl_sync(0xffffffffu, x, h0 * 4),
+                           __shfl_sync(0xffffffffu, x, (h0 + 1) * 4));
+      };
+      cs = of_heads(down);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        cs[h] = __shfl_sync(0xffffffffu, down, (h0 + h) * 4);
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-          qs[g][h] = sc * __shfl_sync(0xffffffffu, sum[g], (h0 + h) * 4);
-      }
+      for (int g = 0; g < G; ++g) qs[g] = of_heads(sum[g] * up * 0x1p-24f);
     }
-    float acc[MT][4], zs[G][2];
+    float acc[MT][4];
+    float2 zs[G];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
 #pragma unroll
-    for (int g = 0; g < G; ++g) zs[g][0] = zs[g][1] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY};  // reference of the exponents (log2)
-    float l[2] = {0.f, 0.f};              // this lane's share of the sums
+    for (int g = 0; g < G; ++g) zs[g] = make_float2(0.f, 0.f);
+    // references of the exponents (log2, whole numbers), this lane's share of the sums of
+    // p, and the powers of two of P
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float2 pw[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) pw[g] = make_float2(1.f, 1.f);
+    bool begun = false;  // whether a tile had a key
     const int64_t mrow = ((int64_t)w.mask_hi << 32 | (uint32_t)w.mask_lo) +
                          (int64_t)w.q_local0 * w.kv_len;
     const uint32_t t1 = w.t1;
 
-    // One tile of keys a0 .. a0 + 31.  ALL: every key is there and seen.
+    // One tile of keys a0 .. a0 + 31.  ALL: every key is there and seen.  Pairs are of the
+    // lane's two heads; b and y name the keys: my_key + 8 y of the lane's blocks.
     auto tile = [&](auto all, uint32_t a0) {
       constexpr bool ALL = decltype(all)::value;
       const uint32_t at = ring + stage * S::STAGE;
-      // q . c per group, of keys my_key and my_key + 8 of the lane's blocks
-      float sg[NB][G][4];
+      auto key_of = [&](int b, int y) { return 16 * (HALF ? my_block : b) + 8 * y + my_key; };
+      auto v_words = [&](int b, int y, uint32_t (&vw)[G]) {
+        lds_words<G>(at + 2 * S::CODES + S::WORDS + key_of(b, y) * (4 * G), vw);
+      };
+      float2 s[NB][2];  // scores
+      {
+        uint32_t kw[NB][2][G];
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        float d[2][4];
+        for (int b = 0; b < NB; ++b) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          d[b][0] = d[b][1] = d[b][2] = d[b][3] = 0.f;
-#pragma unroll
-          for (int j = g * (GR / 32); j < (g + 1) * (GR / 32); ++j) {
-            const uint32_t from = at + k_lane + b * 16 * S::ROW + ((j ^ k_swap) << 4);
-            const uint32_t w0 = lds32(from), w1 = lds32(from + 8 * S::ROW);
-            const uint32_t u0 = w0 >> 8, u1 = w1 >> 8;
-            mma16816(d[b], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u,
-                     w1 & 0x00f000f0u, qf[2 * j][0], qf[2 * j][1]);
-            mma16816(d[b], u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u,
-                     u1 & 0x00f000f0u, qf[2 * j + 1][0], qf[2 * j + 1][1]);
+          for (int y = 0; y < 2; ++y) {
+            lds_words<G>(at + 2 * S::CODES + key_of(b, y) * (4 * G), kw[b][y]);
+            s[b][y] = make_float2(0.f, 0.f);
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (HALF) {
-            sg[0][g][i] = my_block ? d[1][i] : d[0][i];
-          } else {
-            sg[0][g][i] = d[0][i];
-            sg[NB - 1][g][i] = d[1][i];
+        for (int g = 0; g < G; ++g) {
+          float d[2][4];  // q . c over the group
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            d[b][0] = d[b][1] = d[b][2] = d[b][3] = 0.f;
+#pragma unroll
+            for (int j = g * (GR / 32); j < (g + 1) * (GR / 32); ++j) {
+              const uint32_t from = at + k_lane + b * 16 * S::ROW + ((j ^ k_swap) << 4);
+              const uint32_t w0 = lds32(from), w1 = lds32(from + 8 * S::ROW);
+              const uint32_t u0 = w0 >> 8, u1 = w1 >> 8;
+              mma16816(d[b], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u,
+                       w1 & 0x00f000f0u, qf[2 * j][0], qf[2 * j][1]);
+              mma16816(d[b], u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u,
+                       u1 & 0x00f000f0u, qf[2 * j + 1][0], qf[2 * j + 1][1]);
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float2 x = make_float2(d[b][2 * y], d[b][2 * y + 1]);
+              if constexpr (HALF)
+                if (my_block) x = make_float2(d[1][2 * y], d[1][2 * y + 1]);
+              const float ks = step_of(kw[b][y][g]), kz = origin_of(kw[b][y][g]);
+              s[b][y] = __ffma2_rn(make_float2(kz, kz), qs[g], s[b][y]);
+              s[b][y] = __ffma2_rn(make_float2(ks, ks), x, s[b][y]);
+            }
           }
         }
       }
-      float s[NB][4];                             // scores: [key 0, key 1] x [head 0, head 1]
-      float vstep[NB][2][G], vorig[NB][2][G];
-      float top[2] = {-INFINITY, -INFINITY};
+      float most = -INFINITY;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        float up[2];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const int key = 16 * (HALF ? my_block : b) + 8 * y + my_key;
-          uint32_t kw[G], vw[G];
-          lds_words<G>(at + 2 * S::CODES + key * (4 * G), kw);
-          lds_words<G>(at + 2 * S::CODES + S::WORDS + key * (4 * G), vw);
-          float d0 = 0.f, d1 = 0.f, z0 = 0.f, z1 = 0.f;
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            const float ks = step_of(kw[g]), kz = origin_of(kw[g]);
-            d0 = fmaf(ks, sg[b][g][2 * y], d0);
-            d1 = fmaf(ks, sg[b][g][2 * y + 1], d1);
-            z0 = fmaf(kz, qs[g][0], z0);
-            z1 = fmaf(kz, qs[g][1], z1);
-          }
-          s[b][2 * y] = fmaf(d0, cs[0], z0);
-          s[b][2 * y + 1] = fmaf(d1, cs[1], z1);
-          float most = 0.f;
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            vstep[b][y][g] = step_of(vw[g]);
-            vorig[b][y][g] = y ? fmaf(15.f, vstep[b][y][g], origin_of(vw[g])) : origin_of(vw[g]);
-          }
+          s[b][y] = __fmul2_rn(s[b][y], cs);
           if constexpr (!ALL) {
+            const int key = key_of(b, y);
             bool seen = a0 + key < t1;
             if (a.mask_mode == PKA_MASK_CUSTOM && seen) {
               const int64_t bit = mrow + a0 + key;
               seen = (a.mask[bit >> 3] >> (bit & 7)) & 1;
             }
-            if (!seen) {  // its words may hold anything
-              s[b][2 * y] = s[b][2 * y + 1] = -INFINITY;
+            if (!seen) s[b][y] = make_float2(-INFINITY, -INFINITY);
+          }
+          most = max3(most, s[b][y].x - m[0], s[b][y].y - m[1]);
+        }
+      }
+      // the first tile with a key (m = -inf) or a maximum well past its reference: the state
+      // is rescaled, the same in all lanes of a column, and P's powers of two found anew,
+      // from this tile's p * step and the earlier ones' (at most 2^kHeadroom / pw)
+      if (__any_sync(0xffffffffu, most > kRescale - kBelow)) {
+        // (all reductions a level at a time: a first tile waits for them)
+        float2 top[1] = {make_float2(-INFINITY, -INFINITY)}, grown[G];
 #pragma unroll
-              for (int g = 0; g < G; ++g) vstep[b][y][g] = vorig[b][y][g] = 0.f;
+        for (int b = 0; b < NB; ++b)
+          top[0] = make_float2(max3(top[0].x, s[b][0].x, s[b][1].x),
+                               max3(top[0].y, s[b][0].y, s[b][1].y));
+        max_keys<HALF>(top);
+        const float2 to = make_float2(fmaxf(m[0], ceilf(top[0].x) + kBelow),
+                                      fmaxf(m[1], ceilf(top[0].y) + kBelow));
+#pragma unroll
+        for (int g = 0; g < G; ++g) grown[g] = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            uint32_t vw[G];
+            v_words(b, y, vw);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              const float step = lg2(fmaxf(fabsf(step_of(vw[g])), kLeastStep));
+              grown[g].x = fmaxf(grown[g].x, s[b][y].x - to.x + step);
+              grown[g].y = fmaxf(grown[g].y, s[b][y].y - to.y + step);
             }
           }
-#pragma unroll
-          for (int g = 0; g < G; ++g) most = fmaxf(most, fabsf(vstep[b][y][g]));
-          up[y] = lg2(most + kLeastStep);
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          top[h] = max3(top[h], s[b][h] + up[0], s[b][2 + h] + up[1]);
-      }
-#pragma unroll
-      for (int off = HALF ? 2 : 4; off < 32; off <<= 1) {
-        top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], off));
-        top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], off));
-      }
-      // the first tile with a key (m = -inf) or a maximum well past the reference:
-      // the state is rescaled, the same in all lanes of a column
-      if (top[0] - kHeadroom > m[0] + kRescale || top[1] - kHeadroom > m[1] + kRescale) {
+        max_keys<HALF>(grown);
+        float al[2][G + 1];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float want = top[h] - kHeadroom;
-          if (!(want > m[h] + kRescale)) continue;
-          const float al = ex2(m[h] - want);  // 0 while m is -inf
-          m[h] = want;
-          l[h] *= al;
 #pragma unroll
-          for (int g = 0; g < G; ++g) zs[g][h] *= al;
+          for (int g = 0; g <= G; ++g) al[h][g] = 1.f;
+          const float ref = h ? to.y : to.x;
+          if (ref == -INFINITY) continue;  // no key yet
+          const float far = fmaxf(m[h] - ref, -1000.f);  // -1000: no key before
+          m[h] = ref;
+          al[h][G] = pow2(far);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            acc[mt][h] *= al;
-            acc[mt][2 + h] *= al;
+          for (int g = 0; g < G; ++g) {
+            float& w = h ? pw[g].y : pw[g].x;
+            const float before = far - pow2_log(w);
+            const float now = clamp_log(
+                fmaxf(before, ceilf(h ? grown[g].y : grown[g].x) - kHeadroom));
+            al[h][g] = pow2(before - now);
+            w = pow2(-now);
           }
         }
+        if (begun) {  // not all zeros
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            l[h] *= al[h][G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              (h ? zs[g].y : zs[g].x) *= al[h][G];
+#pragma unroll
+              for (int mt = g * (MT / G); mt < (g + 1) * (MT / G); ++mt) {
+                acc[mt][h] *= al[h][g];
+                acc[mt][2 + h] *= al[h][g];
+              }
+            }
+          }
+        }
+        begun = true;
       }
-      // O^T += V^T . P^T
-      float e[NB][4];
+      float2 e[NB][2];  // p
+      uint32_t vw[NB][2][G];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          e[b][i] = ex2(s[b][i] - m[i & 1]);
-          if constexpr (!ALL) e[b][i] = s[b][i] == -INFINITY ? 0.f : e[b][i];  // not -inf + inf
+        for (int y = 0; y < 2; ++y) {
+          v_words(b, y, vw[b][y]);
+          e[b][y] = make_float2(ex2(s[b][y].x - m[0]), ex2(s[b][y].y - m[1]));
+          if constexpr (!ALL) {
+            if (s[b][y].x == -INFINITY) e[b][y].x = 0.f;  // not -inf + inf
+            if (s[b][y].y == -INFINITY) e[b][y].y = 0.f;
+            // an unseen key's words may hold anything
+            if (s[b][y].x == -INFINITY && s[b][y].y == -INFINITY)
+#pragma unroll
+              for (int g = 0; g < G; ++g) vw[b][y][g] = 0u;
+          }
+          l[0] += e[b][y].x;
+          l[1] += e[b][y].y;
         }
-        l[0] += e[b][0] + e[b][2];
-        l[1] += e[b][1] + e[b][3];
       }
+      // O^T += V^T . P^T, with P = p * step * pw
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         uint32_t pb[2][2];
+        auto weigh = [&]() {
+          uint32_t most_p = 0;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float step = step_of(vw[b][y][g]);
+              const float2 p = __fmul2_rn(e[b][y], __fmul2_rn(make_float2(step, step), pw[g]));
+              pb[b][y] = float2_to_f16x2(p.x, p.y);
+              most_p = max_f16x2(most_p, pb[b][y] & 0x7fff7fffu);
+            }
+          }
+          return ((most_p + (0x7fffu - kMostP) * 0x10001u) & 0x80008000u) != 0;
+        };
+        if (__any_sync(0xffffffffu, weigh())) {  // a P past f16's middle: a smaller power of two
+          float2 grown[1] = {make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float step = fabsf(step_of(vw[b][y][g]));
+              grown[0].x = fmaxf(grown[0].x, e[b][y].x * step);
+              grown[0].y = fmaxf(grown[0].y, e[b][y].y * step);
+            }
+          }
+          max_keys<HALF>(grown);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float before = -pow2_log(h ? pw[g].y : pw[g].x);
+            const float now =
+                clamp_log(fmaxf(before, ceilf(lg2(h ? grown[0].y : grown[0].x)) - kHeadroom));
+            const float al = pow2(before - now);
+            (h ? pw[g].y : pw[g].x) = pow2(-now);
+#pragma unroll
+            for (int mt = g * (MT / G); mt < (g + 1) * (MT / G); ++mt) {
+              acc[mt][h] *= al;
+              acc[mt][2 + h] *= al;
+            }
+          }
+          weigh();
+        }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const float s0 = vstep[b][0][g], s1 = vstep[b][1][g];
-          const float o0 = vorig[b][0][g], o1 = vorig[b][1][g];
-          zs[g][0] = fmaf(e[b][0], o0, fmaf(e[b][2], o1, zs[g][0]));
-          zs[g][1] = fmaf(e[b][1], o0, fmaf(e[b][3], o1, zs[g][1]));
-          pb[b][0] = transpose8x8(float2_to_f16x2(e[b][0] * s0, e[b][1] * s0));
-          pb[b][1] = transpose8x8(float2_to_f16x2(e[b][2] * -s1, e[b][3] * -s1));
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float z = origin_of(vw[b][y][g]);
+            const float from = y ? fmaf(15.f, step_of(vw[b][y][g]), z) : z;
+            zs[g] = __ffma2_rn(e[b][y], make_float2(from, from), zs[g]);
+            pb[b][y] = transpose8x8(y ? pb[b][y] ^ 0x80008000u : pb[b][y]);
+          }
         }
         if constexpr (HALF) {
 #pragma unroll
@@ -642,6 +769,15 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 
+    // from P's powers of two and the codes' 2^-24 and 2^-20 to what p weighs
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const float2 w = pw[mt / (MT / G)];
+      const float inv[2] = {pow2_inverse(w.x), pow2_inverse(w.y)};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) acc[mt][x] *= inv[x & 1] * (x < 2 ? 16777216.f : 1048576.f);
+    }
+
     // ---- the head's warps bring their states together, pair by pair; which warp
     // ends an item goes round, so that the others are at the next one meanwhile ----
     const int turn = (ii - i0) % n_split;
@@ -660,7 +796,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
           slot[32 * i++] = m[h];
           slot[32 * i++] = l[h];
 #pragma unroll
-          for (int g = 0; g < G; ++g) slot[32 * i++] = zs[g][h];
+          for (int g = 0; g < G; ++g) slot[32 * i++] = h ? zs[g].y : zs[g].x;
         }
       }
       asm volatile("bar.sync %0, %1;" ::"r"(hl + 1), "r"(32 * n_split) : "memory");
@@ -676,8 +812,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
           m[h] = to;
           l[h] = l[h] * mine[h] + tail[32 * (h * (2 + G) + 1)] * other[h];
 #pragma unroll
-          for (int g = 0; g < G; ++g)
-            zs[g][h] = zs[g][h] * mine[h] + tail[32 * (h * (2 + G) + 2 + g)] * other[h];
+          for (int g = 0; g < G; ++g) {
+            float& z = h ? zs[g].y : zs[g].x;
+            z = z * mine[h] + tail[32 * (h * (2 + G) + 2 + g)] * other[h];
+          }
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -695,7 +833,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     for (int h = 0; h < 2; ++h) {
       l[h] = sum_keys<HALF>(l[h]);
 #pragma unroll
-      for (int g = 0; g < G; ++g) zs[g][h] = sum_keys<HALF>(zs[g][h]);
+      for (int g = 0; g < G; ++g) {
+        float& z = h ? zs[g].y : zs[g].x;
+        z = sum_keys<HALF>(z);
+      }
     }
     if constexpr (HALF) {
 #pragma unroll
@@ -710,7 +851,6 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
       // a NaN among the words of a seen key makes the sums NaN, which is not "no key"
       const bool none = l[h] == 0.f;
       const float inv = none ? 0.f : 1.f / l[h];
-      const float even = inv * 16777216.f, odd = inv * 1048576.f;  // 2^24, 2^20
       const float lse = none ? -INFINITY : m[h] + log2f(l[h]);
       const int rec = w.out_rec + (head - w.kv_head0 * group);
       uint16_t* orow = a.o + ((int64_t)w.q_row0 * Hq + head) * D;
@@ -720,9 +860,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
 #pragma unroll
         for (int q = 0; q < S::DL / 4; ++q) {
           const int mt = (g * (S::DL / 4) + q) * 2;
-          const float z = zs[g][h] * inv;
-          const float x0 = fmaf(acc[mt][h], even, z), x1 = fmaf(acc[mt][2 + h], odd, z);
-          const float x2 = fmaf(acc[mt + 1][h], even, z), x3 = fmaf(acc[mt + 1][2 + h], odd, z);
+          const float z = (h ? zs[g].y : zs[g].x) * inv;
+          const float x0 = fmaf(acc[mt][h], inv, z), x1 = fmaf(acc[mt][2 + h], inv, z);
+          const float x2 = fmaf(acc[mt + 1][h], inv, z), x3 = fmaf(acc[mt + 1][2 + h], inv, z);
           const int d = g * GR + grp * S::DL + 4 * q;
           if (w.out_rec < 0)
             *reinterpret_cast<uint2*>(orow + d) =

@@ -476,6 +476,64 @@ def test_decode_steps_of_all_sizes():
         _assert_decode(o, lse, b.want())
 
 
+@pytest.mark.parametrize("apart", [2.0 ** -12, 2.0 ** -24, 2.0 ** -32, 2.0 ** -60, 2.0 ** -90])
+@pytest.mark.parametrize("d,group,hq", [(64, 32, 4), (64, 32, 8), (128, 32, 4), (128, 32, 8),
+                                        (128, 64, 4), (128, 64, 8)])
+def test_decode_groups_of_unlike_magnitudes(d, group, hq, apart):
+    """V's groups of one head far apart in size, one request with the large one first and one
+    with it last, and a third where they change places from key to key: each output within
+    the bits of what it sums."""
+    kv = [70, 300, 130]
+    b = Batch(41, kv, page=4, hq=hq, hk=1, d=d, group=group)
+    rng = np.random.default_rng(13)
+    n = d // group
+    sizes = apart ** (np.arange(n) / (n - 1))
+    rows = [rng.standard_normal((m, 1, d)) * np.repeat(s, group)
+            for m, s in zip(kv, (sizes, sizes[::-1], sizes))]
+    rows[2][::2] = rows[2][::2, :, ::-1]
+    kv4.fill(b.v, b.kv_indptr, b.kv_indices, b.kv_lens, rows)
+    for split in ("off", "auto"):
+        o, lse, _ = b.run(split_mode=split)
+        _assert_decode(o, lse, b.want())
+
+
+@pytest.mark.parametrize("order", [1, -1])
+def test_decode_weights_against_sizes(order):
+    """Keys whose V is the larger the less they weigh, over 2^60: what each adds to an output
+    is of one size, however large or small its step."""
+    n, d = 240, 64
+    b = Batch(42, [n], page=4, hq=4, hk=1, d=d, group=32)
+    rng = np.random.default_rng(14)
+    sign = np.where(np.arange(d) % 2 == 0, 1.0, -1.0)
+    b.q[:] = (np.where(sign > 0, 0x3F80, 0xBF80)).astype(np.uint16)
+    weight = np.linspace(-60, 0, n)[::order]  # log2
+    k = np.zeros((n, 1, d)) + weight[:, None, None] * sign / (d ** 0.5 * np.log2(np.e))
+    v = rng.standard_normal((n, 1, d)) * 2.0 ** -weight[:, None, None]
+    for pool, rows in ((b.k, k), (b.v, v)):
+        kv4.fill(pool, b.kv_indptr, b.kv_indices, b.kv_lens, [rows])
+    for split in ("off", "auto"):
+        o, lse, _ = b.run(split_mode=split)
+        _assert_decode(o, lse, b.want())
+
+
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -60, 2.0 ** 40, 2.0 ** 100, 2.0 ** 112])
+def test_decode_values_of_any_size(size):
+    """V of any size, among it rows of one value, which have no steps; the other request's
+    V is of ordinary size."""
+    b = Batch(43, [150, 40], page=4, hq=8, hk=2, d=128, group=64)
+    rng = np.random.default_rng(15)
+    rows = [size * rng.standard_normal((150, 2, 128)), rng.standard_normal((40, 2, 128))]
+    rows[0][::5] = size * rng.standard_normal((30, 2, 1))
+    kv4.fill(b.v, b.kv_indptr, b.kv_indices, b.kv_lens, rows)
+    for split in ("off", "auto"):
+        o, lse, _ = b.run(split_mode=split)
+        _assert_decode(o, lse, b.want())
+    rows[0][:] = size * rng.standard_normal((150, 2, 1))
+    kv4.fill(b.v, b.kv_indptr, b.kv_indices, b.kv_lens, rows)
+    o, lse, _ = b.run()
+    _assert_decode(o, lse, b.want())
+
+
 @pytest.mark.parametrize("hq,hk", [(4, 1), (8, 1)])
 def test_long_flat_rows_keep_their_precision(hq, hk):
     """160,000 keys of near equal weight in one piece: the output, the mean of as many
