@@ -17,10 +17,11 @@
 // every product, whose cancellation costs the statistics 2^-17 or so.
 //   Q is scaled to f16 by a power of two per head that puts its largest element
 // in [2^14, 2^15): bf16 values down to 2^-27 of it stay exact.
-//   The second 8 keys of each 16 take V's codes from above, as 15 - c under -P and
-// an origin of z + 15 s: an output's sum then runs up by as much as down.  With c
-// alone all its terms are positive, it grows with the keys, and so does what each
-// MMA cuts off of it: 2% of an output that is the mean of 160,000 values.
+//   The second 8 keys of each 16 take V's codes from above, as 15 - c under -P,
+// with 15 of the same rounded P beside them: an output's sum then runs up by as much
+// as down.  With c alone all its terms are positive, it grows with the keys, and so
+// does what each MMA cuts off of it: 2% of an output that is the mean of 160,000
+// values.
 //   P goes to f16 with V's step in it, 11 bits against the 8 of bf16: p * s times a
 // power of two of its own for each head and group, which puts the largest p * s seen
 // at 2^11 (a larger one may pass it by 2^4 before the state is rescaled).  So the 11
@@ -135,6 +136,14 @@ __device__ __forceinline__ uint32_t float2_to_f16x2(float a, float b) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
+}
+
+__device__ __forceinline__ float2 f16x2_to_float2(uint32_t x) {
+  float2 f;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(x));
+  return f;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -710,10 +719,14 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const float z = origin_of(vw[b][y][g]);
-            const float from = y ? fmaf(15.f, step_of(vw[b][y][g]), z) : z;
-            zs[g] = __ffma2_rn(e[b][y], make_float2(from, from), zs[g]);
-            pb[b][y] = transpose8x8(y ? pb[b][y] ^ 0x80008000u : pb[b][y]);
+            zs[g] = __ffma2_rn(e[b][y], make_float2(z, z), zs[g]);
           }
+          // 15 of the second keys' P as it is rounded, which the MMAs take (15 - c) of
+          const float2 p = f16x2_to_float2(pb[b][1]);
+          zs[g] = __ffma2_rn(p, make_float2(15.f * pow2_inverse(pw[g].x),
+                                            15.f * pow2_inverse(pw[g].y)), zs[g]);
+          pb[b][0] = transpose8x8(pb[b][0]);
+          pb[b][1] = transpose8x8(pb[b][1] ^ 0x80008000u);
         }
         if constexpr (HALF) {
 #pragma unroll

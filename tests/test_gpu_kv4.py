@@ -534,6 +534,27 @@ def test_decode_values_of_any_size(size):
     _assert_decode(o, lse, b.want())
 
 
+@pytest.mark.parametrize("n", [1, 9, 16, 40, 400, 3000])
+@pytest.mark.parametrize("d,group,hq", [(64, 32, 4), (64, 64, 8), (128, 32, 8), (128, 64, 4),
+                                        (128, 128, 4), (128, 128, 8)])
+def test_decode_of_values_from_zero_up(d, group, hq, n):
+    """V without negative values, some elements 0 in every key: their outputs are 0 but for
+    the sums' own rounding.  An output adds what its second keys' codes lack of 15, so it
+    sums magnitudes of at most 15 steps a key, 1.01 here, where an MMA of 16 keys rounds
+    2^-23 of its sum (accumulation may truncate), and the few terms beside it as much."""
+    b = Batch(44 + n, [n, 33], page=16, hq=hq, hk=1, d=d, group=group)
+    rng = np.random.default_rng(16)
+    none = np.arange(d) % group % 8 == 3
+    rows = [np.where(none, 0.0, rng.random((m, 1, d))) for m in (n, 33)]
+    kv4.fill(b.v, b.kv_indptr, b.kv_indices, b.kv_lens, rows)
+    want = b.want()
+    assert not want[0][..., none].any()
+    for split in ("off", "auto"):
+        o, lse, _ = b.run(split_mode=split)
+        _assert_decode(np.where(none, 0.0, o), lse, want)
+        assert np.abs(o[..., none]).max() <= 1.01 * 2.0 ** -22 * (n / 16 + 4)
+
+
 @pytest.mark.parametrize("hq,hk", [(4, 1), (8, 1)])
 def test_long_flat_rows_keep_their_precision(hq, hk):
     """160,000 keys of near equal weight in one piece: the output, the mean of as many
