@@ -988,7 +988,7 @@ def test_staged_long_tails(below):
     q = sign.expand(2, hq, d).contiguous().to(torch.bfloat16)
     attn = pka.BatchAttention()
     attn.plan(np.array([0, 2], np.int32), ptr, last, num_qo_heads=hq, num_kv_heads=hk, head_dim=d,
-              page_size=64, mask_mode="none", kv_dtype="int4_g32")
+              page_size=64, mask_mode="none", split_mode="off", kv_dtype="int4_g32")
     o, lse = attn.run(q, *pools, i32(idx))
     torch.cuda.synchronize()
     kp, vp = (kv4.Pool(p.cpu().numpy(), 64, hk, d, 32, "NHD") for p in pools)
