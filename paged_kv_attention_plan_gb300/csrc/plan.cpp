@@ -487,8 +487,10 @@ void plan_decode(const pka_params* p, const std::vector<Batch>& lv, int num_sms,
       };
       target = (total + over * (int64_t)units.size() + num_sms - 1) / num_sms;
       chunk = std::max<int64_t>((target + 15) / 16 * 16, kMinDecodeChunk + over);
-      for (int64_t step = 16; ctas(chunk) > num_sms; chunk += step, step += step / 2 / 16 * 16) {
-      }
+      // A CTA that closes has less than over + 16 of its share left, and cutting units
+      // makes at most an item a CTA more: a share of target + 2 over + 17 always fits, so
+      // that at most 17 are tried.
+      while (ctas(chunk) > num_sms) chunk += 16;
     }
   }
   L->decode_chunk = (int)std::min<int64_t>(chunk, INT32_MAX);

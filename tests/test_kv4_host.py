@@ -212,6 +212,31 @@ def test_decode_plans_fill_the_sms_once(seed):
         assert max(per) <= -(-len(plan["decode_items"]) // 152) + 1
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_decode_shares_are_found_in_few_tries(seed):
+    """The share of a CTA is tried in steps of 16 keys from its least value on; it never goes
+    past that value by two items' cost and two tiles."""
+    rng = np.random.default_rng(100 + seed)
+    n, sms = int(rng.integers(1, 1500)), int(rng.choice([1, 7, 148, 152]))
+    kv = rng.integers(1, [2, 17, 300, 9000][seed % 4], n)
+    if seed % 3 == 0:
+        kv[: n // 2] = 112 + 64  # units as long as the least share
+    hq, hk = [(32, 8), (8, 1), (13, 13), (64, 16)][seed // 6]
+    ptr = np.concatenate([[0], np.cumsum(kv)]).astype(np.int32)
+    p = pka.make_params(hq, hk, 128, 1, kv_dtype="int4_g64", num_sms=sms)
+    h = pka.pka_plan_create()
+    buf = np.zeros(16 << 20, np.uint8)
+    s = pka.pka_plan(h, p, None, ptr, np.ones(n, np.int32), None, buf, check=False)
+    assert s == OK
+    info = pka.pka_plan_get_info(h)
+    per_cta = parse(buf)["header"]["decode_heads_per_cta"]
+    pka.pka_plan_destroy(h)
+    units = hk // per_cta
+    least = max(-(-int(kv.sum() * units + 112 * n * units) // sms), 64 + 112)
+    assert info.num_decode_ctas <= sms
+    assert info.decode_chunk_tokens <= least + 2 * 112 + 32
+
+
 @pytest.mark.parametrize("lens", [(1, 33, 0, 250), (0,), (0, 0, 5000, 0), (64, 0, 64)])
 def test_rows_without_keys_are_planned(lens):
     """A decode row whose request has no keys is an item of none, which writes its zeros;
