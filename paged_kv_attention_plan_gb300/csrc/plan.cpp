@@ -88,10 +88,12 @@ struct pka_plan_s {
 namespace {
 
 constexpr int kMinDecodeChunk = 64;
-// 4-bit pools: what starting and ending an item takes, in keys (3 us at 25 ns a key).
-// A token pool of 37 requests: 31.3 us with 0, 29.4 with 56, 28.3 with 112, 28.1 with
-// 224; 64 requests of 512 to 4096 keys 42.0, 41.2, 40.6 and 40.5.
-constexpr int kItemCost4 = 112;
+// 4-bit pools: what starting and ending an item takes, 3 us, in keys of one kv head (3.2
+// ns each).  A CTA of fewer heads has as many warps and walks a key faster, so its items
+// count as more keys.  64 requests of 512 to 4096 keys, in us with 112, 448 and 896 keys
+// an item: one kv head a CTA 23.0, 17.0, 14.7; two 21.5, 19.5, 18.8; eight 41.7, 42.6,
+// 44.3 (and 42.0 with none).
+constexpr int kItemCost4 = 896;
 
 thread_local char g_last_error[256] = "";
 
@@ -464,9 +466,9 @@ void plan_decode(const pka_params* p, const std::vector<Batch>& lv, int num_sms,
     target = (target + pka::kDecodeTileTokens - 1) / pka::kDecodeTileTokens * pka::kDecodeTileTokens;
     chunk = std::max<int64_t>(target, kMinDecodeChunk);
     if (pka::kv4_group(p->kv_dtype)) {
-      // An item costs a CTA kItemCost4 keys besides its own, and no more CTAs than
-      // SMs: one fills an SM there (shared memory), so that the next starts after it.
-      over = kItemCost4;
+      // An item costs a CTA `over` keys besides its own, and no more CTAs than SMs: one
+      // fills an SM there (shared memory), so that the next starts after it.
+      over = kItemCost4 / hpc;
       auto ctas = [&](int64_t share) {
         int64_t n = 0, load = 0;
         for (const Unit& u : units) {
@@ -489,8 +491,8 @@ void plan_decode(const pka_params* p, const std::vector<Batch>& lv, int num_sms,
       chunk = std::max<int64_t>((target + 15) / 16 * 16, kMinDecodeChunk + over);
       // A CTA that closes has less than over + 16 of its share left, and cutting units
       // makes at most an item a CTA more: a share of target + 2 over + 17 always fits, so
-      // that at most 17 are tried.
-      while (ctas(chunk) > num_sms) chunk += 16;
+      // that at most 18 are tried.
+      while (ctas(chunk) > num_sms) chunk += (over / 8 + 15) / 16 * 16;
     }
   }
   L->decode_chunk = (int)std::min<int64_t>(chunk, INT32_MAX);

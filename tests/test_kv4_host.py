@@ -214,13 +214,11 @@ def test_decode_plans_fill_the_sms_once(seed):
 
 @pytest.mark.parametrize("seed", range(24))
 def test_decode_shares_are_found_in_few_tries(seed):
-    """The share of a CTA is tried in steps of 16 keys from its least value on; it never goes
-    past that value by two items' cost and two tiles."""
+    """The share of a CTA is tried in steps of an eighth of an item's cost from its least value
+    on; it never goes past that value by two items' cost, two tiles and a step."""
     rng = np.random.default_rng(100 + seed)
     n, sms = int(rng.integers(1, 1500)), int(rng.choice([1, 7, 148, 152]))
     kv = rng.integers(1, [2, 17, 300, 9000][seed % 4], n)
-    if seed % 3 == 0:
-        kv[: n // 2] = 112 + 64  # units as long as the least share
     hq, hk = [(32, 8), (8, 1), (13, 13), (64, 16)][seed // 6]
     ptr = np.concatenate([[0], np.cumsum(kv)]).astype(np.int32)
     p = pka.make_params(hq, hk, 128, 1, kv_dtype="int4_g64", num_sms=sms)
@@ -232,9 +230,10 @@ def test_decode_shares_are_found_in_few_tries(seed):
     per_cta = parse(buf)["header"]["decode_heads_per_cta"]
     pka.pka_plan_destroy(h)
     units = hk // per_cta
-    least = max(-(-int(kv.sum() * units + 112 * n * units) // sms), 64 + 112)
+    over = 896 // per_cta  # keys that an item costs besides its own
+    least = max(-(-int(kv.sum() * units + over * n * units) // sms), 64 + over)
     assert info.num_decode_ctas <= sms
-    assert info.decode_chunk_tokens <= least + 2 * 112 + 32
+    assert info.decode_chunk_tokens <= least + 2 * over + 32 + (over // 8 + 15) // 16 * 16
 
 
 @pytest.mark.parametrize("lens", [(1, 33, 0, 250), (0,), (0, 0, 5000, 0), (64, 0, 64)])
