@@ -340,20 +340,31 @@ __global__ void __launch_bounds__(256) dequant_kernel(
     const uint8_t* __restrict__ k8, const uint8_t* __restrict__ v8, int64_t page_stride, int P,
     int layout, int ragged, int hk, int d, uint16_t* __restrict__ out_k,
     uint16_t* __restrict__ out_v) {
+  // Graph mode: the up to 127 rows behind the plan's last that a tile of keys may read
+  // become zeros.  They may hold anything, and 0 * NaN in P V would reach a tile's rows.
+  int64_t end = rows;
   if (counts) {
     n_units = min(max(counts[0], 0), n_units);
     rows = min((int64_t)max(counts[2], 0), rows);
+    end = min(rows + 127, end);
   }
   if (n_units <= 0) return;
   const int vec_per_head = d / 16;  // 16 codes per thread
   const int64_t vec_per_row = (int64_t)hk * vec_per_head;
-  const int64_t total = rows * vec_per_row;
+  const int64_t total = end * vec_per_row;
   for (int64_t x = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; x < total;
        x += (int64_t)gridDim.x * blockDim.x) {
     const int64_t row = x / vec_per_row;
     const int rem = (int)(x - row * vec_per_row);
     const int h = rem / vec_per_head;
     const int c = rem - h * vec_per_head;
+    const int64_t dst = (row * hk + h) * d + c * 16;
+    uint4* dk = reinterpret_cast<uint4*>(out_k + dst);
+    uint4* dv = reinterpret_cast<uint4*>(out_v + dst);
+    if (row >= rows) {
+      dk[0] = dk[1] = dv[0] = dv[1] = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
     int lo = 0, hi = n_units - 1;  // last unit with dst_row0 <= row
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -371,7 +382,6 @@ __global__ void __launch_bounds__(256) dequant_kernel(
       src += layout == PKA_NHD ? ((int64_t)slot * hk + h) * d : ((int64_t)h * P + slot) * d;
     }
     src += c * 16;
-    const int64_t dst = (row * hk + h) * d + c * 16;
     const uint4 kc = *reinterpret_cast<const uint4*>(k8 + src);
     const uint4 vc = *reinterpret_cast<const uint4*>(v8 + src);
     const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w}, vw[4] = {vc.x, vc.y, vc.z, vc.w};
@@ -383,8 +393,6 @@ __global__ void __launch_bounds__(256) dequant_kernel(
       vo[2 * i] = e4m3x2_to_bf16x2(vw[i] & 0xffffu);
       vo[2 * i + 1] = e4m3x2_to_bf16x2(vw[i] >> 16);
     }
-    uint4* dk = reinterpret_cast<uint4*>(out_k + dst);
-    uint4* dv = reinterpret_cast<uint4*>(out_v + dst);
     dk[0] = make_uint4(ko[0], ko[1], ko[2], ko[3]);
     dk[1] = make_uint4(ko[4], ko[5], ko[6], ko[7]);
     dv[0] = make_uint4(vo[0], vo[1], vo[2], vo[3]);

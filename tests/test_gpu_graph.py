@@ -233,3 +233,38 @@ def test_graph_mode_e4m3_capture_serves_new_plans():
         assert pka.pka_get_device_error() == 0
         n = b.nnz_q
         assert_parity(f64(o_buf[:n]), f64(lse_buf[:n]), *run_oracle(b))
+
+
+@pytest.mark.parametrize("kv", [41, 128, 129, 200])
+@pytest.mark.parametrize("kv_dtype", ["e4m3", "int4_g64"])
+def test_graph_mode_scratch_holds_anything_before_a_run(kv_dtype, kv):
+    """Graph mode lays the scratch of decoded keys out for its capacity; what lies behind a
+    plan's last key (here NaN everywhere) reaches no row, with the capacity just a few rows
+    longer than the batch and much longer."""
+    hq, hk, d, page = 8, 2, 128, 16
+    b = W.make_paged_batch(90, [9, 3], [kv, 20], page_size=page, hq=hq, hk=hk, d=d)
+    n = b.nnz_q
+    params = pka.make_params(hq, hk, d, page, kv_dtype=kv_dtype)
+    pages = b.k_pool.shape[0]
+    if kv_dtype == "e4m3":
+        shape = (pages, page, hk, d)
+    else:
+        shape = (pages, pka.pka_kv_page_bytes(params))
+    pools = [torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    rows = [torch.randn(kv + 20, hk, d, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    table = i32(b.kv_indptr), i32(b.kv_indices), i32(b.last_page_len)
+    pka.pka_append_paged_kv_cache(params, *rows, i32([0, kv, kv + 20]), *table, *pools,
+                                  pools[0].stride(0))
+    kw = dict(num_qo_heads=hq, num_kv_heads=hk, head_dim=d, page_size=page, kv_dtype=kv_dtype)
+    want = pka.BatchAttention()
+    want.plan(b.qo_indptr, b.kv_indptr, b.last_page_len, **kw)
+    ow, lw = want.run(bf16(b.q), *pools, table[1])
+    for capacity in (kv + 20, kv + 23, kv + 900):
+        attn = pka.BatchAttention()
+        attn.plan(b.qo_indptr, b.kv_indptr, b.last_page_len, graph_max_batch=4,
+                  graph_max_qo_rows=n, graph_max_kv_tokens=capacity, **kw)
+        attn.float_ws.fill_(255)
+        o, lse = attn.run(bf16(b.q), *pools, table[1])
+        torch.cuda.synchronize()
+        assert pka.pka_get_device_error() == 0
+        assert torch.equal(o, ow) and torch.equal(lse, lw)
