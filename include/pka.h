@@ -102,20 +102,22 @@ typedef enum pka_mask_mode {
  * codes round((x - origin) / step) clamped to 0 .. 15 (nearest, ties to even;
  * differences and quotients in float32); a group whose hi - lo is not finite
  * (NaN, infinities) is stored as NaN, and one whose step would be no normal
- * bf16 as its origin alone.  Decode rows read the codes and words without
- * rounding them (a key's weight times V's step is rounded to 11 bits, on a scale
- * of each group's own); rows with qo_len >= 2 (and decode_on_tensor_cores) read an f16
- * scratch, each value rounded once more, to 11 bits (Q, too, is brought to f16,
- * where its bf16 values are exact; Q is scaled by a power of two for each head of
- * a row, K and V for each kv head of a request, whose values below 2^-28 of its
- * largest have an error of 2^-39 of that).  A kv head of a request some of whose
- * groups of K or of V, seen or not, have their largest values more than 2^16
- * apart is read from a bf16 scratch, 8 bits of whatever magnitude.  Paged K/V only (PKA_ERR_UNSUPPORTED for ragged, for a group
- * above head_dim, for pages of 2 GB and over 4096 kv heads); everything else as
- * over e4m3 pools.  A NaN group of a key that a row sees makes the row NaN (a
- * decode row: of V, its own elements of it), and so do groups of V whose words
- * hold other values that are not finite (a decode row: infinite or NaN); rows
- * that do not see the key are not touched by it. */
+ * bf16 as its origin alone.
+ *   Decode rows read the codes and words without rounding them (a key's weight
+ * times V's step is rounded to 11 bits, on a scale of each group's own).  Rows
+ * with qo_len >= 2 (and decode_on_tensor_cores) read an f16 scratch, each value
+ * rounded once more, to 11 bits (Q, too, is brought to f16, where its bf16 values
+ * are exact; Q is scaled by a power of two for each head of a row, K and V for
+ * each kv head of a request, whose values below 2^-28 of its largest have an error
+ * of 2^-39 of that).  A kv head of a request some of whose groups of K or of V,
+ * seen or not, have their largest values more than 2^16 apart is read from a bf16
+ * scratch, 8 bits of whatever magnitude.
+ *   A NaN group of a key that a row sees makes the row NaN (a decode row: of V, its
+ * own elements of it), and so do groups of V whose words hold other values that
+ * are not finite (a decode row: infinite or NaN); rows that do not see the key are
+ * not touched by it.
+ *   Paged K/V only (PKA_ERR_UNSUPPORTED for ragged, for a group above head_dim,
+ * for pages of 2 GB and over 4096 kv heads); everything else as over e4m3 pools. */
 typedef enum pka_kv_dtype {
   PKA_KV_BF16 = 0,
   PKA_KV_FP8_E4M3 = 1,

@@ -38,13 +38,14 @@
 //   A CTA fills an SM (16 warps of 128 registers), at most one is launched on each.
 //
 // What bounds it: long rows run at 6.6 TB/s with groups of 128 of a head of 128
-// (25 ns a key of 8 heads on an SM), 6.2 with 64 and 5.2 with 32, where two or four
-// words a key instead of one are applied to the scores; D = 64 at 4.7, pages of one
-// key at 4.8.  Groups of 128 are bound by memory, the others by the warps' chains of
-// MMA, shuffle and exponential (issue slots 40 to 62% used, 16 warps).  An item's
-// start and end are 3 us, the kernel's about 10: the first copies, four look-ups
-// deep, and at the end the states' meeting, the write, the count and the join, each
-// a round trip.
+// (25 ns a key of 8 heads on an SM), 6.4 with 64 and 4.7 with 32, where two or four
+// words a key instead of one are applied to the scores (and, with 32, registers spill);
+// D = 64 at 5.2 and 4.8 (groups of 64 and 32), pages of one key at 4.3, one kv head a
+// CTA at 4.7.  Groups of 128 are bound by memory, the others by the warps' chains of
+// MMA, vote and exponential (issue slots 40 to 61% used, 16 warps).  An item's start and
+// end are 3 us, the kernel's about 10: the first copies, four look-ups deep, the first
+// tile's rescaling (0.3 us, most of it instructions on their way), and at the end the
+// states' meeting, the write, the count and the join, each a round trip.
 #include "pka_device.cuh"
 #include "pka_kv4.h"
 
@@ -246,7 +247,7 @@ __device__ __forceinline__ float sum_keys(float x) {
 // the statistics of pieces k, k + 32, ..; then the rows come in, from other SMs
 // through L2 (.cg).  Two heads at a time, R rows of each in flight: the call is a
 // chain of such round trips at the end of the kernel.  With R = 8 it is shorter, but
-// its registers are taken from the main loop's (64 requests 45.6 us, 40.5 with 4).
+// its registers are taken from the main loop's (64 requests 45.1 us, 41.2 with 4).
 template <int D>
 __device__ __noinline__ void join_heads(const AttnArgs& a, const PkaDecodeJoin j, int row,
                                         int head0, int group, int first, int step, int lane) {
@@ -342,7 +343,7 @@ __device__ __noinline__ void join_heads(const AttnArgs& a, const PkaDecodeJoin j
 // exponentials, words and products a tile.  P^T then holds the blocks in columns
 // 0..3 and 4..7; each block's V takes its own columns (the others as zeros), and
 // the two halves of O meet at the end.  With 4 qo heads a kv head: 8 requests of
-// 32K to 128K keys 138.8 us (148.0 without), 64 of 512 to 4096 40.6 (41.8).
+// 32K to 128K keys 139.2 us (152.7 without), 64 of 512 to 4096 41.2 (42.3).
 template <int D, int GR, bool HALF>
 __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     decode4_kernel(const __grid_constant__ Decode4Args p) {

@@ -179,7 +179,7 @@ __device__ __forceinline__ Group4 group4(float lo, float hi) {
 
 // 8 codes of a group, element i in bits 4i.
 //   The quotient (x - origin) / step is the product with an approximate
-// reciprocal, corrected by its residual: exact where the quotient is a float32,
+// reciprocal, corrected by its residual (a step of Newton's iteration): exact where the quotient is a float32,
 // so ties round to even as after a division, and elsewhere no quotient of 24-bit
 // by 8-bit numbers that matters lies near a tie.  The sum with 1.5 * 2^23 rounds
 // it; the code is then the low bits.  CLAMP: the origin may lie off the least

@@ -176,10 +176,11 @@ __device__ __forceinline__ void from_shared(const float* p, float (&x)[8]) {
 //   Into 4-bit pools as well.  A lane's pieces are elements 8u .. and D/2 + 8u .. of
 // a head, so a group is a power of two of lanes; only half layouts that rotate a part
 // of a head (kPartOfHalf) hand their floats on through shared memory, 16 in a row to
-// a lane.  Bound by instructions: 9,101 rows of 48 heads of 128 with the read-back of
-// what they wrote take 52.8 us with groups of a head, 55 with smaller ones, 59.4 where
-// half of each head rotates (through shared memory for all: 61.3, 60.5 and 59.6;
-// group sizes known at run time only: 64.1; four blocks an SM 59.4, two 62).
+// a lane.  Three blocks of 80 registers fill neither issue slots (54%) nor DRAM (50%):
+// 9,101 rows of 48 heads of 128 with the read-back of what they wrote take 52.6 us with
+// groups of a head, 55 with smaller ones, 59.4 where half of each head rotates (through
+// shared memory for all: 61.3, 60.5 and 59.6; group sizes known at run time only: 64.1;
+// four blocks an SM 59.4, two 62).
 constexpr int kInFlight = 2;
 
 template <int D, int L, bool APPEND, int POOL>
