@@ -105,13 +105,13 @@ class Batch:
                              kv_lens=self.kv_lens, hq=self.hq, hk=self.hk, **kw)
 
 
-def _assert_decode(o, lse, want, rows=None, staged=False, half=2.0 ** -11):
+def _assert_decode(o, lse, want, rows=None, staged=False):
     ow, lw, a_k, a_v, a_2 = want if rows is None else tuple(x[rows] for x in want)
     if rows is not None:
         o, lse = o[rows], lse[rows]
-    score = 2.0 ** -19 * a_k + (3.5 * half * a_2 if staged else 0)
+    score = 2.0 ** -19 * a_k + (3.5 * 2.0 ** -11 * a_2 if staged else 0)
     r = 2 * np.log(2) * score[..., None] + 2.0 ** -20
-    tol = (2 * r + (2 if staged else 1) * half + 2.0 ** -13) * a_v + 2.0 ** -8 * np.abs(ow)
+    tol = (2 * r + (2 if staged else 1) * 2.0 ** -11 + 2.0 ** -13) * a_v + 2.0 ** -8 * np.abs(ow)
     assert np.all(np.isfinite(o)) and np.all(np.abs(o - ow) <= tol)
     fin = np.isfinite(lw)
     assert np.array_equal(fin, np.isfinite(lse)) and np.all(lse[~fin] == -np.inf)
@@ -124,7 +124,16 @@ def _assert_staged(o, lse, want, rows=None):
 
 
 def _assert_wide(o, lse, want, rows=None):
-    _assert_decode(o, lse, want, rows, staged=True, half=2.0 ** -8)
+    rows = slice(None) if rows is None else rows
+    o, lse, (ow, lw, a_k, a_v, a_2) = o[rows], lse[rows], (x[rows] for x in want)
+    score = 2.0 ** -19 * a_k + 3.5 * 2.0 ** -8 * a_2
+    r = 2 * np.log(2) * score[..., None] + 2.0 ** -20
+    tol = (2 * r + 2 * 2.0 ** -8 + 2.0 ** -13) * a_v + 2.0 ** -8 * np.abs(ow)
+    assert np.all(np.isfinite(o)) and np.all(np.abs(o - ow) <= tol)
+    fin = np.isfinite(lw)
+    assert np.array_equal(fin, np.isfinite(lse)) and np.all(lse[~fin] == -np.inf)
+    lse, lw, score = lse[fin], lw[fin], score[fin]
+    assert np.all(np.abs(lse - lw) <= score + 2.0 ** -19 * (1 + np.abs(lw)))
 
 
 # ---------------------------------------------------------------------------
